@@ -93,8 +93,8 @@ def draw(rng):
         query = rng.choice([1, 1, _log(rng, 2, 200)])
         k = _log(rng, 2, 256)
         return dict(op=op, seqs=_log(rng, 1, 64 if query == 1 else 6), query=query,
-                    median=_log(rng, 20, 30000 if query == 1 else 2500), hkv=hkv, block=block, k=k, init=rng.randint(0, min(2, k // 2)), local=rng.randint(0, min(4, k // 2)),
-                    ties=rng.random() < 0.5)
+                    median=_log(rng, 20, 30000 if query == 1 else 2500), hkv=hkv, block=block, k=k,
+                    init=rng.randint(0, min(2, k // 2)), local=rng.randint(0, min(4, k // 2)), ties=rng.random() < 0.5)
     query = rng.choice([1, 1, 1, _log(rng, 2, 16)])
     k = max(2, _log(rng, 2, 64) * 16 // block)
     return dict(op=op, seqs=_log(rng, 1, 64 if query == 1 else 4), query=query, median=_log(rng, 20, 9000), hq=hq, hkv=hkv,
