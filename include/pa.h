@@ -9,6 +9,10 @@
  *   pa_attention_grouped  decode attention reading a shared prefix once per group
  *   pa_copy_blocks  copy whole physical blocks (the copy step of copy-on-write)
  *   pa_swap_blocks  move whole blocks between the GPU pool and a CPU pool (preemption)
+ *   pa_advance_batch    a step's block tables, slots and positions from request lengths, on the GPU
+ *   pa_norm_rope_write  RMS norm and rotary positions of query and key heads, and the cache write
+ *   pa_block_bounds / pa_block_scores / pa_select_blocks / pa_attention_sparse
+ *                   attention over the blocks that a cheap score selects for each query token
  *   pa_bm_*         host-side block accounting: free queue, block tables, ref counts, CoW
  *
  * Conventions shared by every entry point:
@@ -82,6 +86,8 @@ typedef enum {
 #define PA_DEVERR_SEQ_RANGE    0x4u  /* seq_len > max_blocks_per_seq * block_size, or q_len > seq_len */
 #define PA_DEVERR_TIMEOUT      0x8u  /* a pipeline wait gave up (the kernel returned early) */
 #define PA_DEVERR_SLOT_MISMATCH 0x10u /* pa_write_attention: a decode token's slot is not its position's slot */
+#define PA_DEVERR_NO_BLOCKS    0x20u  /* pa_advance_batch: the free list does not hold the blocks of the step */
+#define PA_DEVERR_POSITION     0x40u  /* pa_norm_rope_write: a position outside [0, max_position) */
 
 const char* pa_status_string(int status);
 int pa_last_cuda_error(void);
@@ -323,6 +329,167 @@ int pa_swap_blocks(const void* src_k, const void* src_v, void* dst_k, void* dst_
                    const int64_t* block_mapping, int64_t num_pairs, int64_t src_num_blocks,
                    int64_t dst_num_blocks, int block_size, int num_kv_heads, int head_dim,
                    pa_dtype dtype, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * pa_advance_batch -- the metadata of a step, from request lengths, on the device: [flow]
+ * 3.3 KV Manager and 3.5 Attention (block_table, slot_mapping, query_start_loc); [docs]
+ * PagedAttention, algorithm flow (a token that must go into a full block takes a new one);
+ * [read] 5.1.1 (ceil(n / B) blocks hold n tokens).
+ *
+ * Request s holds c = seq_lens[s] tokens in the first ceil(c / B) entries of its table row and
+ * gets n = query_lens[s] >= 0 new ones. In request order it takes the next
+ * ceil((c + n) / B) - ceil(c / B) blocks of the free list -- what the host block manager
+ * takes for the same appends with its free queue in the same order -- and
+ *     block_table[s, ceil(c / B) + i] = its i-th new block
+ *     query_start_loc[s + 1] = n_0 + ... + n_s,  query_start_loc[0] = 0
+ *     seq_lens_out[s] = c + n
+ *     for token t = query_start_loc[s] + j, p = c + j:
+ *         positions[t] = p,  slot_mapping[t] = block_table[s, p / B] * B + p % B
+ *     free_head_out = free_head + the blocks taken
+ * Tokens behind the last request's (up to num_tokens) get slot -1 (padding: nothing is
+ * written for them) and position 0. Nothing here knows about shared blocks: a request whose
+ * last, partly filled block is shared must have been given its copy first (pa_copy_blocks).
+ *
+ * A step that cannot be built changes neither table nor lengths: with a negative length, more
+ * than num_tokens new tokens, or a request longer than its table row (PA_DEVERR_SEQ_RANGE), or
+ * too few blocks in the free list (PA_DEVERR_NO_BLOCKS), query_start_loc is all 0, every slot
+ * -1, seq_lens_out = seq_lens and free_head_out = free_head. A block id outside
+ * [0, num_blocks) gives its tokens slot -1 (PA_DEVERR_BLOCK_RANGE).
+ *
+ * block_table   device, int32 [num_seqs, max_blocks_per_seq]; only the new entries are written
+ * seq_lens, query_lens  device, int32 [num_seqs]
+ * free_blocks   device, int32 [num_free]; free_head: device, int32 [1], entries already taken
+ * seq_lens_out, free_head_out  device; each may be its input array (a captured graph can then be
+ *               replayed step after step), else must not overlap any input
+ * query_start_loc  device, int32 [num_seqs + 1]; slot_mapping: device, int64 [num_tokens];
+ *               positions: device, int32 [num_tokens]
+ * num_tokens    entries of slot_mapping and positions: at least the new tokens of the step
+ * num_seqs and num_tokens may be 0 (num_seqs = 0: padding only). One launch, no workspace.
+ * --------------------------------------------------------------------------- */
+int pa_advance_batch(int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                     const int32_t* query_lens, const int32_t* free_blocks, int num_free,
+                     const int32_t* free_head, int32_t* seq_lens_out, int32_t* free_head_out,
+                     int32_t* query_start_loc, int64_t* slot_mapping, int32_t* positions,
+                     int num_seqs, int num_tokens, int block_size, int64_t num_blocks,
+                     pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * pa_norm_rope_write -- the rows a projection made, turned into queries and cached keys and
+ * values in one pass: [docs] PagedAttention, algorithm flow (store each new token's KV in its
+ * physical block); [flow] 3.5 (positions and slot_mapping of the flattened token batch). The
+ * norm and the rotation have no counterpart in the pages.
+ *
+ * For every token t, and every head row x of q[t] and k[t] (head_dim elements):
+ *     y = x / sqrt(mean(x^2) + eps) * weight          (q_weight / k_weight; null: y = x)
+ *     for each pair i in [0, rot_dim / 2), elements (a, b) = (i, i + rot_dim / 2), or
+ *     (2 i, 2 i + 1) when `interleaved`:
+ *         y'_a = y_a cos - y_b sin,  y'_b = y_b cos + y_a sin
+ *         cos = cos_sin[p, i], sin = cos_sin[p, rot_dim / 2 + i], p = the position of i's axis
+ *     (elements from rot_dim on keep y), then q_out[t] = y' of q, and with slot = slot_mapping[t]
+ *     >= 0: k_cache[slot] = y' of k, v_cache[slot] = v[t] (negative: nothing is cached).
+ * Arithmetic in fp32, rounded once, to the output's type; E4M3 caches store
+ * E4M3(x / k_scale) (v_scale) as pa_kv_write_fp8 does.
+ *
+ * q, k, v       device, `dtype` (PA_BF16 / PA_F32): token t's heads are contiguous at
+ *               q + t * q_stride elements (k_stride, v_stride alike), so all three may be slices
+ *               of one projection's output. Strides are multiples of 16 bytes and at least the
+ *               row; pointers are 16-byte aligned.
+ * q_out         device, [num_tokens, num_heads, head_dim], `dtype`, contiguous; may be q itself
+ *               when q is contiguous, else must not overlap the inputs
+ * q_weight, k_weight  device, [head_dim], `dtype`, or null
+ * cos_sin       device, fp32 [max_position, rot_dim]: the cosines of a position's rot_dim / 2
+ *               angles, then their sines
+ * positions     device, int32 [num_axes, num_tokens]. A token with a position outside
+ *               [0, max_position) is skipped: its q_out row and cache slot stay as they are
+ *               (PA_DEVERR_POSITION)
+ * num_axes      1 to 4; sections: host, [num_axes] pair counts that sum to rot_dim / 2: axis 0
+ *               turns the first sections[0] pairs, and so on (null with one axis). E.g. time,
+ *               height and width of an image's tokens
+ * slot_mapping  device, int64 [num_tokens], distinct non-negative slots
+ * cache_dtype   `dtype`, or PA_FP8_E4M3; caches as everywhere
+ * Supported: head_dim 64 / 128, rot_dim a multiple of 16 up to head_dim.
+ * --------------------------------------------------------------------------- */
+int pa_norm_rope_write(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, const void* q_weight, const void* k_weight,
+                       float eps, const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                       const int32_t* positions, int num_axes, const int* sections,
+                       const int64_t* slot_mapping, void* k_cache, void* v_cache, int64_t num_tokens,
+                       int64_t num_blocks, int block_size, int num_heads, int num_kv_heads,
+                       int head_dim, pa_dtype dtype, pa_dtype cache_dtype, float k_scale,
+                       float v_scale, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Block-sparse attention: each query token attends only to the blocks that a cheap score
+ * selects for it. No counterpart in the pages; built on their blocks and tables ([docs]
+ * PagedAttention, [flow] 3.5). A step runs
+ *     pa_block_bounds -> pa_block_scores -> pa_select_blocks -> pa_attention_sparse
+ * on one stream after the cache write, over the same batch arguments as pa_attention
+ * (block_table, seq_lens, query_start_loc: token t of request s sits at position
+ * p = seq_lens[s] - q_len + t - query_start_loc[s]; its context is blocks 0 .. p / block_size).
+ * Rows of tokens that belong to no request (behind the last one) are left as they are. A request
+ * with q_len > seq_len, or longer than its table row, sets PA_DEVERR_SEQ_RANGE and its rows are
+ * left as they are.
+ * Supported: head_dim 64 / 128; num_heads / num_kv_heads in {1, 2, 4, 8}; block_size a multiple
+ * of 16; bf16 queries over bf16 or E4M3 caches (any of them for bounds, scores and selection,
+ * which never read the queries' cache). No workspace; every kernel on `stream`.
+ *
+ * pa_block_bounds: for every block that holds one of the request's new tokens (positions
+ * seq_lens - q_len .. seq_lens - 1), id = its physical block:
+ *     bounds[id, g, 0, :] = min_i K_i[g, :],  bounds[id, g, 1, :] = max_i K_i[g, :]
+ * over the block's positions below seq_lens, recomputed from the cache (E4M3: the codes'
+ * values, without k_scale). Exact. bounds: device, bf16 [num_blocks, num_kv_heads, 2, head_dim],
+ * kept beside the cache by the caller. Blocks that came to hold keys in another way (copied,
+ * swapped in, cached prefixes of another pool) get their bounds by a call whose
+ * query_start_loc covers their positions. Two requests that share a block must agree on its
+ * keys (shared blocks are full, or hold the same tokens).
+ *
+ * pa_block_scores: for block b of token t's context and KV head g
+ *     scores[t, g, b] = max_h sum_d max(q_hd lo_d, q_hd hi_d)      (h: the group's query heads)
+ * -- no logit of the block, before the softmax scale (and k_scale), is larger -- and -inf for
+ * the blocks behind the context. scores: device, fp32 [num_tokens, num_kv_heads, score_width],
+ * score_width >= ceil(max_seq_len / block_size). A block id outside [0, num_blocks) scores
+ * -inf (PA_DEVERR_BLOCK_RANGE). Bounds and queries are taken as finite: a NaN or infinite one
+ * gives scores of no meaning, never an access out of range.
+ *
+ * pa_select_blocks: block_idx[t, g, :] = the token's blocks in ascending order: the first
+ * `init_blocks` and the last `local_blocks` blocks of its context always, the others by the
+ * largest score, equal scores by the lowest block, never one of score -inf or NaN; entries
+ * behind them are -1. block_idx: device, int32 [num_tokens, num_kv_heads, num_select],
+ * init_blocks + local_blocks <= num_select.
+ *
+ * pa_attention_sparse: with the blocks listed in block_idx[t, g, :] (entries below 0 are
+ * skipped, in any order; a block listed twice counts twice, one behind the context not at all):
+ *     out[t, h, :] = sum_i softmax_i(scale <q[t, h, :], K_i>) V_i
+ * over their positions i <= p; zeros where there is none. Keys past the request's length are
+ * never read. K and V are value(code) * k_scale (v_scale) for E4M3 caches, as in
+ * pa_attention_fp8 (with its range of q); k_scale and v_scale are 1 for bf16 caches. An entry
+ * >= max_blocks_per_seq or a block id outside [0, num_blocks) is skipped
+ * (PA_DEVERR_BLOCK_RANGE). out, q: device, bf16 [num_tokens, num_heads, head_dim]. The result
+ * does not depend on which physical blocks hold the tokens, nor on what else runs.
+ * --------------------------------------------------------------------------- */
+int pa_block_bounds(void* bounds, const void* k_cache, const int32_t* block_table, int max_blocks_per_seq,
+                    const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
+                    int max_query_len, int max_seq_len, int num_kv_heads, int head_dim,
+                    int block_size, int64_t num_blocks, pa_dtype cache_dtype, pa_stream_t stream);
+
+int pa_block_scores(float* scores, int score_width, const void* q, const void* bounds,
+                    const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                    const int32_t* query_start_loc, int num_seqs, int num_tokens, int max_query_len,
+                    int max_seq_len, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                    int64_t num_blocks, pa_stream_t stream);
+
+int pa_select_blocks(int32_t* block_idx, int num_select, const float* scores, int score_width,
+                     const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
+                     int num_tokens, int num_kv_heads, int block_size, int init_blocks,
+                     int local_blocks, pa_stream_t stream);
+
+int pa_attention_sparse(void* out, const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* query_start_loc, const int32_t* block_idx, int num_select,
+                        int num_seqs, int num_tokens, int max_seq_len, int num_heads,
+                        int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                        float scale, pa_dtype cache_dtype, float k_scale, float v_scale,
+                        pa_stream_t stream);
 
 /* ------------------------------------------------------------------------------
  * pa_attention_fixed_scratch -- no counterpart in the pages: an addition for callers that

@@ -29,13 +29,20 @@ __all__ = [
     "kv_write_fp8",
     "attention_fp8",
     "attention_workspace_size",
+    "advance_batch",
+    "norm_rope_write",
+    "block_bounds",
+    "block_scores",
+    "select_blocks",
+    "attention_sparse",
     "read_device_errors",
     "lib",
     "LIB_PATH",
 ]
 
 PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
-PA_DEVERR = {"slot_range": 0x1, "block_range": 0x2, "seq_range": 0x4, "timeout": 0x8, "slot_mismatch": 0x10}
+PA_DEVERR = {"slot_range": 0x1, "block_range": 0x2, "seq_range": 0x4, "timeout": 0x8, "slot_mismatch": 0x10,
+             "no_blocks": 0x20, "position": 0x40}
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -65,6 +72,14 @@ _sig = {
     "pa_attention_grouped_workspace_size": (_i, [_i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "pa_attention_grouped": (_i, [_p, _p, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64, _f, _i, _p, _p,
                                   _p, _i, _p, _sz, _p]),
+    "pa_advance_batch": (_i, [_p, _i, _p, _p, _p, _i, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i64, _p]),
+    "pa_norm_rope_write": (_i, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _f, _p, _i, _i, _i, _p, _i, _p, _p, _p, _p,
+                                _i64, _i64, _i, _i, _i, _i, _i, _i, _f, _f, _p]),
+    "pa_block_bounds": (_i, [_p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _p]),
+    "pa_block_scores": (_i, [_p, _i, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i64, _p]),
+    "pa_select_blocks": (_i, [_p, _i, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _p]),
+    "pa_attention_sparse": (_i, [_p, _p, _p, _p, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i64, _f, _i, _f,
+                                 _f, _p]),
     "pa_bm_batch_groups": (_i, [_p, _p, _i64, _i, _p, _p, _p, _i64, ctypes.POINTER(_i64)]),
     "pa_bm_enable_swap": (_i, [_p, _i64, _p]),
     "pa_bm_swap_out": (_i, [_p, _p, _i64, _p, _i64, ctypes.POINTER(_i64)]),
@@ -397,6 +412,187 @@ def attention_grouped(out, q, k_cache, v_cache, block_table, seq_lens, query_sta
                                   workspace.data_ptr() if workspace.numel() else 0, workspace.numel(),
                                   _stream(stream, k_cache.device))
     _check(st, "pa_attention_grouped")
+    return out
+
+
+def _on_device(dev: torch.device, stream, *named):
+    """Checks (name, tensor, dtype, shape) of contiguous tensors on ``dev``; None entries of a
+    shape are free. Returns the tensors' addresses and the stream to launch on."""
+    ptrs = []
+    for name, t, dtype, shape in named:
+        if not isinstance(t, torch.Tensor) or t.device != dev:
+            raise ValueError(f"{name} must be a tensor on {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        ptrs.append(t.data_ptr())
+    return ptrs, _stream(stream, dev)
+
+
+def _cuda_device(t, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _call(dev: torch.device, fn: str, *args):
+    """The library call with ``dev`` current (the library works on the current device)."""
+    if torch.cuda.current_device() == dev.index:
+        st = getattr(lib, fn)(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib, fn)(*args)
+    _check(st, fn)
+
+
+def _dims(t, name: str, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dims, got {tuple(t.shape)}")
+    return t.shape
+
+
+def advance_batch(block_table, seq_lens, query_lens, free_blocks, free_head, seq_lens_out, free_head_out,
+                  query_start_loc, slot_mapping, positions, *, block_size: int, num_blocks: int, stream=None):
+    """pa_advance_batch: a step's block tables, slots and positions from request lengths, on the GPU.
+
+    block_table int32 [S, W] (new entries written), seq_lens and query_lens int32 [S],
+    free_blocks int32 [F] with free_head int32 [1] entries already taken; writes seq_lens_out
+    [S] and free_head_out [1] (each may be its input), query_start_loc int32 [S + 1],
+    slot_mapping int64 [T] and positions int32 [T]; tokens behind the last request's get slot
+    -1 and position 0. A step that does not fit changes nothing (read_device_errors tells)."""
+    dev = _cuda_device(block_table, "block_table")
+    S, W = _dims(block_table, "block_table", 2)
+    (T,), (F,) = _dims(slot_mapping, "slot_mapping", 1), _dims(free_blocks, "free_blocks", 1)
+    i32 = torch.int32
+    p, s = _on_device(dev, stream, ("block_table", block_table, i32, (S, W)), ("seq_lens", seq_lens, i32, (S,)),
+                      ("query_lens", query_lens, i32, (S,)), ("free_blocks", free_blocks, i32, (F,)),
+                      ("free_head", free_head, i32, (1,)), ("seq_lens_out", seq_lens_out, i32, (S,)),
+                      ("free_head_out", free_head_out, i32, (1,)), ("query_start_loc", query_start_loc, i32, (S + 1,)),
+                      ("slot_mapping", slot_mapping, torch.int64, (T,)), ("positions", positions, i32, (T,)))
+    _call(dev, "pa_advance_batch", p[0], W, p[1], p[2], p[3], F, *p[4:], S, T, block_size, num_blocks, s)
+
+
+def _token_rows(t, name: str, dev, dtype, shape) -> int:
+    """A [num_tokens, heads, head_dim] tensor whose tokens may lie apart (a slice of a wider
+    projection); returns the elements between tokens."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    D = shape[2]
+    if (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != D)) and t.numel() > 0:
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if shape[0] > 1 else shape[1] * D
+
+
+def norm_rope_write(q_out, q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, k_cache, v_cache, *,
+                    eps: float = 1e-6, interleaved: bool = False, sections=None, k_scale: float = 1.0,
+                    v_scale: float = 1.0, stream=None):
+    """pa_norm_rope_write: RMS norm of each query and key head (weights [head_dim], or None: no
+    norm), rotary positions, and the cache write, in one pass.
+
+    q [T, Hq, D], k and v [T, Hkv, D]: bfloat16 or float32, tokens may lie apart (slices of one
+    projection); q_out [T, Hq, D] contiguous (may be q). cos_sin float32 [max_position,
+    rot_dim] (cosines, then sines); positions int32 [T], or [axes, T] with ``sections`` = the
+    pair counts of the axes. Caches in q's dtype or float8_e4m3fn (codes of x / scale)."""
+    NB, B, Hkv, D = _cache_geometry(k_cache, v_cache)
+    dev = _cuda_device(k_cache, "k_cache")
+    T, Hq, _ = _dims(q, "q", 3)
+    dt = q.dtype
+    axes = 1 if sections is None else len(sections)
+    limit, rot = _dims(cos_sin, "cos_sin", 2)
+    pshape = (T,) if sections is None else (axes, T)
+    qs = _token_rows(q, "q", dev, dt, (T, Hq, D))
+    ks, vs = _token_rows(k, "k", dev, dt, (T, Hkv, D)), _token_rows(v, "v", dev, dt, (T, Hkv, D))
+    named = [("q_out", q_out, dt, (T, Hq, D)), ("cos_sin", cos_sin, torch.float32, (limit, rot)),
+             ("positions", positions, torch.int32, pshape), ("slot_mapping", slot_mapping, torch.int64, (T,)),
+             ("k_cache", k_cache, k_cache.dtype, (NB, B, Hkv, D)), ("v_cache", v_cache, k_cache.dtype, (NB, B, Hkv, D))]
+    weights = [None if w is None else w.data_ptr() for w in (q_weight, k_weight)]
+    named += [(n, w, dt, (D,)) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
+    p, s = _on_device(dev, stream, *named)
+    sec = None if sections is None else (ctypes.c_int * axes)(*sections)
+    _call(dev, "pa_norm_rope_write", p[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, weights[0], weights[1],
+          eps, p[1], limit, rot, int(interleaved), p[2], axes, sec, p[3], p[4], p[5], T, NB, B, Hq, Hkv, D,
+          _dtype_code(q), _dtype_code(k_cache), k_scale, v_scale, s)
+    return q_out
+
+
+def block_bounds(bounds, k_cache, block_table, seq_lens, query_start_loc, *, max_query_len: int, max_seq_len: int,
+                 stream=None):
+    """pa_block_bounds: bounds[block, head, 0 / 1] = the smallest / largest cached key per dimension,
+    for every block that holds one of the batch's query tokens. bounds bfloat16 [num_blocks,
+    Hkv, 2, D]; caches bfloat16 or float8_e4m3fn (bounds of the codes' values)."""
+    NB, B, Hkv, D = _dims(k_cache, "k_cache", 4)
+    dev = _cuda_device(k_cache, "k_cache")
+    S, W = _dims(block_table, "block_table", 2)
+    i32 = torch.int32
+    p, s = _on_device(dev, stream, ("bounds", bounds, torch.bfloat16, (NB, Hkv, 2, D)),
+                      ("k_cache", k_cache, k_cache.dtype, (NB, B, Hkv, D)), ("block_table", block_table, i32, (S, W)),
+                      ("seq_lens", seq_lens, i32, (S,)), ("query_start_loc", query_start_loc, i32, (S + 1,)))
+    _call(dev, "pa_block_bounds", p[0], p[1], p[2], W, p[3], p[4], S, max_query_len, max_seq_len, Hkv, D, B, NB,
+          _dtype_code(k_cache), s)
+    return bounds
+
+
+def block_scores(scores, q, bounds, block_table, seq_lens, query_start_loc, *, block_size: int, max_query_len: int,
+                 max_seq_len: int, stream=None):
+    """pa_block_scores: scores[t, head, block] = an upper bound of the block's logits (before the
+    softmax scale) over the head's query group; -inf behind the token's context. scores float32
+    [T, Hkv, score_width], score_width * block_size >= max_seq_len; q bfloat16 [T, Hq, D]."""
+    T, Hq, D = _dims(q, "q", 3)
+    NB, Hkv, _, _ = _dims(bounds, "bounds", 4)
+    dev = _cuda_device(q, "q")
+    S, W = _dims(block_table, "block_table", 2)
+    width = int(_dims(scores, "scores", 3)[2])
+    i32, bf16 = torch.int32, torch.bfloat16
+    p, s = _on_device(dev, stream, ("scores", scores, torch.float32, (T, Hkv, width)), ("q", q, bf16, (T, Hq, D)),
+                      ("bounds", bounds, bf16, (NB, Hkv, 2, D)), ("block_table", block_table, i32, (S, W)),
+                      ("seq_lens", seq_lens, i32, (S,)), ("query_start_loc", query_start_loc, i32, (S + 1,)))
+    _call(dev, "pa_block_scores", p[0], width, p[1], p[2], p[3], W, p[4], p[5], S, T, max_query_len, max_seq_len, Hq,
+          Hkv, D, block_size, NB, s)
+    return scores
+
+
+def select_blocks(block_idx, scores, seq_lens, query_start_loc, *, block_size: int, init_blocks: int = 0,
+                  local_blocks: int = 0, stream=None):
+    """pa_select_blocks: block_idx[t, head] = the first init_blocks and last local_blocks of the
+    token's context and the blocks of the largest scores (equal ones: the lowest), ascending,
+    -1 behind them. block_idx int32 [T, Hkv, num_select], scores float32 [T, Hkv, width]."""
+    T, Hkv, width = _dims(scores, "scores", 3)
+    dev = _cuda_device(scores, "scores")
+    (S,) = _dims(seq_lens, "seq_lens", 1)
+    k = int(_dims(block_idx, "block_idx", 3)[2])
+    i32 = torch.int32
+    p, s = _on_device(dev, stream, ("block_idx", block_idx, i32, (T, Hkv, k)),
+                      ("scores", scores, torch.float32, (T, Hkv, width)), ("seq_lens", seq_lens, i32, (S,)),
+                      ("query_start_loc", query_start_loc, i32, (S + 1,)))
+    _call(dev, "pa_select_blocks", p[0], k, p[1], width, p[2], p[3], S, T, Hkv, block_size, init_blocks, local_blocks, s)
+    return block_idx
+
+
+def attention_sparse(out, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, block_idx, *, max_seq_len: int,
+                     scale: float, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """pa_attention_sparse: attention of each query token over the blocks listed in block_idx
+    [T, Hkv, num_select] (logical blocks of its request, entries < 0 skipped), causal; zeros for
+    an empty list. out, q bfloat16 [T, Hq, D]; caches bfloat16, or float8_e4m3fn with scales."""
+    NB, B, Hkv, D = _cache_geometry(k_cache, v_cache)
+    dev = _cuda_device(k_cache, "k_cache")
+    T, Hq, _ = _dims(q, "q", 3)
+    S, W = _dims(block_table, "block_table", 2)
+    k = int(_dims(block_idx, "block_idx", 3)[2])
+    i32, bf16 = torch.int32, torch.bfloat16
+    p, s = _on_device(dev, stream, ("out", out, bf16, (T, Hq, D)), ("q", q, bf16, (T, Hq, D)),
+                      ("k_cache", k_cache, k_cache.dtype, (NB, B, Hkv, D)),
+                      ("v_cache", v_cache, k_cache.dtype, (NB, B, Hkv, D)), ("block_table", block_table, i32, (S, W)),
+                      ("seq_lens", seq_lens, i32, (S,)), ("query_start_loc", query_start_loc, i32, (S + 1,)),
+                      ("block_idx", block_idx, i32, (T, Hkv, k)))
+    _call(dev, "pa_attention_sparse", p[0], p[1], p[2], p[3], p[4], W, p[5], p[6], p[7], k, S, T, max_seq_len, Hq, Hkv, D,
+          B, NB, scale, _dtype_code(k_cache), k_scale, v_scale, s)
     return out
 
 

@@ -1,0 +1,224 @@
+// pa_advance_batch: the metadata of a step (block tables, slot mapping, positions, query
+// offsets) from request lengths, on the device (vLLM 0.10.0 flow page, 3.3 KV Manager and
+// 3.5 Attention: slot_mapping, block_table, query_start_loc; "vLLM" docs page, algorithm
+// flow: a token that must go into a full block takes a new one; ceil(n / B) blocks for n
+// tokens).
+//
+// With c_s cached and q_s new tokens, request s takes need_s = ceil((c_s + q_s) / B) -
+// ceil(c_s / B) blocks from the free list, in request order: two exclusive prefix sums
+// (of q for the token offsets, of need for the list offsets), then every token on its own:
+// its request by binary search in the offsets, its block from the table or the free list.
+// The first token of a new block also stores the block's id in the table.
+//
+// Bound by latency, not bytes (about 28 bytes a request and token): one launch of one
+// cluster of up to 8 CTAs. Each CTA scans all requests itself (1024 at a time, from L2),
+// which costs less than handing the offsets over, and takes every C-th batch of tokens.
+// The cluster barrier before the last writes lets seq_lens_out and free_head_out be the
+// input arrays, so that one captured graph can be replayed step after step.
+#include "common.cuh"
+#include "launch.h"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 1024;
+
+struct AdvanceParams {
+  int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* query_lens;
+  const int32_t* free_blocks;
+  const int32_t* free_head;
+  int32_t* seq_lens_out;
+  int32_t* free_head_out;
+  int32_t* qsl;
+  int64_t* slots;
+  int32_t* positions;
+  unsigned int* err;
+  int64_t num_blocks;
+  int num_seqs, num_tokens, width, block_size, num_free;
+};
+
+struct Request {
+  int ctx, q, need;
+  bool bad;
+};
+
+__device__ __forceinline__ Request load_request(const AdvanceParams& p, int s) {
+  Request r;
+  r.ctx = p.seq_lens[s];  // not __ldg: seq_lens_out may be the same array
+  r.q = p.query_lens[s];
+  r.bad = r.ctx < 0 || r.q < 0 || int64_t(r.ctx) + r.q > int64_t(p.width) * p.block_size || r.q > p.num_tokens;
+  if (r.bad) r.ctx = r.q = 0;
+  const int B = p.block_size;
+  r.need = (r.ctx + r.q) / B - r.ctx / B + ((r.ctx + r.q) % B != 0) - (r.ctx % B != 0);
+  return r;
+}
+
+// Inclusive scan over the block of (need << 32 | q): neither half overflows once the
+// totals have been checked; the unchecked first pass sums halves of at most 2^31 each.
+__device__ uint64_t block_inclusive_scan(uint64_t x, uint64_t* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) red[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    uint64_t w = red[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += y;
+    }
+    red[lane] = w;
+  }
+  __syncthreads();
+  return x + (warp ? red[warp - 1] : 0);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvanceParams p) {
+  __shared__ uint64_t red[32];
+  __shared__ int qoff[kThreads + 1], noff[kThreads + 1], ctx[kThreads];
+  __shared__ unsigned long long total_q, total_need;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, S = p.num_seqs, B = p.block_size;
+  const int rank = int(cluster_rank()), ranks = int(cluster_size());
+  const int head = *p.free_head;  // every thread, before the barrier: free_head_out may be the same word
+
+  // Totals and checks first: a step that cannot be built changes nothing.
+  bool bad = false;
+  uint64_t sq = 0, sn = 0;
+  Request mine = {0, 0, 0, false};  // of the first tile, kept
+  for (int s = tid; s < S; s += kThreads) {
+    const Request r = load_request(p, s);
+    if (s == tid) mine = r;
+    bad |= r.bad;
+    sq += r.q;
+    sn += r.need;
+  }
+  if (tid == 0) total_q = total_need = 0;
+  bad = __syncthreads_or(bad);
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) {
+    sq += __shfl_xor_sync(0xffffffffu, sq, m);
+    sn += __shfl_xor_sync(0xffffffffu, sn, m);
+  }
+  if ((tid & 31) == 0) {
+    atomicAdd(&total_q, sq);
+    atomicAdd(&total_need, sn);
+  }
+  __syncthreads();
+  const uint64_t need_all = total_need;
+  const bool range = bad || total_q > uint64_t(p.num_tokens);
+  const bool blocks = head < 0 || uint64_t(max(head, 0)) + need_all > uint64_t(p.num_free);
+  const bool fail = range || blocks;
+  if (fail && rank == 0 && tid == 0) {
+    if (range) raise_error(p.err, PA_DEVERR_SEQ_RANGE);
+    if (blocks) raise_error(p.err, PA_DEVERR_NO_BLOCKS);
+  }
+  const int tokens = fail ? 0 : int(total_q);
+
+  int q_base = 0, n_base = head;  // of the tile
+  for (int base = 0; base < S; base += kThreads) {
+    const int s = base + tid;
+    if (base > 0 && s < S) mine = load_request(p, s);
+    const bool have = s < S && !fail;
+    const uint64_t x = have ? (uint64_t(mine.need) << 32 | uint32_t(mine.q)) : 0;
+    const uint64_t inc = block_inclusive_scan(x, red), ex = inc - x;
+    qoff[tid] = q_base + int(uint32_t(ex));
+    noff[tid] = n_base + int(ex >> 32);
+    ctx[tid] = mine.ctx;
+    if (tid == kThreads - 1) {
+      qoff[kThreads] = q_base + int(uint32_t(inc));
+      noff[kThreads] = n_base + int(inc >> 32);
+    }
+    if (rank == 0 && s < S) p.qsl[s + 1] = q_base + int(uint32_t(inc));
+    __syncthreads();
+    const int n = min(kThreads, S - base), t_end = qoff[kThreads];
+    for (int t = q_base + rank * kThreads + tid; t < t_end; t += ranks * kThreads) {
+      int lo = 0, hi = n - 1;  // the last request whose offset is <= t (requests without tokens come before it)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (qoff[mid] <= t)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int c = ctx[lo], pos = c + (t - qoff[lo]), b = pos / B, in = pos - b * B;
+      const int first_new = c / B + (c % B != 0);
+      int32_t* entry = p.table + int64_t(base + lo) * p.width + b;
+      int32_t id;
+      if (b >= first_new) {
+        id = __ldg(p.free_blocks + noff[lo] + (b - first_new));
+        if (in == 0) *entry = id;
+      } else {
+        id = *entry;
+      }
+      const bool ok = id >= 0 && id < p.num_blocks;
+      if (!ok) raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
+      p.slots[t] = ok ? int64_t(id) * B + in : -1;
+      p.positions[t] = pos;
+    }
+    q_base = t_end;
+    n_base = noff[kThreads];
+    __syncthreads();
+  }
+  if (rank == 0 && tid == 0) p.qsl[0] = 0;
+  for (int t = tokens + rank * kThreads + tid; t < p.num_tokens; t += ranks * kThreads) {
+    p.slots[t] = -1;
+    p.positions[t] = 0;
+  }
+  // every CTA has read the lengths and the head: they may now be overwritten
+  cluster_barrier();
+  if (rank != 0) return;
+  for (int s = tid; s < S; s += kThreads) p.seq_lens_out[s] = p.seq_lens[s] + (fail ? 0 : p.query_lens[s]);
+  if (tid == 0) *p.free_head_out = fail ? head : head + int(need_all);
+}
+
+}  // namespace
+
+cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t* seq_lens, const int32_t* query_lens,
+                                 const int32_t* free_blocks, int num_free, const int32_t* free_head,
+                                 int32_t* seq_lens_out, int32_t* free_head_out, int32_t* query_start_loc,
+                                 int64_t* slot_mapping, int32_t* positions, int num_seqs, int num_tokens,
+                                 int block_size, int64_t num_blocks, unsigned int* err, cudaStream_t stream) {
+  AdvanceParams p = {block_table, seq_lens,      query_lens,      free_blocks,  free_head, seq_lens_out,
+                     free_head_out, query_start_loc, slot_mapping, positions,    err,       num_blocks,
+                     num_seqs,    num_tokens,    width,           block_size,   num_free};
+  // one token a thread up to 8 CTAs (the portable cluster size), more per thread beyond
+  int ctas = 1;
+  while (ctas < 8 && int64_t(ctas) * kThreads < num_tokens) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, advance_batch_kernel, p);
+}
+
+}  // namespace pa

@@ -551,3 +551,271 @@ int pa_attention_grouped(void* out, const void* q, const void* k_cache, const vo
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- serving-step operators
+namespace {
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an > 0 && bn > 0 && x < y + uintptr_t(bn) && y < x + uintptr_t(an);
+}
+
+// The batch arguments of the block-sparse entry points; `table` false: none is read.
+int check_batch(const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                const int32_t* query_start_loc, int num_seqs, int num_tokens, int max_query_len, int max_seq_len,
+                int block_size, int64_t num_blocks, bool table, bool& nothing) {
+  if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || max_seq_len < 0 || block_size < 1 || num_blocks < 1)
+    return PA_ERR_INVALID_ARG;
+  if (block_size % 16 != 0) return PA_ERR_UNSUPPORTED;
+  nothing = num_seqs == 0 || num_tokens == 0;
+  if (nothing) return PA_OK;
+  if (!seq_lens || !query_start_loc || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4)) return PA_ERR_INVALID_ARG;
+  if (max_query_len > max_seq_len) return PA_ERR_INVALID_ARG;
+  if (!table) return PA_OK;
+  if (!block_table || !aligned(block_table, 4) || max_blocks_per_seq < 1) return PA_ERR_INVALID_ARG;
+  if (int64_t(max_blocks_per_seq) * block_size > 0x7fffffff) return PA_ERR_INVALID_ARG;
+  if (int64_t(max_blocks_per_seq) * block_size < max_seq_len) return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+int check_heads(int num_heads, int num_kv_heads, int head_dim) {
+  if (num_kv_heads < 1 || num_heads < 1 || head_dim < 1 || num_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (!pow2_le8(num_heads / num_kv_heads) || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+bool positive_finite(float x) { return x > 0.f && x != INFINITY; }
+
+}  // namespace
+
+extern "C" {
+
+int pa_advance_batch(int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_lens,
+                     const int32_t* free_blocks, int num_free, const int32_t* free_head, int32_t* seq_lens_out,
+                     int32_t* free_head_out, int32_t* query_start_loc, int64_t* slot_mapping, int32_t* positions,
+                     int num_seqs, int num_tokens, int block_size, int64_t num_blocks, pa_stream_t stream) {
+  if (num_seqs < 0 || num_tokens < 0 || num_free < 0 || block_size < 1 || num_blocks < 1) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && max_blocks_per_seq < 1) return PA_ERR_INVALID_ARG;
+  if (int64_t(max_blocks_per_seq) * block_size > 0x7fffffff) return PA_ERR_INVALID_ARG;
+  if (!free_head || !free_head_out || !query_start_loc) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!block_table || !seq_lens || !query_lens || !seq_lens_out)) return PA_ERR_INVALID_ARG;
+  if (num_free > 0 && !free_blocks) return PA_ERR_INVALID_ARG;
+  if (num_tokens > 0 && (!slot_mapping || !positions)) return PA_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(query_lens), static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(free_head), static_cast<const void*>(seq_lens_out),
+                        static_cast<const void*>(free_head_out), static_cast<const void*>(query_start_loc),
+                        static_cast<const void*>(positions)})
+    if (!aligned(p, 4)) return PA_ERR_INVALID_ARG;
+  if (!aligned(slot_mapping, 8)) return PA_ERR_INVALID_ARG;
+  // The outputs (but for the two that may be their input arrays) against everything else.
+  struct Range {
+    const void* p;
+    int64_t bytes;
+  };
+  const int64_t lens = int64_t(num_seqs) * 4;
+  const Range in[] = {{seq_lens, lens}, {query_lens, lens}, {free_blocks, int64_t(num_free) * 4}, {free_head, 4}};
+  const Range out[] = {{block_table, lens * max_blocks_per_seq}, {query_start_loc, lens + 4},
+                       {slot_mapping, int64_t(num_tokens) * 8},  {positions, int64_t(num_tokens) * 4},
+                       {seq_lens_out, lens},                     {free_head_out, 4}};
+  for (int i = 0; i < 6; ++i) {
+    for (const Range& r : in) {
+      if ((i == 4 && r.p == seq_lens && seq_lens_out == seq_lens) || (i == 5 && r.p == free_head && free_head_out == free_head))
+        continue;
+      if (overlap(out[i].p, out[i].bytes, r.p, r.bytes)) return PA_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return PA_ERR_INVALID_ARG;
+  }
+  cudaError_t e;
+  unsigned int* err = pa::device_error_word(&e);
+  if (!err) return cuda_fail(e);
+  e = pa::launch_advance_batch(block_table, max_blocks_per_seq, seq_lens, query_lens, free_blocks, num_free, free_head,
+                               seq_lens_out, free_head_out, query_start_loc, slot_mapping, positions, num_seqs,
+                               num_tokens, block_size, num_blocks, err, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_norm_rope_write(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
+                       int max_position, int rot_dim, int interleaved, const int32_t* positions, int num_axes,
+                       const int* sections, const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                       int64_t num_tokens, int64_t num_blocks, int block_size, int num_heads, int num_kv_heads,
+                       int head_dim, pa_dtype dtype, pa_dtype cache_dtype, float k_scale, float v_scale,
+                       pa_stream_t stream) {
+  int st = check_cache(k_cache, v_cache, num_blocks, block_size, num_kv_heads, head_dim, cache_dtype);
+  if (st != PA_OK) return st;
+  if (dtype != PA_BF16 && dtype != PA_F32) return PA_ERR_INVALID_ARG;
+  if (cache_dtype != dtype && cache_dtype != PA_FP8_E4M3) return PA_ERR_INVALID_ARG;
+  if (!positive_finite(k_scale) || !positive_finite(v_scale)) return PA_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_heads < 1 || max_position < 1 || rot_dim < 2 || !(eps >= 0.f) || eps == INFINITY)
+    return PA_ERR_INVALID_ARG;
+  if (num_axes < 1 || num_axes > pa::kMaxAxes || (num_axes > 1 && !sections)) return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (rot_dim % 16 != 0 || rot_dim > head_dim) return PA_ERR_UNSUPPORTED;
+  pa::NormRopeArgs a = {};
+  if (sections) {
+    int64_t pairs = 0;
+    for (int i = 0; i < num_axes; ++i) {
+      if (sections[i] < 0) return PA_ERR_INVALID_ARG;
+      a.section_start[i] = int(pairs);
+      pairs += sections[i];
+      if (pairs > rot_dim / 2) return PA_ERR_INVALID_ARG;
+    }
+    if (pairs != rot_dim / 2) return PA_ERR_INVALID_ARG;
+  }
+  for (int i = num_axes; i < pa::kMaxAxes; ++i) a.section_start[i] = rot_dim;  // behind every pair
+  if (num_tokens == 0) return PA_OK;
+  if (!q_out || !q || !k || !v || !cos_sin || !positions || !slot_mapping) return PA_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(q_out), q, k, v, q_weight, k_weight, static_cast<const void*>(cos_sin)})
+    if (!aligned16(p)) return PA_ERR_INVALID_ARG;
+  if (!aligned(positions, 4) || !aligned(slot_mapping, 8)) return PA_ERR_INVALID_ARG;
+  const int64_t eb = elem_bytes(dtype), q_row = int64_t(num_heads) * head_dim, kv_row = int64_t(num_kv_heads) * head_dim;
+  if (num_tokens > 1 && (q_stride < q_row || k_stride < kv_row || v_stride < kv_row)) return PA_ERR_INVALID_ARG;
+  if (q_stride * eb % 16 != 0 || k_stride * eb % 16 != 0 || v_stride * eb % 16 != 0) return PA_ERR_INVALID_ARG;
+  const int64_t rows = num_heads + 2 * int64_t(num_kv_heads);
+  if (rows > 0x7fffff || num_tokens * rows > int64_t(0x7fffffff) * 8) return PA_ERR_UNSUPPORTED;  // grid
+  {  // q_out against the inputs: only q itself, in the same layout
+    const int64_t n = num_tokens - 1, out = num_tokens * q_row * eb;
+    const bool same = q_out == q && q_stride == q_row;
+    if ((!same && overlap(q_out, out, q, (n * q_stride + q_row) * eb)) ||
+        overlap(q_out, out, k, (n * k_stride + kv_row) * eb) || overlap(q_out, out, v, (n * v_stride + kv_row) * eb))
+      return PA_ERR_INVALID_ARG;
+  }
+  cudaError_t e;
+  a.err = pa::device_error_word(&e);
+  if (!a.err) return cuda_fail(e);
+  a.q_out = q_out;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.slot_mapping = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.num_tokens = num_tokens;
+  a.num_slots = num_blocks * block_size;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.rot_dim = rot_dim;
+  a.max_position = max_position;
+  a.num_axes = num_axes;
+  a.interleaved = interleaved != 0;
+  a.eps = eps;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  e = pa::launch_norm_rope_write(a, head_dim, dtype, cache_dtype, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_block_bounds(void* bounds, const void* k_cache, const int32_t* block_table, int max_blocks_per_seq,
+                    const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs, int max_query_len,
+                    int max_seq_len, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                    pa_dtype cache_dtype, pa_stream_t stream) {
+  bool nothing = false;
+  int st = check_cache(k_cache, k_cache, num_blocks, block_size, num_kv_heads, head_dim, cache_dtype);
+  if (st != PA_OK) return st;
+  if (!bounds || !aligned16(bounds)) return PA_ERR_INVALID_ARG;
+  st = check_heads(num_kv_heads, num_kv_heads, head_dim);
+  if (st != PA_OK) return st;
+  if (cache_dtype != PA_BF16 && cache_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+  st = check_batch(block_table, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, max_query_len, max_query_len,
+                   max_seq_len, block_size, num_blocks, true, nothing);
+  if (st != PA_OK || nothing) return st;
+  if (int64_t(num_seqs) * num_kv_heads * 16 > int64_t(0x7fffffff) * 256) return PA_ERR_UNSUPPORTED;  // grid
+  cudaError_t e;
+  pa::BatchArgs b = {block_table, seq_lens, query_start_loc, pa::device_error_word(&e), num_blocks, max_blocks_per_seq,
+                     num_seqs, 0, max_query_len, block_size};
+  if (!b.err) return cuda_fail(e);
+  e = pa::launch_block_bounds(b, bounds, k_cache, num_kv_heads, head_dim, cache_dtype,
+                              reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_block_scores(float* scores, int score_width, const void* q, const void* bounds, const int32_t* block_table,
+                    int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
+                    int num_tokens, int max_query_len, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                    int block_size, int64_t num_blocks, pa_stream_t stream) {
+  bool nothing = false;
+  int st = check_heads(num_heads, num_kv_heads, head_dim);
+  if (st != PA_OK) return st;
+  st = check_batch(block_table, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, num_tokens, max_query_len,
+                   max_seq_len, block_size, num_blocks, true, nothing);
+  if (st != PA_OK) return st;
+  if (score_width < 1 || (int64_t(max_seq_len) + block_size - 1) / block_size > score_width) return PA_ERR_INVALID_ARG;
+  if (nothing) return PA_OK;
+  if (!scores || !q || !bounds || !aligned(scores, 4) || !aligned16(q) || !aligned16(bounds)) return PA_ERR_INVALID_ARG;
+  const int64_t pairs = (int64_t(score_width) + 15) / 16 * num_kv_heads;
+  if (num_seqs * (pairs / 32 + 1) > 0x7fffffff) return PA_ERR_UNSUPPORTED;  // grid
+  cudaError_t e;
+  pa::BatchArgs b = {block_table, seq_lens, query_start_loc, pa::device_error_word(&e), num_blocks, max_blocks_per_seq,
+                     num_seqs, num_tokens, max_query_len, block_size};
+  if (!b.err) return cuda_fail(e);
+  e = pa::launch_block_scores(b, scores, score_width, q, bounds, num_heads, num_kv_heads, head_dim,
+                              reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_select_blocks(int32_t* block_idx, int num_select, const float* scores, int score_width, const int32_t* seq_lens,
+                     const int32_t* query_start_loc, int num_seqs, int num_tokens, int num_kv_heads, int block_size,
+                     int init_blocks, int local_blocks, pa_stream_t stream) {
+  bool nothing = false;
+  int st = check_batch(nullptr, 0, seq_lens, query_start_loc, num_seqs, num_tokens, 0, 0, block_size, 1, false, nothing);
+  if (st != PA_OK) return st;
+  if (num_kv_heads < 1 || num_select < 1 || score_width < 1 || init_blocks < 0 || local_blocks < 0)
+    return PA_ERR_INVALID_ARG;
+  if (int64_t(init_blocks) + local_blocks > num_select) return PA_ERR_INVALID_ARG;
+  if (int64_t(score_width) * block_size > 0x7fffffff) return PA_ERR_INVALID_ARG;
+  if (nothing) return PA_OK;
+  if (!block_idx || !scores || !aligned(block_idx, 4) || !aligned(scores, 4)) return PA_ERR_INVALID_ARG;
+  if (int64_t(num_tokens) * num_kv_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;  // grid
+  cudaError_t e;
+  pa::BatchArgs b = {nullptr, seq_lens, query_start_loc, pa::device_error_word(&e), 1, score_width,
+                     num_seqs, num_tokens, 0, block_size};
+  if (!b.err) return cuda_fail(e);
+  e = pa::launch_select_blocks(b, block_idx, num_select, scores, score_width, num_kv_heads, init_blocks, local_blocks,
+                               reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_attention_sparse(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                        int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start_loc,
+                        const int32_t* block_idx, int num_select, int num_seqs, int num_tokens, int max_seq_len,
+                        int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+                        pa_dtype cache_dtype, float k_scale, float v_scale, pa_stream_t stream) {
+  bool nothing = false;
+  int st = check_cache(k_cache, v_cache, num_blocks, block_size, num_kv_heads, head_dim, cache_dtype);
+  if (st != PA_OK) return st;
+  st = check_heads(num_heads, num_kv_heads, head_dim);
+  if (st != PA_OK) return st;
+  if (cache_dtype != PA_BF16 && cache_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+  if (!positive_finite(scale) || !positive_finite(k_scale) || !positive_finite(v_scale)) return PA_ERR_INVALID_ARG;
+  if (cache_dtype == PA_BF16 && (k_scale != 1.f || v_scale != 1.f)) return PA_ERR_INVALID_ARG;
+  st = check_batch(block_table, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, num_tokens, 0, max_seq_len,
+                   block_size, num_blocks, true, nothing);
+  if (st != PA_OK) return st;
+  if (num_select < 1) return PA_ERR_INVALID_ARG;
+  if (nothing) return PA_OK;
+  if (!out || !q || !block_idx || !aligned16(out) || !aligned16(q) || !aligned(block_idx, 4)) return PA_ERR_INVALID_ARG;
+  if (int64_t(num_tokens) * num_kv_heads > 0x7fffffff / 8) return PA_ERR_UNSUPPORTED;  // grid
+  if (int64_t(num_select) * (block_size / 16) > 0x7fffffff / 64) return PA_ERR_UNSUPPORTED;
+  cudaError_t e;
+  pa::BatchArgs b = {block_table, seq_lens, query_start_loc, pa::device_error_word(&e), num_blocks, max_blocks_per_seq,
+                     num_seqs, num_tokens, 0, block_size};
+  if (!b.err) return cuda_fail(e);
+  const pa::SparseAttnArgs a = {out, q, k_cache, v_cache, block_idx, num_select, num_heads, num_kv_heads, head_dim,
+                                scale, k_scale, v_scale, cache_dtype};
+  e = pa::launch_attention_sparse(b, a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -147,4 +147,74 @@ cudaError_t prepare_prefill_tc(const AttnArgs& a, PrefillTcPlan* plan);
 cudaError_t launch_prefill_tc(const AttnArgs& a, const PrefillTcPlan& plan, int num_ctas, cudaStream_t stream,
                               const PrefillLaunch& how);
 
+// ---------------------------------------------------------------- serving-step operators
+// pa_advance_batch: one cluster of up to 8 CTAs.
+cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t* seq_lens, const int32_t* query_lens,
+                                 const int32_t* free_blocks, int num_free, const int32_t* free_head,
+                                 int32_t* seq_lens_out, int32_t* free_head_out, int32_t* query_start_loc,
+                                 int64_t* slot_mapping, int32_t* positions, int num_seqs, int num_tokens,
+                                 int block_size, int64_t num_blocks, unsigned int* err, cudaStream_t stream);
+
+constexpr int kMaxAxes = 4;  // position axes of pa_norm_rope_write
+
+struct NormRopeArgs {
+  void* q_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int64_t* slot_mapping;
+  void* k_cache;
+  void* v_cache;
+  unsigned int* err;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  int64_t num_tokens, num_slots;
+  int num_heads, num_kv_heads, rot_dim, max_position, num_axes;
+  int section_start[kMaxAxes];  // first pair of each axis
+  bool interleaved;
+  float eps, k_scale, v_scale;
+};
+cudaError_t launch_norm_rope_write(const NormRopeArgs& p, int head_dim, pa_dtype dtype, pa_dtype cache_dtype,
+                                   cudaStream_t stream);
+
+// Block-sparse attention. The batch as the attention kernels take it.
+struct BatchArgs {
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  unsigned int* err;
+  int64_t num_blocks;
+  int max_blocks_per_seq;
+  int num_seqs;
+  int num_tokens;
+  int max_query_len;
+  int block_size;
+};
+// bounds[block, KV head, 0 / 1, :] = min / max over the block's keys; bf16 (E4M3 caches: of the codes' values).
+cudaError_t launch_block_bounds(const BatchArgs& b, void* bounds, const void* k_cache, int num_kv_heads, int head_dim,
+                                pa_dtype cache_dtype, cudaStream_t stream);
+// scores[t, KV head, block] (score_width blocks a row).
+cudaError_t launch_block_scores(const BatchArgs& b, float* scores, int score_width, const void* q, const void* bounds,
+                                int num_heads, int num_kv_heads, int head_dim, cudaStream_t stream);
+cudaError_t launch_select_blocks(const BatchArgs& b, int32_t* block_idx, int num_select, const float* scores,
+                                 int score_width, int num_kv_heads, int init_blocks, int local_blocks,
+                                 cudaStream_t stream);
+struct SparseAttnArgs {
+  void* out;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_idx;
+  int num_select;
+  int num_heads;
+  int num_kv_heads;
+  int head_dim;
+  float scale, k_scale, v_scale;
+  pa_dtype cache_dtype;
+};
+cudaError_t launch_attention_sparse(const BatchArgs& b, const SparseAttnArgs& a, cudaStream_t stream);
+
 }  // namespace pa
