@@ -156,6 +156,14 @@ def _stream(stream, device) -> int:
     return s.cuda_stream
 
 
+_I32, _BF16 = torch.int32, torch.bfloat16
+# The serving-step calls below take a few microseconds on the GPU at decode sizes: these two
+# answer in 0.1 us what torch.cuda.current_stream(...).cuda_stream and current_device() take 2
+# us for (a machine without CUDA has neither, and refuses every tensor before).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _cache_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor):
     if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, num_kv_heads, head_dim]")
@@ -415,42 +423,43 @@ def attention_grouped(out, q, k_cache, v_cache, block_table, seq_lens, query_sta
     return out
 
 
-def _on_device(dev: torch.device, stream, *named):
-    """Checks (name, tensor, dtype, shape) of contiguous tensors on ``dev``; None entries of a
-    shape are free. Returns the tensors' addresses and the stream to launch on."""
-    ptrs = []
-    for name, t, dtype, shape in named:
-        if not isinstance(t, torch.Tensor) or t.device != dev:
-            raise ValueError(f"{name} must be a tensor on {dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        ptrs.append(t.data_ptr())
-    return ptrs, _stream(stream, dev)
-
-
-def _cuda_device(t, name: str) -> torch.device:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _index(t, name: str) -> int:
+    """The CUDA device index of a tensor."""
+    d = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if d < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return d
 
 
-def _call(dev: torch.device, fn: str, *args):
-    """The library call with ``dev`` current (the library works on the current device)."""
-    if torch.cuda.current_device() == dev.index:
-        st = getattr(lib, fn)(*args)
+def _ptr(t, name: str, dev: int, dtype, shape) -> int:
+    """Address of a contiguous tensor of the given device, dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _call(name: str, fn, dev: int, stream, *args):
+    """The library call with device ``dev`` current (the library works on the current device), on
+    ``stream`` or that device's current stream."""
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if _current_device() == dev:
+        st = fn(*args, s)
     else:
         with torch.cuda.device(dev):
-            st = getattr(lib, fn)(*args)
-    _check(st, fn)
+            st = fn(*args, s)
+    if st != 0:
+        raise PAError(st, name)
 
 
 def _dims(t, name: str, n: int):
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dims, got {tuple(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a tensor of {n} dims")
     return t.shape
 
 
@@ -463,31 +472,30 @@ def advance_batch(block_table, seq_lens, query_lens, free_blocks, free_head, seq
     [S] and free_head_out [1] (each may be its input), query_start_loc int32 [S + 1],
     slot_mapping int64 [T] and positions int32 [T]; tokens behind the last request's get slot
     -1 and position 0. A step that does not fit changes nothing (read_device_errors tells)."""
-    dev = _cuda_device(block_table, "block_table")
+    dev = _index(block_table, "block_table")
     S, W = _dims(block_table, "block_table", 2)
     (T,), (F,) = _dims(slot_mapping, "slot_mapping", 1), _dims(free_blocks, "free_blocks", 1)
-    i32 = torch.int32
-    p, s = _on_device(dev, stream, ("block_table", block_table, i32, (S, W)), ("seq_lens", seq_lens, i32, (S,)),
-                      ("query_lens", query_lens, i32, (S,)), ("free_blocks", free_blocks, i32, (F,)),
-                      ("free_head", free_head, i32, (1,)), ("seq_lens_out", seq_lens_out, i32, (S,)),
-                      ("free_head_out", free_head_out, i32, (1,)), ("query_start_loc", query_start_loc, i32, (S + 1,)),
-                      ("slot_mapping", slot_mapping, torch.int64, (T,)), ("positions", positions, i32, (T,)))
-    _call(dev, "pa_advance_batch", p[0], W, p[1], p[2], p[3], F, *p[4:], S, T, block_size, num_blocks, s)
+    _call("pa_advance_batch", lib.pa_advance_batch, dev, stream, _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
+          _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_lens, "query_lens", dev, _I32, (S,)),
+          _ptr(free_blocks, "free_blocks", dev, _I32, (F,)), F, _ptr(free_head, "free_head", dev, _I32, (1,)),
+          _ptr(seq_lens_out, "seq_lens_out", dev, _I32, (S,)), _ptr(free_head_out, "free_head_out", dev, _I32, (1,)),
+          _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)),
+          _ptr(slot_mapping, "slot_mapping", dev, torch.int64, (T,)), _ptr(positions, "positions", dev, _I32, (T,)), S, T,
+          block_size, num_blocks)
 
 
-def _token_rows(t, name: str, dev, dtype, shape) -> int:
-    """A [num_tokens, heads, head_dim] tensor whose tokens may lie apart (a slice of a wider
-    projection); returns the elements between tokens."""
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype != dtype:
+def _token_rows(t, name: str, dev: int, dtype, shape) -> int:
+    """Elements between the tokens of a [num_tokens, heads, head_dim] tensor whose tokens may lie
+    apart (a slice of a wider projection)."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    D = shape[2]
-    if (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != D)) and t.numel() > 0:
+    if t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} on cuda:{dev}, got {list(t.shape)} on {t.device}")
+    T, H, D = shape
+    st = t.stride()
+    if (st[2] != 1 or (st[1] != D and H > 1)) and T > 0:
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.stride(0) if shape[0] > 1 else shape[1] * D
+    return st[0] if T > 1 else H * D
 
 
 def norm_rope_write(q_out, q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, k_cache, v_cache, *,
@@ -500,25 +508,26 @@ def norm_rope_write(q_out, q, k, v, q_weight, k_weight, cos_sin, positions, slot
     projection); q_out [T, Hq, D] contiguous (may be q). cos_sin float32 [max_position,
     rot_dim] (cosines, then sines); positions int32 [T], or [axes, T] with ``sections`` = the
     pair counts of the axes. Caches in q's dtype or float8_e4m3fn (codes of x / scale)."""
-    NB, B, Hkv, D = _cache_geometry(k_cache, v_cache)
-    dev = _cuda_device(k_cache, "k_cache")
+    NB, B, Hkv, D = _dims(k_cache, "k_cache", 4)
+    dev = _index(k_cache, "k_cache")
     T, Hq, _ = _dims(q, "q", 3)
-    dt = q.dtype
-    axes = 1 if sections is None else len(sections)
     limit, rot = _dims(cos_sin, "cos_sin", 2)
-    pshape = (T,) if sections is None else (axes, T)
-    qs = _token_rows(q, "q", dev, dt, (T, Hq, D))
-    ks, vs = _token_rows(k, "k", dev, dt, (T, Hkv, D)), _token_rows(v, "v", dev, dt, (T, Hkv, D))
-    named = [("q_out", q_out, dt, (T, Hq, D)), ("cos_sin", cos_sin, torch.float32, (limit, rot)),
-             ("positions", positions, torch.int32, pshape), ("slot_mapping", slot_mapping, torch.int64, (T,)),
-             ("k_cache", k_cache, k_cache.dtype, (NB, B, Hkv, D)), ("v_cache", v_cache, k_cache.dtype, (NB, B, Hkv, D))]
-    weights = [None if w is None else w.data_ptr() for w in (q_weight, k_weight)]
-    named += [(n, w, dt, (D,)) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
-    p, s = _on_device(dev, stream, *named)
-    sec = None if sections is None else (ctypes.c_int * axes)(*sections)
-    _call(dev, "pa_norm_rope_write", p[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, weights[0], weights[1],
-          eps, p[1], limit, rot, int(interleaved), p[2], axes, sec, p[3], p[4], p[5], T, NB, B, Hq, Hkv, D,
-          _dtype_code(q), _dtype_code(k_cache), k_scale, v_scale, s)
+    dt, cache_dt, kv = q.dtype, k_cache.dtype, (T, Hkv, D)
+    if sections is None:
+        axes, sec, pos = 1, None, (T,)
+    else:
+        axes = len(sections)
+        sec, pos = (ctypes.c_int * axes)(*sections), (axes, T)
+    _call("pa_norm_rope_write", lib.pa_norm_rope_write, dev, stream, _ptr(q_out, "q_out", dev, dt, (T, Hq, D)),
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_rows(q, "q", dev, dt, (T, Hq, D)),
+          _token_rows(k, "k", dev, dt, kv), _token_rows(v, "v", dev, dt, kv),
+          None if q_weight is None else _ptr(q_weight, "q_weight", dev, dt, (D,)),
+          None if k_weight is None else _ptr(k_weight, "k_weight", dev, dt, (D,)), eps,
+          _ptr(cos_sin, "cos_sin", dev, torch.float32, (limit, rot)), limit, rot, interleaved,
+          _ptr(positions, "positions", dev, _I32, pos), axes, sec,
+          _ptr(slot_mapping, "slot_mapping", dev, torch.int64, (T,)), _ptr(k_cache, "k_cache", dev, cache_dt, (NB, B, Hkv, D)),
+          _ptr(v_cache, "v_cache", dev, cache_dt, (NB, B, Hkv, D)), T, NB, B, Hq, Hkv, D, _dtype_code(q),
+          _dtype_code(k_cache), k_scale, v_scale)
     return q_out
 
 
@@ -528,14 +537,12 @@ def block_bounds(bounds, k_cache, block_table, seq_lens, query_start_loc, *, max
     for every block that holds one of the batch's query tokens. bounds bfloat16 [num_blocks,
     Hkv, 2, D]; caches bfloat16 or float8_e4m3fn (bounds of the codes' values)."""
     NB, B, Hkv, D = _dims(k_cache, "k_cache", 4)
-    dev = _cuda_device(k_cache, "k_cache")
+    dev = _index(k_cache, "k_cache")
     S, W = _dims(block_table, "block_table", 2)
-    i32 = torch.int32
-    p, s = _on_device(dev, stream, ("bounds", bounds, torch.bfloat16, (NB, Hkv, 2, D)),
-                      ("k_cache", k_cache, k_cache.dtype, (NB, B, Hkv, D)), ("block_table", block_table, i32, (S, W)),
-                      ("seq_lens", seq_lens, i32, (S,)), ("query_start_loc", query_start_loc, i32, (S + 1,)))
-    _call(dev, "pa_block_bounds", p[0], p[1], p[2], W, p[3], p[4], S, max_query_len, max_seq_len, Hkv, D, B, NB,
-          _dtype_code(k_cache), s)
+    _call("pa_block_bounds", lib.pa_block_bounds, dev, stream, _ptr(bounds, "bounds", dev, _BF16, (NB, Hkv, 2, D)),
+          _ptr(k_cache, "k_cache", dev, k_cache.dtype, (NB, B, Hkv, D)), _ptr(block_table, "block_table", dev, _I32, (S, W)),
+          W, _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S,
+          max_query_len, max_seq_len, Hkv, D, B, NB, _dtype_code(k_cache))
     return bounds
 
 
@@ -546,15 +553,14 @@ def block_scores(scores, q, bounds, block_table, seq_lens, query_start_loc, *, b
     [T, Hkv, score_width], score_width * block_size >= max_seq_len; q bfloat16 [T, Hq, D]."""
     T, Hq, D = _dims(q, "q", 3)
     NB, Hkv, _, _ = _dims(bounds, "bounds", 4)
-    dev = _cuda_device(q, "q")
+    dev = _index(q, "q")
     S, W = _dims(block_table, "block_table", 2)
-    width = int(_dims(scores, "scores", 3)[2])
-    i32, bf16 = torch.int32, torch.bfloat16
-    p, s = _on_device(dev, stream, ("scores", scores, torch.float32, (T, Hkv, width)), ("q", q, bf16, (T, Hq, D)),
-                      ("bounds", bounds, bf16, (NB, Hkv, 2, D)), ("block_table", block_table, i32, (S, W)),
-                      ("seq_lens", seq_lens, i32, (S,)), ("query_start_loc", query_start_loc, i32, (S + 1,)))
-    _call(dev, "pa_block_scores", p[0], width, p[1], p[2], p[3], W, p[4], p[5], S, T, max_query_len, max_seq_len, Hq,
-          Hkv, D, block_size, NB, s)
+    width = _dims(scores, "scores", 3)[2]
+    _call("pa_block_scores", lib.pa_block_scores, dev, stream,
+          _ptr(scores, "scores", dev, torch.float32, (T, Hkv, width)), width, _ptr(q, "q", dev, _BF16, (T, Hq, D)),
+          _ptr(bounds, "bounds", dev, _BF16, (NB, Hkv, 2, D)), _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
+          _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S, T,
+          max_query_len, max_seq_len, Hq, Hkv, D, block_size, NB)
     return scores
 
 
@@ -564,14 +570,12 @@ def select_blocks(block_idx, scores, seq_lens, query_start_loc, *, block_size: i
     token's context and the blocks of the largest scores (equal ones: the lowest), ascending,
     -1 behind them. block_idx int32 [T, Hkv, num_select], scores float32 [T, Hkv, width]."""
     T, Hkv, width = _dims(scores, "scores", 3)
-    dev = _cuda_device(scores, "scores")
+    dev = _index(scores, "scores")
     (S,) = _dims(seq_lens, "seq_lens", 1)
-    k = int(_dims(block_idx, "block_idx", 3)[2])
-    i32 = torch.int32
-    p, s = _on_device(dev, stream, ("block_idx", block_idx, i32, (T, Hkv, k)),
-                      ("scores", scores, torch.float32, (T, Hkv, width)), ("seq_lens", seq_lens, i32, (S,)),
-                      ("query_start_loc", query_start_loc, i32, (S + 1,)))
-    _call(dev, "pa_select_blocks", p[0], k, p[1], width, p[2], p[3], S, T, Hkv, block_size, init_blocks, local_blocks, s)
+    k = _dims(block_idx, "block_idx", 3)[2]
+    _call("pa_select_blocks", lib.pa_select_blocks, dev, stream, _ptr(block_idx, "block_idx", dev, _I32, (T, Hkv, k)), k,
+          _ptr(scores, "scores", dev, torch.float32, (T, Hkv, width)), width, _ptr(seq_lens, "seq_lens", dev, _I32, (S,)),
+          _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S, T, Hkv, block_size, init_blocks, local_blocks)
     return block_idx
 
 
@@ -580,19 +584,17 @@ def attention_sparse(out, q, k_cache, v_cache, block_table, seq_lens, query_star
     """pa_attention_sparse: attention of each query token over the blocks listed in block_idx
     [T, Hkv, num_select] (logical blocks of its request, entries < 0 skipped), causal; zeros for
     an empty list. out, q bfloat16 [T, Hq, D]; caches bfloat16, or float8_e4m3fn with scales."""
-    NB, B, Hkv, D = _cache_geometry(k_cache, v_cache)
-    dev = _cuda_device(k_cache, "k_cache")
+    NB, B, Hkv, D = cache = _dims(k_cache, "k_cache", 4)
+    dev, cache_dt = _index(k_cache, "k_cache"), k_cache.dtype
     T, Hq, _ = _dims(q, "q", 3)
     S, W = _dims(block_table, "block_table", 2)
-    k = int(_dims(block_idx, "block_idx", 3)[2])
-    i32, bf16 = torch.int32, torch.bfloat16
-    p, s = _on_device(dev, stream, ("out", out, bf16, (T, Hq, D)), ("q", q, bf16, (T, Hq, D)),
-                      ("k_cache", k_cache, k_cache.dtype, (NB, B, Hkv, D)),
-                      ("v_cache", v_cache, k_cache.dtype, (NB, B, Hkv, D)), ("block_table", block_table, i32, (S, W)),
-                      ("seq_lens", seq_lens, i32, (S,)), ("query_start_loc", query_start_loc, i32, (S + 1,)),
-                      ("block_idx", block_idx, i32, (T, Hkv, k)))
-    _call(dev, "pa_attention_sparse", p[0], p[1], p[2], p[3], p[4], W, p[5], p[6], p[7], k, S, T, max_seq_len, Hq, Hkv, D,
-          B, NB, scale, _dtype_code(k_cache), k_scale, v_scale, s)
+    k = _dims(block_idx, "block_idx", 3)[2]
+    _call("pa_attention_sparse", lib.pa_attention_sparse, dev, stream, _ptr(out, "out", dev, _BF16, (T, Hq, D)),
+          _ptr(q, "q", dev, _BF16, (T, Hq, D)), _ptr(k_cache, "k_cache", dev, cache_dt, cache),
+          _ptr(v_cache, "v_cache", dev, cache_dt, cache), _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
+          _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)),
+          _ptr(block_idx, "block_idx", dev, _I32, (T, Hkv, k)), k, S, T, max_seq_len, Hq, Hkv, D, B, NB, scale,
+          _dtype_code(k_cache), k_scale, v_scale)
     return out
 
 
