@@ -9,10 +9,13 @@
 // for a decode step. All arithmetic is fp32 with a single rounding to the output type: the
 // norm's result is not rounded before the rotation, which costs nothing in registers.
 //
-// A head row is D / 8 lanes of 8 elements, so a warp takes 256 / D rows at a time; the
-// sum of squares and the rotation's partner elements travel by shuffles. A warp keeps one
-// token's cos and sin in registers over kRows rows of that token, whose loads are all issued
-// before the first is used.
+// A head row is D / 8 lanes of 8 elements: 4 elements of each half of the rotated part, so that
+// every pair lies in one lane and only the sum of squares travels by shuffles (8-byte accesses,
+// each half's contiguous over the lanes). A warp takes up to kRows x 256 / D rows of one kind
+// (query, key or value heads) of one token, whose loads are all issued before the first is
+// used; the token's cosines and sines and the weights stay in registers over them. Arithmetic
+// on pairs of fp32 values (packed instructions): instructions, not bytes, were the bound of
+// the kernel with shuffled partners and scalar arithmetic.
 #include <type_traits>
 
 #include "common.cuh"
@@ -22,208 +25,222 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kRows = 4;
 
-// 8 consecutive elements -> fp32, as one or two 16-byte loads.
+__device__ __forceinline__ float2 mul2(const float2 a, const float2 b) {
+  unsigned long long d;
+  const unsigned long long aa = (static_cast<unsigned long long>(__float_as_uint(a.y)) << 32) | __float_as_uint(a.x);
+  const unsigned long long bb = (static_cast<unsigned long long>(__float_as_uint(b.y)) << 32) | __float_as_uint(b.x);
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(aa), "l"(bb));
+  return make_float2(__uint_as_float(static_cast<uint32_t>(d)), __uint_as_float(static_cast<uint32_t>(d >> 32)));
+}
+
+// 4 consecutive elements, as loaded.
 template <typename T>
-struct Vec8;
+struct Quad;
 template <>
-struct Vec8<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void unpack(float* f) const { Elem<__nv_bfloat16>::unpack(a, f); }
-  __device__ __forceinline__ void copy(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f, float) {
-    *reinterpret_cast<uint4*>(p) = Elem<__nv_bfloat16>::pack(f);
+struct Quad<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void copy(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = u; }
+  __device__ __forceinline__ void unpack(float2* f) const {
+    f[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+    f[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
   }
 };
 template <>
-struct Vec8<float> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const uint4*>(p)[0];
-    b = reinterpret_cast<const uint4*>(p)[1];
-  }
-  __device__ __forceinline__ void unpack(float* f) const {
-    Elem<float>::unpack(a, f);
-    Elem<float>::unpack(b, f + 4);
-  }
-  __device__ __forceinline__ void copy(float* p) const {
-    reinterpret_cast<uint4*>(p)[0] = a;
-    reinterpret_cast<uint4*>(p)[1] = b;
-  }
-  static __device__ __forceinline__ void store(float* p, const float* f, float) {
-    reinterpret_cast<uint4*>(p)[0] = Elem<float>::pack(f);
-    reinterpret_cast<uint4*>(p)[1] = Elem<float>::pack(f + 4);
-  }
-};
-template <>
-struct Vec8<Fp8E4M3> {
-  // E4M3(x / scale): one binary32 division, round to nearest even, saturating (as pa_kv_write_fp8)
-  static __device__ __forceinline__ void store(Fp8E4M3* p, const float* f, float scale) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      w[i] = float2_to_fp8x2(__fdiv_rn(f[4 * i], scale), __fdiv_rn(f[4 * i + 1], scale)) |
-             float2_to_fp8x2(__fdiv_rn(f[4 * i + 2], scale), __fdiv_rn(f[4 * i + 3], scale)) << 16;
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+struct Quad<float> {
+  float4 u;
+  __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void copy(float* p) const { *reinterpret_cast<float4*>(p) = u; }
+  __device__ __forceinline__ void unpack(float2* f) const {
+    f[0] = make_float2(u.x, u.y);
+    f[1] = make_float2(u.z, u.w);
   }
 };
 
-// T: type of q, k, v, weights and q_out; KV: cache type; kRows: rows a lane holds at once.
-template <typename T, typename KV, int D, int kRows>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_write_kernel(const __grid_constant__ NormRopeArgs p,
-                                                                     int warps_per_token) {
-  constexpr int LPR = D / 8;      // lanes per row
-  constexpr int RPW = 32 / LPR;   // rows a warp holds per step
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float2* f, float) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0].x, f[0].y), b = __floats2bfloat162_rn(f[1].x, f[1].y);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(float* p, const float2* f, float) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+}
+// E4M3(x / scale): one binary32 division, round to nearest even, saturating (as pa_kv_write_fp8)
+__device__ __forceinline__ void store4(Fp8E4M3* p, const float2* f, float scale) {
+  *reinterpret_cast<uint32_t*>(p) = float2_to_fp8x2(__fdiv_rn(f[0].x, scale), __fdiv_rn(f[0].y, scale)) |
+                                    float2_to_fp8x2(__fdiv_rn(f[1].x, scale), __fdiv_rn(f[1].y, scale)) << 16;
+}
+
+// T: type of q, k, v, weights and q_out; KV: cache type.
+template <typename T, typename KV, int D>
+__global__ void __launch_bounds__(kWarps * 32) norm_rope_write_kernel(const __grid_constant__ NormRopeArgs p, int q_warps,
+                                                                     int kv_warps) {
+  constexpr int LPR = D / 8;     // lanes per row
+  constexpr int RPW = 32 / LPR;  // rows a warp holds per step
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
   const int64_t w = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t t = w / warps_per_token;
+  const int per_token = q_warps + 2 * kv_warps;
+  const int64_t t = w / per_token;
   if (t >= p.num_tokens) return;
-  const int sub = lane / LPR, l = lane % LPR, d0 = l * 8;
-  const int Hq = p.num_heads, Hkv = p.num_kv_heads, R = Hq + 2 * Hkv;
-  const int row0 = int(w - t * warps_per_token) * (RPW * kRows) + sub;
+  const int part = int(w - t * per_token);
+  const bool is_q = part < q_warps, is_v = part >= q_warps + kv_warps;
+  const int heads = is_q ? p.num_heads : p.num_kv_heads;
+  const int row0 = (is_q ? part : is_v ? part - q_warps - kv_warps : part - q_warps) * (RPW * kRows) + sub;
 
-  Vec8<T> in[kRows];
+  // this lane's elements: [a, a + 4) and [b, b + 4)
+  const int rot = p.rot_dim, half = rot / 2;
+  const bool rotated = l < rot / 8;
+  const int a = p.interleaved || !rotated ? 8 * l : 4 * l, b = p.interleaved || !rotated ? a + 4 : half + a;
+  const T* src = is_q   ? static_cast<const T*>(p.q) + t * p.q_stride
+                 : is_v ? static_cast<const T*>(p.v) + t * p.v_stride
+                        : static_cast<const T*>(p.k) + t * p.k_stride;
+  Quad<T> in[kRows][2];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = row0 + i * RPW;
-    if (r < R) {
-      const T* src = r < Hq ? static_cast<const T*>(p.q) + t * p.q_stride + int64_t(r) * D
-                     : r < Hq + Hkv ? static_cast<const T*>(p.k) + t * p.k_stride + int64_t(r - Hq) * D
-                                    : static_cast<const T*>(p.v) + t * p.v_stride + int64_t(r - Hq - Hkv) * D;
-      in[i].load(src + d0);
+    if (r < heads) {
+      in[i][0].load(src + r * D + a);
+      in[i][1].load(src + r * D + b);
     }
   }
-  const int64_t slot = __ldg(p.slot_mapping + t);
-
-  // the token's cos and sin for this lane's 8 elements: of pairs pair0 .. (interleaved: 4 of them)
-  const int rot = p.rot_dim, half = rot / 2;
-  const bool rotated = d0 < rot;
-  float cs[8], sn[8];
+  int64_t slot = 0;
+  if (!is_q) slot = __ldg(p.slot_mapping + t);
+  // ---- positions (every part of the token checks them: a bad one skips the token)
+  int pos[kMaxAxes];
   bool bad = false;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
-  {
-    const int pair0 = p.interleaved ? d0 / 2 : d0 % half;
-    if (p.num_axes == 1) {
-      const int pos = __ldg(p.positions + t);
-      bad = pos < 0 || pos >= p.max_position;
-      if (rotated && !bad) {
-        const float* row = p.cos_sin + int64_t(pos) * rot + pair0;
-        const float4 c0 = __ldg(reinterpret_cast<const float4*>(row));
-        const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half));
-        cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-        sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
-        if (!p.interleaved) {
-          const float4 c1 = __ldg(reinterpret_cast<const float4*>(row + 4));
-          const float4 s1 = __ldg(reinterpret_cast<const float4*>(row + half + 4));
-          cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-          sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
-        }
-      }
-    } else {
-      int pos[kMaxAxes];
-#pragma unroll
-      for (int a = 0; a < kMaxAxes; ++a) {
-        pos[a] = a < p.num_axes ? __ldg(p.positions + int64_t(a) * p.num_tokens + t) : 0;
-        bad |= pos[a] < 0 || pos[a] >= p.max_position;
-      }
-      if (rotated && !bad) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (e >= 4 && p.interleaved) break;
-          const int pair = pair0 + e;
-          int at = pos[0];
-#pragma unroll
-          for (int a = 1; a < kMaxAxes; ++a)
-            if (pair >= p.section_start[a]) at = pos[a];
-          const float* row = p.cos_sin + int64_t(at) * rot + pair;
-          cs[e] = __ldg(row);
-          sn[e] = __ldg(row + half);
-        }
-      }
+  for (int x = 0; x < kMaxAxes; ++x) {
+    if (x < p.num_axes) {
+      pos[x] = __ldg(p.positions + x * p.num_tokens + t);
+      bad |= pos[x] < 0 || pos[x] >= p.max_position;
     }
   }
   if (bad) {  // the whole warp: one token
     if (lane == 0) raise_error(p.err, PA_DEVERR_POSITION);
     return;
   }
-  const bool write = slot >= 0 && slot < p.num_slots;
-  if (slot >= p.num_slots && row0 == 0 && l == 0) raise_error(p.err, PA_DEVERR_SLOT_RANGE);
-  // the lane holding the partner elements (half-split pairs), or this lane
-  const int hop = half / 8, partner = p.interleaved || !rotated ? lane : d0 < half ? lane + hop : lane - hop;
-  const float sign = d0 < half ? -1.f : 1.f;
+  if (!is_q) {
+    if (slot >= p.num_slots && row0 == 0 && l == 0) raise_error(p.err, PA_DEVERR_SLOT_RANGE);
+    if (slot < 0 || slot >= p.num_slots) return;  // nothing is cached
+  }
+  KV* cache = static_cast<KV*>(is_v ? p.v_cache : p.k_cache) + slot * p.num_kv_heads * D;
+  if (is_v) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = row0 + i * RPW;
+      if (r >= heads) break;
+      if constexpr (std::is_same<T, KV>::value) {  // V's bytes as they are
+        in[i][0].copy(cache + r * D + a);
+        in[i][1].copy(cache + r * D + b);
+      } else {
+        float2 f[4];
+        in[i][0].unpack(f);
+        in[i][1].unpack(f + 2);
+        store4(cache + r * D + a, f, p.v_scale);
+        store4(cache + r * D + b, f + 2, p.v_scale);
+      }
+    }
+    return;
+  }
+  // ---- the lane's 4 pairs: cosines and sines
+  float2 cs[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  if (rotated) {
+    const int pair = 4 * l;
+    int first = pos[0], last = pos[0];  // the positions of the lane's first and last pair
+#pragma unroll
+    for (int x = 1; x < kMaxAxes; ++x) {
+      if (x < p.num_axes && pair >= p.section_start[x]) first = pos[x];
+      if (x < p.num_axes && pair + 3 >= p.section_start[x]) last = pos[x];
+    }
+    if (first == last) {
+      const float* at = p.cos_sin + int64_t(first) * rot + pair;
+      const float4 c = __ldg(reinterpret_cast<const float4*>(at)), s = __ldg(reinterpret_cast<const float4*>(at + half));
+      cs[0] = make_float2(c.x, c.y), cs[1] = make_float2(c.z, c.w);
+      sn[0] = make_float2(s.x, s.y), sn[1] = make_float2(s.z, s.w);
+    } else {  // a section ends inside
+      float c[4], s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        int at = pos[0];
+#pragma unroll
+        for (int x = 1; x < kMaxAxes; ++x)
+          if (x < p.num_axes && pair + e >= p.section_start[x]) at = pos[x];
+        c[e] = __ldg(p.cos_sin + int64_t(at) * rot + pair + e);
+        s[e] = __ldg(p.cos_sin + int64_t(at) * rot + half + pair + e);
+      }
+      cs[0] = make_float2(c[0], c[1]), cs[1] = make_float2(c[2], c[3]);
+      sn[0] = make_float2(s[0], s[1]), sn[1] = make_float2(s[2], s[3]);
+    }
+  }
+  const T* weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+  float2 wt[4];
+  if (weight) {
+    Quad<T> x;
+    x.load(weight + a);
+    x.unpack(wt);
+    x.load(weight + b);
+    x.unpack(wt + 2);
+  }
 
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = row0 + i * RPW;
-    if (r - sub >= R) break;  // warp-uniform: no row of this step
-    float f[8];
-    if (r < R) {
-      in[i].unpack(f);
-    } else {
+    if (r - sub >= heads) break;  // no row of this step
+    float2 f[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    for (int e = 0; e < 4; ++e) f[e] = make_float2(0.f, 0.f);
+    if (r < heads) {
+      in[i][0].unpack(f);
+      in[i][1].unpack(f + 2);
     }
-    const bool is_q = r < Hq, is_v = r >= Hq + Hkv;
-    const T* weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-    float ss = 0.f;
+    if (weight) {
+      float2 q2 = mul2(f[0], f[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+      for (int e = 1; e < 4; ++e) q2 = ffma2v(f[e], f[e], q2);
+      float ss = q2.x + q2.y;
 #pragma unroll
-    for (int m = LPR / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    if (!is_v && weight) {
+      for (int m = LPR / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
       const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-      Vec8<T> wv;
-      wv.load(weight + d0);
-      float wf[8];
-      wv.unpack(wf);
+      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * inv * wf[e];
+      for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(f[e], inv2), wt[e]);
     }
-    if (p.interleaved) {
-      if (!is_v && rotated) {
+    if (p.interleaved) {  // pairs (x, y) of f[e]: e-th pair of the lane
+      if (rotated) {
+        const float c[4] = {cs[0].x, cs[0].y, cs[1].x, cs[1].y}, s[4] = {sn[0].x, sn[0].y, sn[1].x, sn[1].y};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = f[2 * e], b = f[2 * e + 1];
-          f[2 * e] = a * cs[e] - b * sn[e];
-          f[2 * e + 1] = b * cs[e] + a * sn[e];
-        }
+        for (int e = 0; e < 4; ++e) f[e] = make_float2(f[e].x * c[e] - f[e].y * s[e], f[e].y * c[e] + f[e].x * s[e]);
       }
-    } else {
+    } else if (rotated) {  // pairs (f[e], f[e + 2]), element by element
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_sync(0xffffffffu, f[e], partner);
-        if (!is_v && rotated) f[e] = f[e] * cs[e] + sign * o * sn[e];
+      for (int e = 0; e < 2; ++e) {
+        const float2 u = f[e], v = f[e + 2], ns = make_float2(-sn[e].x, -sn[e].y);
+        f[e] = ffma2v(u, cs[e], mul2(v, ns));
+        f[e + 2] = ffma2v(v, cs[e], mul2(u, sn[e]));
       }
     }
-    if (r >= R) continue;
+    if (r >= heads) continue;
     if (is_q) {
-      Vec8<T>::store(static_cast<T*>(p.q_out) + (t * Hq + r) * D + d0, f, 1.f);
-    } else if (write) {
-      const int h = is_v ? r - Hq - Hkv : r - Hq;
-      KV* dst = static_cast<KV*>(is_v ? p.v_cache : p.k_cache) + (slot * Hkv + h) * D + d0;
-      if constexpr (std::is_same<T, KV>::value) {
-        if (is_v) {  // V's bytes as they are
-          in[i].copy(dst);
-          continue;
-        }
-      }
-      Vec8<KV>::store(dst, f, is_v ? p.v_scale : p.k_scale);
+      T* dst = static_cast<T*>(p.q_out) + (t * heads + r) * D;
+      store4(dst + a, f, 1.f);
+      store4(dst + b, f + 2, 1.f);
+    } else {
+      store4(cache + r * D + a, f, p.k_scale);
+      store4(cache + r * D + b, f + 2, p.k_scale);
     }
   }
 }
 
 template <typename T, typename KV, int D>
 cudaError_t launch(const NormRopeArgs& p, cudaStream_t stream) {
-  constexpr int kRows = 4;
-  const int rows = p.num_heads + 2 * p.num_kv_heads, per_warp = 32 / (D / 8) * kRows;
-  const int wpt = (rows + per_warp - 1) / per_warp;
-  const int64_t ctas = (p.num_tokens * wpt + kWarps - 1) / kWarps;
-  return launch_pdl(norm_rope_write_kernel<T, KV, D, kRows>, dim3(unsigned(ctas)), dim3(kWarps * 32), 0, stream, p,
-                    wpt);
+  constexpr int per_warp = 256 / D * kRows;
+  const int q_warps = (p.num_heads + per_warp - 1) / per_warp, kv_warps = (p.num_kv_heads + per_warp - 1) / per_warp;
+  const int64_t ctas = (p.num_tokens * (q_warps + 2 * kv_warps) + kWarps - 1) / kWarps;
+  return launch_pdl(norm_rope_write_kernel<T, KV, D>, dim3(unsigned(ctas)), dim3(kWarps * 32), 0, stream, p, q_warps,
+                    kv_warps);
 }
 
 template <int D>
