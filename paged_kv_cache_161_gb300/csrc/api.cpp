@@ -677,7 +677,7 @@ int pa_norm_rope_write(void* q_out, const void* q, const void* k, const void* v,
   if (num_tokens > 1 && (q_stride < q_row || k_stride < kv_row || v_stride < kv_row)) return PA_ERR_INVALID_ARG;
   if (q_stride * eb % 16 != 0 || k_stride * eb % 16 != 0 || v_stride * eb % 16 != 0) return PA_ERR_INVALID_ARG;
   const int64_t rows = num_heads + 2 * int64_t(num_kv_heads);
-  if (rows > 0x7fffff || num_tokens * rows > int64_t(0x7fffffff) * 8) return PA_ERR_UNSUPPORTED;  // grid
+  if (rows > 0x7fffff || num_tokens > 0x7fffffff / rows) return PA_ERR_UNSUPPORTED;  // grid: at most a warp a row
   {  // q_out against the inputs: only q itself, in the same layout
     const int64_t n = num_tokens - 1, out = num_tokens * q_row * eb;
     const bool same = q_out == q && q_stride == q_row;

@@ -24,8 +24,10 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kRows = 4;
+constexpr int kBatches = 2;
+constexpr int64_t kFill = 152 * 32 * 4;  // warps
 
 __device__ __forceinline__ float2 mul2(const float2 a, const float2 b) {
   unsigned long long d;
@@ -74,21 +76,22 @@ __device__ __forceinline__ void store4(Fp8E4M3* p, const float2* f, float scale)
 
 // T: type of q, k, v, weights and q_out; KV: cache type.
 template <typename T, typename KV, int D>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_write_kernel(const __grid_constant__ NormRopeArgs p, int q_warps,
-                                                                     int kv_warps) {
+__global__ void __launch_bounds__(kWarps * 32, 7) norm_rope_write_kernel(const __grid_constant__ NormRopeArgs p, int q_warps,
+                                                                        int kv_warps, int batches) {
   constexpr int LPR = D / 8;     // lanes per row
   constexpr int RPW = 32 / LPR;  // rows a warp holds per step
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-  const int64_t w = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int per_token = q_warps + 2 * kv_warps;
+  const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5), per_token = q_warps + 2 * kv_warps;
   const int64_t t = w / per_token;
   if (t >= p.num_tokens) return;
-  const int part = int(w - t * per_token);
+  const int part = int(w % per_token);
   const bool is_q = part < q_warps, is_v = part >= q_warps + kv_warps;
   const int heads = is_q ? p.num_heads : p.num_kv_heads;
-  const int row0 = (is_q ? part : is_v ? part - q_warps - kv_warps : part - q_warps) * (RPW * kRows) + sub;
+  // the warp's rows: `batches` times RPW x kRows of them
+  const int row_begin = (is_q ? part : is_v ? part - q_warps - kv_warps : part - q_warps) * (batches * RPW * kRows);
+  const int row_end = min(row_begin + batches * RPW * kRows, heads);
 
   // this lane's elements: [a, a + 4) and [b, b + 4)
   const int rot = p.rot_dim, half = rot / 2;
@@ -98,14 +101,15 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_write_kernel(const __gr
                  : is_v ? static_cast<const T*>(p.v) + t * p.v_stride
                         : static_cast<const T*>(p.k) + t * p.k_stride;
   Quad<T> in[kRows][2];
+  auto load_rows = [&](int row0) {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = row0 + i * RPW;
-    if (r < heads) {
+    for (int i = 0; i < kRows; ++i) {
+      const int r = min(row0 + sub + i * RPW, heads - 1);  // past the last: that row again, not stored
       in[i][0].load(src + r * D + a);
       in[i][1].load(src + r * D + b);
     }
-  }
+  };
+  load_rows(row_begin);
   int64_t slot = 0;
   if (!is_q) slot = __ldg(p.slot_mapping + t);
   // ---- positions (every part of the token checks them: a bad one skips the token)
@@ -123,14 +127,15 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_write_kernel(const __gr
     return;
   }
   if (!is_q) {
-    if (slot >= p.num_slots && row0 == 0 && l == 0) raise_error(p.err, PA_DEVERR_SLOT_RANGE);
+    if (slot >= p.num_slots && row_begin == 0 && lane == 0) raise_error(p.err, PA_DEVERR_SLOT_RANGE);
     if (slot < 0 || slot >= p.num_slots) return;  // nothing is cached
   }
   KV* cache = static_cast<KV*>(is_v ? p.v_cache : p.k_cache) + slot * p.num_kv_heads * D;
   if (is_v) {
+    for (int row0 = row_begin;;) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int r = row0 + i * RPW;
+      const int r = row0 + sub + i * RPW;
       if (r >= heads) break;
       if constexpr (std::is_same<T, KV>::value) {  // V's bytes as they are
         in[i][0].copy(cache + r * D + a);
@@ -143,7 +148,10 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_write_kernel(const __gr
         store4(cache + r * D + b, f + 2, p.v_scale);
       }
     }
-    return;
+    row0 += RPW * kRows;
+    if (row0 >= row_end) return;
+    load_rows(row0);
+    }
   }
   // ---- the lane's 4 pairs: cosines and sines
   float2 cs[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -175,26 +183,56 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_write_kernel(const __gr
       sn[0] = make_float2(s[0], s[1]), sn[1] = make_float2(s[2], s[3]);
     }
   }
+  // ---- a row is then y' = inv (f P + g Q), g the partners of f: P = w cos, Q = -/+ (the
+  // partner's w) sin (w = inv = 1 without a norm)
   const T* weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-  float2 wt[4];
-  if (weight) {
-    Quad<T> x;
-    x.load(weight + a);
-    x.unpack(wt);
-    x.load(weight + b);
-    x.unpack(wt + 2);
+  float2 P[4], Q[4];
+  {
+    float2 wt[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) wt[e] = make_float2(1.f, 1.f);
+    if (weight) {
+      Quad<T> x;
+      x.load(weight + a);
+      x.unpack(wt);
+      x.load(weight + b);
+      x.unpack(wt + 2);
+    }
+    if (p.interleaved) {
+      const float c[4] = {cs[0].x, cs[0].y, cs[1].x, cs[1].y}, z[4] = {sn[0].x, sn[0].y, sn[1].x, sn[1].y};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        P[e] = make_float2(wt[e].x * c[e], wt[e].y * c[e]);
+        Q[e] = make_float2(-wt[e].y * z[e], wt[e].x * z[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        P[e] = mul2(wt[e], cs[e]);
+        P[e + 2] = mul2(wt[e + 2], cs[e]);
+        Q[e] = mul2(wt[e + 2], make_float2(-sn[e].x, -sn[e].y));
+        Q[e + 2] = mul2(wt[e], sn[e]);
+      }
+    }
   }
 
+  for (int row0 = row_begin;;) {
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int r = row0 + i * RPW;
+    const int r = row0 + sub + i * RPW;
     if (r - sub >= heads) break;  // no row of this step
-    float2 f[4];
+    float2 f[4], y[4];
+    in[i][0].unpack(f);
+    in[i][1].unpack(f + 2);
+    if (!rotated) {  // (no product with a partner: it may be infinite)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = make_float2(0.f, 0.f);
-    if (r < heads) {
-      in[i][0].unpack(f);
-      in[i][1].unpack(f + 2);
+      for (int e = 0; e < 4; ++e) y[e] = mul2(f[e], P[e]);
+    } else if (p.interleaved) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = ffma2v(f[e], P[e], mul2(make_float2(f[e].y, f[e].x), Q[e]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = ffma2v(f[e], P[e], mul2(f[e ^ 2], Q[e]));
     }
     if (weight) {
       float2 q2 = mul2(f[0], f[0]);
@@ -204,43 +242,36 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_write_kernel(const __gr
 #pragma unroll
       for (int m = LPR / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
       const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(f[e], inv2), wt[e]);
-    }
-    if (p.interleaved) {  // pairs (x, y) of f[e]: e-th pair of the lane
-      if (rotated) {
-        const float c[4] = {cs[0].x, cs[0].y, cs[1].x, cs[1].y}, s[4] = {sn[0].x, sn[0].y, sn[1].x, sn[1].y};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = make_float2(f[e].x * c[e] - f[e].y * s[e], f[e].y * c[e] + f[e].x * s[e]);
-      }
-    } else if (rotated) {  // pairs (f[e], f[e + 2]), element by element
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 u = f[e], v = f[e + 2], ns = make_float2(-sn[e].x, -sn[e].y);
-        f[e] = ffma2v(u, cs[e], mul2(v, ns));
-        f[e + 2] = ffma2v(v, cs[e], mul2(u, sn[e]));
-      }
+      for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], make_float2(inv, inv));
     }
     if (r >= heads) continue;
     if (is_q) {
       T* dst = static_cast<T*>(p.q_out) + (t * heads + r) * D;
-      store4(dst + a, f, 1.f);
-      store4(dst + b, f + 2, 1.f);
+      store4(dst + a, y, 1.f);
+      store4(dst + b, y + 2, 1.f);
     } else {
-      store4(cache + r * D + a, f, p.k_scale);
-      store4(cache + r * D + b, f + 2, p.k_scale);
+      store4(cache + r * D + a, y, p.k_scale);
+      store4(cache + r * D + b, y + 2, p.k_scale);
     }
+  }
+  row0 += RPW * kRows;
+  if (row0 >= row_end) return;
+  load_rows(row0);
   }
 }
 
 template <typename T, typename KV, int D>
 cudaError_t launch(const NormRopeArgs& p, cudaStream_t stream) {
-  constexpr int per_warp = 256 / D * kRows;
+  // one batch of rows a warp while that is needed to fill the SMs, then up to kBatches: a warp's
+  // setup (positions, angles, weights) costs about as much as one batch
+  const int64_t once = p.num_tokens * ((p.num_heads + 2 * p.num_kv_heads) / (256 / D * kRows));
+  const int batches = once > kFill ? kBatches : 1;
+  const int per_warp = 256 / D * kRows * batches;
   const int q_warps = (p.num_heads + per_warp - 1) / per_warp, kv_warps = (p.num_kv_heads + per_warp - 1) / per_warp;
   const int64_t ctas = (p.num_tokens * (q_warps + 2 * kv_warps) + kWarps - 1) / kWarps;
   return launch_pdl(norm_rope_write_kernel<T, KV, D>, dim3(unsigned(ctas)), dim3(kWarps * 32), 0, stream, p, q_warps,
-                    kv_warps);
+                    kv_warps, batches);
 }
 
 template <int D>
