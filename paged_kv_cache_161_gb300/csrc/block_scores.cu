@@ -14,6 +14,7 @@
 // order, so the KV heads of a block, which are adjacent in memory, are read together.
 #include "block_rows.cuh"
 #include "mma.cuh"
+#include "tcgen05.cuh"
 
 namespace pa {
 namespace {
@@ -32,6 +33,14 @@ __device__ __forceinline__ uint32_t bf16x2_pos_part(uint32_t x) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Requests with more query rows than this (columns of the product) go to the tcgen05 kernel.
+constexpr int kMaxFewCols = 32;
+__device__ __forceinline__ bool is_chunk(int q_len, int G) { return int64_t(q_len) * G > kMaxFewCols; }
+__device__ __forceinline__ bool fits(const BatchArgs& b, int q0, int q_len, int L, int width) {
+  return q0 >= 0 && q0 <= b.num_tokens - q_len && q_len <= L && L <= int64_t(b.max_blocks_per_seq) * b.block_size && (L - 1) / b.block_size < width;
+}
+
+// ---------------------------------------------------------------- few query rows: mma.sync
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     block_scores_kernel(const __grid_constant__ BatchArgs b, float* __restrict__ scores, int width,
@@ -44,8 +53,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int q0 = __ldg(b.query_start_loc + s), q_len = __ldg(b.query_start_loc + s + 1) - q0;
   const int L = __ldg(b.seq_lens + s);
-  if (q_len <= 0) return;
-  if (q_len > L || L > int64_t(b.max_blocks_per_seq) * b.block_size || (L - 1) / b.block_size >= width) {
+  if (q_len <= 0 || is_chunk(q_len, G)) return;
+  if (!fits(b, q0, q_len, L, width)) {
     if (threadIdx.x == 0) raise_error(b.err, PA_DEVERR_SEQ_RANGE);
     return;
   }
@@ -112,6 +121,292 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   }
 }
 
+// ---------------------------------------------------------------- chunks: tcgen05
+// Requests of many query rows: a matrix product of 128 blocks (rows of TMEM) with up to 256
+// columns (query heads of consecutive tokens of one KV head), K = 2 D.
+//
+// A CTA keeps its columns' [q-, q+] in shared memory -- split from q once, 128 KB at D = 128 --
+// and streams the request's blocks past them: 128 rows of lo, then 128 of hi, gathered by 16-byte
+// asynchronous copies (a block's row is 2 D contiguous bytes per half) into a ring of 3 stages.
+// With 256 columns a byte of bounds read from L2 feeds 256 products; with 128 the copies, not
+// the tensor cores, were the bound. Blocks are the M side so that the maximum over a group's
+// heads runs over a thread's own accumulator columns, and 32 lanes store 32 consecutive blocks.
+// Two accumulators of 256 columns: the epilogue of one tile runs beside the next tile's MMAs.
+// Warps 0-3: epilogue (TMEM lanes 32 w ..), 4-7: producers, 8: MMA issue.
+constexpr int kChunkCols = 256;
+constexpr int kTileBlocks = 128;
+constexpr int kStages = 3;
+constexpr int kChunkThreads = 9 * 32;
+
+template <int D>
+struct ChunkLayout {
+  static constexpr uint32_t kHalfA = kTileBlocks * 128;          // 128 rows x 64 elements, 128-byte swizzle
+  static constexpr uint32_t kHalfB = kChunkCols * 128;
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t B = 0;                               // q- halves, then q+ halves
+  static constexpr uint32_t A = B + 2 * kHalves * kHalfB;        // kStages x (lo or hi)
+  static constexpr uint32_t kStageBytes = kHalves * kHalfA;
+  static constexpr uint32_t LAST = A + kStages * kStageBytes;    // int[kChunkCols]: each token's last block
+  static constexpr uint32_t BAR = LAST + kChunkCols * 4;         // full[3], empty[3], acc_full[2], acc_empty[2], done
+  static constexpr uint32_t MISC = BAR + 11 * 8;                 // TMEM address
+  static constexpr uint32_t BYTES = MISC + 8;
+  static constexpr uint32_t SMEM = BYTES + 1024;                 // + alignment slack
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  const int n = real ? 16 : 0;  // 0: nothing is read, 16 zero bytes are written
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The first column tile of request s in the grid: no scan is needed, since s + (columns before
+// it) / 256 leaves room for every request's last, partial tile.
+__device__ __forceinline__ int64_t tile_base(const BatchArgs& b, int G, int s) {
+  return int64_t(__ldg(b.query_start_loc + s)) * G / kChunkCols + s;
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    block_scores_chunk_kernel(const __grid_constant__ BatchArgs b, float* __restrict__ scores, int width,
+                              const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ bounds, int Hkv,
+                              int tiles_per_cta) {
+  using LY = ChunkLayout<D>;
+  constexpr int NH = LY::kHalves;
+  constexpr int kTokens = kChunkCols / G;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms need 1024-byte alignment
+  unsigned char* sm = smem_raw + (base - raw);
+  int* last_of = reinterpret_cast<int*>(sm + LY::LAST);
+  const uint32_t full0 = base + LY::BAR, empty0 = full0 + 8 * kStages, acc_full0 = empty0 + 8 * kStages,
+                 acc_empty0 = acc_full0 + 16, done = acc_empty0 + 16;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- this CTA's request and columns
+  const int head = blockIdx.x % Hkv;
+  const int64_t id = blockIdx.x / Hkv;
+  int lo = 0, n = b.num_seqs;  // the last request whose first tile is <= id, as in find_row
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, at < lo + n && tile_base(b, G, at) <= id);
+    const int k = m ? 31 - __clz(m) : 0, next = lo + k * step;
+    n = min(step, lo + n - next);
+    lo = next;
+  }
+  const int s = lo;
+  const int q0 = __ldg(b.query_start_loc + s), q_len = __ldg(b.query_start_loc + s + 1) - q0;
+  const int L = __ldg(b.seq_lens + s);
+  const int64_t tile64 = id - tile_base(b, G, s);
+  if (!is_chunk(q_len, G) || tile64 < 0 || tile64 * kTokens >= q_len) return;
+  if (!fits(b, q0, q_len, L, width)) {
+    if (threadIdx.x == 0) raise_error(b.err, PA_DEVERR_SEQ_RANGE);
+    return;
+  }
+  const int j0 = int(tile64) * kTokens, ntok = min(kTokens, q_len - j0), cols = ntok * G;
+  const int pos0 = L - q_len + j0;                                  // position of the first token
+  const int last_max = (pos0 + ntok - 1) / b.block_size;            // the last token's last block
+  const int tile_begin = blockIdx.y * tiles_per_cta, tiles = (width + kTileBlocks - 1) / kTileBlocks;
+  const int tile_end = min(tile_begin + tiles_per_cta, tiles);
+  const int live_end = min(tile_end, last_max / kTileBlocks + 1);   // tiles behind it are all -inf
+  const int32_t* table = b.block_table + int64_t(s) * b.max_blocks_per_seq;
+
+  // ---- setup: barriers, TMEM, the columns' [q-, q+], every token's last block
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full0 + 8 * i, 4);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full0 + 8 * i, 1);
+      mbar_init(acc_empty0 + 8 * i, 4);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tc::tmem_alloc(base + LY::MISC, 512);
+    tc::tmem_relinquish();
+  }
+  for (int j = threadIdx.x; j < kTokens; j += kChunkThreads) last_of[j] = j < ntok ? (pos0 + j) / b.block_size : -1;
+  for (int i = threadIdx.x; i < kChunkCols * (D / 8); i += kChunkThreads) {
+    const int c = i / (D / 8), piece = i % (D / 8);
+    if (c >= (cols + 15) / 16 * 16) break;  // columns the MMA does not read
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (c < cols)
+      u = __ldg(reinterpret_cast<const uint4*>(
+          q + ((int64_t(q0) + j0 + c / G) * (Hkv * G) + head * G + c % G) * D + piece * 8));
+    unsigned char* at = sm + LY::B + (piece / 8) * LY::kHalfB + c * 128 + (((piece & 7) ^ (c & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(bf16x2_neg_part(u.x), bf16x2_neg_part(u.y), bf16x2_neg_part(u.z),
+                                               bf16x2_neg_part(u.w));
+    *reinterpret_cast<uint4*>(at + NH * LY::kHalfB) =
+        make_uint4(bf16x2_pos_part(u.x), bf16x2_pos_part(u.y), bf16x2_pos_part(u.z), bf16x2_pos_part(u.w));
+  }
+  tc::fence_proxy_async_smem();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + LY::MISC);
+
+  if (warp >= 4 && warp < 8) {
+    // =========================== producers: 32 rows each ===========================
+    const int pw = warp - 4;
+    int stage = 0, it = 0;
+    bool ok = true;
+    auto hand_over = [&](int st) {  // this warp's rows of stage st have landed
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full0 + 8 * st);
+    };
+    for (int tile = tile_begin; tile < live_end && ok; ++tile) {
+      const int blk = tile * kTileBlocks + pw * 32 + lane;  // lane i looks up row i
+      int my = blk <= last_max ? __ldg(table + blk) : -1;
+      if (blk <= last_max && (my < 0 || my >= b.num_blocks)) {
+        raise_error(b.err, PA_DEVERR_BLOCK_RANGE);
+        my = -1;
+      }
+      for (int part = 0; part < 2; ++part, ++it) {
+        ok = mbar_wait(empty0 + 8 * stage, ((it / kStages) & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = base + LY::A + uint32_t(stage) * LY::kStageBytes;
+        constexpr int PPR = D / 8;                 // 16-byte pieces of a row
+        constexpr int RPI = 32 / PPR;              // rows per instruction
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += RPI) {
+          const int sub = r0 + lane / PPR, piece = lane % PPR;
+          const int idr = __shfl_sync(0xffffffffu, my, sub);
+          const int r = pw * 32 + sub;
+          const __nv_bfloat16* row = bounds + ((int64_t(max(idr, 0)) * Hkv + head) * 2 + part) * D + piece * 8;
+          cp_async16(dst + (piece / 8) * LY::kHalfA + uint32_t(r * 128) + uint32_t(((piece & 7) ^ (r & 7)) << 4), row, idr >= 0);
+        }
+        cp_async_commit();
+        if (it > 0) {  // one stage behind: its copies have had the time of this one's issue
+          cp_async_wait<1>();
+          hand_over(stage == 0 ? kStages - 1 : stage - 1);
+        }
+        if (++stage == kStages) stage = 0;
+      }
+    }
+    cp_async_wait<0>();
+    if (ok && it > 0) hand_over(stage == 0 ? kStages - 1 : stage - 1);
+    if (!ok && lane == 0) raise_error(b.err, PA_DEVERR_TIMEOUT);
+  } else if (warp == 8) {
+    // =========================== MMA issue (one thread) ===========================
+    if (lane == 0) {
+      const uint32_t idesc = tc::idesc_bf16_f32(kTileBlocks, (cols + 15) / 16 * 16, 0);
+      int stage = 0, it = 0;
+      bool ok = true;
+      for (int tile = tile_begin; tile < live_end && ok; ++tile) {
+        const int i = tile - tile_begin, buf = i & 1;
+        ok = mbar_wait(acc_empty0 + 8 * buf, ((i >> 1) & 1) ^ 1);
+        for (int part = 0; part < 2 && ok; ++part, ++it) {
+          ok = mbar_wait(full0 + 8 * stage, (it / kStages) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t a = tc::smem_desc_sw128(base + LY::A + uint32_t(stage) * LY::kStageBytes, 16, 1024);
+          const uint64_t c = tc::smem_desc_sw128(base + LY::B + uint32_t(part * NH) * LY::kHalfB, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t ko = uint32_t(k % 4) * 32;  // bytes within a 64-element half
+            tc::mma_f16(tmem + uint32_t(buf) * kChunkCols, a + ((uint32_t(k / 4) * LY::kHalfA + ko) >> 4),
+                        c + ((uint32_t(k / 4) * LY::kHalfB + ko) >> 4), idesc, (part > 0 || k > 0) ? 1u : 0u);
+          }
+          tc::mma_commit(empty0 + 8 * stage);
+          if (++stage == kStages) stage = 0;
+        }
+        if (ok) tc::mma_commit(acc_full0 + 8 * buf);
+      }
+      tc::mma_commit(done);  // nothing may still write TMEM when it is freed
+      if (!mbar_wait(done, 0)) ok = false;
+      if (!ok) raise_error(b.err, PA_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // =========================== epilogue ===========================
+    const int64_t pitch = int64_t(Hkv) * width;  // between tokens
+    float* out = scores + ((int64_t(q0) + j0) * Hkv + head) * width;
+    for (int tile = tile_begin; tile < tile_end; ++tile) {
+      const int blk = tile * kTileBlocks + warp * 32 + lane;
+      const bool live = tile < live_end;
+      bool have = false;
+      const int i = tile - tile_begin, buf = i & 1;
+      if (live) {
+        if (blk <= last_max) {
+          const int id_ = __ldg(table + blk);
+          have = id_ >= 0 && id_ < b.num_blocks;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(acc_full0 + 8 * buf, (i >> 1) & 1))) {
+          if (lane == 0) raise_error(b.err, PA_DEVERR_TIMEOUT);
+          break;
+        }
+        tc::fence_after_sync();
+      }
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        float v[32];
+        if (live) {
+          tc::tmem_ld32(tmem + uint32_t(buf) * kChunkCols + uint32_t(c0) + (uint32_t(warp * 32) << 16), v);
+          tc::tmem_wait_ld();
+        }
+#pragma unroll
+        for (int x = 0; x < 32 / G; ++x) {
+          const int j = c0 / G + x;
+          if (j >= ntok) break;
+          float m = -INFINITY;
+          if (live && have && blk <= last_of[j]) {
+            m = v[x * G];
+#pragma unroll
+            for (int h = 1; h < G; ++h) m = fmaxf(m, v[x * G + h]);
+          }
+          if (blk < width) out[j * pitch + blk] = m;
+        }
+      }
+      if (live) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty0 + 8 * buf);
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D, int G>
+cudaError_t launch_chunk(const BatchArgs& b, float* scores, int width, const __nv_bfloat16* q,
+                         const __nv_bfloat16* bounds, int Hkv, cudaStream_t stream) {
+  using LY = ChunkLayout<D>;
+  constexpr auto kern = block_scores_chunk_kernel<D, G>;
+  const cudaError_t e = ensure_smem<kern>(LY::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t x = (int64_t(b.num_tokens) * G / kChunkCols + b.num_seqs) * Hkv;
+  // few columns: the blocks are split too, until there are two CTAs a SM
+  const int tiles = (width + kTileBlocks - 1) / kTileBlocks;
+  int64_t split = (2 * 152 + x - 1) / x;
+  if (split > tiles) split = tiles;
+  const int per = int((tiles + split - 1) / split);
+  return launch_pdl(kern, dim3(unsigned(x), unsigned((tiles + per - 1) / per)), dim3(kChunkThreads), LY::SMEM, stream, b,
+                    scores, width, q, bounds, Hkv, per);
+}
+
+template <int D>
+cudaError_t dispatch_chunk(const BatchArgs& b, float* scores, int width, const __nv_bfloat16* q,
+                           const __nv_bfloat16* bounds, int Hkv, int G, cudaStream_t stream) {
+  switch (G) {
+    case 1: return launch_chunk<D, 1>(b, scores, width, q, bounds, Hkv, stream);
+    case 2: return launch_chunk<D, 2>(b, scores, width, q, bounds, Hkv, stream);
+    case 4: return launch_chunk<D, 4>(b, scores, width, q, bounds, Hkv, stream);
+    default: return launch_chunk<D, 8>(b, scores, width, q, bounds, Hkv, stream);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_block_scores(const BatchArgs& b, float* scores, int score_width, const void* q, const void* bounds,
@@ -122,6 +417,12 @@ cudaError_t launch_block_scores(const BatchArgs& b, float* scores, int score_wid
   const auto* qp = static_cast<const __nv_bfloat16*>(q);
   const auto* bp = static_cast<const __nv_bfloat16*>(bounds);
   const int G = num_heads / num_kv_heads;
+  if (int64_t(b.max_query_len) * G > kMaxFewCols) {
+    const cudaError_t e = head_dim == 64
+                              ? dispatch_chunk<64>(b, scores, score_width, qp, bp, num_kv_heads, G, stream)
+                              : dispatch_chunk<128>(b, scores, score_width, qp, bp, num_kv_heads, G, stream);
+    if (e != cudaSuccess) return e;
+  }
   if (head_dim == 64)
     return launch_pdl(block_scores_kernel<64>, grid, dim3(kWarps * 32), 0, stream, b, scores, score_width, qp, bp,
                       num_kv_heads, G, ctas_per_seq);

@@ -164,6 +164,42 @@ def test_scores(pa, name):
     assert (np.abs(got[fin] - ref[fin]) <= 2 * b.D * 2.0 ** -23 * size[fin]).all()
 
 
+CHUNKS = {  # several column tiles, several block tiles, both kernels in one call
+    "long_g4": dict(lens=[4500, 700], qs=[70, 150], Hq=8, Hkv=2),
+    "g1_d64": dict(lens=[600, 40], qs=[300, 1], Hq=2, Hkv=2, D=64),
+    "g2": dict(lens=[2100], qs=[129], Hq=4, Hkv=2),
+    "g8_mixed": dict(lens=[300, 50, 2300, 9], qs=[100, 4, 33, 9], Hq=8, Hkv=1),
+    "g8_d64": dict(lens=[500], qs=[64], Hq=16, Hkv=2, D=64),
+    "edge_32_and_33_columns": dict(lens=[200, 200, 200], qs=[8, 9, 16], Hq=4, Hkv=1),
+    "padded_wide": dict(lens=[90, 77], qs=[64, 65], Hq=4, Hkv=1, pad=5, wide=140),
+}
+
+
+@pytest.mark.parametrize("name", CHUNKS)
+def test_scores_of_chunks(pa, name):
+    b = Batch(**CHUNKS[name], seed=len(name))
+    bounds = _full_bounds(pa, b)
+    for _ in range(2):
+        got = _f64(b.scores(pa, bounds))
+        assert pa.read_device_errors() == 0
+        ref, size = ss.scores_ref(_f64(b.q), _f64(bounds), b.table, b.lens, b.qsl, b.B, b.W)
+        assert np.array_equal(np.isnan(ref), np.isnan(got))
+        assert np.array_equal(ref == -np.inf, got == -np.inf)
+        fin = np.isfinite(ref)
+        assert (np.abs(got[fin] - ref[fin]) <= 2 * b.D * 2.0 ** -23 * size[fin]).all()
+
+
+def test_scores_of_chunks_with_bad_blocks(pa):
+    b = Batch([400, 300], [100, 20], Hq=8, Hkv=2)
+    bounds = _full_bounds(pa, b)
+    b.meta[0][0, 7], b.meta[0][1, 2] = b.NB, -1
+    s = b.scores(pa, bounds)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == pa.PA_DEVERR["block_range"]
+    assert (s[:100, :, 7] == -float("inf")).all() and (s[100:, :, 2] == -float("inf")).all()
+    assert torch.isfinite(s[:100, :, 8]).all() and torch.isfinite(s[100:, :, 3]).all()
+
+
 @pytest.mark.parametrize("ties", [False, True])
 @pytest.mark.parametrize("name", BATCHES)
 def test_select(pa, name, ties):
