@@ -132,11 +132,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 // the tensor cores, were the bound. Blocks are the M side so that the maximum over a group's
 // heads runs over a thread's own accumulator columns, and 32 lanes store 32 consecutive blocks.
 // Two accumulators of 256 columns: the epilogue of one tile runs beside the next tile's MMAs.
-// Warps 0-3: epilogue (TMEM lanes 32 w ..), 4-7: producers, 8: MMA issue.
+// Warps 0-7: the columns' split, then the epilogue (TMEM lanes 32 (w % 4) .., every second 32
+// columns), 8-11: producers, 12: MMA issue.
 constexpr int kChunkCols = 256;
 constexpr int kTileBlocks = 128;
 constexpr int kStages = 3;
-constexpr int kChunkThreads = 9 * 32;
+constexpr int kEpiWarps = 8, kProdWarps = 4, kMmaWarp = kEpiWarps + kProdWarps;
+constexpr int kChunkThreads = (kMmaWarp + 1) * 32;
 
 template <int D>
 struct ChunkLayout {
@@ -146,9 +148,8 @@ struct ChunkLayout {
   static constexpr uint32_t B = 0;                               // q- halves, then q+ halves
   static constexpr uint32_t A = B + 2 * kHalves * kHalfB;        // kStages x (lo or hi)
   static constexpr uint32_t kStageBytes = kHalves * kHalfA;
-  static constexpr uint32_t LAST = A + kStages * kStageBytes;    // int[kChunkCols]: each token's last block
-  static constexpr uint32_t BAR = LAST + kChunkCols * 4;         // full[3], empty[3], acc_full[2], acc_empty[2], done
-  static constexpr uint32_t MISC = BAR + 11 * 8;                 // TMEM address
+  static constexpr uint32_t BAR = A + kStages * kStageBytes;     // full[3], empty[3], acc_full[2], acc_empty[2], done, b_full
+  static constexpr uint32_t MISC = BAR + 12 * 8;                 // TMEM address
   static constexpr uint32_t BYTES = MISC + 8;
   static constexpr uint32_t SMEM = BYTES + 1024;                 // + alignment slack
 };
@@ -181,9 +182,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms need 1024-byte alignment
   unsigned char* sm = smem_raw + (base - raw);
-  int* last_of = reinterpret_cast<int*>(sm + LY::LAST);
   const uint32_t full0 = base + LY::BAR, empty0 = full0 + 8 * kStages, acc_full0 = empty0 + 8 * kStages,
-                 acc_empty0 = acc_full0 + 16, done = acc_empty0 + 16;
+                 acc_empty0 = acc_full0 + 16, done = acc_empty0 + 16, b_full = done + 8;
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,46 +216,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int live_end = min(tile_end, last_max / kTileBlocks + 1);   // tiles behind it are all -inf
   const int32_t* table = b.block_table + int64_t(s) * b.max_blocks_per_seq;
 
-  // ---- setup: barriers, TMEM, the columns' [q-, q+], every token's last block
+  // ---- setup: barriers, TMEM
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(full0 + 8 * i, 4);
+      mbar_init(full0 + 8 * i, kProdWarps);
       mbar_init(empty0 + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full0 + 8 * i, 1);
-      mbar_init(acc_empty0 + 8 * i, 4);
+      mbar_init(acc_empty0 + 8 * i, kEpiWarps);
     }
     mbar_init(done, 1);
+    mbar_init(b_full, kEpiWarps);
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     tc::tmem_alloc(base + LY::MISC, 512);
     tc::tmem_relinquish();
   }
-  for (int j = threadIdx.x; j < kTokens; j += kChunkThreads) last_of[j] = j < ntok ? (pos0 + j) / b.block_size : -1;
-  for (int i = threadIdx.x; i < kChunkCols * (D / 8); i += kChunkThreads) {
-    const int c = i / (D / 8), piece = i % (D / 8);
-    if (c >= (cols + 15) / 16 * 16) break;  // columns the MMA does not read
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (c < cols)
-      u = __ldg(reinterpret_cast<const uint4*>(
-          q + ((int64_t(q0) + j0 + c / G) * (Hkv * G) + head * G + c % G) * D + piece * 8));
-    unsigned char* at = sm + LY::B + (piece / 8) * LY::kHalfB + c * 128 + (((piece & 7) ^ (c & 7)) << 4);
-    *reinterpret_cast<uint4*>(at) = make_uint4(bf16x2_neg_part(u.x), bf16x2_neg_part(u.y), bf16x2_neg_part(u.z),
-                                               bf16x2_neg_part(u.w));
-    *reinterpret_cast<uint4*>(at + NH * LY::kHalfB) =
-        make_uint4(bf16x2_pos_part(u.x), bf16x2_pos_part(u.y), bf16x2_pos_part(u.z), bf16x2_pos_part(u.w));
-  }
-  tc::fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + LY::MISC);
 
-  if (warp >= 4 && warp < 8) {
+  if (warp >= kEpiWarps && warp < kMmaWarp) {
     // =========================== producers: 32 rows each ===========================
-    const int pw = warp - 4;
+    const int pw = warp - kEpiWarps;
     int stage = 0, it = 0;
     bool ok = true;
     auto hand_over = [&](int st) {  // this warp's rows of stage st have landed
@@ -263,10 +249,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(full0 + 8 * st);
     };
+    auto look_up = [&](int tile) {  // lane i: row i's block
+      const int blk = tile * kTileBlocks + pw * 32 + lane;
+      return tile < live_end && blk <= last_max ? __ldg(table + blk) : -1;
+    };
+    int next = look_up(tile_begin);
     for (int tile = tile_begin; tile < live_end && ok; ++tile) {
-      const int blk = tile * kTileBlocks + pw * 32 + lane;  // lane i looks up row i
-      int my = blk <= last_max ? __ldg(table + blk) : -1;
-      if (blk <= last_max && (my < 0 || my >= b.num_blocks)) {
+      int my = next;
+      next = look_up(tile + 1);
+      if (tile * kTileBlocks + pw * 32 + lane <= last_max && (my < 0 || my >= b.num_blocks)) {
         raise_error(b.err, PA_DEVERR_BLOCK_RANGE);
         my = -1;
       }
@@ -296,12 +287,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     cp_async_wait<0>();
     if (ok && it > 0) hand_over(stage == 0 ? kStages - 1 : stage - 1);
     if (!ok && lane == 0) raise_error(b.err, PA_DEVERR_TIMEOUT);
-  } else if (warp == 8) {
+  } else if (warp == kMmaWarp) {
     // =========================== MMA issue (one thread) ===========================
     if (lane == 0) {
       const uint32_t idesc = tc::idesc_bf16_f32(kTileBlocks, (cols + 15) / 16 * 16, 0);
       int stage = 0, it = 0;
-      bool ok = true;
+      bool ok = mbar_wait(b_full, 0);
       for (int tile = tile_begin; tile < live_end && ok; ++tile) {
         const int i = tile - tile_begin, buf = i & 1;
         ok = mbar_wait(acc_empty0 + 8 * buf, ((i >> 1) & 1) ^ 1);
@@ -328,11 +319,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     __syncwarp();
   } else {
-    // =========================== epilogue ===========================
+    // =========================== columns, then epilogue ===========================
+    // the columns' [q-, q+], beside the producers' first copies: 16 bytes of a query row per
+    // step, kBatch steps' loads in flight
+    {
+      constexpr int PPR = D / 8, kBatch = 8, kThr = kEpiWarps * 32;
+      const int pieces = (cols + 15) / 16 * 16 * PPR;  // columns past them are not read by the MMA
+      const __nv_bfloat16* qp = q + ((int64_t(q0) + j0) * (Hkv * G) + head * G) * D;
+      for (int i0 = threadIdx.x; i0 < pieces; i0 += kBatch * kThr) {
+        uint4 u[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * kThr, c = i / PPR;
+          u[k] = c < cols ? __ldg(reinterpret_cast<const uint4*>(qp + (int64_t(c / G) * (Hkv * G) + c % G) * D + i % PPR * 8))
+                          : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * kThr, c = i / PPR, piece = i % PPR;
+          if (i >= pieces) break;
+          unsigned char* at = sm + LY::B + (piece / 8) * LY::kHalfB + c * 128 + (((piece & 7) ^ (c & 7)) << 4);
+          *reinterpret_cast<uint4*>(at) = make_uint4(bf16x2_neg_part(u[k].x), bf16x2_neg_part(u[k].y),
+                                                     bf16x2_neg_part(u[k].z), bf16x2_neg_part(u[k].w));
+          *reinterpret_cast<uint4*>(at + NH * LY::kHalfB) =
+              make_uint4(bf16x2_pos_part(u[k].x), bf16x2_pos_part(u[k].y), bf16x2_pos_part(u[k].z),
+                         bf16x2_pos_part(u[k].w));
+        }
+      }
+    }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_full);
+    const int quarter = warp & 3, c_first = (warp >> 2) * 32;
     const int64_t pitch = int64_t(Hkv) * width;  // between tokens
     float* out = scores + ((int64_t(q0) + j0) * Hkv + head) * width;
     for (int tile = tile_begin; tile < tile_end; ++tile) {
-      const int blk = tile * kTileBlocks + warp * 32 + lane;
+      const int blk = tile * kTileBlocks + quarter * 32 + lane;
       const bool live = tile < live_end;
       bool have = false;
       const int i = tile - tile_begin, buf = i & 1;
@@ -347,23 +369,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         tc::fence_after_sync();
       }
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        float v[32];
+      // token j sees this thread's block from position blk * B on
+      const int first_j = have ? blk * b.block_size - pos0 : 0x7fffffff;
+      for (int c0 = c_first; c0 < cols; c0 += kEpiWarps / 4 * 32) {
+        float v[32] = {};
         if (live) {
-          tc::tmem_ld32(tmem + uint32_t(buf) * kChunkCols + uint32_t(c0) + (uint32_t(warp * 32) << 16), v);
+          tc::tmem_ld32(tmem + uint32_t(buf) * kChunkCols + uint32_t(c0) + (uint32_t(quarter * 32) << 16), v);
           tc::tmem_wait_ld();
         }
+        const int jc = c0 / G, nj = min(32 / G, ntok - jc);
+        float* at = out + jc * pitch + blk;
 #pragma unroll
         for (int x = 0; x < 32 / G; ++x) {
-          const int j = c0 / G + x;
-          if (j >= ntok) break;
-          float m = -INFINITY;
-          if (live && have && blk <= last_of[j]) {
-            m = v[x * G];
+          float m = v[x * G];
 #pragma unroll
-            for (int h = 1; h < G; ++h) m = fmaxf(m, v[x * G + h]);
-          }
-          if (blk < width) out[j * pitch + blk] = m;
+          for (int h = 1; h < G; ++h) m = fmaxf(m, v[x * G + h]);
+          if (!(live && jc + x >= first_j)) m = -INFINITY;
+          if (x < nj && blk < width) *at = m;
+          at += pitch;
         }
       }
       if (live) {
@@ -376,7 +399,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 8) tc::tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
 template <int D, int G>
