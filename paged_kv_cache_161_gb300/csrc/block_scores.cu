@@ -45,9 +45,19 @@ template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     block_scores_kernel(const __grid_constant__ BatchArgs b, float* __restrict__ scores, int width,
                         const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ bounds, int Hkv, int G,
-                        int ctas_per_seq) {
+                        int ctas_per_seq, bool after_chunks) {
   constexpr int CH = D / 32;  // 32-element chunks of a row: 16 bytes a lane, two MMA steps
-  griddep_wait();
+  // Behind the chunk kernel of the same call, which this grid needs nothing of: it starts once
+  // every CTA of that kernel has (each of which then has waited for the grids before), runs
+  // beside its last ones, and waits for it only before it ends, so that what follows this grid
+  // follows both.
+  struct Ending {
+    bool wait;
+    __device__ ~Ending() {
+      if (wait) griddep_wait();
+    }
+  } ending{after_chunks};
+  if (!after_chunks) griddep_wait();
   griddep_launch_dependents();
   const int s = blockIdx.x / ctas_per_seq, part = blockIdx.x % ctas_per_seq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -216,7 +226,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int live_end = min(tile_end, last_max / kTileBlocks + 1);   // tiles behind it are all -inf
   const int32_t* table = b.block_table + int64_t(s) * b.max_blocks_per_seq;
 
-  // ---- setup: barriers, TMEM
+  // ---- setup: the query rows' loads (the epilogue warps'; 16 bytes a piece), barriers, TMEM
+  constexpr int PPR = D / 8, kEpiThreads = kEpiWarps * 32, kPieces = kChunkCols * PPR / kEpiThreads;
+  uint4 qv[kPieces];
+  if (warp < kEpiWarps) {
+    const __nv_bfloat16* qp = q + ((int64_t(q0) + j0) * (Hkv * G) + head * G) * D + int(threadIdx.x) % PPR * 8;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = (int(threadIdx.x) + k * kEpiThreads) / PPR;
+      qv[k] = c < cols ? __ldg(reinterpret_cast<const uint4*>(qp + (int64_t(c / G) * (Hkv * G) + c % G) * D))
+                       : make_uint4(0, 0, 0, 0);
+    }
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(full0 + 8 * i, kProdWarps);
@@ -266,7 +287,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t dst = base + LY::A + uint32_t(stage) * LY::kStageBytes;
-        constexpr int PPR = D / 8;                 // 16-byte pieces of a row
         constexpr int RPI = 32 / PPR;              // rows per instruction
 #pragma unroll 4
         for (int r0 = 0; r0 < 32; r0 += RPI) {
@@ -320,32 +340,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
   } else {
     // =========================== columns, then epilogue ===========================
-    // the columns' [q-, q+], beside the producers' first copies: 16 bytes of a query row per
-    // step, kBatch steps' loads in flight
-    {
-      constexpr int PPR = D / 8, kBatch = 8, kThr = kEpiWarps * 32;
-      const int pieces = (cols + 15) / 16 * 16 * PPR;  // columns past them are not read by the MMA
-      const __nv_bfloat16* qp = q + ((int64_t(q0) + j0) * (Hkv * G) + head * G) * D;
-      for (int i0 = threadIdx.x; i0 < pieces; i0 += kBatch * kThr) {
-        uint4 u[kBatch];
+    // the columns' [q-, q+], beside the producers' first copies
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int i = i0 + k * kThr, c = i / PPR;
-          u[k] = c < cols ? __ldg(reinterpret_cast<const uint4*>(qp + (int64_t(c / G) * (Hkv * G) + c % G) * D + i % PPR * 8))
-                          : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int i = i0 + k * kThr, c = i / PPR, piece = i % PPR;
-          if (i >= pieces) break;
-          unsigned char* at = sm + LY::B + (piece / 8) * LY::kHalfB + c * 128 + (((piece & 7) ^ (c & 7)) << 4);
-          *reinterpret_cast<uint4*>(at) = make_uint4(bf16x2_neg_part(u[k].x), bf16x2_neg_part(u[k].y),
-                                                     bf16x2_neg_part(u[k].z), bf16x2_neg_part(u[k].w));
-          *reinterpret_cast<uint4*>(at + NH * LY::kHalfB) =
-              make_uint4(bf16x2_pos_part(u[k].x), bf16x2_pos_part(u[k].y), bf16x2_pos_part(u[k].z),
-                         bf16x2_pos_part(u[k].w));
-        }
-      }
+    for (int k = 0; k < kPieces; ++k) {
+      const int i = threadIdx.x + k * kEpiThreads, c = i / PPR, piece = i % PPR;
+      if (c >= (cols + 15) / 16 * 16) break;  // the MMA does not read them
+      unsigned char* at = sm + LY::B + (piece / 8) * LY::kHalfB + c * 128 + (((piece & 7) ^ (c & 7)) << 4);
+      *reinterpret_cast<uint4*>(at) = make_uint4(bf16x2_neg_part(qv[k].x), bf16x2_neg_part(qv[k].y),
+                                                 bf16x2_neg_part(qv[k].z), bf16x2_neg_part(qv[k].w));
+      *reinterpret_cast<uint4*>(at + NH * LY::kHalfB) =
+          make_uint4(bf16x2_pos_part(qv[k].x), bf16x2_pos_part(qv[k].y), bf16x2_pos_part(qv[k].z),
+                     bf16x2_pos_part(qv[k].w));
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
@@ -410,11 +415,22 @@ cudaError_t launch_chunk(const BatchArgs& b, float* scores, int width, const __n
   const cudaError_t e = ensure_smem<kern>(LY::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t x = (int64_t(b.num_tokens) * G / kChunkCols + b.num_seqs) * Hkv;
-  // few columns: the blocks are split too, until there are two CTAs a SM
+  // Blocks per CTA: a CTA's setup (its request, the columns' split, the pipeline's filling) costs
+  // about as much as kSetup tiles, and one CTA runs on a SM at a time: the fewest waves x (setup
+  // + tiles). Four 512-token chunks (288 column tiles of 5 block
+  // tiles): 38.0 us in parts of 3 and 2 tiles, 29.5 us whole.
+  constexpr int64_t kSetup = 2;
   const int tiles = (width + kTileBlocks - 1) / kTileBlocks;
-  int64_t split = (2 * 152 + x - 1) / x;
-  if (split > tiles) split = tiles;
-  const int per = int((tiles + split - 1) / split);
+  int per = tiles;
+  int64_t best = INT64_MAX;
+  for (int split = 1; split <= tiles && split <= 2 * 152; ++split) {
+    const int p = (tiles + split - 1) / split;
+    const int64_t ctas = x * ((tiles + p - 1) / p), cost = (ctas + 151) / 152 * (kSetup + p);
+    if (cost < best) {
+      best = cost;
+      per = p;
+    }
+  }
   return launch_pdl(kern, dim3(unsigned(x), unsigned((tiles + per - 1) / per)), dim3(kChunkThreads), LY::SMEM, stream, b,
                     scores, width, q, bounds, Hkv, per);
 }
@@ -440,7 +456,8 @@ cudaError_t launch_block_scores(const BatchArgs& b, float* scores, int score_wid
   const auto* qp = static_cast<const __nv_bfloat16*>(q);
   const auto* bp = static_cast<const __nv_bfloat16*>(bounds);
   const int G = num_heads / num_kv_heads;
-  if (int64_t(b.max_query_len) * G > kMaxFewCols) {
+  const bool chunks = int64_t(b.max_query_len) * G > kMaxFewCols;
+  if (chunks) {
     const cudaError_t e = head_dim == 64
                               ? dispatch_chunk<64>(b, scores, score_width, qp, bp, num_kv_heads, G, stream)
                               : dispatch_chunk<128>(b, scores, score_width, qp, bp, num_kv_heads, G, stream);
@@ -448,9 +465,9 @@ cudaError_t launch_block_scores(const BatchArgs& b, float* scores, int score_wid
   }
   if (head_dim == 64)
     return launch_pdl(block_scores_kernel<64>, grid, dim3(kWarps * 32), 0, stream, b, scores, score_width, qp, bp,
-                      num_kv_heads, G, ctas_per_seq);
+                      num_kv_heads, G, ctas_per_seq, chunks);
   return launch_pdl(block_scores_kernel<128>, grid, dim3(kWarps * 32), 0, stream, b, scores, score_width, qp, bp,
-                    num_kv_heads, G, ctas_per_seq);
+                    num_kv_heads, G, ctas_per_seq, chunks);
 }
 
 }  // namespace pa
