@@ -755,7 +755,9 @@ int pa_block_scores(float* scores, int score_width, const void* q, const void* b
   if (nothing) return PA_OK;
   if (!scores || !q || !bounds || !aligned(scores, 4) || !aligned16(q) || !aligned16(bounds)) return PA_ERR_INVALID_ARG;
   const int64_t pairs = (int64_t(score_width) + 15) / 16 * num_kv_heads;
-  if (num_seqs * (pairs / 32 + 1) > 0x7fffffff) return PA_ERR_UNSUPPORTED;  // grid
+  if (pairs > 0x7fffffff / 2 || num_seqs * (pairs / 16 + 1) > 0x7fffffff) return PA_ERR_UNSUPPORTED;  // grid
+  if ((int64_t(num_tokens) * (num_heads / num_kv_heads) / 256 + num_seqs) * num_kv_heads > 0x7fffffff)
+    return PA_ERR_UNSUPPORTED;  // grid
   cudaError_t e;
   pa::BatchArgs b = {block_table, seq_lens, query_start_loc, pa::device_error_word(&e), num_blocks, max_blocks_per_seq,
                      num_seqs, num_tokens, max_query_len, block_size};

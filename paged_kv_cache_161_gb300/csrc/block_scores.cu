@@ -7,11 +7,11 @@
 // <[q-, q+], [lo, hi]>: a matrix product of the blocks' bounds (rows) with the query heads
 // (columns), whose products of bf16 values are exact in fp32 and whose sums are fp32.
 //
-// Decode is bound by the bytes of the bounds (1/16 of the keys at 16 tokens a block and bf16):
-// a warp loads 16 blocks of one KV head straight into MMA fragments -- the order of the
-// product's terms is free, so a lane takes 16 consecutive bytes of a row as the k slots of two
-// MMA steps, and no shared memory is needed. The 8 warps of a CTA take (tile, KV head) pairs in
-// order, so the KV heads of a block, which are adjacent in memory, are read together.
+// Few query rows (decode, drafts): bound by the bytes of the bounds (1/16 of the keys at 16
+// tokens a block and bf16). A warp streams tiles of 16 blocks of one KV head through a private
+// ring of kRing stages of 16-byte asynchronous copies, as pa_attention_sparse streams keys
+// (loads straight into MMA fragments, in bursts of 8 KB a warp, reached 0.81 of the copy rate).
+// Many query rows (prompt chunks): a tcgen05 product, below.
 #include "block_rows.cuh"
 #include "mma.cuh"
 #include "tcgen05.cuh"
@@ -19,8 +19,21 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kPairs = 4;  // (tile, head) pairs a warp takes
+constexpr int kWarps = 4;
+// Stages of a warp's ring: 64 x 32768 positions, 8 heads: 86.2 us with 2 (three CTAs a SM), 99.5
+// with 3 (two): more warps hide the products' latency better than deeper rings.
+constexpr int kRing = 2;
+constexpr int kTiles = 8;  // tiles of 16 blocks a warp takes
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  const int n = real ? 16 : 0;  // 0: nothing is read, 16 zero bytes are written
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ uint32_t bf16x2_neg_part(uint32_t x) {
   const __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
@@ -41,12 +54,27 @@ __device__ __forceinline__ bool fits(const BatchArgs& b, int q0, int q_len, int 
 }
 
 // ---------------------------------------------------------------- few query rows: mma.sync
+// How a CTA's warps share the KV heads and tiles: with at least kWarps heads each warp has its
+// own head (kWarps consecutive ones a CTA: adjacent in memory); with fewer, `lanes` warps per
+// head take every `lanes`-th tile.
+struct Sharing {
+  int groups, lanes, tiles;  // head groups, warps per head, tiles per CTA and head
+};
+__host__ __device__ inline Sharing sharing(int Hkv) {
+  if (Hkv >= kWarps) return {(Hkv + kWarps - 1) / kWarps, 1, kTiles};
+  return {1, kWarps / Hkv, kTiles * (kWarps / Hkv)};
+}
+
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kWarps * 32)
     block_scores_kernel(const __grid_constant__ BatchArgs b, float* __restrict__ scores, int width,
                         const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ bounds, int Hkv, int G,
                         int ctas_per_seq, bool after_chunks) {
-  constexpr int CH = D / 32;  // 32-element chunks of a row: 16 bytes a lane, two MMA steps
+  constexpr int KC = D / 16;            // MMA steps of lo (and of hi)
+  constexpr int RB = 4 * D;             // bytes of a block's row: lo, hi
+  constexpr int PPR = RB / 16;          // 16-byte pieces of it
+  constexpr int kStage = 16 * RB;
+  extern __shared__ __align__(128) unsigned char smem[];
   // Behind the chunk kernel of the same call, which this grid needs nothing of: it starts once
   // every CTA of that kernel has (each of which then has waited for the grids before), runs
   // beside its last ones, and waits for it only before it ends, so that what follows this grid
@@ -59,6 +87,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   } ending{after_chunks};
   if (!after_chunks) griddep_wait();
   griddep_launch_dependents();
+  const Sharing sh = sharing(Hkv);
   const int s = blockIdx.x / ctas_per_seq, part = blockIdx.x % ctas_per_seq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int q0 = __ldg(b.query_start_loc + s), q_len = __ldg(b.query_start_loc + s + 1) - q0;
@@ -70,53 +99,108 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   }
   const int tiles = (width + 15) / 16, blocks = (L - 1) / b.block_size + 1;
   const int32_t* table = b.block_table + int64_t(s) * b.max_blocks_per_seq;
-  const int cols = q_len * G;  // column = token * G + query head of the group
-  const float ninf = -INFINITY;
+  const int lg = __ffs(G) - 1, cols = q_len << lg;  // column = token * G + query head of the group
 
-  for (int i = 0; i < kPairs; ++i) {
-    const int64_t pair = (int64_t(part) * kPairs + i) * kWarps + warp;
-    if (pair >= int64_t(tiles) * Hkv) return;
-    const int tile = int(pair / Hkv), head = int(pair % Hkv);
-    uint4 lo[2][CH], hi[2][CH];  // rows g and g + 8 of the tile
-    bool have[2];
+  // ---- this warp's head and tiles first_tile, first_tile + sh.lanes, ..
+  const int head = sh.lanes == 1 ? part % sh.groups * kWarps + warp : warp % Hkv;
+  const int lane_of = sh.lanes == 1 ? 0 : warp / Hkv;
+  const int tile0 = part / sh.groups * sh.tiles;
+  const int first_tile = tile0 + lane_of, end_tile = min(tile0 + sh.tiles, tiles);
+  if (head >= Hkv || lane_of >= sh.lanes || first_tile >= end_tile) return;
+  const int n = (end_tile - first_tile + sh.lanes - 1) / sh.lanes;
+  // lane l < 16 looks up row l's block of a tile one tile ahead of its copies
+  auto look_up = [&](int i) {
+    const int blk = (first_tile + i * sh.lanes) * 16 + (lane & 15);
+    if (i >= n || blk >= blocks) return -1;
+    const int id = __ldg(table + blk);
+    if (id >= 0 && id < b.num_blocks) return id;
+    raise_error(b.err, PA_DEVERR_BLOCK_RANGE);
+    return -1;
+  };
+  const uint32_t ring = smem_u32(smem) + uint32_t(warp * kRing * kStage);
+  int next = look_up(0);
+  uint32_t have_ring[kRing];  // bit r: row r of the tile in that stage exists
+  auto issue = [&](int i) {
+    const int my = next;
+    next = look_up(i + 1);
+    const unsigned have = __ballot_sync(0xffffffffu, my >= 0) & 0xffffu;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int blk = tile * 16 + g + 8 * r;
-      int id = blk < blocks ? __ldg(table + blk) : -1;
-      have[r] = id >= 0 && id < b.num_blocks;
-      if (blk < blocks && !have[r]) raise_error(b.err, PA_DEVERR_BLOCK_RANGE);
-      const __nv_bfloat16* row = bounds + (int64_t(have[r] ? id : 0) * Hkv + head) * 2 * D + t * 8;
+    for (int st = 0; st < kRing; ++st)
+      if (i % kRing == st) have_ring[st] = have;
+    if (have) {
+      const uint32_t dst = ring + uint32_t(i % kRing * kStage);
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        lo[r][c] = have[r] ? __ldg(reinterpret_cast<const uint4*>(row + 32 * c)) : make_uint4(0, 0, 0, 0);
-        hi[r][c] = have[r] ? __ldg(reinterpret_cast<const uint4*>(row + D + 32 * c)) : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 16 * PPR / 32; ++k) {
+        const int r = (k * 32 + lane) / PPR, piece = (k * 32 + lane) % PPR;
+        const int id = __shfl_sync(0xffffffffu, my, r);
+        const char* src = reinterpret_cast<const char*>(bounds) + (int64_t(max(id, 0)) * Hkv + head) * RB + piece * 16;
+        cp_async16(dst + uint32_t(r * RB + ((piece ^ (r & 7)) << 4)), src, id >= 0);
       }
     }
-    for (int n0 = 0; n0 < cols; n0 += 8) {
-      const int col = n0 + g;  // this lane's B column
-      float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
-      const __nv_bfloat16* qp =
-          q + ((int64_t(q0) + (col < cols ? col / G : 0)) * (Hkv * G) + head * G + (col < cols ? col % G : 0)) * D + t * 8;
+    cp_async_commit();  // one group a tile, empty ones too
+  };
+
+  // ---- the columns' values as B fragments (k slots 2t, 2t + 1 and 2t + 8, 2t + 9 of column g)
+  uint32_t qneg[KC][2], qpos[KC][2];  // of q- and q+
+  auto load_q = [&](int n0) {
+    const int col = n0 + g;
+    const bool in = col < cols;
+    const __nv_bfloat16* row =
+        q + ((int64_t(q0) + (in ? col >> lg : 0)) * (Hkv << lg) + (head << lg) + (in ? col & (G - 1) : 0)) * D;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const uint4 u = col < cols ? __ldg(reinterpret_cast<const uint4*>(qp + 32 * c)) : make_uint4(0, 0, 0, 0);
-        mma_16816(acc, lo[0][c].x, lo[1][c].x, lo[0][c].y, lo[1][c].y, bf16x2_neg_part(u.x), bf16x2_neg_part(u.y), false);
-        mma_16816(acc2, hi[0][c].x, hi[1][c].x, hi[0][c].y, hi[1][c].y, bf16x2_pos_part(u.x), bf16x2_pos_part(u.y), false);
-        mma_16816(acc, lo[0][c].z, lo[1][c].z, lo[0][c].w, lo[1][c].w, bf16x2_neg_part(u.z), bf16x2_neg_part(u.w), false);
-        mma_16816(acc2, hi[0][c].z, hi[1][c].z, hi[0][c].w, hi[1][c].w, bf16x2_pos_part(u.z), bf16x2_pos_part(u.w), false);
+    for (int kc = 0; kc < KC; ++kc) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = in ? __ldg(reinterpret_cast<const uint32_t*>(row + 16 * kc + 8 * h + 2 * t)) : 0u;
+        qneg[kc][h] = bf16x2_neg_part(x);
+        qpos[kc][h] = bf16x2_pos_part(x);
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(i);
+  load_q(0);
+  const int64_t pitch = int64_t(Hkv) * width;  // between tokens
+  float* out = scores + (int64_t(q0) * Hkv + head) * width;
+  const int pos0 = L - q_len;
+  for (int i = 0; i < n; ++i) {
+    issue(i + kRing - 1);
+    cp_async_wait<kRing - 1>();
+    __syncwarp();  // every lane's copies of tile i have landed
+    uint32_t have = 0;
+#pragma unroll
+    for (int st = 0; st < kRing; ++st)
+      if (i % kRing == st) have = have_ring[st];
+    const int tile = first_tile + i * sh.lanes;
+    const uint32_t at = ring + uint32_t(i % kRing * kStage);
+    for (int n0 = 0; n0 < cols; n0 += 8) {
+      if (cols > 8) load_q(n0);
+      float acc[4][4] = {};  // four chains of MMAs
+      if (have) {
+        const int row = lane & 15, half = lane >> 4;  // ldmatrix: rows 0-7, 8-15 of k 0-7, then of k 8-15
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+          uint32_t a0, a1, a2, a3;
+          const int piece = 2 * kc + half;
+          ldsm_x4(at + uint32_t(row * RB + ((piece ^ (row & 7)) << 4)), a0, a1, a2, a3);
+          mma_16816(acc[kc & 1], a0, a1, a2, a3, qneg[kc][0], qneg[kc][1], false);
+          ldsm_x4(at + uint32_t(row * RB + (((piece + 2 * KC) ^ (row & 7)) << 4)), a0, a1, a2, a3);
+          mma_16816(acc[2 + (kc & 1)], a0, a1, a2, a3, qpos[kc][0], qpos[kc][1], false);
+        }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] += acc2[e];
+      for (int e = 0; e < 4; ++e) acc[0][e] += acc[1][e] + acc[2][e] + acc[3][e];
       // accumulators: rows g (e 0, 1) and g + 8 (e 2, 3), columns n0 + 2t and n0 + 2t + 1
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int blk = tile * 16 + g + 8 * r;
-        float x = acc[2 * r], y = acc[2 * r + 1];
+        const bool is = (have >> (g + 8 * r)) & 1u;
         auto put = [&](int column, float v) {
           if (column >= cols || blk >= width) return;
-          const int j = column / G, last = (L - q_len + j) / b.block_size;
-          scores[((int64_t(q0) + j) * Hkv + head) * width + blk] = blk <= last && have[r] ? v : ninf;
+          const int j = column >> lg;
+          out[j * pitch + blk] = is && blk * b.block_size <= pos0 + j ? v : -INFINITY;
         };
+        const float x = acc[0][2 * r], y = acc[0][2 * r + 1];
         if (G == 1) {
           put(n0 + 2 * t, x);
           put(n0 + 2 * t + 1, y);
@@ -124,11 +208,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           float m = fmaxf(x, y);
           if (G >= 4) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
           if (G >= 8) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          if ((2 * t) % G == 0) put(n0 + 2 * t, m);
+          if (((2 * t) & (G - 1)) == 0) put(n0 + 2 * t, m);
         }
       }
     }
+    __syncwarp();  // the stage may be refilled
   }
+  cp_async_wait<0>();
+}
+
+template <int D>
+cudaError_t launch_few(const BatchArgs& b, float* scores, int width, const __nv_bfloat16* q,
+                       const __nv_bfloat16* bounds, int Hkv, int G, bool after_chunks, cudaStream_t stream) {
+  constexpr auto kern = block_scores_kernel<D>;
+  constexpr size_t smem = size_t(kWarps) * kRing * 16 * 4 * D;
+  const cudaError_t e = ensure_smem<kern>(smem);
+  if (e != cudaSuccess) return e;
+  const Sharing sh = sharing(Hkv);
+  const int per_seq = ((width + 15) / 16 + sh.tiles - 1) / sh.tiles * sh.groups;
+  return launch_pdl(kern, dim3(unsigned(int64_t(b.num_seqs) * per_seq)), dim3(kWarps * 32), smem, stream, b, scores,
+                    width, q, bounds, Hkv, G, per_seq, after_chunks);
 }
 
 // ---------------------------------------------------------------- chunks: tcgen05
@@ -163,16 +262,6 @@ struct ChunkLayout {
   static constexpr uint32_t BYTES = MISC + 8;
   static constexpr uint32_t SMEM = BYTES + 1024;                 // + alignment slack
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  const int n = real ? 16 : 0;  // 0: nothing is read, 16 zero bytes are written
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // The first column tile of request s in the grid: no scan is needed, since s + (columns before
 // it) / 256 leaves room for every request's last, partial tile.
@@ -450,9 +539,6 @@ cudaError_t dispatch_chunk(const BatchArgs& b, float* scores, int width, const _
 
 cudaError_t launch_block_scores(const BatchArgs& b, float* scores, int score_width, const void* q, const void* bounds,
                                 int num_heads, int num_kv_heads, int head_dim, cudaStream_t stream) {
-  const int64_t pairs = int64_t((score_width + 15) / 16) * num_kv_heads;
-  const int ctas_per_seq = int((pairs + kWarps * kPairs - 1) / (kWarps * kPairs));
-  const dim3 grid(unsigned(int64_t(b.num_seqs) * ctas_per_seq));
   const auto* qp = static_cast<const __nv_bfloat16*>(q);
   const auto* bp = static_cast<const __nv_bfloat16*>(bounds);
   const int G = num_heads / num_kv_heads;
@@ -463,11 +549,8 @@ cudaError_t launch_block_scores(const BatchArgs& b, float* scores, int score_wid
                               : dispatch_chunk<128>(b, scores, score_width, qp, bp, num_kv_heads, G, stream);
     if (e != cudaSuccess) return e;
   }
-  if (head_dim == 64)
-    return launch_pdl(block_scores_kernel<64>, grid, dim3(kWarps * 32), 0, stream, b, scores, score_width, qp, bp,
-                      num_kv_heads, G, ctas_per_seq, chunks);
-  return launch_pdl(block_scores_kernel<128>, grid, dim3(kWarps * 32), 0, stream, b, scores, score_width, qp, bp,
-                    num_kv_heads, G, ctas_per_seq, chunks);
+  return head_dim == 64 ? launch_few<64>(b, scores, score_width, qp, bp, num_kv_heads, G, chunks, stream)
+                        : launch_few<128>(b, scores, score_width, qp, bp, num_kv_heads, G, chunks, stream);
 }
 
 }  // namespace pa
