@@ -13,17 +13,27 @@ struct QueryRow {
   int pos;  // the token's position: seq_lens[s] - q_len + index among the request's queries
 };
 
-// The last request whose query_start_loc is <= t, by a 32-way search of the warp (all 32
-// lanes call it with one t): one dependent load up to 31 requests, two up to 991, ...
-// A decode batch answers with its first load.
+// The request of token t (all 32 lanes of a warp call it with one t). A decode batch (request t
+// is token t) and batches of up to 31 requests answer after one round of loads; others search
+// query_start_loc 32 ways: two more rounds up to 991 requests, three up to 31743.
 __device__ __forceinline__ QueryRow find_row(const BatchArgs& b, int t) {
   const int lane = threadIdx.x & 31, S = b.num_seqs;
   const int32_t* qsl = b.query_start_loc;
-  int s = -1;
-  if (t < S && __ldg(qsl + t) == t && __ldg(qsl + t + 1) == t + 1) {
+  const bool few = S <= 31;
+  const int mine = min(few ? lane : t, S), mine_len = __ldg(b.seq_lens + min(mine, S - 1));
+  int q0 = __ldg(qsl + mine), q1 = few ? 0 : __ldg(qsl + min(t + 1, S)), L = mine_len, s = -1;
+  if (few) {
+    const unsigned m = __ballot_sync(0xffffffffu, lane <= S && q0 <= t);  // non-decreasing: the lowest lanes
+    const int at = m ? 31 - __clz(m) : 0;
+    const int a = __shfl_sync(0xffffffffu, q0, at), z = __shfl_sync(0xffffffffu, q0, min(at + 1, S));
+    L = __shfl_sync(0xffffffffu, mine_len, at);
+    q0 = a;
+    q1 = z;
+    if (m && at < S && t < q1) s = at;
+  } else if (t < S && q0 == t && q1 == t + 1) {
     s = t;
   } else {
-    int lo = 0, n = S + 1;  // the wanted entry is in [lo, lo + n): entries [0, S], non-decreasing
+    int lo = 0, n = S + 1;  // the last entry <= t is in [lo, lo + n): entries [0, S], non-decreasing
     while (n > 1) {
       const int step = (n + 31) / 32;
       const int at = lo + lane * step;
@@ -35,10 +45,14 @@ __device__ __forceinline__ QueryRow find_row(const BatchArgs& b, int t) {
       n = min(step, lo + n - next);
       lo = next;
     }
-    if (lo < S && __ldg(qsl + lo) <= t && t < __ldg(qsl + lo + 1)) s = lo;
+    if (lo < S) {
+      q0 = __ldg(qsl + lo);
+      q1 = __ldg(qsl + lo + 1);
+      L = __ldg(b.seq_lens + lo);
+      if (q0 <= t && t < q1) s = lo;
+    }
   }
   if (s < 0) return {-1, -1};
-  const int q0 = __ldg(qsl + s), q1 = __ldg(qsl + s + 1), L = __ldg(b.seq_lens + s);
   const int64_t cap = int64_t(b.max_blocks_per_seq) * b.block_size;
   if (L > cap || q1 - q0 > L) {
     if (lane == 0) raise_error(b.err, PA_DEVERR_SEQ_RANGE);
