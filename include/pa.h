@@ -441,7 +441,8 @@ int pa_norm_rope_write(void* q_out, const void* q, const void* k, const void* v,
  * kept beside the cache by the caller. Blocks that came to hold keys in another way (copied,
  * swapped in, cached prefixes of another pool) get their bounds by a call whose
  * query_start_loc covers their positions. Two requests that share a block must agree on its
- * keys (shared blocks are full, or hold the same tokens).
+ * keys (shared blocks are full, or hold the same tokens). num_tokens: query_start_loc[num_seqs]
+ * or more (it sizes the grid).
  *
  * pa_block_scores: for block b of token t's context and KV head g
  *     scores[t, g, b] = max_h sum_d max(q_hd lo_d, q_hd hi_d)      (h: the group's query heads)
@@ -469,8 +470,9 @@ int pa_norm_rope_write(void* q_out, const void* q, const void* k, const void* v,
  * --------------------------------------------------------------------------- */
 int pa_block_bounds(void* bounds, const void* k_cache, const int32_t* block_table, int max_blocks_per_seq,
                     const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
-                    int max_query_len, int max_seq_len, int num_kv_heads, int head_dim,
-                    int block_size, int64_t num_blocks, pa_dtype cache_dtype, pa_stream_t stream);
+                    int num_tokens, int max_query_len, int max_seq_len, int num_kv_heads,
+                    int head_dim, int block_size, int64_t num_blocks, pa_dtype cache_dtype,
+                    pa_stream_t stream);
 
 int pa_block_scores(float* scores, int score_width, const void* q, const void* bounds,
                     const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,

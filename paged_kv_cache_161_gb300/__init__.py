@@ -75,7 +75,7 @@ _sig = {
     "pa_advance_batch": (_i, [_p, _i, _p, _p, _p, _i, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i64, _p]),
     "pa_norm_rope_write": (_i, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _f, _p, _i, _i, _i, _p, _i, _p, _p, _p, _p,
                                 _i64, _i64, _i, _i, _i, _i, _i, _i, _f, _f, _p]),
-    "pa_block_bounds": (_i, [_p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _p]),
+    "pa_block_bounds": (_i, [_p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64, _i, _p]),
     "pa_block_scores": (_i, [_p, _i, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i64, _p]),
     "pa_select_blocks": (_i, [_p, _i, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _p]),
     "pa_attention_sparse": (_i, [_p, _p, _p, _p, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i64, _f, _i, _f,
@@ -532,17 +532,19 @@ def norm_rope_write(q_out, q, k, v, q_weight, k_weight, cos_sin, positions, slot
 
 
 def block_bounds(bounds, k_cache, block_table, seq_lens, query_start_loc, *, max_query_len: int, max_seq_len: int,
-                 stream=None):
+                 num_tokens=None, stream=None):
     """pa_block_bounds: bounds[block, head, 0 / 1] = the smallest / largest cached key per dimension,
     for every block that holds one of the batch's query tokens. bounds bfloat16 [num_blocks,
-    Hkv, 2, D]; caches bfloat16 or float8_e4m3fn (bounds of the codes' values)."""
+    Hkv, 2, D]; caches bfloat16 or float8_e4m3fn (bounds of the codes' values). ``num_tokens`` is
+    the batch's query tokens (or more: it sizes the grid; None: S * max_query_len)."""
     NB, B, Hkv, D = _dims(k_cache, "k_cache", 4)
     dev = _index(k_cache, "k_cache")
     S, W = _dims(block_table, "block_table", 2)
     _call("pa_block_bounds", lib.pa_block_bounds, dev, stream, _ptr(bounds, "bounds", dev, _BF16, (NB, Hkv, 2, D)),
           _ptr(k_cache, "k_cache", dev, k_cache.dtype, (NB, B, Hkv, D)), _ptr(block_table, "block_table", dev, _I32, (S, W)),
           W, _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S,
-          max_query_len, max_seq_len, Hkv, D, B, NB, _dtype_code(k_cache))
+          min(S * max_query_len, 0x7fffffff) if num_tokens is None else num_tokens, max_query_len, max_seq_len, Hkv, D, B,
+          NB, _dtype_code(k_cache))
     return bounds
 
 

@@ -718,9 +718,9 @@ int pa_norm_rope_write(void* q_out, const void* q, const void* k, const void* v,
 }
 
 int pa_block_bounds(void* bounds, const void* k_cache, const int32_t* block_table, int max_blocks_per_seq,
-                    const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs, int max_query_len,
-                    int max_seq_len, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
-                    pa_dtype cache_dtype, pa_stream_t stream) {
+                    const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs, int num_tokens,
+                    int max_query_len, int max_seq_len, int num_kv_heads, int head_dim, int block_size,
+                    int64_t num_blocks, pa_dtype cache_dtype, pa_stream_t stream) {
   bool nothing = false;
   int st = check_cache(k_cache, k_cache, num_blocks, block_size, num_kv_heads, head_dim, cache_dtype);
   if (st != PA_OK) return st;
@@ -728,13 +728,14 @@ int pa_block_bounds(void* bounds, const void* k_cache, const int32_t* block_tabl
   st = check_heads(num_kv_heads, num_kv_heads, head_dim);
   if (st != PA_OK) return st;
   if (cache_dtype != PA_BF16 && cache_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
-  st = check_batch(block_table, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, max_query_len, max_query_len,
+  st = check_batch(block_table, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, num_tokens, max_query_len,
                    max_seq_len, block_size, num_blocks, true, nothing);
-  if (st != PA_OK || nothing) return st;
-  if (int64_t(num_seqs) * num_kv_heads * 16 > int64_t(0x7fffffff) * 256) return PA_ERR_UNSUPPORTED;  // grid
+  if (st != PA_OK || nothing || max_query_len == 0) return st;
+  if ((int64_t(num_tokens) / block_size + 2 * int64_t(num_seqs)) * ((int64_t(num_kv_heads) * 16 + 31) / 32) > 0x7fffffff)
+    return PA_ERR_UNSUPPORTED;  // grid
   cudaError_t e;
   pa::BatchArgs b = {block_table, seq_lens, query_start_loc, pa::device_error_word(&e), num_blocks, max_blocks_per_seq,
-                     num_seqs, 0, max_query_len, block_size};
+                     num_seqs, num_tokens, max_query_len, block_size};
   if (!b.err) return cuda_fail(e);
   e = pa::launch_block_bounds(b, bounds, k_cache, num_kv_heads, head_dim, cache_dtype,
                               reinterpret_cast<cudaStream_t>(stream));

@@ -62,13 +62,14 @@ def test_norm_rope_write():
 
 
 def test_block_bounds():
-    good = [_at(1), _at(2), _at(3), 8, _at(4), _at(5), 4, 3, 100, 8, 128, 16, 64, 1, None]
+    good = [_at(1), _at(2), _at(3), 8, _at(4), _at(5), 4, 9, 3, 100, 8, 128, 16, 64, 1, None]
     _check("pa_block_bounds", good, [
         (0, None, INVALID), (0, _at(1) + 8, INVALID), (1, None, INVALID), (1, _at(2) + 8, INVALID), (2, None, INVALID),
         (2, _at(3) + 2, INVALID), (3, 0, INVALID), (3, 6, INVALID), (3, 1 << 30, INVALID), (4, None, INVALID),
-        (5, None, INVALID), (6, -1, INVALID), (6, 0, OK), (7, -1, INVALID), (7, 0, OK), (7, 101, INVALID),
-        (8, -1, INVALID), (8, 129, INVALID), (9, 0, INVALID), (10, 96, UNSUPPORTED), (11, 0, INVALID),
-        (11, 8, UNSUPPORTED), (11, 24, UNSUPPORTED), (12, 0, INVALID), (13, 0, UNSUPPORTED), (13, 5, INVALID),
+        (5, None, INVALID), (6, -1, INVALID), (6, 0, OK), (7, -1, INVALID), (7, 0, OK), (8, -1, INVALID), (8, 0, OK),
+        (8, 101, INVALID), (9, -1, INVALID), (9, 129, INVALID), (10, 0, INVALID), (11, 96, UNSUPPORTED),
+        (12, 0, INVALID), (12, 8, UNSUPPORTED), (12, 24, UNSUPPORTED), (13, 0, INVALID), (14, 0, UNSUPPORTED),
+        (14, 5, INVALID), (10, 1 << 29, UNSUPPORTED),
     ])
 
 
