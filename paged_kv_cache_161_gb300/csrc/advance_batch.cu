@@ -11,7 +11,7 @@
 // The first token of a new block also stores the block's id in the table.
 //
 // Bound by latency, not bytes (about 28 bytes a request and token): one launch of one
-// cluster of up to 8 CTAs. Each CTA scans all requests itself (1024 at a time, from L2),
+// cluster of up to 16 CTAs. Each CTA scans all requests itself (1024 at a time, from L2),
 // which costs less than handing the offsets over, and takes every C-th batch of tokens.
 // The cluster barrier before the last writes lets seq_lens_out and free_head_out be the
 // input arrays, so that one captured graph can be replayed step after step.
@@ -79,6 +79,13 @@ __device__ uint64_t block_inclusive_scan(uint64_t x, uint64_t* red) {
   return x + (warp ? red[warp - 1] : 0);
 }
 
+// Sum over the warp of values below 2^48, in two parts of 24 bits, whose sums cannot overflow.
+__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
+  const uint64_t lo = __reduce_add_sync(0xffffffffu, unsigned(x & 0xffffff));
+  const uint64_t hi = __reduce_add_sync(0xffffffffu, unsigned(x >> 24));
+  return lo + (hi << 24);
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -93,6 +100,8 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// kRun: tokens of a lane whose loads are in flight together.
+template <int kRun>
 __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvanceParams p) {
   __shared__ uint64_t red[32];
   __shared__ int qoff[kThreads + 1], noff[kThreads + 1], ctx[kThreads];
@@ -116,11 +125,8 @@ __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvancePa
   }
   if (tid == 0) total_q = total_need = 0;
   bad = __syncthreads_or(bad);
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) {
-    sq += __shfl_xor_sync(0xffffffffu, sq, m);
-    sn += __shfl_xor_sync(0xffffffffu, sn, m);
-  }
+  sq = warp_sum(sq);
+  sn = warp_sum(sn);
   if ((tid & 31) == 0) {
     atomicAdd(&total_q, sq);
     atomicAdd(&total_need, sn);
@@ -153,8 +159,9 @@ __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvancePa
     if (rank == 0 && s < S) p.qsl[s + 1] = q_base + int(uint32_t(inc));
     __syncthreads();
     const int n = min(kThreads, S - base), t_end = qoff[kThreads];
-    for (int t = q_base + rank * kThreads + tid; t < t_end; t += ranks * kThreads) {
-      int lo = 0, hi = n - 1;  // the last request whose offset is <= t (requests without tokens come before it)
+    // the last request of the tile whose offset is <= t (requests without tokens come before it)
+    auto request_of = [&](int t, int lo) {
+      int hi = n - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (qoff[mid] <= t)
@@ -162,20 +169,42 @@ __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvancePa
         else
           hi = mid - 1;
       }
-      const int c = ctx[lo], pos = c + (t - qoff[lo]), b = pos / B, in = pos - b * B;
-      const int first_new = c / B + (c % B != 0);
-      int32_t* entry = p.table + int64_t(base + lo) * p.width + b;
-      int32_t id;
-      if (b >= first_new) {
-        id = __ldg(p.free_blocks + noff[lo] + (b - first_new));
-        if (in == 0) *entry = id;
-      } else {
-        id = *entry;
+      return lo;
+    };
+    // A warp takes 32 x kRun consecutive tokens: mostly one request's (a prompt chunk) or one
+    // each of consecutive requests (decodes); other tokens search.
+    const int warp = tid >> 5, lane = tid & 31, stride = ranks * kThreads * kRun;
+    for (int t0 = q_base + (rank * (kThreads / 32) + warp) * (32 * kRun); t0 < t_end; t0 += stride) {
+      int first = request_of(t0, 0);
+      int pos[kRun], from[kRun];  // from >= 0: the request's from-th new block
+      int32_t id[kRun];
+      int32_t* entry[kRun];
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        const int t = min(t0 + k * 32 + lane, t_end - 1);
+        int r = first;
+        if (t >= (r + 1 < n ? qoff[r + 1] : t_end)) {
+          r = min(first + lane, n - 1);
+          if (t < qoff[r] || t >= (r + 1 < n ? qoff[r + 1] : t_end)) r = request_of(t, first);
+        }
+        first = __shfl_sync(0xffffffffu, r, 31);
+        const int c = ctx[r];
+        pos[k] = c + (t - qoff[r]);
+        const int b = pos[k] / B, first_new = c / B + (c % B != 0);
+        from[k] = b - first_new;
+        entry[k] = p.table + int64_t(base + r) * p.width + b;
+        id[k] = from[k] >= 0 ? __ldg(p.free_blocks + noff[r] + from[k]) : *entry[k];
       }
-      const bool ok = id >= 0 && id < p.num_blocks;
-      if (!ok) raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
-      p.slots[t] = ok ? int64_t(id) * B + in : -1;
-      p.positions[t] = pos;
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        const int t = t0 + k * 32 + lane, in = pos[k] % B;
+        if (t >= t_end) break;
+        if (from[k] >= 0 && in == 0) *entry[k] = id[k];
+        const bool ok = id[k] >= 0 && id[k] < p.num_blocks;
+        if (!ok) raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
+        p.slots[t] = ok ? int64_t(id[k]) * B + in : -1;
+        p.positions[t] = pos[k];
+      }
     }
     q_base = t_end;
     n_base = noff[kThreads];
@@ -193,6 +222,21 @@ __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvancePa
   if (tid == 0) *p.free_head_out = fail ? head : head + int(need_all);
 }
 
+// Clusters of 16 are opted into once per device.
+cudaError_t allow_cluster_of_16() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(advance_batch_kernel<4>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t* seq_lens, const int32_t* query_lens,
@@ -203,9 +247,15 @@ cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t*
   AdvanceParams p = {block_table, seq_lens,      query_lens,      free_blocks,  free_head, seq_lens_out,
                      free_head_out, query_start_loc, slot_mapping, positions,    err,       num_blocks,
                      num_seqs,    num_tokens,    width,           block_size,   num_free};
-  // one token a thread up to 8 CTAs (the portable cluster size), more per thread beyond
+  // one token a lane up to 8 CTAs (the portable cluster size), beyond that four at once and, from
+  // two rounds of 8 on, 16 CTAs (480 decodes and 32 chunks of 2048 tokens: 8.5 us, 11.2 with 8)
   int ctas = 1;
   while (ctas < 8 && int64_t(ctas) * kThreads < num_tokens) ctas *= 2;
+  if (num_tokens > 8 * kThreads * 4) {
+    const cudaError_t e = allow_cluster_of_16();
+    if (e != cudaSuccess) return e;
+    ctas = 16;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(kThreads);
@@ -218,7 +268,7 @@ cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t*
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, advance_batch_kernel, p);
+  return cudaLaunchKernelEx(&cfg, int64_t(ctas) * kThreads < num_tokens ? advance_batch_kernel<4> : advance_batch_kernel<1>, p);
 }
 
 }  // namespace pa

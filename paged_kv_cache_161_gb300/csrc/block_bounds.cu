@@ -200,7 +200,7 @@ cudaError_t launch(const BatchArgs& b, void* bounds, const void* k_cache, int nu
   const int64_t places = b.max_query_len <= 1 ? b.num_seqs : int64_t(b.num_tokens) / b.block_size + 2 * int64_t(b.num_seqs);
   const int64_t items = places * chunks;
   int share = 1;
-  while (share < kWarps && share * kWarpRows < b.block_size && items * share < 152 * 32) share *= 2;
+  while (share < kWarps && share * kWarpRows < b.block_size && items * share < 152 * 16) share *= 2;
   const int64_t per_cta = kWarps / share, ctas = (items + per_cta - 1) / per_cta;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   return launch_pdl(block_bounds_kernel<KV>, dim3(unsigned(ctas)), dim3(kWarps * 32), 0, stream, b,

@@ -148,7 +148,7 @@ cudaError_t launch_prefill_tc(const AttnArgs& a, const PrefillTcPlan& plan, int 
                               const PrefillLaunch& how);
 
 // ---------------------------------------------------------------- serving-step operators
-// pa_advance_batch: one cluster of up to 8 CTAs.
+// pa_advance_batch: one cluster of up to 16 CTAs.
 cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t* seq_lens, const int32_t* query_lens,
                                  const int32_t* free_blocks, int num_free, const int32_t* free_head,
                                  int32_t* seq_lens_out, int32_t* free_head_out, int32_t* query_start_loc,

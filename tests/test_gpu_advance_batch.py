@@ -58,6 +58,7 @@ CASES = [  # requests, block size, chunk length, share of chunks / requests with
     ("tile_edge", 1024, 16, 3, 0.1, 0.2, 1),
     ("two_tiles", 1025, 8, 5, 0.5, 0.1, 0),
     ("many_tiles", 3500, 16, 20, 0.2, 0.3, 77),
+    ("sixteen_ctas", 90, 16, 1000, 0.5, 0.1, 40),
     ("block_1", 40, 1, 33, 0.5, 0.1, 2),
     ("wide_block", 70, 128, 500, 0.5, 0.1, 0),
 ]
