@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -109,6 +110,8 @@ _sig = {
     "pa_bm_append_tokens_batch": (_i, [_p, _p, _p, _i64, _p, _p, _p]),
     "pa_bm_prefix_stats": (_i, [_p, ctypes.POINTER(_i64), ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
 }
+_packed_call = lib.pa_packed_call
+_packed_call.restype, _packed_call.argtypes = _i, [_i, ctypes.c_char_p]
 for _name, (_res, _args) in _sig.items():
     _fn = getattr(lib, _name)
     _fn.restype = _res
@@ -423,6 +426,24 @@ def attention_grouped(out, q, k_cache, v_cache, block_table, seq_lens, query_sta
     return out
 
 
+_CODE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.float8_e4m3fn: PA_FP8_E4M3}
+# The serving-step calls: their number in the library's packed entry, and their arguments, one
+# 8-byte field each (P an address, q an integer, d a float).
+_ADVANCE = (0, "pa_advance_batch", struct.Struct("@PqPPPqPPPPPPqqqqP"))
+_NORM_ROPE = (1, "pa_norm_rope_write", struct.Struct("@PPPPqqqPPdPqqqPqqqqqPPPqqqqqqqqddP"))
+_BOUNDS = (2, "pa_block_bounds", struct.Struct("@PPPqPPqqqqqqqqqP"))
+_SCORES = (3, "pa_block_scores", struct.Struct("@PqPPPqPPqqqqqqqqqP"))
+_SELECT = (4, "pa_select_blocks", struct.Struct("@PqPqPPqqqqqqP"))
+_SPARSE = (5, "pa_attention_sparse", struct.Struct("@PPPPPqPPPqqqqqqqqqdqddP"))
+
+
+def _code(t, name: str) -> int:
+    c = _CODE.get(t.dtype)
+    if c is None:
+        raise TypeError(f"unsupported {name} dtype {t.dtype} (float32, bfloat16 or float8_e4m3fn)")
+    return c
+
+
 def _index(t, name: str) -> int:
     """The CUDA device index of a tensor."""
     d = t.get_device() if isinstance(t, torch.Tensor) else -1
@@ -444,16 +465,17 @@ def _ptr(t, name: str, dev: int, dtype, shape) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
-def _call(name: str, fn, dev: int, stream, *args):
+def _call(op, dev: int, stream, *args):
     """The library call with device ``dev`` current (the library works on the current device), on
     ``stream`` or that device's current stream."""
-    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    number, name, fields = op
+    packed = fields.pack(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if _current_device() == dev:
-        st = fn(*args, s)
+        st = _packed_call(number, packed)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, s)
-    if st != 0:
+            st = _packed_call(number, packed)
+    if st:
         raise PAError(st, name)
 
 
@@ -475,7 +497,7 @@ def advance_batch(block_table, seq_lens, query_lens, free_blocks, free_head, seq
     dev = _index(block_table, "block_table")
     S, W = _dims(block_table, "block_table", 2)
     (T,), (F,) = _dims(slot_mapping, "slot_mapping", 1), _dims(free_blocks, "free_blocks", 1)
-    _call("pa_advance_batch", lib.pa_advance_batch, dev, stream, _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
+    _call(_ADVANCE, dev, stream, _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
           _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_lens, "query_lens", dev, _I32, (S,)),
           _ptr(free_blocks, "free_blocks", dev, _I32, (F,)), F, _ptr(free_head, "free_head", dev, _I32, (1,)),
           _ptr(seq_lens_out, "seq_lens_out", dev, _I32, (S,)), _ptr(free_head_out, "free_head_out", dev, _I32, (1,)),
@@ -514,20 +536,22 @@ def norm_rope_write(q_out, q, k, v, q_weight, k_weight, cos_sin, positions, slot
     limit, rot = _dims(cos_sin, "cos_sin", 2)
     dt, cache_dt, kv = q.dtype, k_cache.dtype, (T, Hkv, D)
     if sections is None:
-        axes, sec, pos = 1, None, (T,)
+        axes, sec, pos = 1, (rot // 2, 0, 0, 0), (T,)
     else:
         axes = len(sections)
-        sec, pos = (ctypes.c_int * axes)(*sections), (axes, T)
-    _call("pa_norm_rope_write", lib.pa_norm_rope_write, dev, stream, _ptr(q_out, "q_out", dev, dt, (T, Hq, D)),
+        if not 1 <= axes <= 4:
+            raise ValueError("sections: one to four axes")
+        sec, pos = (*sections, 0, 0, 0)[:4], (axes, T)
+    _call(_NORM_ROPE, dev, stream, _ptr(q_out, "q_out", dev, dt, (T, Hq, D)),
           q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_rows(q, "q", dev, dt, (T, Hq, D)),
           _token_rows(k, "k", dev, dt, kv), _token_rows(v, "v", dev, dt, kv),
-          None if q_weight is None else _ptr(q_weight, "q_weight", dev, dt, (D,)),
-          None if k_weight is None else _ptr(k_weight, "k_weight", dev, dt, (D,)), eps,
+          0 if q_weight is None else _ptr(q_weight, "q_weight", dev, dt, (D,)),
+          0 if k_weight is None else _ptr(k_weight, "k_weight", dev, dt, (D,)), eps,
           _ptr(cos_sin, "cos_sin", dev, torch.float32, (limit, rot)), limit, rot, interleaved,
-          _ptr(positions, "positions", dev, _I32, pos), axes, sec,
+          _ptr(positions, "positions", dev, _I32, pos), axes, *sec,
           _ptr(slot_mapping, "slot_mapping", dev, torch.int64, (T,)), _ptr(k_cache, "k_cache", dev, cache_dt, (NB, B, Hkv, D)),
-          _ptr(v_cache, "v_cache", dev, cache_dt, (NB, B, Hkv, D)), T, NB, B, Hq, Hkv, D, _dtype_code(q),
-          _dtype_code(k_cache), k_scale, v_scale)
+          _ptr(v_cache, "v_cache", dev, cache_dt, (NB, B, Hkv, D)), T, NB, B, Hq, Hkv, D, _code(q, "q"),
+          _code(k_cache, "k_cache"), k_scale, v_scale)
     return q_out
 
 
@@ -540,11 +564,11 @@ def block_bounds(bounds, k_cache, block_table, seq_lens, query_start_loc, *, max
     NB, B, Hkv, D = _dims(k_cache, "k_cache", 4)
     dev = _index(k_cache, "k_cache")
     S, W = _dims(block_table, "block_table", 2)
-    _call("pa_block_bounds", lib.pa_block_bounds, dev, stream, _ptr(bounds, "bounds", dev, _BF16, (NB, Hkv, 2, D)),
+    _call(_BOUNDS, dev, stream, _ptr(bounds, "bounds", dev, _BF16, (NB, Hkv, 2, D)),
           _ptr(k_cache, "k_cache", dev, k_cache.dtype, (NB, B, Hkv, D)), _ptr(block_table, "block_table", dev, _I32, (S, W)),
           W, _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S,
           min(S * max_query_len, 0x7fffffff) if num_tokens is None else num_tokens, max_query_len, max_seq_len, Hkv, D, B,
-          NB, _dtype_code(k_cache))
+          NB, _code(k_cache, "k_cache"))
     return bounds
 
 
@@ -558,7 +582,7 @@ def block_scores(scores, q, bounds, block_table, seq_lens, query_start_loc, *, b
     dev = _index(q, "q")
     S, W = _dims(block_table, "block_table", 2)
     width = _dims(scores, "scores", 3)[2]
-    _call("pa_block_scores", lib.pa_block_scores, dev, stream,
+    _call(_SCORES, dev, stream,
           _ptr(scores, "scores", dev, torch.float32, (T, Hkv, width)), width, _ptr(q, "q", dev, _BF16, (T, Hq, D)),
           _ptr(bounds, "bounds", dev, _BF16, (NB, Hkv, 2, D)), _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
           _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S, T,
@@ -575,7 +599,7 @@ def select_blocks(block_idx, scores, seq_lens, query_start_loc, *, block_size: i
     dev = _index(scores, "scores")
     (S,) = _dims(seq_lens, "seq_lens", 1)
     k = _dims(block_idx, "block_idx", 3)[2]
-    _call("pa_select_blocks", lib.pa_select_blocks, dev, stream, _ptr(block_idx, "block_idx", dev, _I32, (T, Hkv, k)), k,
+    _call(_SELECT, dev, stream, _ptr(block_idx, "block_idx", dev, _I32, (T, Hkv, k)), k,
           _ptr(scores, "scores", dev, torch.float32, (T, Hkv, width)), width, _ptr(seq_lens, "seq_lens", dev, _I32, (S,)),
           _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S, T, Hkv, block_size, init_blocks, local_blocks)
     return block_idx
@@ -591,12 +615,12 @@ def attention_sparse(out, q, k_cache, v_cache, block_table, seq_lens, query_star
     T, Hq, _ = _dims(q, "q", 3)
     S, W = _dims(block_table, "block_table", 2)
     k = _dims(block_idx, "block_idx", 3)[2]
-    _call("pa_attention_sparse", lib.pa_attention_sparse, dev, stream, _ptr(out, "out", dev, _BF16, (T, Hq, D)),
+    _call(_SPARSE, dev, stream, _ptr(out, "out", dev, _BF16, (T, Hq, D)),
           _ptr(q, "q", dev, _BF16, (T, Hq, D)), _ptr(k_cache, "k_cache", dev, cache_dt, cache),
           _ptr(v_cache, "v_cache", dev, cache_dt, cache), _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
           _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)),
           _ptr(block_idx, "block_idx", dev, _I32, (T, Hkv, k)), k, S, T, max_seq_len, Hq, Hkv, D, B, NB, scale,
-          _dtype_code(k_cache), k_scale, v_scale)
+          _code(k_cache, "k_cache"), k_scale, v_scale)
     return out
 
 

@@ -28,7 +28,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libpa_gb300.so")
 CU_SOURCES = ["errors.cu", "kv_write.cu", "copy_blocks.cu", "decode_attention.cu", "decode_mma.cu", "prefill_attention.cu",
               "attention_fixed_scratch.cu", "prefill_tcgen05.cu", "advance_batch.cu", "norm_rope_write.cu",
               "block_bounds.cu", "block_scores.cu", "select_blocks.cu", "attention_sparse.cu"]
-CPP_SOURCES = ["api.cpp", "block_manager.cpp"]
+CPP_SOURCES = ["api.cpp", "binding.cpp", "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
