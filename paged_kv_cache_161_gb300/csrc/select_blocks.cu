@@ -31,6 +31,18 @@ __device__ __forceinline__ int order_of(float x) {
 }
 __device__ __forceinline__ float value_of(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)) + 0.f; }
 
+// Minimum and maximum that keep a NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 constexpr int kRowsPerCta = 4;  // of one warp each
 constexpr int kBins = 256;
 
@@ -77,7 +89,8 @@ __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerCta * 32 : WARPS * 32)
   // always selected: blocks [0, head) and [tail, n); the scores that count are those between
   const int head = min(init, n), tail = max(n - local, head), forced = head + n - tail;
   const int from = head - seg, to = min(tail, end) - seg;  // within the warp's part
-  auto mask = [&](int i, float v) { return i >= from && i < to ? v : NAN; };  // i: within the warp's part
+  // i: within the warp's part; NaN: not to be counted (outside, NaN or -inf)
+  auto mask = [&](int i, float v) { return i >= from && i < to && v > -INFINITY ? v : NAN; };
   // calls f(j, score) for the warp's scores
   auto each = [&](auto f) {
     if constexpr (kReload) {
@@ -136,10 +149,9 @@ __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerCta * 32 : WARPS * 32)
   constexpr int kSample = 8;
   float mn = INFINITY, mx = -INFINITY;
   auto sample = [&](float v) {
-    if (v > -INFINITY && v < INFINITY) {
-      mx = fmaxf(mx, v);
-      mn = fminf(mn, v);
-    }
+    const float w = v < INFINITY ? v : NAN;  // fmaxf and fminf pass NaN over
+    mx = fmaxf(mx, w);
+    mn = fminf(mn, w);
   };
   if constexpr (kReload) {
     for (int k = 0; k < min(kSample, steps); ++k) {
@@ -163,20 +175,69 @@ __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerCta * 32 : WARPS * 32)
   if (lane == 0 && warp == 0) ncand_all[slot] = 0;
   if (WARPS == 1) __syncwarp();
   row_range(mn, mx);  // (with several warps its barriers also order the zeroing)
-  // ---- the histogram: scores below the sample's range in bin 0, above it in the last
-  const float ratio = (kBins - 2) / (mx - mn);
-  const bool flat = !(mx > mn) || !(ratio < INFINITY);
-  const float scale = flat ? 0.f : ratio, off = flat ? 0.f : 1.f - mn * ratio;
-  auto bin_of = [&](float v) { return int(fminf(fmaxf(fmaf(v, scale, off), 0.f), float(kBins - 1))); };
-  each([&](int, float s) {
-    if (s > -INFINITY) atomicAdd(hist + bin_of(s), 1);
-  });
+  // ---- the histogram: bin 0 for what does not count, the scores in bins 1 (below the sample's
+  // range) to 255 (above it)
+  const float ratio = (kBins - 3) / (mx - mn);
+  // (without a usable range a scale that keeps infinities and their order)
+  const bool flat = !(ratio > 0.f && ratio < INFINITY) || !(fabsf(mn * ratio) < INFINITY);
+  const float scale = flat ? 2e-38f : ratio, off = flat ? 1.f : 2.f - mn * ratio;
+  auto bin_of = [&](float v) {
+    return __float2int_rz(min_nan(max_nan(fmaf(v, scale, off), 1.f), float(kBins - 1)));  // NaN: 0
+  };
+  // the lane's bins, four to a word, so that the border bin's scores are found without another
+  // computation of them
+  uint32_t bins[kReload ? 1 : PER / 4];
+  if constexpr (kReload) {
+    each([&](int, float s) { atomicAdd(hist + bin_of(s), 1); });
+  } else {
+#pragma unroll
+    for (int j0 = 0; j0 < PER; j0 += kGroup) {
+      if (j0 < steps) {
+#pragma unroll
+        for (int j = j0; j < j0 + kGroup; j += 4) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int bin = bin_of(x[j + e]);
+            atomicAdd(hist + bin, 1);
+            word |= uint32_t(bin) << (8 * e);
+          }
+          bins[j / 4] = word;
+        }
+      }
+    }
+  }
+  // calls f(score) for the warp's scores in a bin
+  auto each_in = [&](int bin, auto f) {
+    if constexpr (kReload) {
+      each([&](int, float s) {
+        if (bin_of(s) == bin) f(s);
+      });
+    } else {
+      const uint32_t want = uint32_t(bin) * 0x01010101u;
+#pragma unroll
+      for (int j0 = 0; j0 < PER; j0 += kGroup) {
+        if (j0 < steps) {
+#pragma unroll
+          for (int j = j0; j < j0 + kGroup; j += 4) {
+            const uint32_t d = bins[j / 4] ^ want;
+            if ((d - 0x01010101u) & ~d & 0x80808080u) {  // a byte of d is 0
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (((d >> (8 * e)) & 0xffu) == 0) f(x[j + e]);
+            }
+          }
+        }
+      }
+    }
+  };
   sync_row();
   // lane l holds bins 255 - 8 l .. 248 - 8 l: from the top down
   int c[8], mine = 0;
   {
     const int4 u = reinterpret_cast<const int4*>(hist)[63 - 2 * lane], v = reinterpret_cast<const int4*>(hist)[62 - 2 * lane];
     c[0] = u.w, c[1] = u.z, c[2] = u.y, c[3] = u.x, c[4] = v.w, c[5] = v.z, c[6] = v.y, c[7] = v.x;
+    if (lane == 31) c[7] = 0;  // bin 0
 #pragma unroll
     for (int i = 0; i < 8; ++i) mine += c[i];
   }
@@ -209,9 +270,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerCta * 32 : WARPS * 32)
     above = __shfl_sync(0xffffffffu, above, owner);  // scores in the bins above
     in_bin = __shfl_sync(0xffffffffu, in_bin, owner);
     if (in_bin <= 32) {
-      each([&](int, float s) {
-        if (s > -INFINITY && bin_of(s) == bin) cand[atomicAdd(&ncand_all[slot], 1)] = s;
-      });
+      each_in(bin, [&](float s) { cand[atomicAdd(&ncand_all[slot], 1)] = s; });
       sync_row();
       // the (need - above)-th largest of them, by counting (in any order: only values matter)
       const float v = lane < in_bin ? cand[lane] : -INFINITY;
@@ -228,11 +287,9 @@ __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerCta * 32 : WARPS * 32)
     } else {
       float hi = -INFINITY;
       thr = INFINITY;
-      each([&](int, float s) {
-        if (s > -INFINITY && bin_of(s) == bin) {
-          thr = fminf(thr, s);
-          hi = fmaxf(hi, s);
-        }
+      each_in(bin, [&](float s) {
+        thr = fminf(thr, s);
+        hi = fmaxf(hi, s);
       });
       row_range(thr, hi);
       ge = above + in_bin;  // scores >= thr, the bin's lowest

@@ -216,7 +216,8 @@ def test_select(pa, name, ties):
 
 
 @pytest.mark.parametrize("n", [1, 31, 32, 33, 1000, 1024, 1025, 4096, 4097, 16385, 32768, 32800, 70000])
-@pytest.mark.parametrize("kind", ["normal", "ties", "one_value", "huge_range", "infinities", "zeros_and_subnormals"])
+@pytest.mark.parametrize("kind", ["normal", "ties", "one_value", "huge_range", "infinities", "zeros_and_subnormals",
+                                  "flat_and_infinite", "far_apart"])
 def test_select_widths(pa, n, kind):
     """Every width's variant, at its edges: one query token over n blocks."""
     rng = np.random.default_rng(n)
@@ -230,6 +231,12 @@ def test_select_widths(pa, n, kind):
     if kind == "infinities":
         x[x > 1.5], x[x < -1], x[np.abs(x) < 0.05] = np.inf, -np.inf, np.nan
         x[0, 0, :3] = [0.0, -0.0, 0.0][: min(3, n)]
+    if kind == "flat_and_infinite":  # one value and infinities
+        x = rng.choice(np.array([1.5, 1.5, 1.5, np.inf, -np.inf], np.float32), (1, 2, n))
+    if kind == "far_apart":  # two close groups of huge values: no linear range separates them
+        x = (rng.choice(np.array([3e38, -3e38]), (1, 2, n)) * (1 + 1e-3 * rng.random((1, 2, n)))).astype(np.float32)
+        x[0, 1] = 1e30 + rng.integers(0, 3, n) * 2.0 ** 77
+        x[0, :, ::5] = np.inf
     if kind == "zeros_and_subnormals":
         x = rng.choice(np.array([0.0, -0.0, 1e-45, -1e-45, 3e-45, -3e-45, 1e-38], np.float32), (1, 2, n))
     lens = torch.tensor([n * 16], dtype=I32, device="cuda")
