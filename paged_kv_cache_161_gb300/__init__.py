@@ -1,8 +1,11 @@
-"""GB300 (sm_103a) paged-KV-cache hot path: a thin ctypes binding over libpa_gb300.so.
+"""GB300 (sm_103a) paged-KV-cache hot path: a thin binding over libpa_gb300.so.
 
 Names follow the C ABI in include/pa.h (pa_kv_write -> kv_write, ...). The binding only
 checks tensors and marshals pointers, sizes and the current CUDA stream; every step of
-the path runs in the library's kernels. PyTorch provides device memory and streams.
+the path runs in the library's kernels. PyTorch provides device memory and streams. Most
+calls go through ctypes; the serving-step calls (advance_batch, norm_rope_write,
+block_bounds, block_scores, select_blocks, attention_sparse), a few microseconds each on the
+GPU, through a small extension, _pa_torch.so, whose host time is 3 us a call.
 
 The library is built in-tree by ``python paged_kv_cache_161_gb300/build.py`` (or the
 repository's ``__graft_entry__.build()``). Importing this package without it raises.
@@ -10,12 +13,13 @@ repository's ``__graft_entry__.build()``). Importing this package without it rai
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 
 import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libpa_gb300.so")
+EXT_PATH = os.path.join(os.path.dirname(LIB_PATH), "_pa_torch.so")
 
 __all__ = [
     "PAError",
@@ -45,10 +49,11 @@ PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
 PA_DEVERR = {"slot_range": 0x1, "block_range": 0x2, "seq_range": 0x4, "timeout": 0x8, "slot_mismatch": 0x10,
              "no_blocks": 0x20, "position": 0x40}
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(
-        f"{LIB_PATH} is missing: build it with `python paged_kv_cache_161_gb300/build.py` "
-        "(there is no fallback path)")
+for _path in (LIB_PATH, EXT_PATH):
+    if not os.path.exists(_path):
+        raise ImportError(
+            f"{_path} is missing: build it with `python paged_kv_cache_161_gb300/build.py` "
+            "(there is no fallback path)")
 
 lib = ctypes.CDLL(LIB_PATH)
 
@@ -110,8 +115,6 @@ _sig = {
     "pa_bm_append_tokens_batch": (_i, [_p, _p, _p, _i64, _p, _p, _p]),
     "pa_bm_prefix_stats": (_i, [_p, ctypes.POINTER(_i64), ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
 }
-_packed_call = lib.pa_packed_call
-_packed_call.restype, _packed_call.argtypes = _i, [_i, ctypes.c_char_p]
 for _name, (_res, _args) in _sig.items():
     _fn = getattr(lib, _name)
     _fn.restype = _res
@@ -158,13 +161,6 @@ def _stream(stream, device) -> int:
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return s.cuda_stream
 
-
-_I32, _BF16 = torch.int32, torch.bfloat16
-# The serving-step calls below take a few microseconds on the GPU at decode sizes: these two
-# answer in 0.1 us what torch.cuda.current_stream(...).cuda_stream and current_device() take 2
-# us for (a machine without CUDA has neither, and refuses every tensor before).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _cache_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor):
@@ -426,202 +422,17 @@ def attention_grouped(out, q, k_cache, v_cache, block_table, seq_lens, query_sta
     return out
 
 
-_CODE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.float8_e4m3fn: PA_FP8_E4M3}
-# The serving-step calls: their number in the library's packed entry, and their arguments, one
-# 8-byte field each (P an address, q an integer, d a float).
-_ADVANCE = (0, "pa_advance_batch", struct.Struct("@PqPPPqPPPPPPqqqqP"))
-_NORM_ROPE = (1, "pa_norm_rope_write", struct.Struct("@PPPPqqqPPdPqqqPqqqqqPPPqqqqqqqqddP"))
-_BOUNDS = (2, "pa_block_bounds", struct.Struct("@PPPqPPqqqqqqqqqP"))
-_SCORES = (3, "pa_block_scores", struct.Struct("@PqPPPqPPqqqqqqqqqP"))
-_SELECT = (4, "pa_select_blocks", struct.Struct("@PqPqPPqqqqqqP"))
-_SPARSE = (5, "pa_attention_sparse", struct.Struct("@PPPPPqPPPqqqqqqqqqdqddP"))
-
-
-def _code(t, name: str) -> int:
-    c = _CODE.get(t.dtype)
-    if c is None:
-        raise TypeError(f"unsupported {name} dtype {t.dtype} (float32, bfloat16 or float8_e4m3fn)")
-    return c
-
-
-def _index(t, name: str) -> int:
-    """The CUDA device index of a tensor."""
-    d = t.get_device() if isinstance(t, torch.Tensor) else -1
-    if d < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return d
-
-
-def _ptr(t, name: str, dev: int, dtype, shape) -> int:
-    """Address of a contiguous tensor of the given device, dtype and shape."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a tensor on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _call(op, dev: int, stream, *args):
-    """The library call with device ``dev`` current (the library works on the current device), on
-    ``stream`` or that device's current stream."""
-    number, name, fields = op
-    packed = fields.pack(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if _current_device() == dev:
-        st = _packed_call(number, packed)
-    else:
-        with torch.cuda.device(dev):
-            st = _packed_call(number, packed)
-    if st:
-        raise PAError(st, name)
-
-
-def _dims(t, name: str, n: int):
-    if not isinstance(t, torch.Tensor) or t.dim() != n:
-        raise ValueError(f"{name} must be a tensor of {n} dims")
-    return t.shape
-
-
-def advance_batch(block_table, seq_lens, query_lens, free_blocks, free_head, seq_lens_out, free_head_out,
-                  query_start_loc, slot_mapping, positions, *, block_size: int, num_blocks: int, stream=None):
-    """pa_advance_batch: a step's block tables, slots and positions from request lengths, on the GPU.
-
-    block_table int32 [S, W] (new entries written), seq_lens and query_lens int32 [S],
-    free_blocks int32 [F] with free_head int32 [1] entries already taken; writes seq_lens_out
-    [S] and free_head_out [1] (each may be its input), query_start_loc int32 [S + 1],
-    slot_mapping int64 [T] and positions int32 [T]; tokens behind the last request's get slot
-    -1 and position 0. A step that does not fit changes nothing (read_device_errors tells)."""
-    dev = _index(block_table, "block_table")
-    S, W = _dims(block_table, "block_table", 2)
-    (T,), (F,) = _dims(slot_mapping, "slot_mapping", 1), _dims(free_blocks, "free_blocks", 1)
-    _call(_ADVANCE, dev, stream, _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
-          _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_lens, "query_lens", dev, _I32, (S,)),
-          _ptr(free_blocks, "free_blocks", dev, _I32, (F,)), F, _ptr(free_head, "free_head", dev, _I32, (1,)),
-          _ptr(seq_lens_out, "seq_lens_out", dev, _I32, (S,)), _ptr(free_head_out, "free_head_out", dev, _I32, (1,)),
-          _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)),
-          _ptr(slot_mapping, "slot_mapping", dev, torch.int64, (T,)), _ptr(positions, "positions", dev, _I32, (T,)), S, T,
-          block_size, num_blocks)
-
-
-def _token_rows(t, name: str, dev: int, dtype, shape) -> int:
-    """Elements between the tokens of a [num_tokens, heads, head_dim] tensor whose tokens may lie
-    apart (a slice of a wider projection)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev or t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)} on cuda:{dev}, got {list(t.shape)} on {t.device}")
-    T, H, D = shape
-    st = t.stride()
-    if (st[2] != 1 or (st[1] != D and H > 1)) and T > 0:
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return st[0] if T > 1 else H * D
-
-
-def norm_rope_write(q_out, q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, k_cache, v_cache, *,
-                    eps: float = 1e-6, interleaved: bool = False, sections=None, k_scale: float = 1.0,
-                    v_scale: float = 1.0, stream=None):
-    """pa_norm_rope_write: RMS norm of each query and key head (weights [head_dim], or None: no
-    norm), rotary positions, and the cache write, in one pass.
-
-    q [T, Hq, D], k and v [T, Hkv, D]: bfloat16 or float32, tokens may lie apart (slices of one
-    projection); q_out [T, Hq, D] contiguous (may be q). cos_sin float32 [max_position,
-    rot_dim] (cosines, then sines); positions int32 [T], or [axes, T] with ``sections`` = the
-    pair counts of the axes. Caches in q's dtype or float8_e4m3fn (codes of x / scale)."""
-    NB, B, Hkv, D = _dims(k_cache, "k_cache", 4)
-    dev = _index(k_cache, "k_cache")
-    T, Hq, _ = _dims(q, "q", 3)
-    limit, rot = _dims(cos_sin, "cos_sin", 2)
-    dt, cache_dt, kv = q.dtype, k_cache.dtype, (T, Hkv, D)
-    if sections is None:
-        axes, sec, pos = 1, (rot // 2, 0, 0, 0), (T,)
-    else:
-        axes = len(sections)
-        if not 1 <= axes <= 4:
-            raise ValueError("sections: one to four axes")
-        sec, pos = (*sections, 0, 0, 0)[:4], (axes, T)
-    _call(_NORM_ROPE, dev, stream, _ptr(q_out, "q_out", dev, dt, (T, Hq, D)),
-          q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_rows(q, "q", dev, dt, (T, Hq, D)),
-          _token_rows(k, "k", dev, dt, kv), _token_rows(v, "v", dev, dt, kv),
-          0 if q_weight is None else _ptr(q_weight, "q_weight", dev, dt, (D,)),
-          0 if k_weight is None else _ptr(k_weight, "k_weight", dev, dt, (D,)), eps,
-          _ptr(cos_sin, "cos_sin", dev, torch.float32, (limit, rot)), limit, rot, interleaved,
-          _ptr(positions, "positions", dev, _I32, pos), axes, *sec,
-          _ptr(slot_mapping, "slot_mapping", dev, torch.int64, (T,)), _ptr(k_cache, "k_cache", dev, cache_dt, (NB, B, Hkv, D)),
-          _ptr(v_cache, "v_cache", dev, cache_dt, (NB, B, Hkv, D)), T, NB, B, Hq, Hkv, D, _code(q, "q"),
-          _code(k_cache, "k_cache"), k_scale, v_scale)
-    return q_out
-
-
-def block_bounds(bounds, k_cache, block_table, seq_lens, query_start_loc, *, max_query_len: int, max_seq_len: int,
-                 num_tokens=None, stream=None):
-    """pa_block_bounds: bounds[block, head, 0 / 1] = the smallest / largest cached key per dimension,
-    for every block that holds one of the batch's query tokens. bounds bfloat16 [num_blocks,
-    Hkv, 2, D]; caches bfloat16 or float8_e4m3fn (bounds of the codes' values). ``num_tokens`` is
-    the batch's query tokens (or more: it sizes the grid; None: S * max_query_len)."""
-    NB, B, Hkv, D = _dims(k_cache, "k_cache", 4)
-    dev = _index(k_cache, "k_cache")
-    S, W = _dims(block_table, "block_table", 2)
-    _call(_BOUNDS, dev, stream, _ptr(bounds, "bounds", dev, _BF16, (NB, Hkv, 2, D)),
-          _ptr(k_cache, "k_cache", dev, k_cache.dtype, (NB, B, Hkv, D)), _ptr(block_table, "block_table", dev, _I32, (S, W)),
-          W, _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S,
-          min(S * max_query_len, 0x7fffffff) if num_tokens is None else num_tokens, max_query_len, max_seq_len, Hkv, D, B,
-          NB, _code(k_cache, "k_cache"))
-    return bounds
-
-
-def block_scores(scores, q, bounds, block_table, seq_lens, query_start_loc, *, block_size: int, max_query_len: int,
-                 max_seq_len: int, stream=None):
-    """pa_block_scores: scores[t, head, block] = an upper bound of the block's logits (before the
-    softmax scale) over the head's query group; -inf behind the token's context. scores float32
-    [T, Hkv, score_width], score_width * block_size >= max_seq_len; q bfloat16 [T, Hq, D]."""
-    T, Hq, D = _dims(q, "q", 3)
-    NB, Hkv, _, _ = _dims(bounds, "bounds", 4)
-    dev = _index(q, "q")
-    S, W = _dims(block_table, "block_table", 2)
-    width = _dims(scores, "scores", 3)[2]
-    _call(_SCORES, dev, stream,
-          _ptr(scores, "scores", dev, torch.float32, (T, Hkv, width)), width, _ptr(q, "q", dev, _BF16, (T, Hq, D)),
-          _ptr(bounds, "bounds", dev, _BF16, (NB, Hkv, 2, D)), _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
-          _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S, T,
-          max_query_len, max_seq_len, Hq, Hkv, D, block_size, NB)
-    return scores
-
-
-def select_blocks(block_idx, scores, seq_lens, query_start_loc, *, block_size: int, init_blocks: int = 0,
-                  local_blocks: int = 0, stream=None):
-    """pa_select_blocks: block_idx[t, head] = the first init_blocks and last local_blocks of the
-    token's context and the blocks of the largest scores (equal ones: the lowest), ascending,
-    -1 behind them. block_idx int32 [T, Hkv, num_select], scores float32 [T, Hkv, width]."""
-    T, Hkv, width = _dims(scores, "scores", 3)
-    dev = _index(scores, "scores")
-    (S,) = _dims(seq_lens, "seq_lens", 1)
-    k = _dims(block_idx, "block_idx", 3)[2]
-    _call(_SELECT, dev, stream, _ptr(block_idx, "block_idx", dev, _I32, (T, Hkv, k)), k,
-          _ptr(scores, "scores", dev, torch.float32, (T, Hkv, width)), width, _ptr(seq_lens, "seq_lens", dev, _I32, (S,)),
-          _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)), S, T, Hkv, block_size, init_blocks, local_blocks)
-    return block_idx
-
-
-def attention_sparse(out, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, block_idx, *, max_seq_len: int,
-                     scale: float, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
-    """pa_attention_sparse: attention of each query token over the blocks listed in block_idx
-    [T, Hkv, num_select] (logical blocks of its request, entries < 0 skipped), causal; zeros for
-    an empty list. out, q bfloat16 [T, Hq, D]; caches bfloat16, or float8_e4m3fn with scales."""
-    NB, B, Hkv, D = cache = _dims(k_cache, "k_cache", 4)
-    dev, cache_dt = _index(k_cache, "k_cache"), k_cache.dtype
-    T, Hq, _ = _dims(q, "q", 3)
-    S, W = _dims(block_table, "block_table", 2)
-    k = _dims(block_idx, "block_idx", 3)[2]
-    _call(_SPARSE, dev, stream, _ptr(out, "out", dev, _BF16, (T, Hq, D)),
-          _ptr(q, "q", dev, _BF16, (T, Hq, D)), _ptr(k_cache, "k_cache", dev, cache_dt, cache),
-          _ptr(v_cache, "v_cache", dev, cache_dt, cache), _ptr(block_table, "block_table", dev, _I32, (S, W)), W,
-          _ptr(seq_lens, "seq_lens", dev, _I32, (S,)), _ptr(query_start_loc, "query_start_loc", dev, _I32, (S + 1,)),
-          _ptr(block_idx, "block_idx", dev, _I32, (T, Hkv, k)), k, S, T, max_seq_len, Hq, Hkv, D, B, NB, scale,
-          _code(k_cache, "k_cache"), k_scale, v_scale)
-    return out
+# The serving-step calls come from an extension of their own: see csrc/torch_binding.cpp.
+_spec = importlib.util.spec_from_file_location("_pa_torch", EXT_PATH)
+_pa_torch = importlib.util.module_from_spec(_spec)
+_spec.loader.exec_module(_pa_torch)
+_pa_torch.init(PAError)
+advance_batch = _pa_torch.advance_batch
+norm_rope_write = _pa_torch.norm_rope_write
+block_bounds = _pa_torch.block_bounds
+block_scores = _pa_torch.block_scores
+select_blocks = _pa_torch.select_blocks
+attention_sparse = _pa_torch.attention_sparse
 
 
 def read_device_errors(clear: bool = True) -> int:

@@ -1,4 +1,5 @@
-"""Build the C-ABI shared library libpa_gb300.so in-tree (sm_103a only).
+"""Build the C-ABI shared library libpa_gb300.so in-tree (sm_103a only), and the Python extension
+_pa_torch.so of the serving-step calls beside it.
 
     python paged_kv_cache_161_gb300/build.py [--force] [--verbose] [--ptxas]
 
@@ -6,15 +7,18 @@
 
 Each CUDA translation unit is compiled by nvcc in parallel, the host units by g++, and
 nvcc links them with the static CUDA runtime, so the library needs only the driver at
-run time (and loads, without calling into CUDA, on a machine with no GPU).
+run time (and loads, without calling into CUDA, on a machine with no GPU). The extension is
+compiled against the installed torch's headers and linked to its libraries.
 """
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,11 +28,12 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpa_gb300.so")
+EXT_PATH = os.path.join(LIB_DIR, "_pa_torch.so")
 
 CU_SOURCES = ["errors.cu", "kv_write.cu", "copy_blocks.cu", "decode_attention.cu", "decode_mma.cu", "prefill_attention.cu",
               "attention_fixed_scratch.cu", "prefill_tcgen05.cu", "advance_batch.cu", "norm_rope_write.cu",
               "block_bounds.cu", "block_scores.cu", "select_blocks.cu", "attention_sparse.cu"]
-CPP_SOURCES = ["api.cpp", "binding.cpp", "block_manager.cpp"]
+CPP_SOURCES = ["api.cpp", "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -88,13 +93,26 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         if force or _stale(obj, src):
             jobs.append([cxx, "-std=c++17", "-O2", "-fPIC", "-Wall", "-I", INCLUDE, "-I",
                          os.path.join(cuda, "include"), "-c", src, "-o", obj])
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    ext_src, ext_obj = os.path.join(CSRC, "torch_binding.cpp"), os.path.join(BUILD_DIR, "torch_binding.cpp.o")
+    ext_new = force or _stale(ext_obj, ext_src)
+    if ext_new:
+        inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+        jobs.append([cxx, "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", *[f"-I{d}" for d in inc], "-c", ext_src, "-o",
+                     ext_obj])
     if jobs:
         with ThreadPoolExecutor(max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
             list(ex.map(lambda c: _run(c, verbose), jobs))
     if jobs or not os.path.exists(LIB_PATH):
         tmp = LIB_PATH + ".tmp"
-        _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], verbose)
+        _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libpa_gb300.so", "-o", tmp, *objs], verbose)
         os.replace(tmp, LIB_PATH)
+    if ext_new or not os.path.exists(EXT_PATH):
+        tmp, lib = EXT_PATH + ".tmp", os.path.join(torch, "lib")
+        _run([cxx, "-shared", "-o", tmp, ext_obj, LIB_PATH, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+              "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], verbose)
+        os.replace(tmp, EXT_PATH)
     return LIB_PATH
 
 
