@@ -21,7 +21,6 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 1024;
 
 struct AdvanceParams {
   int32_t* table;
@@ -57,7 +56,9 @@ __device__ __forceinline__ Request load_request(const AdvanceParams& p, int s) {
 
 // Inclusive scan over the block of (need << 32 | q): neither half overflows once the
 // totals have been checked; the unchecked first pass sums halves of at most 2^31 each.
+template <int kThreads>
 __device__ uint64_t block_inclusive_scan(uint64_t x, uint64_t* red) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -67,13 +68,13 @@ __device__ uint64_t block_inclusive_scan(uint64_t x, uint64_t* red) {
   if (lane == 31) red[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    uint64_t w = red[lane];
+    uint64_t w = lane < kWarps ? red[lane] : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+    for (int d = 1; d < kWarps; d <<= 1) {
       const uint64_t y = __shfl_up_sync(0xffffffffu, w, d);
       if (lane >= d) w += y;
     }
-    red[lane] = w;
+    if (lane < kWarps) red[lane] = w;
   }
   __syncthreads();
   return x + (warp ? red[warp - 1] : 0);
@@ -101,9 +102,9 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // kRun: tokens of a lane whose loads are in flight together.
-template <int kRun>
+template <int kThreads, int kRun>
 __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvanceParams p) {
-  __shared__ uint64_t red[32];
+  __shared__ uint64_t red[kThreads / 32];
   __shared__ int qoff[kThreads + 1], noff[kThreads + 1], ctx[kThreads];
   __shared__ unsigned long long total_q, total_need;
   griddep_wait();
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvancePa
     if (base > 0 && s < S) mine = load_request(p, s);
     const bool have = s < S && !fail;
     const uint64_t x = have ? (uint64_t(mine.need) << 32 | uint32_t(mine.q)) : 0;
-    const uint64_t inc = block_inclusive_scan(x, red), ex = inc - x;
+    const uint64_t inc = block_inclusive_scan<kThreads>(x, red), ex = inc - x;
     qoff[tid] = q_base + int(uint32_t(ex));
     noff[tid] = n_base + int(ex >> 32);
     ctx[tid] = mine.ctx;
@@ -232,7 +233,7 @@ cudaError_t allow_cluster_of_16() {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(advance_batch_kernel<4>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  e = cudaFuncSetAttribute(advance_batch_kernel<1024, 4>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done[dev] = true;
   return e;
 }
@@ -247,28 +248,35 @@ cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t*
   AdvanceParams p = {block_table, seq_lens,      query_lens,      free_blocks,  free_head, seq_lens_out,
                      free_head_out, query_start_loc, slot_mapping, positions,    err,       num_blocks,
                      num_seqs,    num_tokens,    width,           block_size,   num_free};
-  // one token a lane up to 8 CTAs (the portable cluster size), beyond that four at once and, from
-  // two rounds of 8 on, 16 CTAs (480 decodes and 32 chunks of 2048 tokens: 8.5 us, 11.2 with 8)
+  // A small step in one CTA of 256 threads (256 decodes: 3.8 us, 5.4 with 1024 threads). Else one
+  // token a lane up to 8 CTAs (the portable cluster size), beyond that four at once and, from
+  // two rounds of 8 on, 16 CTAs (480 decodes and 32 chunks of 2048 tokens: 8.5 us, 11.2 with 8).
+  constexpr int kFull = 1024;
+  const bool small = num_seqs <= 256 && num_tokens <= 256;
   int ctas = 1;
-  while (ctas < 8 && int64_t(ctas) * kThreads < num_tokens) ctas *= 2;
-  if (num_tokens > 8 * kThreads * 4) {
+  while (ctas < 8 && int64_t(ctas) * kFull < num_tokens) ctas *= 2;
+  if (num_tokens > 8 * kFull * 4) {
     const cudaError_t e = allow_cluster_of_16();
     if (e != cudaSuccess) return e;
     ctas = 16;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(small ? 256 : kFull);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(ctas);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, int64_t(ctas) * kThreads < num_tokens ? advance_batch_kernel<4> : advance_batch_kernel<1>, p);
+  cfg.numAttrs = ctas > 1 ? 2 : 1;  // (a CTA without the attribute is a cluster of its own)
+  return cudaLaunchKernelEx(&cfg,
+                            small                                    ? advance_batch_kernel<256, 1>
+                            : int64_t(ctas) * kFull < num_tokens ? advance_batch_kernel<1024, 4>
+                                                                     : advance_batch_kernel<1024, 1>,
+                            p);
 }
 
 }  // namespace pa
