@@ -61,7 +61,7 @@ class Case:
         return pa.norm_rope_write(self.out, self.q, self.k, self.v, *self.w, self.cos_sin, self.pos, self.slots, self.kc,
                                   self.vc, **args)
 
-    def check(self, skip=()):
+    def check(self, skip=(), tokens=None):
         table = _f64(self.cos_sin)
         pos = self.pos.cpu().numpy().reshape(-1, self.T)
         sections = self.sections or (self.rot // 2,)
@@ -71,8 +71,8 @@ class Case:
         out, v = _f64(self.out), _f64(self.v)
         w = [None if x is None else _f64(x) for x in self.w]
         unit = 2.0 ** -8 if self.out.dtype == BF16 else 2.0 ** -24
-        written = set()
-        for t in range(self.T):
+        written = set() if tokens is None else {x for x in slots if 0 <= x < rows}
+        for t in range(self.T) if tokens is None else tokens:
             if t in skip:
                 assert (out[t] == 7.0).all()
                 continue
@@ -144,6 +144,49 @@ def test_matches_the_oracle(pa, name):
     c.check()
 
 
+LONG = {  # enough tokens for the streaming kernel; checked on a sample of tokens and every untouched slot
+    "fused_gqa": dict(Hq=32, Hkv=8, D=128, fused=True),
+    "three_axes": dict(Hq=8, Hkv=2, D=128, axes=3, fused=True),
+    "odd_heads_d64": dict(Hq=7, Hkv=3, D=64),
+    "odd_sections_interleaved": dict(Hq=4, Hkv=1, D=128, sections=(1, 30, 0, 33), interleaved=True),
+    "partial_rot_f32": dict(Hq=4, Hkv=2, D=128, rot=32, dtype=F32),
+    "e4m3": dict(Hq=8, Hkv=4, D=128, cache=E4M3, axes=2),
+    "e4m3_f32_d64_no_norm": dict(Hq=3, Hkv=1, D=64, dtype=F32, cache=E4M3, norm=(False, False)),
+    "wide_mha_f32": dict(Hq=24, Hkv=24, D=128, dtype=F32),  # a token too large for the ring: the other kernel
+}
+
+
+@pytest.mark.parametrize("name", LONG)
+def test_long_prompts_match_the_oracle(pa, name):
+    spec = LONG[name]
+    row = spec["D"] * (4 if spec.get("dtype") == F32 else 2)
+    T = (40 << 20) // ((spec["Hq"] + 2 * spec["Hkv"]) * row) + 77  # 40 MB of rows: where the stream begins
+    c = Case(T=T, **spec, seed=len(name))
+    c.slots[11] = -1
+    c.slots[T - 1] = -7
+    c.pos.view(-1, T)[0, T // 2] = 1000  # out of range: skipped
+    c.run(pa)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == pa.PA_DEVERR["position"]
+    c.slots[T // 2] = -1
+    c.check(skip=(T // 2,), tokens=sorted({0, 1, 11, 455, 456, T // 2, T - 2, T - 1, *range(5, T, T // 25)}))
+
+
+def test_long_prompt_in_place_and_by_parts(pa):
+    """The streaming kernel on 14000 tokens, in place, equals calls on 500 at a time (the other one)."""
+    c, d = (Case(14000, 8, 2, 128, fused=False, axes=2, seed=4) for _ in range(2))
+    c.out = c.q
+    c.run(pa)
+    whole = (d.q, d.k, d.v, d.pos, d.slots, d.out)
+    for i in range(0, 14000, 500):
+        d.q, d.k, d.v, d.slots, d.out = (x[i:i + 500] for x in (whole[0], whole[1], whole[2], whole[4], whole[5]))
+        d.pos = whole[3][:, i:i + 500].contiguous()
+        d.run(pa)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == 0
+    assert torch.equal(c.q, whole[5]) and torch.equal(c.kc, d.kc) and torch.equal(c.vc, d.vc)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_in_place_equals_out_of_place(pa, dtype):
     c = Case(50, 8, 2, 128, dtype=dtype, axes=2)
@@ -198,6 +241,17 @@ def test_zero_rows_and_no_tokens(pa):
     e.run(pa)
     torch.cuda.synchronize()
     assert pa.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("T", [5, 41000])
+def test_not_a_number_stays_with_its_pair(pa, T):
+    """Without a norm a NaN or infinity spoils its own pair, or (not rotated) only itself."""
+    c = Case(T, 2, 1, 128, rot=32, norm=(False, False))
+    c.q[2, 1, 3], c.q[2, 1, 60], c.q[2, 0, 100] = float("nan"), float("inf"), float("nan")
+    c.run(pa)
+    torch.cuda.synchronize()
+    bad = torch.nonzero(~torch.isfinite(c.out)).tolist()
+    assert bad == [[2, 0, 100], [2, 1, 3], [2, 1, 19], [2, 1, 60]]
 
 
 def test_angles_of_far_positions_come_from_the_table(pa):
