@@ -3,22 +3,25 @@
 //
 //   out[t, h] = sum_i softmax_i(scale <q[t, h], K_i>) V_i,  i over the listed blocks' positions <= p
 //
-// A unit of work is (token, KV head): its G query heads are rows of a 16-row MMA, its keys
-// come in chunks of 16 tokens (one listed block is block_size / 16 of them). Units share no
-// keys by construction -- every head of every token may have chosen other blocks -- so the
-// kernel streams G x 16-row products against keys read once per unit: bound by the bytes of
-// K and V, as decode attention is.
+// A unit of work is (token, KV head): its G query heads are the 8 columns of the MMAs, its keys
+// come in chunks of 16 tokens (one listed block is block_size / 16 of them): S^T = K Q^T with the
+// tokens as rows, O^T += V^T P^T with the dims as rows. (With the heads as the 16 rows, of which
+// G are used, the same takes twice the MMAs and accumulators.) Units share no keys by
+// construction -- every head of every token may have chosen other blocks -- so the kernel is
+// bound by the bytes of K and V, as decode attention is.
 //
 // Each warp streams its own chunks (every C x NW-th of the list) through a private ring of
 // STAGES chunks filled by 16-byte asynchronous copies: K and V rows of one head are 2 D-byte
 // segments scattered over the pool, which a warp's lanes gather directly (no tensor map, no
 // barrier between warps; rows past the causal limit are zero-filled, never read). Running
-// maximum, sum and O stay in fp32 registers.
+// maximum, sum and O stay in fp32 registers; the reference maximum moves only when a score
+// exceeds it by more than 8 (log2 units), so most chunks need no reduction over their tokens
+// and no rescaling of O, and numerators stay below 2^8.
 //
 // Few units (a small batch, a draft of some tokens): a cluster of C = 2, 4 or 8 CTAs shares
-// one unit's list, and merges its partial results through distributed shared memory, so the
-// split needs no workspace and no second launch. The merge runs in a fixed order: same bits
-// every time.
+// one unit's list. Each CTA sends its partial result to the CTAs that write the outputs,
+// through distributed shared memory, so the split needs no workspace and no second launch.
+// The merge runs in a fixed order: same bits every time.
 //
 // Precision as the decode kernel: bf16 caches multiply in bf16 with P rounded to bf16; E4M3
 // caches in f16 (codes exact, P rounded to f16); everything summed in fp32.
@@ -36,13 +39,12 @@ struct SparseCfg {
   static constexpr bool kF16 = EL == 1;
   static constexpr int RB = D * EL;       // bytes of one head's row
   static constexpr int CPR = RB / 16;     // 16-byte pieces of a row
-  static constexpr int KC = D / 16;
-  static constexpr int NT = D / 8;
+  static constexpr int KC = D / 16;        // MMA steps of S^T, tiles of O^T
   static constexpr int kTile = kTok * RB;  // bytes of a chunk's K (or V)
   static constexpr int kWarpBytes = STAGES * 2 * kTile;
-  static constexpr int kPartOff = NW * kWarpBytes;         // the CTA's merged O, for the cluster
-  static constexpr int kMlOff = kPartOff + 8 * D * 4;      // per warp: m[8], l[8]; then the CTA's
-  static constexpr int kSmem = kMlOff + (NW + 1) * 16 * 4;
+  static constexpr int kPartOff = NW * kWarpBytes;         // O from the cluster's CTAs, for this one's outputs
+  static constexpr int kMlOff = kPartOff + 8 * D * 4 + 64;  // per warp, then per CTA of the cluster: m[8], l[8]
+  static constexpr int kSmem = kMlOff + (NW + 8) * 16 * 4;
   static_assert(8 * D * 4 <= kWarpBytes, "a warp's O goes where its ring was");
   // Byte offset of 16-byte piece c of row r: the piece index is XORed with the row so that
   // the 8 rows of an ldmatrix fall in 8 different bank groups.
@@ -62,16 +64,25 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// The address in CTA `rank` of the cluster of what is at `addr` in this one.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(v)
-               : "r"(addr), "r"(rank)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ void st_cluster2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+// An 8 x 8 matrix of 16-bit elements, transposed: lane (g, t) gives row g, columns 2t, 2t + 1.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 template <typename KV, int D, int NW, int STAGES>
@@ -97,21 +108,22 @@ __global__ void __launch_bounds__(NW * 32)
   const int entry0 = entry(0);
   const QueryRow row = find_row(b, tok);
   if (row.s < 0) return;  // the whole cluster: one unit
+  if (csplit > 1) cluster_arrive();
   const int32_t* table = b.block_table + int64_t(row.s) * b.max_blocks_per_seq;
 
-  // ---- the G query rows as A fragments (rows g >= G are zero)
-  uint32_t qa0[C::KC], qa2[C::KC];
+  // ---- the G query heads as B fragments: lane (g, t) holds dims of head g (0 from G on)
+  uint32_t qb[C::KC][2];
   {
     const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + (int64_t(tok) * Hq + head * G + (g < G ? g : 0)) * D;
 #pragma unroll
     for (int kc = 0; kc < C::KC; ++kc) {
       if constexpr (C::kF16) {  // k slots 2t, 2t+1, 2t+8, 2t+9 hold dims 4t .. 4t+3, as K's codes do below
         const uint2 w = g < G ? __ldg(reinterpret_cast<const uint2*>(qp + 16 * kc + 4 * t)) : make_uint2(0u, 0u);
-        qa0[kc] = pack_f16(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
-        qa2[kc] = pack_f16(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+        qb[kc][0] = pack_f16(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+        qb[kc][1] = pack_f16(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
       } else {
-        qa0[kc] = g < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * kc + 2 * t)) : 0u;
-        qa2[kc] = g < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * kc + 8 + 2 * t)) : 0u;
+        qb[kc][0] = g < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * kc + 2 * t)) : 0u;
+        qb[kc][1] = g < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * kc + 8 + 2 * t)) : 0u;
       }
     }
   }
@@ -141,14 +153,15 @@ __global__ void __launch_bounds__(NW * 32)
   };
   constexpr int kPieces = kTok * C::CPR / 32;  // 16-byte copies per lane, for K and for V
   const int64_t pitch = int64_t(Hkv) * C::RB;
-  uint32_t vring = 0;  // 8 bits a stage: valid tokens of the chunk in flight there
+  uint64_t vring = 0;  // 8 bits a stage: valid tokens of the chunk in flight there
+  static_assert(STAGES <= 8, "a byte each");
   auto issue = [&](int k) {
     if (k < n) {
       if ((k & 31) == 0) load_window(k);
       const int64_t r0 = __shfl_sync(0xffffffffu, win_row, k & 31);
       const int valid = __shfl_sync(0xffffffffu, win_valid, k & 31);
       const int st = k % STAGES;
-      vring = (vring & ~(0xffu << (8 * st))) | uint32_t(valid) << (8 * st);
+      vring = (vring & ~(uint64_t(0xff) << (8 * st))) | uint64_t(valid) << (8 * st);
       if (valid > 0) {
         const int64_t off = r0 * pitch + int64_t(head) * C::RB;
         const char* kp = static_cast<const char*>(a.k_cache) + off;
@@ -167,11 +180,16 @@ __global__ void __launch_bounds__(NW * 32)
     cp_async_commit();  // one group a step, empty ones too
   };
 
-  float o[C::NT][4];
+  // O^T: lane (g, t) holds dims 16 i + g (e 0, 1) and 16 i + 8 + g (e 2, 3) of heads 2t, 2t + 1
+  float o[C::KC][4];
 #pragma unroll
-  for (int i = 0; i < C::NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float mrun = -INFINITY, lpart = 0.f;
+  for (int i = 0; i < C::KC; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float mrun[2] = {-INFINITY, -INFINITY}, lpart[2] = {0.f, 0.f};  // of heads 2t, 2t + 1
   const float cscale = a.scale * 1.4426950408889634f * a.k_scale;
+  const int lm = lane >> 3, lr = lane & 7;
+  // this lane's rows g and g + 8 of S^T as tokens of the chunk (E4M3: in the order in which the
+  // transposed codes of V pair tokens, 0 1 4 5 8 9 12 13 | 2 3 6 7 ..)
+  const int tok0 = C::kF16 ? 4 * (g >> 1) + (g & 1) : g, tok1 = C::kF16 ? tok0 + 2 : g + 8;
 
 #pragma unroll
   for (int k = 0; k < STAGES - 1; ++k) issue(k);
@@ -180,97 +198,86 @@ __global__ void __launch_bounds__(NW * 32)
     cp_async_wait<STAGES - 1>();
     __syncwarp();  // every lane's copies of chunk k have landed
     const int st = k % STAGES;
-    const int valid = (vring >> (8 * st)) & 0xff;
+    const int valid = int(vring >> (8 * st)) & 0xff;
     if (valid > 0) {
       const uint32_t kb = ring + uint32_t(st * 2 * C::kTile), vb = kb + C::kTile;
-      // S = Q K^T: two tiles of 8 tokens, two accumulators each (even / odd k steps)
-      float sacc[2][4], sacc2[2][4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sacc[j][e] = sacc2[j][e] = 0.f;
-      const int lm = lane >> 3, lr = lane & 7;
+      // S^T = K Q^T, in four chains
+      float acc[4][4] = {};
 #pragma unroll
       for (int kc = 0; kc < C::KC; ++kc) {
         uint32_t r0, r1, r2, r3;
         if constexpr (C::kF16) {
-          if ((kc & 1) == 0) {  // 16-byte pieces kc, kc + 1 (16 codes each) of the two token tiles
+          if ((kc & 1) == 0) {  // 16-byte pieces kc, kc + 1 (16 codes each) of rows g and g + 8
             ldsm_x4(kb + C::at(4 * (lr >> 1) + (lr & 1) + 2 * (lm & 1), kc + (lm >> 1)), r0, r1, r2, r3);
-            uint32_t a0, a1, b0, b1, c0, c1, d0, d1;
-            e4m3x4_to_f16x2x2(r0, a0, a1);
-            e4m3x4_to_f16x2x2(r1, b0, b1);
-            e4m3x4_to_f16x2x2(r2, c0, c1);
-            e4m3x4_to_f16x2x2(r3, d0, d1);
-            mma_16816(sacc[0], qa0[kc], 0u, qa2[kc], 0u, a0, a1, true);
-            mma_16816(sacc[1], qa0[kc], 0u, qa2[kc], 0u, b0, b1, true);
-            mma_16816(sacc2[0], qa0[kc + 1], 0u, qa2[kc + 1], 0u, c0, c1, true);
-            mma_16816(sacc2[1], qa0[kc + 1], 0u, qa2[kc + 1], 0u, d0, d1, true);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x2x2(r0, a0, a2);
+            e4m3x4_to_f16x2x2(r1, a1, a3);
+            mma_16816(acc[kc & 2], a0, a1, a2, a3, qb[kc][0], qb[kc][1], true);
+            e4m3x4_to_f16x2x2(r2, a0, a2);
+            e4m3x4_to_f16x2x2(r3, a1, a3);
+            mma_16816(acc[(kc & 2) + 1], a0, a1, a2, a3, qb[kc + 1][0], qb[kc + 1][1], true);
           }
         } else {
           ldsm_x4(kb + C::at((lm & 1) * 8 + lr, 2 * kc + (lm >> 1)), r0, r1, r2, r3);
-          mma_16816((kc & 1) ? sacc2[0] : sacc[0], qa0[kc], 0u, qa2[kc], 0u, r0, r2, false);
-          mma_16816((kc & 1) ? sacc2[1] : sacc[1], qa0[kc], 0u, qa2[kc], 0u, r1, r3, false);
+          mma_16816(acc[kc & 3], r0, r1, r2, r3, qb[kc][0], qb[kc][1], false);
         }
       }
-      // online softmax of row g over the chunk; the quad's lanes share the row. The reference
-      // maximum moves only when a score exceeds it by more than 8 (log2 units), so O is
-      // rescaled only then and numerators stay below 2^8.
-      float x[2][2], mx = -INFINITY;
+      // numerators: x[e] token tok0 of heads 2t, 2t + 1; x[2 + e] token tok1
+      float x[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool in = (C::kF16 ? 4 * t + 2 * j + e : 8 * j + 2 * t + e) < valid;
-          x[j][e] = in ? (sacc[j][e] + sacc2[j][e]) * cscale : -INFINITY;
-          mx = fmaxf(mx, x[j][e]);
-        }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mnew = mx > mrun + 8.f ? mx : mrun;
-      const float ms = mnew == -INFINITY ? 0.f : mnew;
-      const float alpha = mnew == mrun ? 1.f : ex2_ftz(mrun - ms);
-      float pv[2][2], psum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int e = 0; e < 4; ++e) {
+        const float v = (acc[0][e] + acc[1][e]) + (acc[2][e] + acc[3][e]);
+        x[e] = (e < 2 ? tok0 : tok1) < valid ? v * cscale : -INFINITY;
+      }
+      float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+      if (__any_sync(0xffffffffu, mx[0] > mrun[0] + 8.f || mx[1] > mrun[1] + 8.f)) {
+        float alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          pv[j][e] = ex2_ftz(x[j][e] - ms);
-          psum += pv[j][e];
-        }
-      lpart = lpart * alpha + psum;
-      mrun = mnew;
-      if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
-        for (int i = 0; i < C::NT; ++i) {
-          o[i][0] *= alpha;
-          o[i][1] *= alpha;
+          for (int m = 4; m <= 16; m *= 2) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], m));
+          const float mnew = mx[e] > mrun[e] + 8.f ? mx[e] : mrun[e];
+          alpha[e] = mnew == mrun[e] ? 1.f : ex2_ftz(mrun[e] - mnew);
+          mrun[e] = mnew;
+          lpart[e] *= alpha[e];
+        }
+#pragma unroll
+        for (int i = 0; i < C::KC; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[1];
+          o[i][2] *= alpha[0];
+          o[i][3] *= alpha[1];
         }
       }
-      // O += P V (rows of V past the causal limit are zeros in shared memory)
+      float pv[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float m = mrun[e & 1];
+        pv[e] = ex2_ftz(x[e] - (m == -INFINITY ? 0.f : m));
+        lpart[e & 1] += pv[e];
+      }
+      // O^T += V^T P^T (rows of V past the causal limit are zeros in shared memory)
       if constexpr (C::kF16) {
-        const uint32_t p0 = pack_f16(pv[0][0], pv[0][1]), p2 = pack_f16(pv[1][0], pv[1][1]);
+        const uint32_t p0 = transpose8x8(pack_f16(pv[0], pv[1])), p1 = transpose8x8(pack_f16(pv[2], pv[3]));
 #pragma unroll
         for (int c2 = 0; c2 < C::KC / 2; ++c2) {
           uint32_t r0, r1, r2, r3;
           ldsm_b8_x2_trans(vb + C::at(lane & 15, 2 * c2 + (lane >> 4)), r0, r1, r2, r3);
-          uint32_t a0, a1, b0, b1, c0, c1, d0, d1;
-          e4m3x4_to_f16x2x2(r0, a0, a1);
-          e4m3x4_to_f16x2x2(r1, b0, b1);
-          e4m3x4_to_f16x2x2(r2, c0, c1);
-          e4m3x4_to_f16x2x2(r3, d0, d1);
-          mma_16816(o[4 * c2 + 0], p0, 0u, p2, 0u, a0, a1, true);
-          mma_16816(o[4 * c2 + 1], p0, 0u, p2, 0u, b0, b1, true);
-          mma_16816(o[4 * c2 + 2], p0, 0u, p2, 0u, c0, c1, true);
-          mma_16816(o[4 * c2 + 3], p0, 0u, p2, 0u, d0, d1, true);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2x2(r0, a0, a2);
+          e4m3x4_to_f16x2x2(r1, a1, a3);
+          mma_16816(o[2 * c2], a0, a1, a2, a3, p0, p1, true);
+          e4m3x4_to_f16x2x2(r2, a0, a2);
+          e4m3x4_to_f16x2x2(r3, a1, a3);
+          mma_16816(o[2 * c2 + 1], a0, a1, a2, a3, p0, p1, true);
         }
       } else {
-        const uint32_t p0 = pack_bf16(pv[0][0], pv[0][1]), p2 = pack_bf16(pv[1][0], pv[1][1]);
+        const uint32_t p0 = transpose8x8(pack_bf16(pv[0], pv[1])), p1 = transpose8x8(pack_bf16(pv[2], pv[3]));
 #pragma unroll
-        for (int i2 = 0; i2 < C::NT / 2; ++i2) {
-          uint32_t r0, r1, r2, r3;
-          ldsm_x4_trans(vb + C::at((lm & 1) * 8 + lr, 2 * i2 + (lm >> 1)), r0, r1, r2, r3);
-          mma_16816(o[2 * i2], p0, 0u, p2, 0u, r0, r1, false);
-          mma_16816(o[2 * i2 + 1], p0, 0u, p2, 0u, r2, r3, false);
+        for (int i = 0; i < C::KC; ++i) {
+          uint32_t r0, r1, r2, r3;  // (tokens 0-7 | 8-15) x (dims 16 i .. | + 8 ..), transposed
+          ldsm_x4_trans(vb + C::at((lm >> 1) * 8 + lr, 2 * i + (lm & 1)), r0, r1, r2, r3);
+          mma_16816(o[i], r0, r1, r2, r3, p0, p1, false);
         }
       }
     }
@@ -279,24 +286,41 @@ __global__ void __launch_bounds__(NW * 32)
   cp_async_wait<0>();
 
   // ---- merge the warps' pieces (each holds O relative to its own reference maximum)
-  lpart += __shfl_xor_sync(0xffffffffu, lpart, 1);
-  lpart += __shfl_xor_sync(0xffffffffu, lpart, 2);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int m = 4; m <= 16; m *= 2) lpart[e] += __shfl_xor_sync(0xffffffffu, lpart[e], m);
   float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
   __syncwarp();
-  if (g < G) {
-    float* po = reinterpret_cast<float*>(smem + warp * C::kWarpBytes) + g * D + 2 * t;
 #pragma unroll
-    for (int i = 0; i < C::NT; ++i) *reinterpret_cast<float2*>(po + 8 * i) = make_float2(o[i][0], o[i][1]);
-    if (t == 0) {
-      ml[warp * 16 + g] = mrun;
-      ml[warp * 16 + 8 + g] = lpart;
+  for (int e = 0; e < 2; ++e) {
+    const int h = 2 * t + e;
+    if (h < G) {
+      float* po = reinterpret_cast<float*>(smem + warp * C::kWarpBytes) + h * D + g;
+#pragma unroll
+      for (int i = 0; i < C::KC; ++i) {
+        po[16 * i] = o[i][e];
+        po[16 * i + 8] = o[i][2 + e];
+      }
+      if (g == 0) {
+        ml[warp * 16 + h] = mrun[e];
+        ml[warp * 16 + 8 + h] = lpart[e];
+      }
     }
   }
+  if (csplit > 1) cluster_wait();  // every CTA of the cluster has started: its shared memory may be written
   __syncthreads();
-  // (m, l, O) of `parts` pieces of row r, dims d, d + 1; a piece without keys has m = -inf
-  float* part = reinterpret_cast<float*>(smem + C::kPartOff);
-  for (int e = threadIdx.x; e < G * D / 2; e += NW * 32) {
-    const int r = 2 * e / D, d = 2 * e % D;
+  // Outputs in pairs of dims; of a split unit CTA r writes pairs [r share, (r + 1) share), from the
+  // pieces that every CTA sends it. A piece without keys has m = -inf and weight 0.
+  const int pairs = G * D / 2, share = (pairs + csplit - 1) / csplit;
+  const uint32_t part_at = smem_u32(smem + C::kPartOff), ml_at = smem_u32(ml + NW * 16);
+  auto write = [&](int e, float l, float x, float y) {
+    const float inv = l == 0.f ? 0.f : a.v_scale / l;  // no keys: zeros
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t(tok) * Hq + head * G) * D + 2 * e) =
+        pack_bf16(x * inv, y * inv);
+  };
+  for (int e = threadIdx.x; e < pairs; e += NW * 32) {
+    const int r = 2 * e / D;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * 16 + r]);
@@ -305,50 +329,49 @@ __global__ void __launch_bounds__(NW * 32)
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float wt = ex2_ftz(ml[w * 16 + r] - Ms);
-      const float2 v = *reinterpret_cast<const float2*>(smem + w * C::kWarpBytes + (r * D + d) * 4);
+      const float2 v = *reinterpret_cast<const float2*>(smem + w * C::kWarpBytes + e * 8);
       l = fmaf(wt, ml[w * 16 + 8 + r], l);
       x = fmaf(wt, v.x, x);
       y = fmaf(wt, v.y, y);
     }
     if (csplit == 1) {
-      const float inv = l == 0.f ? 0.f : a.v_scale / l;  // no keys: zeros
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t(tok) * Hq + head * G + r) * D + d) =
-          pack_bf16(x * inv, y * inv);
+      write(e, l, x, y);
     } else {
-      *reinterpret_cast<float2*>(part + r * D + d) = make_float2(x, y);
-      if (d == 0) {
-        ml[NW * 16 + r] = M;
-        ml[NW * 16 + 8 + r] = l;
+      const int owner = e / share;
+      st_cluster2(cluster_addr(part_at + uint32_t(rank * share + e - owner * share) * 8, owner), x, y);
+      if (2 * e % D == 0) {  // the row's maximum and sum, to every CTA
+        for (int c = 0; c < csplit; ++c) {
+          st_cluster(cluster_addr(ml_at + uint32_t(rank * 16 + r) * 4, c), M);
+          st_cluster(cluster_addr(ml_at + uint32_t(rank * 16 + 8 + r) * 4, c), l);
+        }
       }
     }
   }
   if (csplit == 1) return;
-  // ---- merge the cluster's CTAs: CTA `rank` writes its share of the outputs
-  cluster_sync();
-  const uint32_t part_at = smem_u32(part), ml_at = smem_u32(ml + NW * 16);
-  const int share = (G * D / 2 + csplit - 1) / csplit;
-  for (int e = rank * share + threadIdx.x; e < min(rank * share + share, G * D / 2); e += NW * 32) {
-    const int r = 2 * e / D, d = 2 * e % D;
+  cluster_arrive();  // (release: what was sent is visible after the wait)
+  cluster_wait();
+  const float2* part = reinterpret_cast<const float2*>(smem + C::kPartOff);
+  for (int i = threadIdx.x; i < min(share, pairs - rank * share); i += NW * 32) {
+    const int e = rank * share + i, r = 2 * e / D;
+    const float* from = ml + NW * 16 + r;
     float M = -INFINITY;
-    for (int c = 0; c < csplit; ++c) M = fmaxf(M, ld_cluster(ml_at + r * 4, c));
+    for (int c = 0; c < csplit; ++c) M = fmaxf(M, from[c * 16]);
     const float Ms = M == -INFINITY ? 0.f : M;
     float l = 0.f, x = 0.f, y = 0.f;
     for (int c = 0; c < csplit; ++c) {
-      const float wt = ex2_ftz(ld_cluster(ml_at + r * 4, c) - Ms);
-      l = fmaf(wt, ld_cluster(ml_at + (8 + r) * 4, c), l);
-      x = fmaf(wt, ld_cluster(part_at + (r * D + d) * 4, c), x);
-      y = fmaf(wt, ld_cluster(part_at + (r * D + d + 1) * 4, c), y);
+      const float wt = ex2_ftz(from[c * 16] - Ms);
+      const float2 v = part[c * share + i];
+      l = fmaf(wt, from[c * 16 + 8], l);
+      x = fmaf(wt, v.x, x);
+      y = fmaf(wt, v.y, y);
     }
-    const float inv = l == 0.f ? 0.f : a.v_scale / l;
-    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t(tok) * Hq + head * G + r) * D + d) =
-        pack_bf16(x * inv, y * inv);
+    write(e, l, x, y);
   }
-  cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
 template <typename KV, int D>
 cudaError_t launch(const BatchArgs& b, const SparseAttnArgs& a, cudaStream_t stream) {
-  constexpr int NW = 4, STAGES = 3;
+  constexpr int NW = 4, STAGES = sizeof(KV) == 1 ? 6 : 3;
   using C = SparseCfg<KV, D, NW, STAGES>;
   constexpr auto kern = attention_sparse_kernel<KV, D, NW, STAGES>;
   cudaError_t e = ensure_smem<kern>(C::kSmem);
