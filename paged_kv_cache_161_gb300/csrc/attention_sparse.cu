@@ -85,21 +85,23 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-template <typename KV, int D, int NW, int STAGES>
+// ONE: a unit per warp; else a unit per CTA or cluster of csplit CTAs.
+template <typename KV, int D, int NW, int STAGES, bool ONE>
 __global__ void __launch_bounds__(NW * 32)
     attention_sparse_kernel(const __grid_constant__ BatchArgs b, const __grid_constant__ SparseAttnArgs a, int csplit) {
   using C = SparseCfg<KV, D, NW, STAGES>;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();
   griddep_launch_dependents();
-  const int unit = blockIdx.x / csplit, rank = blockIdx.x % csplit;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = ONE ? int(blockIdx.x) * NW + warp : int(blockIdx.x) / csplit, rank = ONE ? 0 : int(blockIdx.x) % csplit;
   const int Hkv = a.num_kv_heads, Hq = a.num_heads, G = Hq / Hkv;
   const int tok = unit / Hkv, head = unit % Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (ONE && tok >= b.num_tokens) return;
   const int g = lane >> 2, t = lane & 3;
   const int B = b.block_size, CB = B / kTok;
   const int nchunks = a.num_select * CB;
-  const int first = rank * NW + warp, step = csplit * NW;
+  const int first = ONE ? 0 : rank * NW + warp, step = ONE ? 1 : csplit * NW;
   const int n = nchunks > first ? (nchunks - first + step - 1) / step : 0;  // this warp's chunks
   const uint32_t ring = smem_u32(smem) + uint32_t(warp * C::kWarpBytes);
   const int32_t* list = a.block_idx + int64_t(unit) * a.num_select;
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(NW * 32)
   const int entry0 = entry(0);
   const QueryRow row = find_row(b, tok);
   if (row.s < 0) return;  // the whole cluster: one unit
-  if (csplit > 1) cluster_arrive();
+  if (!ONE && csplit > 1) cluster_arrive();
   const int32_t* table = b.block_table + int64_t(row.s) * b.max_blocks_per_seq;
 
   // ---- the G query heads as B fragments: lane (g, t) holds dims of head g (0 from G on)
@@ -308,8 +310,11 @@ __global__ void __launch_bounds__(NW * 32)
       }
     }
   }
-  if (csplit > 1) cluster_wait();  // every CTA of the cluster has started: its shared memory may be written
-  __syncthreads();
+  if (!ONE && csplit > 1) cluster_wait();  // every CTA of the cluster has started: its shared memory may be written
+  if constexpr (ONE)
+    __syncwarp();
+  else
+    __syncthreads();
   // Outputs in pairs of dims; of a split unit CTA r writes pairs [r share, (r + 1) share), from the
   // pieces that every CTA sends it. A piece without keys has m = -inf and weight 0.
   const int pairs = G * D / 2, share = (pairs + csplit - 1) / csplit;
@@ -319,6 +324,13 @@ __global__ void __launch_bounds__(NW * 32)
     *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t(tok) * Hq + head * G) * D + 2 * e) =
         pack_bf16(x * inv, y * inv);
   };
+  if constexpr (ONE) {
+    for (int e = lane; e < pairs; e += 32) {
+      const float2 v = *reinterpret_cast<const float2*>(smem + warp * C::kWarpBytes + e * 8);
+      write(e, ml[warp * 16 + 8 + 2 * e / D], v.x, v.y);
+    }
+    return;
+  }
   for (int e = threadIdx.x; e < pairs; e += NW * 32) {
     const int r = 2 * e / D;
     float M = -INFINITY;
@@ -373,14 +385,27 @@ template <typename KV, int D>
 cudaError_t launch(const BatchArgs& b, const SparseAttnArgs& a, cudaStream_t stream) {
   constexpr int NW = 4, STAGES = sizeof(KV) == 1 ? 6 : 3;
   using C = SparseCfg<KV, D, NW, STAGES>;
-  constexpr auto kern = attention_sparse_kernel<KV, D, NW, STAGES>;
+  const int64_t units = int64_t(b.num_tokens) * a.num_kv_heads;
+  const int chunks = a.num_select * (b.block_size / kTok);
+  // A warp per unit (nothing is merged) or a CTA: 2 CTAs of NW warps fit a SM either way, so the
+  // time goes with the waves of warps (of CTAs) x (chunks a warp takes + what a unit costs
+  // beside them, 2.5 and 5 chunks' time). 256 x 8 units: of 4 blocks 17.2 us by warps, 30.8 by
+  // CTAs, of 32 blocks 81.9 and 88.5; 160 x 8 units (two waves of warps, the second almost
+  // empty) of 128 blocks 244.8 and 194.7.
+  const int64_t slots = 2 * 152, warps_t = (units + slots * NW - 1) / (slots * NW) * (2 * int64_t(chunks) + 5),
+                ctas_t = (units + slots - 1) / slots * (2 * ((int64_t(chunks) + NW - 1) / NW) + 10);
+  if (units >= slots && warps_t < ctas_t) {
+    constexpr auto kern = attention_sparse_kernel<KV, D, NW, STAGES, true>;
+    const cudaError_t e = ensure_smem<kern>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(unsigned((units + NW - 1) / NW)), dim3(NW * 32), C::kSmem, stream, b, a, 1);
+  }
+  constexpr auto kern = attention_sparse_kernel<KV, D, NW, STAGES, false>;
   cudaError_t e = ensure_smem<kern>(C::kSmem);
   if (e != cudaSuccess) return e;
   // CTAs per unit: one a SM at least, while each warp still has two chunks. (Two requests of
   // four tokens, 64 units of 128 blocks, E4M3: 12.3 us with 256 CTAs in clusters of 4, 17.5 with
   // 512 in clusters of 8.)
-  const int64_t units = int64_t(b.num_tokens) * a.num_kv_heads;
-  const int chunks = a.num_select * (b.block_size / kTok);
   int split = 1;
   while (split < 8 && units * split < 152 && chunks >= split * 2 * NW * 2) split *= 2;
   cudaLaunchConfig_t cfg = {};

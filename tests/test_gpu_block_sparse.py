@@ -303,10 +303,12 @@ def test_attention_over_every_block_is_attention(pa, cache):
     assert (np.abs(_f64(out) - ref) <= 1.5e-2 + 1e-2 * np.abs(ref)).all()
 
 
-@pytest.mark.parametrize("lens,qs,k", [([3000], [1], 187), ([9000, 50], [1, 1], 300), ([4000] * 40, [1] * 40, 60)])
-def test_split_and_unsplit_units(pa, lens, qs, k):
-    """Lists long enough for clusters of 8 CTAs, and many units of one CTA each."""
-    b = Batch(lens, qs, Hq=8, Hkv=2)
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("lens,qs,k,Hkv", [([3000], [1], 187, 2), ([9000, 50], [1, 1], 300, 2), ([1500] * 40, [1] * 40, 60, 2),
+                                           ([90] * 41, [1] * 41, 3, 8), ([300, 40] * 30, [2, 9] * 30, 17, 1)])
+def test_split_and_unsplit_units(pa, lens, qs, k, Hkv, cache):
+    """Lists long enough for clusters of 8 CTAs, units of one CTA each, and units of one warp each."""
+    b = Batch(lens, qs, Hq=8, Hkv=Hkv, cache=cache)
     idx = _random_lists(b, k)
     got = b.attend(pa, idx)
     again = b.attend(pa, idx)
