@@ -428,7 +428,7 @@ int pa_norm_rope_write(void* q_out, const void* q, const void* k, const void* v,
  * p = seq_lens[s] - q_len + t - query_start_loc[s]; its context is blocks 0 .. p / block_size).
  * Rows of tokens that belong to no request (behind the last one) are left as they are. A request
  * with q_len > seq_len, or longer than its table row, sets PA_DEVERR_SEQ_RANGE and its rows are
- * left as they are.
+ * left as they are; so may one of more than max_query_len queries.
  * Supported: head_dim 64 / 128; num_heads / num_kv_heads in {1, 2, 4, 8}; block_size a multiple
  * of 16; bf16 queries over bf16 or E4M3 caches (any of them for bounds, scores and selection,
  * which never read the queries' cache). No workspace; every kernel on `stream`.

@@ -600,6 +600,8 @@ int pa_advance_batch(int32_t* block_table, int max_blocks_per_seq, const int32_t
   if (num_seqs < 0 || num_tokens < 0 || num_free < 0 || block_size < 1 || num_blocks < 1) return PA_ERR_INVALID_ARG;
   if (num_seqs > 0 && max_blocks_per_seq < 1) return PA_ERR_INVALID_ARG;
   if (int64_t(max_blocks_per_seq) * block_size > 0x7fffffff) return PA_ERR_INVALID_ARG;
+  // the kernel counts requests and tokens in 32 bits, up to one step of all its threads past the end
+  if (num_seqs > 0x7fffffff - (1 << 17) || num_tokens > 0x7fffffff - (1 << 17)) return PA_ERR_UNSUPPORTED;
   if (!free_head || !free_head_out || !query_start_loc) return PA_ERR_INVALID_ARG;
   if (num_seqs > 0 && (!block_table || !seq_lens || !query_lens || !seq_lens_out)) return PA_ERR_INVALID_ARG;
   if (num_free > 0 && !free_blocks) return PA_ERR_INVALID_ARG;
@@ -780,7 +782,7 @@ int pa_select_blocks(int32_t* block_idx, int num_select, const float* scores, in
   if (int64_t(score_width) * block_size > 0x7fffffff) return PA_ERR_INVALID_ARG;
   if (nothing) return PA_OK;
   if (!block_idx || !scores || !aligned(block_idx, 4) || !aligned(scores, 4)) return PA_ERR_INVALID_ARG;
-  if (int64_t(num_tokens) * num_kv_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;  // grid
+  if (int64_t(num_tokens) * num_kv_heads > 0x7fffffff - 64) return PA_ERR_UNSUPPORTED;  // rows, whole CTAs of them
   cudaError_t e;
   pa::BatchArgs b = {nullptr, seq_lens, query_start_loc, pa::device_error_word(&e), 1, score_width,
                      num_seqs, num_tokens, 0, block_size};

@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) block_bounds_kernel(const __gr
     const Touched w = touched(b, s);
     const int64_t i = at - place(b, s);
     have = i >= 0 && i < w.count;
+    if (b.max_query_len <= 1 && w.count > 1) raise_error(b.err, PA_DEVERR_SEQ_RANGE);  // more queries than announced
     if (have) {
       const int blk = w.first + int(i);
       id = __ldg(b.block_table + int64_t(s) * b.max_blocks_per_seq + blk);

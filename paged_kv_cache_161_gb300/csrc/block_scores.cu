@@ -92,7 +92,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int q0 = __ldg(b.query_start_loc + s), q_len = __ldg(b.query_start_loc + s + 1) - q0;
   const int L = __ldg(b.seq_lens + s);
-  if (q_len <= 0 || is_chunk(q_len, G)) return;
+  if (q_len <= 0) return;
+  if (is_chunk(q_len, G)) {  // the other kernel's, which max_query_len must have called for
+    if (!after_chunks && threadIdx.x == 0) raise_error(b.err, PA_DEVERR_SEQ_RANGE);
+    return;
+  }
   if (!fits(b, q0, q_len, L, width)) {
     if (threadIdx.x == 0) raise_error(b.err, PA_DEVERR_SEQ_RANGE);
     return;

@@ -408,6 +408,51 @@ def test_relabelled_blocks_give_the_same_bits(pa):
     assert pa.read_device_errors() == 0
 
 
+def test_offsets_past_32_bits(pa):
+    """The same requests in the last blocks of a pool of 2.3e9 elements (4.6 GB) a cache."""
+    b = Batch([300, 140, 33], [2, 40, 1])
+    idx = _random_lists(b, 9)
+    far = Batch.__new__(Batch)
+    far.__dict__.update(b.__dict__)
+    far.NB = 140000
+    far.k, far.v = (torch.empty((far.NB, *x.shape[1:]), dtype=BF16, device="cuda") for x in (b.k, b.v))
+    far.k[-b.NB:], far.v[-b.NB:] = b.k, b.v
+    t = b.meta[0]
+    far.meta = (torch.where(t < b.NB, t + (far.NB - b.NB), t), *b.meta[1:])
+    assert torch.equal(b.attend(pa, idx), far.attend(pa, idx))
+    near_bounds, far_bounds = _full_bounds(pa, b), _full_bounds(pa, far)
+    assert torch.equal(near_bounds[b.meta[0][0, :19].long()], far_bounds[far.meta[0][0, :19].long()])
+    assert torch.equal(b.scores(pa, near_bounds), far.scores(pa, far_bounds))
+    # a cache write there, beside the same write in a small pool
+    q, slots = torch.randn((9, 12, 128), device="cuda").to(BF16), torch.tensor([5, 100, -1, 3, 70, 9, 20, 21, 22], device="cuda")
+    cs = torch.rand((50, 128), device="cuda")
+    pos = torch.arange(9, dtype=I32, device="cuda")
+    outs = []
+    for k, v, off in ((b.k, b.v, 0), (far.k, far.v, (far.NB - b.NB) * 16)):
+        out = torch.empty((9, 4, 128), dtype=BF16, device="cuda")
+        q8 = torch.cat([q[:, :4]] * 4, 1)
+        pa.norm_rope_write(out, q[:, :4], q8[:, :8], q8[:, 8:], None, None, cs, pos, torch.where(slots < 0, slots, slots + off),
+                           k, v)
+        outs.append((out, k[-b.NB:].clone(), v[-b.NB:].clone()))
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == 0
+    for x, y in zip(*outs):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+def test_more_queries_than_announced_are_flagged(pa):
+    """max_query_len is an upper bound; a batch beyond it is reported, not answered silently."""
+    b = Batch([300, 64], [50, 1], Hq=8, Hkv=2)
+    b.max_q = 1
+    bounds = torch.zeros((b.NB, b.Hkv, 2, b.D), dtype=BF16, device="cuda")
+    b.scores(pa, bounds)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == pa.PA_DEVERR["seq_range"]
+    b.bounds(pa)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == pa.PA_DEVERR["seq_range"]
+
+
 def test_the_bindings_refuse(pa):
     b = Batch([40], [1])
     bounds = b.bounds(pa)

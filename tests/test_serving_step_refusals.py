@@ -30,7 +30,8 @@ def test_advance_batch():
         (0, None, INVALID), (0, _at(1) + 2, INVALID), (1, 0, INVALID), (1, 1 << 30, INVALID), (2, None, INVALID),
         (3, None, INVALID), (4, None, INVALID), (5, -1, INVALID), (6, None, INVALID), (7, None, INVALID),
         (8, None, INVALID), (9, None, INVALID), (10, None, INVALID), (10, _at(9) + 4, INVALID), (11, None, INVALID),
-        (12, -1, INVALID), (13, -1, INVALID), (14, 0, INVALID), (15, 0, INVALID),
+        (12, -1, INVALID), (13, -1, INVALID), (14, 0, INVALID), (15, 0, INVALID), (12, 2**31 - 1, UNSUPPORTED),
+        (13, 2**31 - 1, UNSUPPORTED),
         # outputs over inputs or one another; seq_lens_out / free_head_out beside, not on, their inputs
         (7, _at(2) + 4, INVALID), (7, _at(3), INVALID), (8, _at(4), INVALID), (9, _at(2), INVALID),
         (10, _at(1), INVALID), (11, _at(9) + 8, INVALID), (11, _at(5), INVALID), (9, _at(6) - 4, INVALID),
