@@ -570,6 +570,7 @@ int check_batch(const int32_t* block_table, int max_blocks_per_seq, const int32_
   if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || max_seq_len < 0 || block_size < 1 || num_blocks < 1)
     return PA_ERR_INVALID_ARG;
   if (block_size % 16 != 0) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 0x7fffffff - 1024) return PA_ERR_UNSUPPORTED;  // searched in 32 bits
   nothing = num_seqs == 0 || num_tokens == 0;
   if (nothing) return PA_OK;
   if (!seq_lens || !query_start_loc || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4)) return PA_ERR_INVALID_ARG;

@@ -50,7 +50,8 @@ __device__ __forceinline__ uint32_t bf16x2_pos_part(uint32_t x) {
 constexpr int kMaxFewCols = 32;
 __device__ __forceinline__ bool is_chunk(int q_len, int G) { return int64_t(q_len) * G > kMaxFewCols; }
 __device__ __forceinline__ bool fits(const BatchArgs& b, int q0, int q_len, int L, int width) {
-  return q0 >= 0 && q0 <= b.num_tokens - q_len && q_len <= L && L <= int64_t(b.max_blocks_per_seq) * b.block_size && (L - 1) / b.block_size < width;
+  return q0 >= 0 && q0 <= b.num_tokens - q_len && q_len <= L && L <= int64_t(b.max_blocks_per_seq) * b.block_size &&
+         (L - 1) / b.block_size < width;
 }
 
 // ---------------------------------------------------------------- few query rows: mma.sync
@@ -241,8 +242,8 @@ cudaError_t launch_few(const BatchArgs& b, float* scores, int width, const __nv_
 // A CTA keeps its columns' [q-, q+] in shared memory -- split from q once, 128 KB at D = 128 --
 // and streams the request's blocks past them: 128 rows of lo, then 128 of hi, gathered by 16-byte
 // asynchronous copies (a block's row is 2 D contiguous bytes per half) into a ring of 3 stages.
-// With 256 columns a byte of bounds read from L2 feeds 256 products; with 128 the copies, not
-// the tensor cores, were the bound. Blocks are the M side so that the maximum over a group's
+// With 256 columns a tile's copies (64 KB at D = 128) take half of the time of its MMAs at L2's
+// rate; with 128 they would take all of it. Blocks are the M side so that the maximum over a group's
 // heads runs over a thread's own accumulator columns, and 32 lanes store 32 consecutive blocks.
 // Two accumulators of 256 columns: the epilogue of one tile runs beside the next tile's MMAs.
 // Warps 0-7: the columns' split, then the epilogue (TMEM lanes 32 (w % 4) .., every second 32
@@ -510,8 +511,8 @@ cudaError_t launch_chunk(const BatchArgs& b, float* scores, int width, const __n
   const int64_t x = (int64_t(b.num_tokens) * G / kChunkCols + b.num_seqs) * Hkv;
   // Blocks per CTA: a CTA's setup (its request, the columns' split, the pipeline's filling) costs
   // about as much as kSetup tiles, and one CTA runs on a SM at a time: the fewest waves x (setup
-  // + tiles). Four 512-token chunks (288 column tiles of 5 block
-  // tiles): 38.0 us in parts of 3 and 2 tiles, 29.5 us whole.
+  // + tiles). Four 512-token chunks (288 column tiles of 5 block tiles): 38.0 us in parts of 3 and
+  // 2 tiles, 29.5 us whole.
   constexpr int64_t kSetup = 2;
   const int tiles = (width + kTileBlocks - 1) / kTileBlocks;
   int per = tiles;
