@@ -268,10 +268,16 @@ struct ChunkLayout {
   static constexpr uint32_t SMEM = BYTES + 1024;                 // + alignment slack
 };
 
-// The first column tile of request s in the grid: no scan is needed, since s + (columns before
-// it) / 256 leaves room for every request's last, partial tile.
+// The first column tile of request s in the grid: no scan is needed, since (columns before it) /
+// 256 and one more tile for every request, or for every kMaxFewCols + 1 columns where those are
+// fewer, leaves room for every request's last, partial tile: a request of this kernel has more
+// than kMaxFewCols columns.
+__host__ __device__ __forceinline__ int64_t tiles_before(int64_t columns, int requests) {
+  const int64_t partial = columns / (kMaxFewCols + 1);
+  return columns / kChunkCols + (partial < requests ? partial : requests);
+}
 __device__ __forceinline__ int64_t tile_base(const BatchArgs& b, int G, int s) {
-  return int64_t(__ldg(b.query_start_loc + s)) * G / kChunkCols + s;
+  return tiles_before(int64_t(__ldg(b.query_start_loc + s)) * G, s);
 }
 
 template <int D, int G>
@@ -508,7 +514,7 @@ cudaError_t launch_chunk(const BatchArgs& b, float* scores, int width, const __n
   constexpr auto kern = block_scores_chunk_kernel<D, G>;
   const cudaError_t e = ensure_smem<kern>(LY::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t x = (int64_t(b.num_tokens) * G / kChunkCols + b.num_seqs) * Hkv;
+  const int64_t x = tiles_before(int64_t(b.num_tokens) * G, b.num_seqs) * Hkv;
   // Blocks per CTA: a CTA's setup (its request, the columns' split, the pipeline's filling) costs
   // about as much as kSetup tiles, and one CTA runs on a SM at a time: the fewest waves x (setup
   // + tiles). Four 512-token chunks (288 column tiles of 5 block tiles): 38.0 us in parts of 3 and
@@ -547,7 +553,7 @@ cudaError_t launch_block_scores(const BatchArgs& b, float* scores, int score_wid
   const auto* qp = static_cast<const __nv_bfloat16*>(q);
   const auto* bp = static_cast<const __nv_bfloat16*>(bounds);
   const int G = num_heads / num_kv_heads;
-  const bool chunks = int64_t(b.max_query_len) * G > kMaxFewCols;
+  const bool chunks = int64_t(min(b.max_query_len, b.num_tokens)) * G > kMaxFewCols;
   if (chunks) {
     const cudaError_t e = head_dim == 64
                               ? dispatch_chunk<64>(b, scores, score_width, qp, bp, num_kv_heads, G, stream)

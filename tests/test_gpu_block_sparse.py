@@ -189,6 +189,32 @@ def test_scores_of_chunks(pa, name):
         assert (np.abs(got[fin] - ref[fin]) <= 2 * b.D * 2.0 ** -23 * size[fin]).all()
 
 
+@pytest.mark.parametrize("G,D", [(1, 64), (2, 128), (4, 64), (8, 128)])
+def test_scores_of_chunks_among_decodes(pa, G, D):
+    """Few long requests between many short and empty ones: the chunks' places in the grid."""
+    few = 32 // G
+    qs = [1] * 90 + [few + 1] + [0, 2, few] * 15 + [3 * few + 5, 0, 256 // G + 1] + [1] * 40 + [few + 2] * 9
+    lens = [q + 7 * i % 150 for i, q in enumerate(qs)]
+    b = Batch(lens, qs, Hq=2 * G, Hkv=2, D=D, seed=G)
+    bounds = _full_bounds(pa, b)
+    got = _f64(b.scores(pa, bounds))
+    assert pa.read_device_errors() == 0
+    ref, size = ss.scores_ref(_f64(b.q), _f64(bounds), b.table, b.lens, b.qsl, b.B, b.W)
+    assert np.array_equal(np.isnan(ref), np.isnan(got))
+    assert np.array_equal(ref == -np.inf, got == -np.inf)
+    fin = np.isfinite(ref)
+    assert (np.abs(got[fin] - ref[fin]) <= 2 * b.D * 2.0 ** -23 * size[fin]).all()
+
+
+def test_scores_of_fewer_tokens_than_the_longest_request_announced(pa):
+    b = Batch([50, 90], [1, 2], Hq=8, Hkv=2)
+    bounds = _full_bounds(pa, b)
+    expect = b.scores(pa, bounds)
+    b.max_q = 80  # at most the longest context
+    assert torch.equal(expect, b.scores(pa, bounds))
+    assert pa.read_device_errors() == 0
+
+
 def test_scores_of_chunks_with_bad_blocks(pa):
     b = Batch([400, 300], [100, 20], Hq=8, Hkv=2)
     bounds = _full_bounds(pa, b)
