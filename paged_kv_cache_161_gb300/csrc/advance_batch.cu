@@ -21,7 +21,6 @@
 namespace pa {
 namespace {
 
-
 struct AdvanceParams {
   int32_t* table;
   const int32_t* seq_lens;
@@ -54,8 +53,8 @@ __device__ __forceinline__ Request load_request(const AdvanceParams& p, int s) {
   return r;
 }
 
-// Inclusive scan over the block of (need << 32 | q): neither half overflows once the
-// totals have been checked; the unchecked first pass sums halves of at most 2^31 each.
+// Inclusive scan over the block of (need << 32 | q): neither half overflows, since the totals
+// have been checked.
 template <int kThreads>
 __device__ uint64_t block_inclusive_scan(uint64_t x, uint64_t* red) {
   constexpr int kWarps = kThreads / 32;
@@ -124,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvancePa
     sq += r.q;
     sn += r.need;
   }
+  bad |= sq > uint64_t(p.num_tokens);  // so that the sums below stay small (a block needs a token)
   if (tid == 0) total_q = total_need = 0;
   bad = __syncthreads_or(bad);
   sq = warp_sum(sq);
