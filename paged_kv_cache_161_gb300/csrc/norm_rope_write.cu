@@ -349,6 +349,11 @@ __global__ void __launch_bounds__((kTurners + 1) * 32, kStreamCtas)
     int64_t slot = -1;
     int pos[kMaxAxes] = {};
     bool bad = false;
+    // The turners have stopped (every stage was filled): nothing may land behind the CTA's end.
+    auto give_up = [&]() {
+      raise_error(p.err, PA_DEVERR_TIMEOUT);
+      for (int i = 0; i < lay.stages; ++i) mbar_wait(full0 + 8 * i, i < stage ? phase : phase ^ 1);
+    };
     for (int64_t k = 0;; ++k) {
       if (first + k * step >= p.num_tokens) break;
       if ((k & 31) == 0) {
@@ -393,7 +398,7 @@ __global__ void __launch_bounds__((kTurners + 1) * 32, kStreamCtas)
         }
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) {
-        raise_error(p.err, PA_DEVERR_TIMEOUT);
+        if (lane == 0) give_up();
         return;
       }
       advance();
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__((kTurners + 1) * 32, kStreamCtas)
         heads[stage] = {-1, -1};
         mbar_arrive(full0 + 8 * stage);
       } else {
-        raise_error(p.err, PA_DEVERR_TIMEOUT);
+        give_up();
       }
     }
     return;
