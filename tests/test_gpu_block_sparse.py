@@ -504,3 +504,37 @@ def test_the_bindings_refuse(pa):
         pa.block_bounds(bounds[:, :4], b.k, *b.meta, max_query_len=1, max_seq_len=40)
     with pytest.raises(pa.PAError):
         pa.block_bounds(bounds, b.k.float(), *b.meta, max_query_len=1, max_seq_len=40)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("lens,qs,k,Hkv,D", [([640, 320], [1, 3], 1, 8, 128), ([640, 320], [1, 3], 12, 2, 64),
+                                             ([320] * 45, [1] * 45, 6, 8, 128)])
+def test_numerators_keep_fp32_precision(pa, lens, qs, k, Hkv, D, cache):
+    """Tokens in pairs v, -v under almost flat weights: the sums cancel to about 1 / 30 of their
+    terms, so what the numerators lose before the second product shows beside the output's own
+    rounding. A numerator is carried in two 16-bit parts: of bf16 within 2^-16 relative, of f16 within
+    2^-22. The fp32 sums: up to 2 k MMAs of a warp, four warps or CTAs merged, each addition
+    2^-23 of the magnitudes; 2^-21 for the exponential: together at most 2^-17 up to k = 12.
+    The logits as above (2 e)."""
+    b = Batch(lens, qs, Hq=4 * Hkv, Hkv=Hkv, D=D, cache=cache, seed=k)
+    v = b.v.float()
+    v[:, 1::2] = -v[:, 0::2]
+    b.v = v.to(cache)
+    b.q = (b.q * 0.05).to(BF16)
+    idx = np.full((b.T, b.Hkv, k), -1, np.int32)
+    rng = np.random.default_rng(k)
+    for t, _, p in ss.rows_of(b.lens, b.qsl):
+        whole = (p + 1) // b.B  # blocks without a token behind the causal limit
+        for g in range(b.Hkv):
+            idx[t, g] = rng.choice(whole, k, replace=False)
+    idx = torch.tensor(idx, device="cuda")
+    got = _f64(b.attend(pa, idx))
+    assert pa.read_device_errors() == 0
+    kv = b.values()
+    ref, mag, logit = ss.attention_sparse_ref(_f64(b.q), *kv, b.table, b.lens, b.qsl, idx.cpu().numpy(), b.scale)
+    assert np.median(np.abs(ref)) < 0.1 * np.median(mag)
+    p = 2.0 ** -22 if cache == E4M3 else 2.0 ** -16
+    tol = (p + 2 * b.D * 2.0 ** -23 * logit + 2.0 ** -17) * mag
+    tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), (int(bad.sum()), (np.abs(got - ref) / tol).max())
