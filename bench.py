@@ -37,12 +37,13 @@ METRIC = "paged decode attention: K/V GB/s (% of GB300 HBM peak) and tokens/s, b
 # from one ncu capture (the first timed step's two launches) of
 #   ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum,gpu__time_duration.sum \
 #       --clock-control none --csv --log-file launches.csv \
-#       python bench.py --steps 2 --warmup 3 --no-cpu-baseline --no-e2e --no-secondary
+#       -k regex:decode -c 12 python bench.py --steps 2 --warmup 3 --no-cpu-baseline --no-e2e --no-secondary
 # It holds only for the kernel sources it was measured on (their SHA-256 below); any
 # change to them makes the reported traffic null until it is measured again.
-DECODE_TRAFFIC = {"sources_sha256": "e29717f03a8df0cfaa62284ccd1132765bfba070981a6dbeeb0bdddb150e47e8", "bytes": 1653156096}
+DECODE_TRAFFIC = {"sources_sha256": "12d6bac5bcb89571792d72a9685c3651bd1529bf0a6ad2dd13f15535d920a88e", "bytes": 1653092608}
 DECODE_SOURCES = ["paged_kv_cache_161_gb300/csrc/decode_attention.cu", "paged_kv_cache_161_gb300/csrc/decode_mma.cu",
-                  "paged_kv_cache_161_gb300/csrc/decode_common.cuh", "paged_kv_cache_161_gb300/csrc/common.cuh"]
+                  "paged_kv_cache_161_gb300/csrc/decode_common.cuh", "paged_kv_cache_161_gb300/csrc/common.cuh",
+                  "paged_kv_cache_161_gb300/csrc/mma.cuh", "paged_kv_cache_161_gb300/csrc/tcgen05.cuh"]
 
 
 def _decode_traffic():
