@@ -8,7 +8,8 @@ _pa_torch.so of the serving-step calls beside it.
 Each CUDA translation unit is compiled by nvcc in parallel, the host units by g++, and
 nvcc links them with the static CUDA runtime, so the library needs only the driver at
 run time (and loads, without calling into CUDA, on a machine with no GPU). The extension is
-compiled against the installed torch's headers and linked to its libraries.
+compiled against the installed torch's headers and linked to its libraries, and again when
+another torch or Python is found.
 """
 from __future__ import annotations
 
@@ -60,6 +61,13 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(p) > t for p in [src] + _headers())
 
 
+def _torch_identity(torch: str) -> str:
+    """What the extension's object belongs to besides its sources: it is compiled against the
+    headers of one torch and one Python (and reads torch's tensors by their layout there)."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return "\n".join([torch, f.read(), str(sysconfig.get_config_var("SOABI"))])
+
+
 def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -95,8 +103,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
                          os.path.join(cuda, "include"), "-c", src, "-o", obj])
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     ext_src, ext_obj = os.path.join(CSRC, "torch_binding.cpp"), os.path.join(BUILD_DIR, "torch_binding.cpp.o")
-    ext_new = force or _stale(ext_obj, ext_src)
+    ext_tag, identity = ext_obj + ".torch", _torch_identity(torch)
+    ext_new = force or _stale(ext_obj, ext_src) or not os.path.exists(ext_tag) or open(ext_tag).read() != identity
     if ext_new:
+        if os.path.exists(ext_tag):  # written again after the link: a build that stops before is taken again
+            os.remove(ext_tag)
         inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
         jobs.append([cxx, "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", *[f"-I{d}" for d in inc], "-c", ext_src, "-o",
@@ -113,6 +124,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         _run([cxx, "-shared", "-o", tmp, ext_obj, LIB_PATH, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
               "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], verbose)
         os.replace(tmp, EXT_PATH)
+        with open(ext_tag, "w") as f:
+            f.write(identity)
     return LIB_PATH
 
 
