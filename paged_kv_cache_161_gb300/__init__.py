@@ -8,7 +8,9 @@ block_bounds, block_scores, select_blocks, attention_sparse), a few microseconds
 GPU, through a small extension, _pa_torch.so, whose host time is 3 us a call.
 
 The library is built in-tree by ``python paged_kv_cache_161_gb300/build.py`` (or the
-repository's ``__graft_entry__.build()``). Importing this package without it raises.
+repository's ``__graft_entry__.build()``). Importing this package without it raises. The
+extension is built against the installed torch; where it is missing or does not load (another
+torch), only the serving-step calls raise.
 """
 from __future__ import annotations
 
@@ -49,11 +51,10 @@ PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
 PA_DEVERR = {"slot_range": 0x1, "block_range": 0x2, "seq_range": 0x4, "timeout": 0x8, "slot_mismatch": 0x10,
              "no_blocks": 0x20, "position": 0x40}
 
-for _path in (LIB_PATH, EXT_PATH):
-    if not os.path.exists(_path):
-        raise ImportError(
-            f"{_path} is missing: build it with `python paged_kv_cache_161_gb300/build.py` "
-            "(there is no fallback path)")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(
+        f"{LIB_PATH} is missing: build it with `python paged_kv_cache_161_gb300/build.py` "
+        "(there is no fallback path)")
 
 lib = ctypes.CDLL(LIB_PATH)
 
@@ -423,16 +424,36 @@ def attention_grouped(out, q, k_cache, v_cache, block_table, seq_lens, query_sta
 
 
 # The serving-step calls come from an extension of their own: see csrc/torch_binding.cpp.
-_spec = importlib.util.spec_from_file_location("_pa_torch", EXT_PATH)
-_pa_torch = importlib.util.module_from_spec(_spec)
-_spec.loader.exec_module(_pa_torch)
-_pa_torch.init(PAError)
-advance_batch = _pa_torch.advance_batch
-norm_rope_write = _pa_torch.norm_rope_write
-block_bounds = _pa_torch.block_bounds
-block_scores = _pa_torch.block_scores
-select_blocks = _pa_torch.select_blocks
-attention_sparse = _pa_torch.attention_sparse
+def _load_extension():
+    spec = importlib.util.spec_from_file_location("_pa_torch", EXT_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.init(PAError)
+    return mod
+
+
+def _without_extension(name: str, why: ImportError):
+    def call(*args, **kwargs):
+        raise ImportError(f"{name} needs {EXT_PATH}, which does not load: build it with "
+                          "`python paged_kv_cache_161_gb300/build.py` (there is no fallback path)") from why
+
+    return call
+
+
+try:
+    _pa_torch = _load_extension()
+except ImportError as e:
+    _pa_torch = None
+    (advance_batch, norm_rope_write, block_bounds, block_scores, select_blocks, attention_sparse) = (
+        _without_extension(n, e) for n in ("advance_batch", "norm_rope_write", "block_bounds", "block_scores",
+                                           "select_blocks", "attention_sparse"))
+else:
+    advance_batch = _pa_torch.advance_batch
+    norm_rope_write = _pa_torch.norm_rope_write
+    block_bounds = _pa_torch.block_bounds
+    block_scores = _pa_torch.block_scores
+    select_blocks = _pa_torch.select_blocks
+    attention_sparse = _pa_torch.attention_sparse
 
 
 def read_device_errors(clear: bool = True) -> int:
