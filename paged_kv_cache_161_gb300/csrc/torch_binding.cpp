@@ -157,7 +157,14 @@ struct On {
   }
 };
 
-PyObject* result(const char* fn, int status, PyObject* value) {
+// Calls the library with the interpreter's lock released, as ctypes does: a launch waits where the
+// stream's queue is full, perhaps for a Python function queued there. (The arguments' tensors are
+// held by the caller.) Returns `value`, or raises.
+template <typename F>
+PyObject* result(const char* fn, PyObject* value, F call) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const int status = call();
+  PyEval_RestoreThread(state);
   if (status != PA_OK) {
     PyObject* e = PyObject_CallFunction(g_error, "is", status, fn);
     if (e) {
@@ -205,10 +212,10 @@ PyObject* advance_batch(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
     const int B = int32(a.v[10], names[10]);
     const int64_t NB = integer(a.v[11]);
     const On on(dev, a.v[12]);
-    return result("pa_advance_batch",
-                  pa_advance_batch(p[0], int(W), p[1], p[2], p[3], int(F), p[4], p[5], p[6], p[7], slots, p[9], int(S),
-                                   int(T), B, NB, on.stream),
-                  Py_None);
+    return result("pa_advance_batch", Py_None, [&] {
+      return pa_advance_batch(p[0], int(W), p[1], p[2], p[3], int(F), p[4], p[5], p[6], p[7], slots, p[9], int(S), int(T),
+                              B, NB, on.stream);
+    });
   });
 }
 
@@ -264,11 +271,11 @@ PyObject* norm_rope_write(PyObject*, PyObject* const* args, Py_ssize_t n, PyObje
     const float k_scale = a.v[14] ? float(real(a.v[14])) : 1.f, v_scale = a.v[15] ? float(real(a.v[15])) : 1.f;
     const pa_dtype dt = code(q, names[1]), cdt = code(kc, names[9]);
     const On on(dev, a.v[16]);
-    return result("pa_norm_rope_write",
-                  pa_norm_rope_write(out, qp, kp, vp, qs, ks, vs, w[0], w[1], eps, table, int(limit), int(rot), interleaved,
-                                     pos, axes, sections, slots, kcp, vcp, T, NB, int(B), int(Hq), int(Hkv), int(D), dt, cdt,
-                                     k_scale, v_scale, on.stream),
-                  a.v[0]);
+    return result("pa_norm_rope_write", a.v[0], [&] {
+      return pa_norm_rope_write(out, qp, kp, vp, qs, ks, vs, w[0], w[1], eps, table, int(limit), int(rot), interleaved,
+                                pos, axes, sections, slots, kcp, vcp, T, NB, int(B), int(Hq), int(Hkv), int(D), dt, cdt,
+                                k_scale, v_scale, on.stream);
+    });
   });
 }
 
@@ -310,9 +317,10 @@ PyObject* block_bounds(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject*
     const int T = a.v[7] && a.v[7] != Py_None ? int32(a.v[7], names[7]) : most > INT32_MAX ? INT32_MAX : int(most);
     const pa_dtype dt = code(kc, names[1]);
     const On on(dev, a.v[8]);
-    return result("pa_block_bounds", pa_block_bounds(bounds, kcp, b.table, b.W, b.lens, b.qsl, b.S, T, max_q, max_s, Hkv, D,
-                                                     B, NB, dt, on.stream),
-                  a.v[0]);
+    return result("pa_block_bounds", a.v[0], [&] {
+      return pa_block_bounds(bounds, kcp, b.table, b.W, b.lens, b.qsl, b.S, T, max_q, max_s, Hkv, D, B, NB, dt,
+                             on.stream);
+    });
   });
 }
 
@@ -332,9 +340,10 @@ PyObject* block_scores(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject*
     const Batch b(a.v, names, 3, dev);
     const int B = int32(a.v[6], names[6]), max_q = int32(a.v[7], names[7]), max_s = int32(a.v[8], names[8]);
     const On on(dev, a.v[9]);
-    return result("pa_block_scores", pa_block_scores(scores, width, qp, bp, b.table, b.W, b.lens, b.qsl, b.S, T, max_q, max_s,
-                                                     Hq, Hkv, D, B, NB, on.stream),
-                  a.v[0]);
+    return result("pa_block_scores", a.v[0], [&] {
+      return pa_block_scores(scores, width, qp, bp, b.table, b.W, b.lens, b.qsl, b.S, T, max_q, max_s, Hq, Hkv, D, B, NB,
+                             on.stream);
+    });
   });
 }
 
@@ -354,8 +363,9 @@ PyObject* select_blocks(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
     const int B = int32(a.v[4], names[4]), init = a.v[5] ? int32(a.v[5], names[5]) : 0,
               local = a.v[6] ? int32(a.v[6], names[6]) : 0;
     const On on(dev, a.v[7]);
-    return result("pa_select_blocks", pa_select_blocks(idx, k, scores, width, lens, qsl, S, T, Hkv, B, init, local, on.stream),
-                  a.v[0]);
+    return result("pa_select_blocks", a.v[0], [&] {
+      return pa_select_blocks(idx, k, scores, width, lens, qsl, S, T, Hkv, B, init, local, on.stream);
+    });
   });
 }
 
@@ -380,10 +390,10 @@ PyObject* attention_sparse(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
                 v_scale = a.v[11] ? float(real(a.v[11])) : 1.f;
     const pa_dtype dt = code(kc, names[2]);
     const On on(dev, a.v[12]);
-    return result("pa_attention_sparse",
-                  pa_attention_sparse(out, qp, kcp, vcp, b.table, b.W, b.lens, b.qsl, idx, k, b.S, T, max_s, Hq, Hkv, D, B, NB,
-                                      scale, dt, k_scale, v_scale, on.stream),
-                  a.v[0]);
+    return result("pa_attention_sparse", a.v[0], [&] {
+      return pa_attention_sparse(out, qp, kcp, vcp, b.table, b.W, b.lens, b.qsl, idx, k, b.S, T, max_s, Hq, Hkv, D, B, NB,
+                                 scale, dt, k_scale, v_scale, on.stream);
+    });
   });
 }
 
