@@ -442,7 +442,8 @@ int pa_norm_rope_write(void* q_out, const void* q, const void* k, const void* v,
  * swapped in, cached prefixes of another pool) get their bounds by a call whose
  * query_start_loc covers their positions. Two requests that share a block must agree on its
  * keys (shared blocks are full, or hold the same tokens). num_tokens: query_start_loc[num_seqs]
- * or more (it sizes the grid).
+ * or more (it sizes the grid when max_query_len > 1; a batch with more tokens then sets
+ * PA_DEVERR_SEQ_RANGE, and some of its blocks keep their old bounds).
  *
  * pa_block_scores: for block b of token t's context and KV head g
  *     scores[t, g, b] = max_h sum_d max(q_hd lo_d, q_hd hi_d)      (h: the group's query heads)

@@ -123,6 +123,9 @@ __global__ void __launch_bounds__(kWarps * 32, 4) block_bounds_kernel(const __gr
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // more tokens than announced: blocks of the last requests have no place in the grid
+  if (b.max_query_len > 1 && blockIdx.x == 0 && threadIdx.x == 0 && __ldg(b.query_start_loc + b.num_seqs) > b.num_tokens)
+    raise_error(b.err, PA_DEVERR_SEQ_RANGE);
   const int chunks = (vecs + 31) / 32, part = warp % share;
   const int64_t item = int64_t(blockIdx.x) * (kWarps / share) + warp / share;
   bool have = item < items;

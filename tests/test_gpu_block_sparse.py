@@ -538,3 +538,19 @@ def test_numerators_keep_fp32_precision(pa, lens, qs, k, Hkv, D, cache):
     tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
     bad = np.abs(got - ref) > tol
     assert not bad.any(), (int(bad.sum()), (np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.parametrize("S,q,flagged", [(100, 8, True), (100, 3, True), (1, 300, True), (100, 2, False), (100, 0, False)])
+def test_more_tokens_than_the_bounds_grid_was_sized_for_are_flagged(pa, S, q, flagged):
+    """num_tokens (S * max_query_len unless given) sizes the grid of pa_block_bounds: a batch with more
+    query tokens is reported, since some of its blocks have no place there."""
+    b = Batch([max(q, 1) + 20] * S, [q] * S, Hq=2, Hkv=2, D=64)
+    out = torch.full((b.NB, b.Hkv, 2, b.D), 5.0, dtype=BF16, device="cuda")
+    pa.block_bounds(out, b.k, *b.meta, max_query_len=2, max_seq_len=b.max_seq)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == (pa.PA_DEVERR["seq_range"] if flagged else 0)
+    pa.block_bounds(out, b.k, *b.meta, max_query_len=max(q, 2), max_seq_len=b.max_seq, num_tokens=max(S * q, 1))
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == 0
+    ref = ss.bounds_ref(np.full(out.shape, 5.0), _f64(b.k), b.table, b.lens, b.qsl)
+    assert np.array_equal(_f64(out), ref)
