@@ -223,19 +223,37 @@ __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvancePa
   if (tid == 0) *p.free_head_out = fail ? head : head + int(need_all);
 }
 
-// Clusters of 16 are opted into once per device.
-cudaError_t allow_cluster_of_16() {
+// Whether the device runs clusters of 16 CTAs of the kernel for long chunks: they need the opt-in
+// and 16 SMs of one GPC to themselves, which a process given part of the GPU may not have. Asked
+// once per device.
+cudaError_t cluster_of_16(bool* fits) {
   static std::mutex mu;
-  static bool done[64] = {};
+  static int known[64] = {};  // 1: yes, -1: no
+  constexpr auto kern = advance_batch_kernel<1024, 4>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
-  if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(advance_batch_kernel<1024, 4>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) done[dev] = true;
-  return e;
+  if (!known[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(1024);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    known[dev] = clusters > 0 ? 1 : -1;
+  }
+  *fits = known[dev] > 0;
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -250,15 +268,16 @@ cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t*
                      num_seqs,    num_tokens,    width,           block_size,   num_free};
   // A small step in one CTA of 256 threads (256 decodes: 3.8 us, 5.4 with 1024 threads). Else one
   // token a lane up to 8 CTAs (the portable cluster size), beyond that four at once and, from
-  // two rounds of 8 on, 16 CTAs (480 decodes and 32 chunks of 2048 tokens: 8.5 us, 11.2 with 8).
+  // two rounds of 8 on, 16 CTAs where they fit (480 decodes and 32 chunks of 2048 tokens: 8.5 us, 11.2 with 8).
   constexpr int kFull = 1024;
   const bool small = num_seqs <= 256 && num_tokens <= 256;
   int ctas = 1;
   while (ctas < 8 && int64_t(ctas) * kFull < num_tokens) ctas *= 2;
   if (num_tokens > 8 * kFull * 4) {
-    const cudaError_t e = allow_cluster_of_16();
+    bool fits = false;
+    const cudaError_t e = cluster_of_16(&fits);
     if (e != cudaSuccess) return e;
-    ctas = 16;
+    if (fits) ctas = 16;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
