@@ -554,3 +554,79 @@ def test_more_tokens_than_the_bounds_grid_was_sized_for_are_flagged(pa, S, q, fl
     assert pa.read_device_errors() == 0
     ref = ss.bounds_ref(np.full(out.shape, 5.0), _f64(b.k), b.table, b.lens, b.qsl)
     assert np.array_equal(_f64(out), ref)
+
+
+def _check_scores(b, bounds, got):
+    """Scores of every token against float64, on the GPU: value, -inf behind the context, rows of no request."""
+    lo, hi = bounds.double().unbind(2)
+    G = b.Hq // b.Hkv
+    seen = torch.zeros(b.T, dtype=torch.bool)
+    for t, s, p in ss.rows_of(b.lens, b.qsl):
+        n = p // b.B + 1
+        ids = b.meta[0][s, :n].long()
+        q = b.q[t].double().view(b.Hkv, G, 1, b.D)
+        x, y = q * lo[ids].transpose(0, 1)[:, None], q * hi[ids].transpose(0, 1)[:, None]
+        want, size = torch.maximum(x, y).sum(-1).amax(1), (x.abs() + y.abs()).sum(-1).amax(1)
+        row = got[t]
+        assert (row[:, n:] == -float("inf")).all(), (t, n)
+        assert ((row[:, :n].double() - want).abs() <= 2 * b.D * 2.0 ** -23 * size).all(), (t, n)
+        seen[t] = True
+    assert torch.isnan(got[~seen.cuda()]).all()
+
+
+RUNS = {  # CTAs of the chunks' kernel that take three to six tiles of blocks, one after another
+    "g4": dict(lens=[8200, 8193, 600, 8199], qs=[512, 500, 512, 64], Hq=32, Hkv=8),  # one context ends inside a run
+    "g4_d64": dict(lens=[8200, 2049, 600, 8199], qs=[512, 512, 511, 512], Hq=32, Hkv=8, D=64),
+    "g1": dict(lens=[8200, 8193, 600, 8199], qs=[512, 33, 600, 512], Hq=8, Hkv=8),
+    "g8_d64_wide": dict(lens=[8200, 8210, 1, 7000], qs=[300, 9, 1, 512], Hq=32, Hkv=4, D=64, wide=200, pad=3),
+    "g2_b48": dict(lens=[24600, 300], qs=[700, 300], Hq=16, Hkv=8, B=48),
+}
+
+
+@pytest.mark.parametrize("name", RUNS)
+def test_scores_of_chunks_over_runs_of_tiles(pa, name):
+    b = Batch(**RUNS[name], seed=len(name))
+    bounds = _full_bounds(pa, b)
+    got = b.scores(pa, bounds)
+    again = b.scores(pa, bounds)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == 0
+    assert torch.equal(got.nan_to_num(nan=7.0), again.nan_to_num(nan=7.0))
+    _check_scores(b, bounds, got)
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 3, 8])
+@pytest.mark.parametrize("G,D,qs", [(4, 128, [1, 4, 2, 1]), (8, 64, [1, 4, 1, 3]), (1, 128, [1, 31, 9, 1])])
+def test_scores_of_long_contexts(pa, Hkv, G, D, qs):
+    """Decodes and drafts over more tiles than a warp's ring has stages, and more than a CTA takes."""
+    b = Batch([5000, 9001, 33, 16400], qs, Hq=G * Hkv, Hkv=Hkv, D=D, seed=Hkv, wide=5)
+    bounds = _full_bounds(pa, b)
+    got = b.scores(pa, bounds)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == 0
+    _check_scores(b, bounds, got)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("lens,qs,k,spec", [
+    # 1216 units: a warp each, over 33, 64 and 70 chunks
+    ([1300] * 4, [38] * 4, 33, dict(Hq=8, Hkv=8, D=64)),
+    ([1300, 1001, 900, 1290], [38] * 4, 64, dict(Hq=16, Hkv=8, D=128)),
+    ([1300, 1001, 900, 1290], [38] * 4, 70, dict(Hq=8, Hkv=8, D=64)),
+    ([2600, 2001], [76] * 2, 18, dict(Hq=16, Hkv=8, D=64, B=64)),
+    # 160 units: a CTA each, over 140 and 33 x 4 chunks
+    ([2500, 2301], [10, 10], 140, dict(Hq=16, Hkv=8, D=128)),
+    ([2500, 2301], [10, 10], 33, dict(Hq=8, Hkv=8, D=64, B=64)),
+    # clusters of 8 CTAs, 1100 chunks
+    ([18000], [1], 1100, dict(Hq=8, Hkv=2, D=64)),
+    ([18000], [2], 1100, dict(Hq=4, Hkv=1, D=128)),
+])
+def test_lists_longer_than_a_window(pa, lens, qs, k, spec, cache):
+    """Lists of which a warp takes more than 32 chunks: its second and third window of look-ups."""
+    b = Batch(lens, qs, cache=cache, seed=k, **spec)
+    idx = _random_lists(b, k)
+    got = b.attend(pa, idx)
+    again = b.attend(pa, idx)
+    torch.cuda.synchronize()
+    assert torch.equal(got, again) and pa.read_device_errors() == 0
+    b.check_attention(got, idx)
