@@ -165,3 +165,84 @@ def test_two_captured_loops_replayed_together(pa):
             table, lens, head, _, _, _ = ss.advance_ref(*state[:2], [1] * 9, loop.free.tolist(), state[2], 9, loop.B, loop.NB)
             state = (table, lens, head)
         loop.check(state)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+def test_a_captured_step_of_chunks_and_decodes(pa, cache):
+    """Both score kernels in one graph, behind the kernels that write their queries and bounds; new rows
+    before each replay, which advances the lengths."""
+    loop = Loop(pa, 5, 100, cache, 6, seed=3)
+    loop.qlens.copy_(torch.tensor([33, 1, 40, 0, 20]))
+    state = (np.full((5, loop.W), -1), [0] * 5, 0)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    loop.qkv.normal_(generator=g)
+    loop.step(40)
+    state = loop.check(state)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loop.step(40)
+    for _ in range(6):
+        loop.qkv.normal_(generator=g)
+        graph.replay()
+        state = loop.check(state)
+
+
+FIRST = """
+import sys, torch
+sys.path.insert(0, "tests")
+import paged_kv_cache_161_gb300 as pa
+from test_gpu_block_sparse import BF16, E4M3, I32, Batch
+
+def everything(b, k):
+    bounds = b.bounds(pa)
+    s = b.scores(pa, bounds)
+    idx = b.select(pa, s, k, 1, 1)
+    return bounds, s, idx, b.attend(pa, idx)
+
+def advance(S, q):
+    i = lambda *shape: torch.ones(shape, dtype=I32, device="cuda")
+    free = torch.arange(S * 2000, dtype=I32, device="cuda")
+    lens, head, qsl, pos = i(S), i(1), i(S + 1), i(S * q)
+    slots = torch.ones(S * q, dtype=torch.int64, device="cuda")
+    table = i(S, 2000)
+    pa.advance_batch(table, i(S), i(S) * q, free, i(1), lens, head, qsl, slots, pos, block_size=16, num_blocks=S * 2000)
+    return table, lens, head, qsl, slots, pos
+
+def norm(T, cache):
+    x = torch.arange(T * 12 * 128, device="cuda").sin().view(T, 12, 128).to(BF16)
+    kc = torch.zeros((T // 16 + 1, 16, 2, 128), device="cuda").to(cache)
+    vc, out = torch.zeros_like(kc), torch.empty((T, 8, 128), dtype=BF16, device="cuda")
+    cs = torch.arange(64 * 128, device="cuda").cos().view(64, 128)
+    pa.norm_rope_write(out, x[:, :8], x[:, 8:10], x[:, 10:], None, None, cs, torch.zeros(T, dtype=I32, device="cuda"),
+                       torch.arange(T, device="cuda"), kc, vc)
+    return out, kc.float(), vc.float()
+
+batches = [Batch(lens=[300, 90], qs=[1, 1], cache=c, **s) for c in (BF16, E4M3) for s in (dict(D=64), dict())]
+batches += [Batch(lens=[300, 90], qs=[100, 30], cache=c, Hq=16, Hkv=8, D=D) for c in (BF16, E4M3) for D in (64, 128)]
+calls = [lambda b=b: everything(b, 4) for b in batches]
+calls += [lambda: advance(3, 1), lambda: advance(3, 1000), lambda: advance(3, 12000), lambda: norm(5, BF16),
+          lambda: norm(5, E4M3), lambda: norm(14000, BF16), lambda: norm(14000, E4M3)]
+for i, call in enumerate(calls):
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    want = call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+assert pa.read_device_errors() == 0
+print("fine")
+"""
+
+
+def test_the_first_call_of_each_kernel_may_be_captured():
+    """What a kernel's first call sets up does not disturb a capture under way."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stdout + r.stderr
