@@ -1,5 +1,9 @@
 // Shared by the block-sparse kernels: the request and position of a query token, found on
 // the device from query_start_loc and seq_lens.
+//
+// These kernels start before the one in front of them has ended, and read what it wrote behind
+// griddep_wait(): none of their pointers is __restrict__, which would let the compiler take the
+// wait's memory clobber as not meant for them and move a load above it.
 #pragma once
 
 #include "common.cuh"

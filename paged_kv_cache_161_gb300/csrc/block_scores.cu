@@ -68,8 +68,8 @@ __host__ __device__ inline Sharing sharing(int Hkv) {
 
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32)
-    block_scores_kernel(const __grid_constant__ BatchArgs b, float* __restrict__ scores, int width,
-                        const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ bounds, int Hkv, int G,
+    block_scores_kernel(const __grid_constant__ BatchArgs b, float* scores, int width,
+                        const __nv_bfloat16* q, const __nv_bfloat16* bounds, int Hkv, int G,
                         int ctas_per_seq, bool after_chunks) {
   constexpr int KC = D / 16;            // MMA steps of lo (and of hi)
   constexpr int RB = 4 * D;             // bytes of a block's row: lo, hi
@@ -283,8 +283,8 @@ __device__ __forceinline__ int64_t tile_base(const BatchArgs& b, int G, int s) {
 
 template <int D, int G>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-    block_scores_chunk_kernel(const __grid_constant__ BatchArgs b, float* __restrict__ scores, int width,
-                              const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ bounds, int Hkv,
+    block_scores_chunk_kernel(const __grid_constant__ BatchArgs b, float* scores, int width,
+                              const __nv_bfloat16* q, const __nv_bfloat16* bounds, int Hkv,
                               int tiles_per_cta) {
   using LY = ChunkLayout<D>;
   constexpr int NH = LY::kHalves;

@@ -50,8 +50,8 @@ constexpr int kBins = 256;
 // WARPS warps per row, PER scores per lane (0: read from global memory each time).
 template <int WARPS, int PER>
 __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerCta * 32 : WARPS * 32)
-    select_blocks_kernel(const __grid_constant__ BatchArgs b, int32_t* __restrict__ block_idx, int num_select,
-                         const float* __restrict__ scores, int width, int Hkv, int init, int local, int rows) {
+    select_blocks_kernel(const __grid_constant__ BatchArgs b, int32_t* block_idx, int num_select,
+                         const float* scores, int width, int Hkv, int init, int local, int rows) {
   constexpr bool kReload = PER == 0;
   constexpr int kGroup = 4;  // scores handled without a test of their number
   static_assert(PER % kGroup == 0, "whole groups");
