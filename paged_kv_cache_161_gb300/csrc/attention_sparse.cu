@@ -23,11 +23,13 @@
 // through distributed shared memory, so the split needs no workspace and no second launch.
 // The merge runs in a fixed order: same bits every time.
 //
-// Precision: bf16 caches multiply in bf16, E4M3 caches in f16 (codes exact); everything is summed
-// in fp32. A numerator goes into the second product as two 16-bit parts, the rounded value and
-// what the rounding left: 2^-16 relative with bf16 parts, 2^-22 with f16, where one part alone
-// (2^-8, 2^-11) shows in sums that cancel. The second set of MMAs runs beside the stream of K and V
-// (256 tokens of 64 blocks, bf16: 161.5 us, 160.5 with one part; 2 x 4 tokens, E4M3: 10.7, 10.3).
+// Precision: bf16 caches multiply in bf16; E4M3 caches in f16, which holds every code's value, and
+// queries of magnitudes from 2^-14 to 65504 exactly. Everything is summed in fp32. A numerator goes
+// into the second product as two 16-bit parts, the rounded value and what the rounding left: 2^-16
+// relative with bf16 parts, 2^-22 with f16 (below 2^-14: 2^-25 of the reference), where one part
+// alone (2^-8, 2^-11) shows in sums that cancel. 256 tokens of 64 blocks: bf16 161.1 us, 160.2 with
+// one part; E4M3 100.7, 96.4; 2 x 4 tokens, E4M3: 10.7, 10.3. (The rests in the columns that four
+// heads leave, without a second set of MMAs, measured the same.)
 #include "block_rows.cuh"
 #include "mma.cuh"
 
@@ -410,9 +412,9 @@ cudaError_t launch(const BatchArgs& b, const SparseAttnArgs& a, cudaStream_t str
   const int chunks = a.num_select * (b.block_size / kTok);
   // A warp per unit (nothing is merged) or a CTA: 2 CTAs of NW warps fit a SM either way, so the
   // time goes with the waves of warps (of CTAs) x (chunks a warp takes + what a unit costs
-  // beside them, 2.5 and 5 chunks' time). 256 x 8 units: of 4 blocks 17.2 us by warps, 30.8 by
-  // CTAs, of 32 blocks 81.9 and 88.5; 160 x 8 units (two waves of warps, the second almost
-  // empty) of 128 blocks 244.8 and 194.7.
+  // beside them, 2.5 and 5 chunks' time). 256 x 8 units: of 4 blocks 17.6 us by warps, 30.8 by
+  // CTAs, of 32 blocks 82.4 and 87.9; 160 x 8 units (two waves of warps, the second almost
+  // empty) of 128 blocks 251.5 and 196.6.
   const int64_t slots = 2 * 152, warps_t = (units + slots * NW - 1) / (slots * NW) * (2 * int64_t(chunks) + 5),
                 ctas_t = (units + slots - 1) / slots * (2 * ((int64_t(chunks) + NW - 1) / NW) + 10);
   if (units >= slots && warps_t < ctas_t) {
@@ -425,8 +427,8 @@ cudaError_t launch(const BatchArgs& b, const SparseAttnArgs& a, cudaStream_t str
   cudaError_t e = ensure_smem<kern>(C::kSmem);
   if (e != cudaSuccess) return e;
   // CTAs per unit: one a SM at least, while each warp still has two chunks. (Two requests of
-  // four tokens, 64 units of 128 blocks, E4M3: 12.3 us with 256 CTAs in clusters of 4, 17.5 with
-  // 512 in clusters of 8.)
+  // four tokens, 64 units of 128 blocks, E4M3: 10.7 us with 256 CTAs in clusters of 4, 13.5 with
+  // 128 in clusters of 2, 15.3 with 512 in clusters of 8.)
   int split = 1;
   while (split < 8 && units * split < 152 && chunks >= split * 2 * NW * 2) split *= 2;
   cudaLaunchConfig_t cfg = {};

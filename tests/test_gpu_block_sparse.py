@@ -506,17 +506,8 @@ def test_the_bindings_refuse(pa):
         pa.block_bounds(bounds, b.k.float(), *b.meta, max_query_len=1, max_seq_len=40)
 
 
-@pytest.mark.parametrize("cache", [BF16, E4M3])
-@pytest.mark.parametrize("lens,qs,k,Hkv,D", [([640, 320], [1, 3], 1, 8, 128), ([640, 320], [1, 3], 12, 2, 64),
-                                             ([320] * 45, [1] * 45, 6, 8, 128)])
-def test_numerators_keep_fp32_precision(pa, lens, qs, k, Hkv, D, cache):
-    """Tokens in pairs v, -v under almost flat weights: the sums cancel to about 1 / 30 of their
-    terms, so what the numerators lose before the second product shows beside the output's own
-    rounding. A numerator is carried in two 16-bit parts: of bf16 within 2^-16 relative, of f16 within
-    2^-22. The fp32 sums: up to 2 k MMAs of a warp, four warps or CTAs merged, each addition
-    2^-23 of the magnitudes; 2^-21 for the exponential: together at most 2^-17 up to k = 12.
-    The logits as above (2 e)."""
-    b = Batch(lens, qs, Hq=4 * Hkv, Hkv=Hkv, D=D, cache=cache, seed=k)
+def _check_numerators(pa, lens, qs, k, G, Hkv, D, cache):
+    b = Batch(lens, qs, Hq=G * Hkv, Hkv=Hkv, D=D, cache=cache, seed=k)
     v = b.v.float()
     v[:, 1::2] = -v[:, 0::2]
     b.v = v.to(cache)
@@ -538,6 +529,27 @@ def test_numerators_keep_fp32_precision(pa, lens, qs, k, Hkv, D, cache):
     tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
     bad = np.abs(got - ref) > tol
     assert not bad.any(), (int(bad.sum()), (np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("lens,qs,k,Hkv,D", [([640, 320], [1, 3], 1, 8, 128), ([640, 320], [1, 3], 12, 2, 64),
+                                             ([320] * 45, [1] * 45, 6, 8, 128)])
+def test_numerators_keep_fp32_precision(pa, lens, qs, k, Hkv, D, cache):
+    """Tokens in pairs v, -v under almost flat weights: the sums cancel to about 1 / 30 of their
+    terms, so what the numerators lose before the second product shows beside the output's own
+    rounding. A numerator is carried in two 16-bit parts: of bf16 within 2^-16 relative, of f16 within
+    2^-22. The fp32 sums: up to 2 k MMAs of a warp, four warps or CTAs merged, each addition
+    2^-23 of the magnitudes; 2^-21 for the exponential: together at most 2^-17 up to k = 12.
+    The logits as above (2 e)."""
+    _check_numerators(pa, lens, qs, k, 4, Hkv, D, cache)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,Hkv,T", [(1, 8, 45), (2, 8, 3), (8, 8, 45), (8, 2, 2)])
+def test_numerators_of_other_groups(pa, G, Hkv, T, D, cache):
+    """The same with one, two and eight query heads a KV head, units of a warp and of a cluster."""
+    _check_numerators(pa, [320] * T, [1] * T, 6, G, Hkv, D, cache)
 
 
 @pytest.mark.parametrize("S,q,flagged", [(100, 8, True), (100, 3, True), (1, 300, True), (100, 2, False), (100, 0, False)])
