@@ -5,7 +5,7 @@ checks tensors and marshals pointers, sizes and the current CUDA stream; every s
 the path runs in the library's kernels. PyTorch provides device memory and streams. Most
 calls go through ctypes; the serving-step calls (advance_batch, norm_rope_write,
 block_bounds, block_scores, select_blocks, attention_sparse), a few microseconds each on the
-GPU, through a small extension, _pa_torch.so, whose host time is 3 us a call.
+GPU, through a small extension, _pa_torch.so, whose host time is 2.0 to 2.5 us a call.
 
 The library is built in-tree by ``python paged_kv_cache_161_gb300/build.py`` (or the
 repository's ``__graft_entry__.build()``). Importing this package without it raises. The

@@ -20,7 +20,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-// Stages of a warp's ring: 64 x 32768 positions, 8 heads: 86.2 us with 2 (three CTAs a SM), 99.5
+// Stages of a warp's ring: 64 x 32768 positions, 8 heads: 85.5 us with 2 (three CTAs a SM), 99.8
 // with 3 (two): more warps hide the products' latency better than deeper rings.
 constexpr int kRing = 2;
 constexpr int kTiles = 8;  // tiles of 16 blocks a warp takes
@@ -242,10 +242,14 @@ cudaError_t launch_few(const BatchArgs& b, float* scores, int width, const __nv_
 // A CTA keeps its columns' [q-, q+] in shared memory -- split from q once, 128 KB at D = 128 --
 // and streams the request's blocks past them: 128 rows of lo, then 128 of hi, gathered by 16-byte
 // asynchronous copies (a block's row is 2 D contiguous bytes per half) into a ring of 3 stages.
-// With 256 columns a tile's copies (64 KB at D = 128) take half of the time of its MMAs at L2's
-// rate; with 128 they would take all of it. Blocks are the M side so that the maximum over a group's
+// With 256 columns a tile's copies (64 KB at D = 128, arriving at about 30 bytes a clock and SM) and
+// its MMAs (2050 clocks at the measured bf16 rate) take about the same time; with 128 the copies
+// would take twice the MMAs'. Blocks are the M side so that the maximum over a group's
 // heads runs over a thread's own accumulator columns, and 32 lanes store 32 consecutive blocks.
 // Two accumulators of 256 columns: the epilogue of one tile runs beside the next tile's MMAs.
+// Clock stamps of four 512-token chunks against 8192 positions (28.5 us): a CTA's 26 k clocks are 6 k
+// until its request is known and its query loads are under way, 6 k more until the first tile's
+// products are there, then a tile every 2.6 to 3.1 k; 256 such CTAs run on 152 SMs as two waves.
 // Warps 0-7: the columns' split, then the epilogue (TMEM lanes 32 (w % 4) .., every second 32
 // columns), 8-11: producers, 12: MMA issue.
 constexpr int kChunkCols = 256;
@@ -271,8 +275,8 @@ struct ChunkLayout {
 // The first column tile of request s in the grid: no scan is needed, since (columns before it) /
 // 256 and one more tile for every request, or for every kMaxFewCols + 1 columns where those are
 // fewer, leaves room for every request's last, partial tile: a request of this kernel has more
-// than kMaxFewCols columns. (480 decodes and a chunk of 512 tokens: 41 us, 57 with one more tile
-// for every request.)
+// than kMaxFewCols columns. (480 decodes and a chunk of 512 tokens, contexts of 1024: 38 us, 55 with
+// one more tile for every request; contexts of 8192: 167 and 187.)
 __host__ __device__ __forceinline__ int64_t tiles_before(int64_t columns, int requests) {
   const int64_t partial = columns / (kMaxFewCols + 1);
   return columns / kChunkCols + (partial < requests ? partial : requests);

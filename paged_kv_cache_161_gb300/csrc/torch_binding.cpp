@@ -1,7 +1,7 @@
 // The serving-step calls of include/pa.h for torch tensors: a Python extension that checks its
 // arguments and calls the library. The other calls go through ctypes; these take a few
 // microseconds on the GPU at decode sizes, and the checks and marshalling of 10 to 31 arguments
-// took 7 to 11 us of host time a call in Python (1 to 2 here). Same rules: contiguous tensors of
+// took 7 to 11 us of host time a call in Python (2.0 to 2.5 here). Same rules: contiguous tensors of
 // one CUDA device, the current stream of that device unless `stream` is given, TypeError /
 // ValueError for tensors that do not fit, PAError for what the library refuses.
 #include <ATen/core/Tensor.h>
