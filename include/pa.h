@@ -83,7 +83,8 @@ typedef enum {
 /* Bits of the per-device error word (see pa_read_device_errors). */
 #define PA_DEVERR_SLOT_RANGE   0x1u  /* a slot >= num_blocks * block_size was skipped */
 #define PA_DEVERR_BLOCK_RANGE  0x2u  /* a block id outside [0, num_blocks) was skipped */
-#define PA_DEVERR_SEQ_RANGE    0x4u  /* seq_len > max_blocks_per_seq * block_size, or q_len > seq_len */
+#define PA_DEVERR_SEQ_RANGE    0x4u  /* seq_len > max_blocks_per_seq * block_size, q_len > seq_len, or more
+                                        queries or tokens than the call announced */
 #define PA_DEVERR_TIMEOUT      0x8u  /* a pipeline wait gave up (the kernel returned early) */
 #define PA_DEVERR_SLOT_MISMATCH 0x10u /* pa_write_attention: a decode token's slot is not its position's slot */
 #define PA_DEVERR_NO_BLOCKS    0x20u  /* pa_advance_batch: the free list does not hold the blocks of the step */
