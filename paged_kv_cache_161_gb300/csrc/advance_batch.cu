@@ -225,19 +225,15 @@ __global__ void __launch_bounds__(kThreads) advance_batch_kernel(const AdvancePa
 
 // Whether the device runs clusters of 16 CTAs of the kernel for long chunks: they need the opt-in
 // and 16 SMs of one GPC to themselves, which a process given part of the GPU may not have. Asked
-// once per device.
-cudaError_t cluster_of_16(bool* fits) {
+// once per device; an answer that cannot be had counts as no.
+bool cluster_of_16_fits() {
   static std::mutex mu;
   static int known[64] = {};  // 1: yes, -1: no
   constexpr auto kern = advance_batch_kernel<1024, 4>;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   std::lock_guard<std::mutex> lock(mu);
   if (!known[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(16);
     cfg.blockDim = dim3(1024);
@@ -248,12 +244,14 @@ cudaError_t cluster_of_16(bool* fits) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-    if (e != cudaSuccess) return e;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // answered here: the launch's status is its own
+      clusters = 0;
+    }
     known[dev] = clusters > 0 ? 1 : -1;
   }
-  *fits = known[dev] > 0;
-  return cudaSuccess;
+  return known[dev] > 0;
 }
 
 }  // namespace
@@ -273,12 +271,7 @@ cudaError_t launch_advance_batch(int32_t* block_table, int width, const int32_t*
   const bool small = num_seqs <= 256 && num_tokens <= 256;
   int ctas = 1;
   while (ctas < 8 && int64_t(ctas) * kFull < num_tokens) ctas *= 2;
-  if (num_tokens > 8 * kFull * 4) {
-    bool fits = false;
-    const cudaError_t e = cluster_of_16(&fits);
-    if (e != cudaSuccess) return e;
-    if (fits) ctas = 16;
-  }
+  if (num_tokens > 8 * kFull * 4 && cluster_of_16_fits()) ctas = 16;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(small ? 256 : kFull);
