@@ -13,6 +13,9 @@
  *   pa_norm_rope_write  RMS norm and rotary positions of query and key heads, and the cache write
  *   pa_block_bounds / pa_block_scores / pa_select_blocks / pa_attention_sparse
  *                   attention over the blocks that a cheap score selects for each query token
+ *   pa_kv_write_int / pa_kv_read_int / pa_attention_int
+ *                   caches of 4- or 8-bit integer codes: quantised as written, read back, attended
+ *   pa_attention_packed  causal attention of whole prompts over packed rows (no pages)
  *   pa_bm_*         host-side block accounting: free queue, block tables, ref counts, CoW
  *
  * Conventions shared by every entry point:
@@ -494,6 +497,108 @@ int pa_attention_sparse(void* out, const void* q, const void* k_cache, const voi
                         int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
                         float scale, pa_dtype cache_dtype, float k_scale, float v_scale,
                         pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Integer-coded caches: keys and values held as 4- or 8-bit codes with a smallest value and a step
+ * for every token and KV head, so that a cache of head_dim 128 takes 68 (132) bytes a row instead of
+ * bf16's 256, and no scale has to be known before the rows are. No counterpart in the pages beyond
+ * their blocks, slots and tables ([docs] PagedAttention, [flow] 3.3, 3.5). A serving loop runs
+ *   prompt   pa_kv_write_int; pa_attention_packed over the prompt's own rows
+ *   chunk    pa_kv_write_int; pa_kv_read_int of the context ahead of the chunk's rows, then
+ *            pa_attention_packed over both
+ *   decode   pa_kv_write_int; pa_attention_int
+ *
+ * Row x (head_dim elements, one token and KV head), with N = 2^bits - 1, in binary32:
+ *     lo   = the largest bfloat16 not above min(x)
+ *     step = max(2^-126, the smallest bfloat16 not below (max(x) - lo) / N)
+ *     code = rint((x - lo) inv), ties to even, inv = 1 / step (the product not rounded before rint)
+ * and a code stands for lo + step code. The error of an element is at most half a step. A row that
+ * holds a NaN or an infinity, or whose spread passes the largest float, reads back as NaN.
+ *
+ * k_cache, v_cache: device, uint8 [num_blocks, num_kv_heads, block_size * (head_dim * bits / 8 + 4)]:
+ * of each block and head first the rows' codes (token after token; element 2 i in the low half of
+ * byte i when bits = 4), then a row's lo and step, both bfloat16, token after token. A block's bytes lie
+ * together: pa_copy_blocks and pa_swap_blocks move them as caches of PA_FP8_E4M3 with one "head" of
+ * block_size * (head_dim * bits / 8 + 4) "elements" and num_kv_heads "tokens" a block.
+ * Supported: head_dim 64 / 128; block_size a multiple of 4; bits 4 / 8; else PA_ERR_UNSUPPORTED.
+ * Every kernel on `stream`.
+ *
+ * pa_kv_write_int: for every t with slot = slot_mapping[t] >= 0 the rows of k[t] and v[t] become the
+ * codes of that slot; negative slots are padding. k, v: device, `dtype` (PA_BF16 / PA_F32), token t's
+ * heads contiguous at k + t * k_stride elements (v_stride alike; strides multiples of 16 bytes and at
+ * least the row). slot_mapping: device, int64 [num_tokens], distinct non-negative slots; one outside
+ * the cache is skipped (PA_DEVERR_SLOT_RANGE).
+ *
+ * pa_kv_read_int: for request s and i in [0, seq_lens[s] - start_pos[s]), the values of position
+ * start_pos[s] + i go to row row_start_loc[s] + i of k_out and v_out (device, [num_rows, num_kv_heads,
+ * head_dim], `dtype` PA_BF16 / PA_F32, computed in fp32 and rounded once). start_pos: device, int32
+ * [num_seqs], or null (all 0). row_start_loc: device, int32 [num_seqs + 1], not decreasing. Rows of a
+ * request behind those (room for a chunk's own rows) and rows of no request are left as they are. A request
+ * whose positions do not fit its rows or its table, or a negative one, sets PA_DEVERR_SEQ_RANGE; a
+ * block id outside [0, num_blocks) PA_DEVERR_BLOCK_RANGE; their rows are left as they are.
+ *
+ * pa_attention_int: pa_attention over such caches, q and out bf16 [num_tokens, num_heads, head_dim]:
+ * token j of a request's q_len sits at position seq_lens - q_len + j and sees the positions up to its
+ * own. Made for decode and a few drafted tokens: 8 / (num_heads / num_kv_heads) tokens share one pass
+ * over a head's codes (any group size that divides num_heads); a long chunk is faster through
+ * pa_kv_read_int and pa_attention_packed. Rows of no request are left as they are; a request with more
+ * than max_query_len queries, more keys than max_seq_len, or q_len > seq_len sets PA_DEVERR_SEQ_RANGE
+ * and its rows are left as they are. A key or value row that reads back as NaN gives NaN to the tokens
+ * that see it, and to no other. workspace: device, pa_attention_int_workspace_size bytes, 16-byte
+ * aligned, no contents needed; calls that may overlap on the GPU need one each. The result depends on
+ * nothing but the arguments' contents and the GPU's number of SMs. num_seqs <= 8192
+ * (PA_ERR_UNSUPPORTED).
+ * --------------------------------------------------------------------------- */
+int pa_kv_write_int(const void* k, const void* v, int64_t k_stride, int64_t v_stride, pa_dtype dtype,
+                    void* k_cache, void* v_cache, const int64_t* slot_mapping, int64_t num_tokens,
+                    int64_t num_blocks, int block_size, int num_kv_heads, int head_dim, int bits,
+                    pa_stream_t stream);
+
+int pa_kv_read_int(void* k_out, void* v_out, pa_dtype dtype, const void* k_cache, const void* v_cache,
+                   const int32_t* block_table, int max_blocks_per_seq, const int32_t* start_pos,
+                   const int32_t* seq_lens, const int32_t* row_start_loc, int num_seqs, int64_t num_rows,
+                   int64_t num_blocks, int block_size, int num_kv_heads, int head_dim, int bits,
+                   pa_stream_t stream);
+
+int pa_attention_int_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
+                                    int head_dim, size_t* bytes_out);
+
+int pa_attention_int(void* out, const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                     const int32_t* query_start_loc, int num_seqs, int num_tokens, int max_query_len,
+                     int max_seq_len, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                     int64_t num_blocks, float scale, int bits, void* workspace,
+                     size_t workspace_bytes, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * pa_attention_packed -- causal attention of prompts, or of chunks behind their contexts, over rows
+ * that are at hand and need no pages: [docs] PagedAttention (the prompt's own attention), [flow] 3.2
+ * and 3.5 (the flattened token batch), [intro] 2.1 (causal mask).
+ *
+ * Request s has the query rows [q_start_loc[s], q_start_loc[s + 1]) and the key and value rows
+ * [k_start_loc[s], k_start_loc[s + 1]); with Q and K of them, query j sees keys 0 .. K - Q + j:
+ *     out[q0 + j, h, :] = sum_i softmax_i(scale <q[q0 + j, h, :], k[k0 + i, g, :]>) v[k0 + i, g, :]
+ * (h in KV head g's group); zeros where it sees none (j < Q - K).
+ *
+ * q, k, v       device, bf16, [num_q_rows, num_heads, head_dim] and [num_k_rows, num_kv_heads,
+ *               head_dim]: token t's heads contiguous at q + t * q_stride elements (k_stride, v_stride
+ *               alike), so that all three may be slices of one projection's output. Strides are multiples of
+ *               16 bytes and at least the row; pointers 16-byte aligned
+ * out           device, bf16 [num_q_rows, num_heads, head_dim], contiguous, apart from the inputs
+ * q_start_loc, k_start_loc  device, int32 [num_seqs + 1], not decreasing. A request outside the rows, or
+ *               of more than max_query_len queries, sets PA_DEVERR_SEQ_RANGE and its rows are left as they
+ *               are; so are rows of no request
+ * Numerators are rounded to bf16 for the second product, as pa_attention's are. A NaN or an infinity in
+ * another request's rows changes nothing; one in a value row reaches the request's queries of the same
+ * 128-key step, and those that see it.
+ * Supported: head_dim 64 / 128, num_heads / num_kv_heads in {1, 2, 4, 8}, num_seqs <= 4096. One
+ * launch on `stream`, no workspace.
+ * --------------------------------------------------------------------------- */
+int pa_attention_packed(void* out, const void* q, const void* k, const void* v, int64_t q_stride,
+                        int64_t k_stride, int64_t v_stride, const int32_t* q_start_loc,
+                        const int32_t* k_start_loc, int num_seqs, int num_q_rows, int num_k_rows,
+                        int max_query_len, int num_heads, int num_kv_heads, int head_dim, float scale,
+                        pa_dtype dtype, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------------
  * pa_attention_fixed_scratch -- no counterpart in the pages: an addition for callers that

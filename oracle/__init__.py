@@ -17,6 +17,7 @@ Contents, each citing the page passage it follows:
   dense_causal_ref: the byte moves and the float64 attention.
 - runner.run_workload: a seeded workload, phase by phase.
 - serving_step: batch metadata from lengths, norm + rotary + write, block-sparse attention.
+- int_cache: caches of 4- and 8-bit codes, their rows, attention over packed rows.
 
 Every function is pinned by the CPU tests (the pages' worked examples, closed
 forms, invariants, brute force and a library cross-check); none is unpinned.
@@ -34,7 +35,7 @@ from .attention import (  # noqa: F401
 from .block_manager import BlockAllocator, NoFreeBlocks, TooLarge  # noqa: F401
 from .prefix_cache import PrefixCachingAllocator  # noqa: F401
 from .fp8 import dequantize, kv_write_fp8_ref, quantize  # noqa: F401
-from . import serving_step  # noqa: F401
+from . import int_cache, serving_step  # noqa: F401
 from .swap import SwappingAllocator, SwappingPrefixAllocator  # noqa: F401
 from .runner import (OracleResult, batch_metadata, run_allocator, run_script, run_script_swaps,  # noqa: F401
                      run_workload, step_ranges)

@@ -5,12 +5,13 @@ checks tensors and marshals pointers, sizes and the current CUDA stream; every s
 the path runs in the library's kernels. PyTorch provides device memory and streams. Most
 calls go through ctypes; the serving-step calls (advance_batch, norm_rope_write,
 block_bounds, block_scores, select_blocks, attention_sparse), a few microseconds each on the
-GPU, through a small extension, _pa_torch.so, whose host time is 2.0 to 2.5 us a call.
+GPU, and those of integer-coded caches and packed prompts (kv_write_int, kv_read_int, attention_int,
+attention_packed) through a small extension, _pa_torch.so, whose host time is 2.0 to 2.5 us a call.
 
 The library is built in-tree by ``python paged_kv_cache_161_gb300/build.py`` (or the
 repository's ``__graft_entry__.build()``). Importing this package without it raises. The
 extension is built against the installed torch; where it is missing or does not load (another
-torch), only the serving-step calls raise.
+torch), only its calls raise.
 """
 from __future__ import annotations
 
@@ -42,6 +43,11 @@ __all__ = [
     "block_scores",
     "select_blocks",
     "attention_sparse",
+    "kv_write_int",
+    "kv_read_int",
+    "attention_int",
+    "attention_int_workspace_size",
+    "attention_packed",
     "read_device_errors",
     "lib",
     "LIB_PATH",
@@ -87,6 +93,11 @@ _sig = {
     "pa_select_blocks": (_i, [_p, _i, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _p]),
     "pa_attention_sparse": (_i, [_p, _p, _p, _p, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i64, _f, _i, _f,
                                  _f, _p]),
+    "pa_kv_write_int": (_i, [_p, _p, _i64, _i64, _i, _p, _p, _p, _i64, _i64, _i, _i, _i, _i, _p]),
+    "pa_kv_read_int": (_i, [_p, _p, _i, _p, _p, _p, _i, _p, _p, _p, _i, _i64, _i64, _i, _i, _i, _i, _p]),
+    "pa_attention_int_workspace_size": (_i, [_i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "pa_attention_int": (_i, [_p, _p, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i64, _f, _i, _p, _sz, _p]),
+    "pa_attention_packed": (_i, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _i, _p]),
     "pa_bm_batch_groups": (_i, [_p, _p, _i64, _i, _p, _p, _p, _i64, ctypes.POINTER(_i64)]),
     "pa_bm_enable_swap": (_i, [_p, _i64, _p]),
     "pa_bm_swap_out": (_i, [_p, _p, _i64, _p, _i64, ctypes.POINTER(_i64)]),
@@ -164,6 +175,17 @@ def _stream(stream, device) -> int:
 
 
 
+def _block_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor):
+    """_cache_geometry and the dtype code of caches that are moved by whole blocks: integer-coded ones
+    [num_blocks, num_kv_heads, bytes] count as num_kv_heads tokens of one head of that many 1-byte elements."""
+    if k_cache.dtype == torch.uint8 and k_cache.dim() == 3:
+        if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+            raise ValueError("k_cache and v_cache must both be [num_blocks, num_kv_heads, bytes]")
+        NB, H, n = (int(x) for x in k_cache.shape)
+        return (NB, H, 1, n), PA_FP8_E4M3
+    return _cache_geometry(k_cache, v_cache), _dtype_code(k_cache)
+
+
 def _cache_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor):
     if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, num_kv_heads, head_dim]")
@@ -186,14 +208,15 @@ def kv_write(k, v, k_cache, v_cache, slot_mapping, stream=None):
 
 
 def copy_blocks(k_cache, v_cache, block_mapping, stream=None):
-    """pa_copy_blocks: for each (src, dst) row of block_mapping [n, 2], cache[dst] = cache[src]."""
-    NB, B, Hkv, D = _cache_geometry(k_cache, v_cache)
+    """pa_copy_blocks: for each (src, dst) row of block_mapping [n, 2], cache[dst] = cache[src]
+    (integer-coded caches, uint8 [num_blocks, num_kv_heads, bytes], too)."""
+    (NB, B, Hkv, D), code = _block_geometry(k_cache, v_cache)
     if block_mapping.dim() != 2 or block_mapping.shape[1] != 2:
         raise ValueError("block_mapping must be [num_pairs, 2]")
     n = int(block_mapping.shape[0])
     ptr = _dev(block_mapping, "block_mapping", torch.int64) if n > 0 else 0
     st = lib.pa_copy_blocks(_dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), ptr, n, NB, B, Hkv, D,
-                            _dtype_code(k_cache), _stream(stream, k_cache.device))
+                            code, _stream(stream, k_cache.device))
     _check(st, "pa_copy_blocks")
 
 
@@ -218,18 +241,20 @@ def _pool_ptr(t: torch.Tensor, name: str) -> int:
 
 def swap_blocks(src_k, src_v, dst_k, dst_v, block_mapping, stream=None):
     """pa_swap_blocks: dst[d] = src[s] for each (s, d) row of block_mapping [n, 2], whole blocks,
-    between two pools of one block geometry; either pool may be pinned host memory."""
+    between two pools of one block geometry; either pool may be pinned host memory. Integer-coded
+    pools, uint8 [num_blocks, num_kv_heads, bytes], too."""
+    coded = src_k.dtype == torch.uint8 and src_k.dim() == 3
     if src_k.shape[1:] != dst_k.shape[1:] or src_k.dtype != dst_k.dtype or src_k.shape != src_v.shape or \
-            dst_k.shape != dst_v.shape or src_k.dim() != 4:
+            dst_k.shape != dst_v.shape or (src_k.dim() != 4 and not coded):
         raise ValueError("pools must be [num_blocks, block_size, num_kv_heads, head_dim] of one geometry and dtype")
     if block_mapping.dim() != 2 or block_mapping.shape[1] != 2 or block_mapping.dtype != torch.int64:
         raise ValueError("block_mapping must be int64 [num_pairs, 2]")
     n = int(block_mapping.shape[0])
-    _, B, Hkv, D = (int(x) for x in src_k.shape)
+    (_, B, Hkv, D), code = _block_geometry(src_k, src_v)
     dev = src_k.device if src_k.is_cuda else dst_k.device
     st = lib.pa_swap_blocks(_pool_ptr(src_k, "src_k"), _pool_ptr(src_v, "src_v"), _pool_ptr(dst_k, "dst_k"),
                             _pool_ptr(dst_v, "dst_v"), _pool_ptr(block_mapping, "block_mapping") if n else None, n,
-                            int(src_k.shape[0]), int(dst_k.shape[0]), B, Hkv, D, _dtype_code(src_k),
+                            int(src_k.shape[0]), int(dst_k.shape[0]), B, Hkv, D, code,
                             _stream(stream, dev))
     _check(st, "pa_swap_blocks")
 
@@ -423,7 +448,20 @@ def attention_grouped(out, q, k_cache, v_cache, block_table, seq_lens, query_sta
     return out
 
 
-# The serving-step calls come from an extension of their own: see csrc/torch_binding.cpp.
+def attention_int_workspace_size(num_seqs: int, num_tokens: int, num_heads: int, num_kv_heads: int,
+                                 head_dim: int) -> int:
+    """pa_attention_int_workspace_size for the current device."""
+    out = ctypes.c_size_t(0)
+    _check(lib.pa_attention_int_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                               ctypes.byref(out)), "pa_attention_int_workspace_size")
+    return int(out.value)
+
+
+# These calls come from an extension of their own: see csrc/torch_binding.cpp.
+_EXTENSION_CALLS = ("advance_batch", "norm_rope_write", "block_bounds", "block_scores", "select_blocks",
+                    "attention_sparse", "kv_write_int", "kv_read_int", "attention_int", "attention_packed")
+
+
 def _load_extension():
     spec = importlib.util.spec_from_file_location("_pa_torch", EXT_PATH)
     mod = importlib.util.module_from_spec(spec)
@@ -442,18 +480,12 @@ def _without_extension(name: str, why: ImportError):
 
 try:
     _pa_torch = _load_extension()
+    _calls = [getattr(_pa_torch, n) for n in _EXTENSION_CALLS]
 except ImportError as e:
     _pa_torch = None
-    (advance_batch, norm_rope_write, block_bounds, block_scores, select_blocks, attention_sparse) = (
-        _without_extension(n, e) for n in ("advance_batch", "norm_rope_write", "block_bounds", "block_scores",
-                                           "select_blocks", "attention_sparse"))
-else:
-    advance_batch = _pa_torch.advance_batch
-    norm_rope_write = _pa_torch.norm_rope_write
-    block_bounds = _pa_torch.block_bounds
-    block_scores = _pa_torch.block_scores
-    select_blocks = _pa_torch.select_blocks
-    attention_sparse = _pa_torch.attention_sparse
+    _calls = [_without_extension(n, e) for n in _EXTENSION_CALLS]
+(advance_batch, norm_rope_write, block_bounds, block_scores, select_blocks, attention_sparse, kv_write_int, kv_read_int,
+ attention_int, attention_packed) = _calls
 
 
 def read_device_errors(clear: bool = True) -> int:

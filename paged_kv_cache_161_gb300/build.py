@@ -33,7 +33,8 @@ EXT_PATH = os.path.join(LIB_DIR, "_pa_torch.so")
 
 CU_SOURCES = ["errors.cu", "kv_write.cu", "copy_blocks.cu", "decode_attention.cu", "decode_mma.cu", "prefill_attention.cu",
               "attention_fixed_scratch.cu", "prefill_tcgen05.cu", "advance_batch.cu", "norm_rope_write.cu",
-              "block_bounds.cu", "block_scores.cu", "select_blocks.cu", "attention_sparse.cu"]
+              "block_bounds.cu", "block_scores.cu", "select_blocks.cu", "attention_sparse.cu",
+              "kv_int.cu", "attention_int.cu", "attention_packed.cu"]
 CPP_SOURCES = ["api.cpp", "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

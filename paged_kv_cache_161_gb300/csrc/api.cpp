@@ -825,3 +825,167 @@ int pa_attention_sparse(void* out, const void* q, const void* k_cache, const voi
 }
 
 }  // extern "C"
+
+namespace {
+
+// An integer-coded cache, and the geometry its kernels take.
+int check_int_cache(const void* k_cache, const void* v_cache, int64_t num_blocks, int block_size, int num_kv_heads,
+                    int head_dim, int bits) {
+  if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+  if (num_blocks < 1 || block_size < 1 || num_kv_heads < 1 || head_dim < 1) return PA_ERR_INVALID_ARG;
+  if (bits != 4 && bits != 8) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size % 4 != 0 || block_size > (1 << 20) || num_kv_heads > (1 << 16)) return PA_ERR_UNSUPPORTED;
+  if (num_blocks > (int64_t(1) << 36) / (int64_t(block_size) * num_kv_heads)) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+// Rows of `row` elements `stride` apart, for n tokens.
+bool rows_ok(const void* p, int64_t stride, int64_t row, int64_t n, int64_t eb) {
+  return p && aligned16(p) && stride * eb % 16 == 0 && (n <= 1 || stride >= row);
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_kv_write_int(const void* k, const void* v, int64_t k_stride, int64_t v_stride, pa_dtype dtype, void* k_cache,
+                    void* v_cache, const int64_t* slot_mapping, int64_t num_tokens, int64_t num_blocks, int block_size,
+                    int num_kv_heads, int head_dim, int bits, pa_stream_t stream) {
+  const int st = check_int_cache(k_cache, v_cache, num_blocks, block_size, num_kv_heads, head_dim, bits);
+  if (st != PA_OK) return st;
+  if (dtype != PA_BF16 && dtype != PA_F32) return PA_ERR_INVALID_ARG;
+  if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  const int64_t row = int64_t(num_kv_heads) * head_dim;
+  if (!rows_ok(k, k_stride, row, num_tokens, elem_bytes(dtype)) || !rows_ok(v, v_stride, row, num_tokens, elem_bytes(dtype)))
+    return PA_ERR_INVALID_ARG;
+  if (!slot_mapping || !aligned(slot_mapping, 8)) return PA_ERR_INVALID_ARG;
+  if (num_tokens > 0x7fffffff / (2 * int64_t(num_kv_heads))) return PA_ERR_UNSUPPORTED;  // grid: at most a warp a row
+  cudaError_t e;
+  const pa::KvIntArgs a = {pa::device_error_word(&e), num_blocks, block_size, num_kv_heads, head_dim, bits, dtype};
+  if (!a.err) return cuda_fail(e);
+  e = pa::launch_kv_write_int(a, k, v, k_stride, v_stride, k_cache, v_cache, slot_mapping, num_tokens,
+                              reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_kv_read_int(void* k_out, void* v_out, pa_dtype dtype, const void* k_cache, const void* v_cache,
+                   const int32_t* block_table, int max_blocks_per_seq, const int32_t* start_pos, const int32_t* seq_lens,
+                   const int32_t* row_start_loc, int num_seqs, int64_t num_rows, int64_t num_blocks, int block_size,
+                   int num_kv_heads, int head_dim, int bits, pa_stream_t stream) {
+  const int st = check_int_cache(k_cache, v_cache, num_blocks, block_size, num_kv_heads, head_dim, bits);
+  if (st != PA_OK) return st;
+  if (dtype != PA_BF16 && dtype != PA_F32) return PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || num_rows < 0) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_rows == 0) return PA_OK;
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return PA_ERR_INVALID_ARG;
+  if (!block_table || !seq_lens || !row_start_loc || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(row_start_loc, 4) || !aligned(start_pos, 4))
+    return PA_ERR_INVALID_ARG;
+  if (max_blocks_per_seq < 1 || int64_t(max_blocks_per_seq) * block_size > 0x7fffffff) return PA_ERR_INVALID_ARG;
+  if (num_rows > 0x7fffffff / (2 * int64_t(num_kv_heads))) return PA_ERR_UNSUPPORTED;  // grid
+  {
+    const int64_t rows = num_rows * num_kv_heads * head_dim * elem_bytes(dtype);
+    const int64_t bytes = num_blocks * num_kv_heads * block_size * (head_dim * bits / 8 + 4);
+    if (overlap(k_out, rows, v_out, rows)) return PA_ERR_INVALID_ARG;
+    for (const void* c : {k_cache, v_cache})
+      if (overlap(k_out, rows, c, bytes) || overlap(v_out, rows, c, bytes)) return PA_ERR_INVALID_ARG;
+  }
+  cudaError_t e;
+  const pa::KvIntArgs a = {pa::device_error_word(&e), num_blocks, block_size, num_kv_heads, head_dim, bits, dtype};
+  if (!a.err) return cuda_fail(e);
+  e = pa::launch_kv_read_int(a, k_out, v_out, k_cache, v_cache, block_table, max_blocks_per_seq, start_pos, seq_lens,
+                             row_start_loc, num_seqs, num_rows, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_attention_int_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                    size_t* bytes_out) {
+  if (!bytes_out || num_seqs < 0 || num_tokens < 0 || num_kv_heads < 1 || num_heads < 1 || num_heads % num_kv_heads != 0)
+    return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const int ctas = pa::decode_num_ctas(dev, &e);
+  if (e != cudaSuccess) return cuda_fail(e);
+  *bytes_out = pa::attention_int_workspace_bytes(head_dim, ctas);
+  return PA_OK;
+}
+
+int pa_attention_int(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                     int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
+                     int num_tokens, int max_query_len, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                     int block_size, int64_t num_blocks, float scale, int bits, void* workspace, size_t workspace_bytes,
+                     pa_stream_t stream) {
+  const int st = check_int_cache(k_cache, v_cache, num_blocks, block_size, num_kv_heads, head_dim, bits);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || max_seq_len < 0) return PA_ERR_INVALID_ARG;
+  if (num_heads < 1 || num_heads % num_kv_heads != 0 || !positive_finite(scale)) return PA_ERR_INVALID_ARG;
+  if (max_query_len > max_seq_len) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
+  if (!out || !q || !aligned16(out) || !aligned16(q)) return PA_ERR_INVALID_ARG;
+  if (!block_table || !seq_lens || !query_start_loc || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(query_start_loc, 4))
+    return PA_ERR_INVALID_ARG;
+  if (max_blocks_per_seq < 1 || int64_t(max_blocks_per_seq) * block_size > 0x7fffffff ||
+      int64_t(max_blocks_per_seq) * block_size < max_seq_len)
+    return PA_ERR_INVALID_ARG;
+  pa::AttnIntArgs a = {out, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, workspace, nullptr, num_blocks,
+                       max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len, num_heads, num_kv_heads,
+                       head_dim, block_size, bits, 0, scale};
+  if (!pa::attention_int_fits(a)) return PA_ERR_UNSUPPORTED;
+  const int64_t rows = int64_t(num_tokens) * num_heads * head_dim * 2;
+  if (overlap(out, rows, q, rows)) return PA_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  a.num_ctas = pa::decode_num_ctas(dev, &e);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (workspace_bytes < pa::attention_int_workspace_bytes(head_dim, a.num_ctas)) return PA_ERR_WORKSPACE;
+  a.err = pa::device_error_word(&e);
+  if (!a.err) return cuda_fail(e);
+  e = pa::launch_attention_int(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_attention_packed(void* out, const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, const int32_t* q_start_loc, const int32_t* k_start_loc, int num_seqs,
+                        int num_q_rows, int num_k_rows, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
+                        float scale, pa_dtype dtype, pa_stream_t stream) {
+  const int st = check_heads(num_heads, num_kv_heads, head_dim);
+  if (st != PA_OK) return st;
+  if (dtype != PA_BF16) return dtype == PA_F32 || dtype == PA_FP8_E4M3 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || num_q_rows < 0 || num_k_rows < 0 || max_query_len < 0 || !positive_finite(scale))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_q_rows == 0 || max_query_len == 0) return PA_OK;
+  const int64_t q_row = int64_t(num_heads) * head_dim, k_row = int64_t(num_kv_heads) * head_dim;
+  if (!out || !aligned16(out) || !rows_ok(q, q_stride, q_row, num_q_rows, 2)) return PA_ERR_INVALID_ARG;
+  if (num_k_rows > 0 && (!rows_ok(k, k_stride, k_row, num_k_rows, 2) || !rows_ok(v, v_stride, k_row, num_k_rows, 2)))
+    return PA_ERR_INVALID_ARG;
+  if (!q_start_loc || !k_start_loc || !aligned(q_start_loc, 4) || !aligned(k_start_loc, 4)) return PA_ERR_INVALID_ARG;
+  // strides of one row say nothing: the row itself, which the tensor maps take
+  pa::PackedArgs a = {out, q, k, v, q_start_loc, k_start_loc, nullptr, num_q_rows > 1 ? q_stride : q_row,
+                      num_k_rows > 1 ? k_stride : k_row, num_k_rows > 1 ? v_stride : k_row, num_seqs, num_q_rows,
+                      num_k_rows, max_query_len, num_heads, num_kv_heads, head_dim, scale};
+  if (!pa::attention_packed_fits(a)) return PA_ERR_UNSUPPORTED;
+  if (a.q_stride >= (int64_t(1) << 39) || a.k_stride >= (int64_t(1) << 39) || a.v_stride >= (int64_t(1) << 39))
+    return PA_ERR_UNSUPPORTED;  // the tensor maps' strides: 2^40 bytes
+  const int64_t rows = int64_t(num_q_rows) * q_row * 2;
+  if (overlap(out, rows, q, ((num_q_rows - 1) * a.q_stride + q_row) * 2)) return PA_ERR_INVALID_ARG;
+  if (num_k_rows > 0 && (overlap(out, rows, k, ((num_k_rows - 1) * a.k_stride + k_row) * 2) ||
+                         overlap(out, rows, v, ((num_k_rows - 1) * a.v_stride + k_row) * 2)))
+    return PA_ERR_INVALID_ARG;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);  // a context for the tensor maps on a thread without one
+  if (e != cudaSuccess) return cuda_fail(e);
+  a.err = pa::device_error_word(&e);
+  if (!a.err) return cuda_fail(e);
+  e = pa::launch_attention_packed(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,766 @@
+// Attention of a few new tokens over integer-coded caches (pa_attention_int): [docs] PagedAttention
+// (attention over a block table); [flow] 3.5. The codes have no counterpart in the pages.
+//
+// With key row j = lo_j + step_j c_j and value row j = lo'_j + step'_j c'_j (codes c, c'):
+//   s_j = scale q.k_j = scale (step_j (q.c_j) + lo_j sum(q)),     p_j = 2^(s_j log2 e - m)
+//   out = (sum_j (p_j step'_j) (c'_j - mid) + sum_j p_j (lo'_j + mid step'_j)) / sum_j p_j
+// so the tensor cores multiply whole codes, and a row's two parameters cost a few instructions a
+// logit instead of one an element. mid is half the codes' range: the codes enter the second product as
+// small whole numbers around 0, so that an average over many rows does not come out as the
+// difference of two large sums.
+//
+// Bound: the cache's bytes (68 a row and head at 128 elements of 4 bits), and the instructions that turn
+// codes into 16-bit operands, about one an element. So: one pass, and every element converted once
+// for up to eight query rows.
+//
+// Work: a unit is unit_keys keys of one segment (request, KV head, tile of 8 query rows: query tokens x
+// the head's query heads). The units of all segments, in order, are dealt to the grid's warps in
+// equal runs; a warp streams its run through a ring of its own in shared memory (bulk copies of the
+// records, one a block where a block is not larger than a unit), and no warp waits for another while
+// it streams. Segments cut between warps leave pieces (m, l, unnormalised output) in the workspace:
+// a CTA joins those of its 16 warps, a second kernel those cut between CTAs.
+//
+// Operands (mma.sync m16n8k16, keys as the 16 rows, query rows as the 8 columns): a code under the
+// bits of the f16 1024 is that number plus the code (4-bit codes one nibble higher: 1024 + 16 c), one
+// logic instruction for two. Which dimension sits where in a contraction is free as long as both sides
+// agree, so a lane takes 16-byte pieces of rows as they lie; so is which key is which row.
+//
+// The kernels start before the one in front of them has ended and read what it wrote behind
+// griddep_wait(): none of their pointers is __restrict__ or read through __ldg.
+#include <type_traits>
+
+#include "int_codes.cuh"
+#include "launch.h"
+#include "mma.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kRows = 8;  // query rows of a tile
+constexpr float kNoMax = -1e30f;  // running maximum before any key: finite, so that differences are not NaN
+
+template <int BITS>
+__host__ __device__ constexpr int unit_keys() { return BITS == 4 ? 32 : 16; }
+template <int D, int BITS>
+__host__ __device__ constexpr int stage_bytes() { return unit_keys<BITS>() * 2 * (code_row_bytes<D, BITS>() + 4); }
+// a piece: eight rows of D sums, then their maxima and their sums of numerators
+template <int D>
+__host__ __device__ constexpr int piece_floats() { return kRows * D + 2 * kRows; }
+
+struct IntParams {
+  __nv_bfloat16* out;
+  const __nv_bfloat16* q;
+  const unsigned char* k_cache;
+  const unsigned char* v_cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* qsl;
+  unsigned int* err;
+  float* pieces;  // [grid * kWarps * 2] of the warps, then [grid * 2] of the CTAs
+  int4* descs;    // [grid * 2]: a CTA's pieces, {first unit of the segment or -1, its last + 1, request, segment}
+  int* per;       // units a warp
+  int64_t num_blocks;
+  int max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len;
+  int num_heads, num_kv_heads, group, block_size;
+  int part;    // keys a bulk copy of codes covers: the largest power of two in block_size, at most a unit
+  int stages;  // of a warp's ring
+  float scale_log2;
+};
+
+// What a request contributes: `tiles` tiles of 8 rows, each over `units` units a KV head.
+struct Request {
+  int q0, q_len, L, tiles, units;
+};
+
+template <int KU>
+__device__ __forceinline__ bool request_of(const IntParams& p, int s, Request& r) {
+  r.q0 = p.qsl[s];
+  const int q1 = p.qsl[s + 1];
+  r.L = p.seq_lens[s];
+  r.tiles = r.units = r.q_len = 0;
+  if (r.q0 < 0 || q1 < r.q0 || q1 > p.num_tokens) return false;
+  r.q_len = q1 - r.q0;
+  if (r.q_len == 0) return true;
+  if (r.q_len > p.max_query_len || r.q_len > r.L || r.L > p.max_seq_len) return false;
+  r.tiles = int((int64_t(r.q_len) * p.group + kRows - 1) / kRows);
+  r.units = (r.L + KU - 1) / KU;
+  return true;
+}
+
+// The segment that holds unit u of the whole call: request s by search in the units' prefix.
+struct Segment {
+  int s, head, tile, begin, end;  // units [begin, end) of the call
+};
+template <int KU>
+__device__ __forceinline__ Segment segment_of(const IntParams& p, const int* prefix, int u) {
+  int s = 0, n = p.num_seqs;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (prefix[s + half] <= u) s += half, n -= half;
+    else n = half;
+  }
+  Request r;
+  request_of<KU>(p, s, r);
+  const int seg = (u - prefix[s]) / r.units;
+  Segment g;
+  g.s = s;
+  g.head = seg / r.tiles;
+  g.tile = seg - g.head * r.tiles;  // tiles fastest: neighbours read the same keys
+  g.begin = prefix[s] + seg * r.units;
+  g.end = g.begin + r.units;
+  return g;
+}
+
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2(uint32_t x, __half2 mul, __half2 add) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), mul, add);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t h2(uint32_t x, __half2 add) {
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&x), add);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The key of a 16-key tile that is row r of the contraction: even r < 8 the keys 0 .. 3, odd ones 5, 4, 7,
+// 6, and 8 more from r = 8 on. A quarter warp's 16-byte loads of key rows then meet rows of both
+// parities, and so do the half warps' 8-byte loads of value rows.
+__device__ __forceinline__ int key_of(int r) {
+  const int h = (r & 7) >> 1;
+  return (r & 8) + ((r & 1) ? (h ^ 1) + 4 : h);
+}
+
+// Joins `count` pieces of one query row, piece i at pieces + index(i): each lane holds D / 32 elements.
+template <int D>
+struct RowJoin {
+  float m = kNoMax, l = 0.f;
+  float o[D / 32] = {};
+  template <typename F>
+  __device__ __forceinline__ void run(const float* pieces, int row, int lane, int count, F index) {
+    for (int i = 0; i < count; ++i) {
+      const float* p = pieces + int64_t(index(i)) * piece_floats<D>();
+      m = fmaxf(m, p[kRows * D + row]);
+    }
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const float* p = pieces + int64_t(index(i)) * piece_floats<D>();
+      const float e = exp2f(p[kRows * D + row] - m);
+      l += e * p[kRows * D + kRows + row];
+      const float* x = p + row * D + lane * (D / 32);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) o[k] += e * x[k];
+    }
+  }
+  __device__ __forceinline__ void store_piece(float* p, int row, int lane) const {
+    if (lane == 0) {
+      p[kRows * D + row] = m;
+      p[kRows * D + kRows + row] = l;
+    }
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) p[row * D + lane * (D / 32) + k] = o[k];
+  }
+  __device__ __forceinline__ void store_out(__nv_bfloat16* out, int lane) const {
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    if (D == 128)
+      *reinterpret_cast<uint2*>(out + lane * 4) =
+          make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[D / 32 - 2] * inv, o[D / 32 - 1] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(out + lane * 2) = pack_bf16(o[0] * inv, o[1] * inv);
+  }
+};
+
+// The output row of row `row` of a tile, or null behind the request's last.
+template <int D>
+__device__ __forceinline__ __nv_bfloat16* out_row(const IntParams& p, int s, int head, int tile, int row) {
+  const int q0 = p.qsl[s], rows = (p.qsl[s + 1] - q0) * p.group, r = tile * kRows + row;
+  if (r >= rows) return nullptr;
+  return p.out + (int64_t(q0 + r / p.group) * p.num_heads + head * p.group + r % p.group) * D;
+}
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const IntParams p) {
+  constexpr int KU = unit_keys<BITS>(), ROW = code_row_bytes<D, BITS>(), STAGE = stage_bytes<D, BITS>();
+  constexpr int HALF = STAGE / 2;                   // keys' part of a stage, then the values'
+  constexpr int NK = D / 16;                        // contraction steps of q.c, and tiles of 16 value dimensions
+  constexpr float kMid = BITS == 4 ? 8.f : 128.f;
+  // the codes in q.c are 64 + c (4 bits, after 1 / 16) or 1024 + c
+  constexpr float kUnscale = BITS == 4 ? 0.0625f : 1.f, kOffset = BITS == 4 ? 64.f : 1024.f;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int wsum[kWarps];
+  __shared__ int4 desc[kWarps * 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int S = p.num_seqs;
+  // shared memory: barriers, rings, the units' prefix over the requests
+  const uint32_t bars = smem_u32(smem) + uint32_t(warp * p.stages) * 8u;
+  const uint32_t bars_bytes = uint32_t(kWarps * p.stages * 8 + 127) & ~127u;
+  const uint32_t ring = smem_u32(smem) + bars_bytes + uint32_t(warp * p.stages) * STAGE;
+  int* prefix = reinterpret_cast<int*>(smem + bars_bytes + kWarps * p.stages * STAGE);
+  if (lane == 0) {
+    for (int i = 0; i < p.stages; ++i) mbar_init(bars + 8u * i, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < kWarps * 2) desc[threadIdx.x] = make_int4(-1, 0, 0, 0);
+  griddep_wait();
+
+  // ---- the plan: units of every request, their prefix, this warp's run
+  int total = 0;
+  for (int b = 0; b < S; b += kWarps * 32) {
+    const int s = b + threadIdx.x;
+    int x = 0;
+    if (s < S) {
+      Request r;
+      if (!request_of<KU>(p, s, r) && blockIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_RANGE);
+      x = r.tiles * r.units * p.num_kv_heads;
+    }
+    int inc = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int off = total, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) off += wsum[w];
+      sum += wsum[w];
+    }
+    if (s < S) prefix[s] = off + inc - x;
+    total += sum;
+    __syncthreads();
+  }
+  const int num_warps = gridDim.x * kWarps;
+  const int per = (total + num_warps - 1) / num_warps;
+  const int w0 = blockIdx.x * kWarps;
+  auto first = [&](int w) { return int(min(int64_t(w) * per, int64_t(total))); };
+  const int u0 = first(w0 + warp), u1 = first(w0 + warp + 1);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.per = per;
+  const int64_t rec_bytes = int64_t(p.block_size) * (ROW + 4);
+
+  // ---- producer: unit i of the run into stage i % stages; the whole warp calls it, in order
+  struct {
+    int seg_end = 0, x = 0, units = 0, blocks = 0, b0 = 0, ent = 0, ent_next = 0;
+    const int32_t* row = nullptr;
+    int64_t head_off = 0;
+  } pr;
+  const bool fused = p.part == p.block_size;  // a record is one copy
+  const int copies = fused ? 2 : 4, which = lane % copies, piece = lane / copies;
+  auto entry = [&](int b) { return b < pr.blocks ? pr.row[b] : -1; };
+  auto fill = [&](int i) {
+    const int u = u0 + i;
+    if (u >= pr.seg_end) {
+      const Segment sg = segment_of<KU>(p, prefix, u);
+      Request r;
+      request_of<KU>(p, sg.s, r);
+      // keys the tile's last row sees, and the blocks and units that hold them
+      const int last = min((sg.tile * kRows + kRows - 1) / p.group, r.q_len - 1);
+      const int n = r.L - r.q_len + last + 1;
+      pr.seg_end = sg.end;
+      pr.x = u - sg.begin;
+      pr.units = (n + KU - 1) / KU;
+      pr.blocks = (n + p.block_size - 1) / p.block_size;
+      pr.row = p.block_table + int64_t(sg.s) * p.max_blocks_per_seq;
+      pr.head_off = int64_t(sg.head) * rec_bytes;
+      pr.b0 = pr.x * KU / p.block_size;
+      pr.ent = entry(pr.b0 + lane);
+      pr.ent_next = entry(pr.b0 + 32 + lane);
+    }
+    const uint32_t bar = bars + 8u * uint32_t(i % p.stages), dst = ring + uint32_t(i % p.stages) * STAGE;
+    if (pr.x < pr.units) {
+      const int key0 = pr.x * KU, key = key0 + piece * p.part;
+      if (key0 / p.block_size >= pr.b0 + 32) {  // table entries come 32 at a time, a batch ahead
+        pr.b0 += 32;
+        pr.ent = pr.ent_next;
+        pr.ent_next = entry(pr.b0 + 32 + lane);
+      }
+      const int b = key / p.block_size, b_at = b - pr.b0;  // below 64: a unit has at most 9 blocks
+      const int e0 = __shfl_sync(0xffffffffu, pr.ent, b_at & 31), e1 = __shfl_sync(0xffffffffu, pr.ent_next, b_at & 31);
+      const int block = b_at < 32 ? e0 : e1;
+      const bool wanted = piece * p.part < KU && b < pr.blocks;
+      const bool good = wanted && block >= 0 && block < p.num_blocks;
+      if (wanted && !good) raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
+      const bool is_v = which >= copies / 2, params = !fused && (which & 1);
+      const int in = key - b * p.block_size;
+      const uint32_t bytes = uint32_t(p.part) * (fused ? ROW + 4 : params ? 4 : ROW);
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, good ? bytes : 0u);
+      if (lane == 0) mbar_arrive_expect_tx(bar, sum);
+      __syncwarp();
+      if (good) {
+        const unsigned char* src = (is_v ? p.v_cache : p.k_cache) + int64_t(block) * p.num_kv_heads * rec_bytes +
+                                   pr.head_off +
+                                   (params ? int64_t(p.block_size) * ROW + int64_t(in) * 4 : int64_t(in) * ROW);
+        bulk_g2s(dst + (is_v ? HALF : 0) + uint32_t(piece * p.part * (ROW + 4) + (params ? p.part * ROW : 0)), src, bytes,
+                 bar);
+      }
+    } else {
+      if (lane == 0) mbar_arrive(bar);
+      __syncwarp();
+    }
+    ++pr.x;
+  };
+
+  // ---- where a lane's rows lie in a stage: keys key_of(g), key_of(g + 8) of a tile as rows of K,
+  // keys key_of(2t), (2t + 1), (2t + 8), (2t + 9) as rows of V; later tiles `next` bytes on
+  const int part_bytes = p.part * (ROW + 4);
+  auto code_at = [&](int key) { return key / p.part * part_bytes + key % p.part * ROW; };
+  auto param_at = [&](int key) { return key / p.part * part_bytes + p.part * ROW + key % p.part * 4; };
+  constexpr int kLane = BITS == 4 ? D / 8 : 16;  // bytes of a key row a lane takes at once
+  int k_at[2], v_at[4], par_at[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    k_at[i] = code_at(key_of(g + 8 * i)) + t * kLane;
+    par_at[i] = param_at(key_of(g + 8 * i));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v_at[i] = HALF + code_at(key_of(2 * t + (i & 1) + 8 * (i >> 1))) + g * (ROW / 8);
+  const int next_code = p.part >= 32 ? 16 * ROW : 16 / min(p.part, 16) * part_bytes;
+  const int next_param = p.part >= 32 ? 64 : next_code;
+
+  const int n_run = u1 - u0;
+  int filled = 0;
+  for (; filled < min(p.stages, n_run); ++filled) fill(filled);
+  bool ok = true;
+  int done = 0;
+  while (done < n_run && ok) {
+    // ---- a segment of the run
+    const Segment sg = segment_of<KU>(p, prefix, u0 + done);
+    Request r;
+    request_of<KU>(p, sg.s, r);
+    const int rows = min(kRows, r.q_len * p.group - sg.tile * kRows);
+    const int x0 = u0 + done - sg.begin, x1 = min(sg.end, u1) - sg.begin;
+    const int j_first = sg.tile * kRows / p.group, j_last = (sg.tile * kRows + rows - 1) / p.group;
+    const int n_min = r.L - r.q_len + j_first + 1, n_max = r.L - r.q_len + j_last + 1;  // keys the rows see
+    // Query row g of the tile as f16 with its largest element in [2^14, 2^15): a power of two, so exact
+    // but for elements 2^28 times smaller than the row's largest. Its factor goes into the logits'.
+    uint32_t qb[NK][2];
+    float qsum = 0.f, qfactor;
+    {
+      float f[D / 4];
+      const int rr = sg.tile * kRows + min(g, rows - 1);
+      const __nv_bfloat16* src = p.q + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D;
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {  // the dimensions of the key row's pieces that this lane takes
+        const int dim = BITS == 4 ? t * (D / 4) + 8 * i : (i / 2) * 64 + t * 16 + (i & 1) * 8;
+        Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(src + dim), f + 8 * i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[8 * i + e]));
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const int ex = int(__float_as_uint(big) >> 23);  // biased exponent; 0 and 255: left unscaled
+      const int shift = (ex == 0 || ex == 255 || g >= rows) ? 0 : min(127, 14 - (ex - 127));
+      const float mul = g >= rows ? 0.f : __uint_as_float(uint32_t(shift + 127) << 23);
+      qfactor = p.scale_log2 * exp2f(float(-shift));
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) f[i] = __half2float(__float2half_rn(f[i] * mul)), qsum += f[i];
+      if (g >= rows) qsum = 0.f;
+      qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
+      qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        if (BITS == 4) {  // word k / 2 of the lane's piece: elements (0, 4), (1, 5), then (2, 6), (3, 7)
+          const float* e = f + 8 * (k / 2) + 2 * (k & 1);
+          qb[k][0] = pack_f16(e[0], e[4]);
+          qb[k][1] = pack_f16(e[1], e[5]);
+        } else {
+          qb[k][0] = pack_f16(f[4 * k], f[4 * k + 1]);
+          qb[k][1] = pack_f16(f[4 * k + 2], f[4 * k + 3]);
+        }
+        if (g >= rows) qb[k][0] = qb[k][1] = 0u;
+      }
+    }
+    // of query rows 2t and 2t + 1, whose logits this lane holds
+    float qs[2], fac[2], m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, mid[2] = {0.f, 0.f};
+    int lim[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      qs[h] = __shfl_sync(0xffffffffu, qsum, (2 * t + h) * 4);
+      fac[h] = __shfl_sync(0xffffffffu, qfactor, (2 * t + h) * 4);
+      lim[h] = r.L - r.q_len + (sg.tile * kRows + min(2 * t + h, rows - 1)) / p.group + 1;
+    }
+    float o[NK][4];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    // Numerators times value steps enter the second product as f16 (rounded to 2^-11 relative at most: an
+    // eighth of the output's own rounding), scaled by the power of two 2^wexp that keeps the steps seen so
+    // far below 2^7 and so the products below 2^15; what rounds to nothing is 2^-31 of the largest.
+    int wexp = 127;
+    float wscale = __uint_as_float(254u << 23);
+
+    auto unit = [&](uint32_t st, int key0, auto tail_c) {
+      constexpr bool kTail = decltype(tail_c)::value;
+#pragma unroll
+      for (int tile = 0; tile < KU / 16; ++tile) {
+        const uint32_t base = st + uint32_t(tile * next_code), pbase = st + uint32_t(tile * next_param);
+        // ---- q.c of 16 keys x 8 query rows
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[2], pv[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          pk[i] = lds32(pbase + par_at[i]);
+          pv[i] = lds32(pbase + HALF + par_at[i]);
+        }
+        if constexpr (BITS == 4) {
+          uint32_t a[2][D / 32];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (D == 128) {
+              const uint4 x = lds128(base + k_at[i]);
+              a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
+            } else {
+              const uint2 x = lds64(base + k_at[i]);
+              a[i][0] = x.x, a[i][1] = x.y;
+            }
+          }
+          constexpr uint32_t M = 0x00f000f0u, C = 0x64006400u;
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {
+            const uint32_t x = a[0][w], y = a[1][w];
+            mma_16816(s, ((x << 4) & M) | C, ((y << 4) & M) | C, (x & M) | C, (y & M) | C, qb[2 * w][0], qb[2 * w][1], true);
+            mma_16816(s1, ((x >> 4) & M) | C, ((y >> 4) & M) | C, ((x >> 8) & M) | C, ((y >> 8) & M) | C, qb[2 * w + 1][0],
+                      qb[2 * w + 1][1], true);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 x4 = lds128(base + k_at[0] + 64 * c), y4 = lds128(base + k_at[1] + 64 * c);
+            const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t H = 0x64646464u;
+              mma_16816((w & 1) ? s1 : s, __byte_perm(x[w], H, 0x4140), __byte_perm(y[w], H, 0x4140),
+                        __byte_perm(x[w], H, 0x4342), __byte_perm(y[w], H, 0x4342), qb[4 * c + w][0], qb[4 * c + w][1],
+                        true);
+            }
+          }
+        }
+        // ---- logits (in powers of two), numerators: [0], [1] key_of(g), [2], [3] key_of(g + 8)
+        float x[4], ws[2], midv[2];
+        bool hidden[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int key = key0 + tile * 16 + key_of(g + 8 * i);
+          if (kTail && key >= n_max) pk[i] = pv[i] = 0u;  // a row behind the last: whatever it holds
+          const float lo = param_lo(pk[i]), step = param_step(pk[i]);
+          const float vstep = param_step(pv[i]);
+          midv[i] = fmaf(vstep, kMid, param_lo(pv[i]));
+          ws[i] = vstep;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float c = fmaf(s[2 * i + h] + s1[2 * i + h], kUnscale, -kOffset * qs[h]);
+            x[2 * i + h] = fmaf(c, step, lo * qs[h]) * fac[h];
+            hidden[2 * i + h] = kTail && key >= lim[h];
+            if (hidden[2 * i + h]) x[2 * i + h] = -INFINITY;
+          }
+        }
+        // The reference maximum moves only when a logit passes it by 2^8, the steps' power of two when
+        // one passes it twofold: then, for the whole warp, the sums so far are scaled.
+        const bool move = fmaxf(x[0], x[2]) - m[0] > 8.f || fmaxf(x[1], x[3]) - m[1] > 8.f ||
+                          fmaxf(ws[0], ws[1]) * wscale > 128.f;
+        if (__any_sync(0xffffffffu, move)) {
+          float alpha[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float top = fmaxf(x[h], x[2 + h]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if (!(top - m[h] > 8.f)) top = m[h];
+            alpha[h] = exp2f(m[h] - top);
+            m[h] = top;
+            l[h] *= alpha[h];
+            mid[h] *= alpha[h];
+          }
+          // NaN steps (of rows that hold NaN) do not count
+          const uint32_t big = __float_as_uint(fmaxf(ws[0], ws[1]));
+          const uint32_t top = __reduce_max_sync(0xffffffffu, big <= 0x7f800000u ? big : 0u);
+          const int want = min(127, 6 - (int(top >> 23) - 126));
+          float beta = 1.f;
+          if (want < wexp) {
+            beta = exp2f(float(want - wexp));
+            wexp = want;
+            wscale = __uint_as_float(uint32_t(want + 127) << 23);
+          }
+#pragma unroll
+          for (int i = 0; i < NK; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e & 1] * beta;
+        }
+        uint32_t pb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float wi = ws[i] * wscale;
+          float w[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float e = ex2_ftz(x[2 * i + h] - m[h]);
+            l[h] += e;
+            w[h] = e * wi;
+            if (hidden[2 * i + h]) {
+              w[h] = 0.f;  // not 0 * NaN
+            } else {
+              mid[h] = fmaf(e, midv[i], mid[h]);
+            }
+          }
+          pb[i] = movm(pack_f16(w[0], w[1]));
+        }
+        // ---- 16 value dimensions x 8 query rows a step: rows of the tile of codes - mid, dimensions
+        // (D / 8) g + 2 i in rows 0 .. 7 and the next in rows 8 .. 15
+        if constexpr (BITS == 4) {
+          const __half2 low = __half2half2(__float2half_rn(-1032.f)), high = __half2half2(__float2half_rn(-72.f)),
+                        six = __half2half2(__float2half_rn(0.0625f));
+          uint32_t v[4][D / 64];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+              const uint2 y = lds64(base + v_at[i]);
+              v[i][0] = y.x, v[i][1] = y.y;
+            } else {
+              v[i][0] = lds32(base + v_at[i]);
+            }
+          }
+          constexpr uint32_t M = 0x000f000fu, N = 0x00f000f0u, C = 0x64006400u;
+#pragma unroll
+          for (int w = 0; w < D / 64; ++w)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // elements 0 .. 3, 4 .. 7 of the words
+              const uint32_t sel = half ? 0x7632 : 0x5410;
+              const uint32_t a = __byte_perm(v[0][w], v[1][w], sel), b = __byte_perm(v[2][w], v[3][w], sel);
+              mma_16816(o[4 * w + 2 * half], h2((a & M) | C, low), h2((a & N) | C, six, high), h2((b & M) | C, low),
+                        h2((b & N) | C, six, high), pb[0], pb[1], true);
+              mma_16816(o[4 * w + 2 * half + 1], h2(((a >> 8) & M) | C, low), h2(((a >> 8) & N) | C, six, high),
+                        h2(((b >> 8) & M) | C, low), h2(((b >> 8) & N) | C, six, high), pb[0], pb[1], true);
+            }
+        } else {
+          const __half2 sub = __half2half2(__float2half_rn(-1152.f));
+          const uint32_t H = 0x64646464u;
+          uint32_t v[4][D / 32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+              const uint4 y = lds128(base + v_at[i]);
+              v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
+            } else {
+              const uint2 y = lds64(base + v_at[i]);
+              v[i][0] = y.x, v[i][1] = y.y;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t sel = half ? 0x7362 : 0x5140;
+              const uint32_t a = __byte_perm(v[0][w], v[1][w], sel), b = __byte_perm(v[2][w], v[3][w], sel);
+              mma_16816(o[2 * w + half], h2(__byte_perm(a, H, 0x4140), sub), h2(__byte_perm(a, H, 0x4342), sub),
+                        h2(__byte_perm(b, H, 0x4140), sub), h2(__byte_perm(b, H, 0x4342), sub), pb[0], pb[1], true);
+            }
+        }
+      }
+    };
+
+    for (int x = x0; x < x1; ++x, ++done) {
+      const uint32_t bar = bars + 8u * uint32_t(done % p.stages);
+      if (!__all_sync(0xffffffffu, mbar_wait(bar, uint32_t(done / p.stages) & 1u))) {
+        ok = false;
+        break;
+      }
+      const int key0 = x * KU;
+      const uint32_t st = ring + uint32_t(done % p.stages) * STAGE;
+      if (key0 + KU <= n_min) {
+        unit(st, key0, std::false_type{});
+      } else if (key0 < n_max) {
+        unit(st, key0, std::true_type{});
+      }
+      __syncwarp();
+      if (filled < n_run) {
+        fill(filled);
+        ++filled;
+      }
+    }
+    if (!ok) break;
+    // ---- the segment's end in this run: sums over the lanes that share a query row, then out or a piece
+    const float unscale = exp2f(float(-wexp));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+        mid[h] += __shfl_xor_sync(0xffffffffu, mid[h], d);
+      }
+    const bool whole = x0 == 0 && x1 == r.units;
+    const int slot = x0 + sg.begin == u0 ? 0 : 1;
+    if (!whole && lane == 0) desc[warp * 2 + slot] = make_int4(sg.begin, sg.end, sg.s, sg.head * r.tiles + sg.tile);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = 2 * t + h;
+      if (row >= rows) continue;
+      float f[D / 8];
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        f[2 * i] = fmaf(o[i][h], unscale, mid[h]);
+        f[2 * i + 1] = fmaf(o[i][2 + h], unscale, mid[h]);
+      }
+      if (whole) {
+        const float inv = l[h] > 0.f ? 1.f / l[h] : (l[h] == 0.f ? 0.f : l[h]);
+        __nv_bfloat16* dst = out_row<D>(p, sg.s, sg.head, sg.tile, row) + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) f[i] *= inv;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) reinterpret_cast<uint4*>(dst)[i] = Elem<__nv_bfloat16>::pack(f + 8 * i);
+      } else {
+        float* dst = p.pieces + int64_t((w0 + warp) * 2 + slot) * piece_floats<D>();
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          reinterpret_cast<float4*>(dst + row * D + g * (D / 8))[i] =
+              make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        if (g == 0) {
+          dst[kRows * D + row] = m[h];
+          dst[kRows * D + kRows + row] = l[h];
+        }
+      }
+    }
+  }
+  if (!ok) {  // a copy did not arrive in time: tell, and wait for those under way before leaving
+    if (lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
+    for (int i = done; i < filled; ++i) mbar_wait(bars + 8u * uint32_t(i % p.stages), uint32_t(i / p.stages) & 1u);
+  }
+  __syncthreads();
+
+  // ---- pieces of segments cut between this CTA's warps, or between CTAs
+  const int c0 = first(w0), c1 = first(w0 + kWarps);
+  float* cta_pieces = p.pieces + int64_t(num_warps) * 2 * piece_floats<D>();
+  if (threadIdx.x < 2) {
+    // slot 0: a segment from before c0, or one from c0 to past c1; slot 1: one that goes on behind c1
+    int4 d = make_int4(-1, 0, 0, 0);
+    if (c0 < c1) {
+      if (threadIdx.x == 0) {
+        const int4 a = desc[0];
+        if (a.x >= 0 && (a.x < c0 || a.y > c1)) d = a;
+      } else {
+        for (int i = 0; i < kWarps * 2; ++i)
+          if (desc[i].x > c0 && desc[i].y > c1) d = desc[i];
+      }
+    }
+    p.descs[blockIdx.x * 2 + threadIdx.x] = d;
+  }
+  // leaders: a CTA's first piece of a segment; a task is one of its rows
+  for (int task = warp; task < kWarps * 2 * kRows; task += kWarps) {
+    const int at = task / kRows, row = task % kRows, w = at >> 1;
+    const int4 d = desc[at];
+    if (d.x < 0 || !((at & 1) || w == 0 || d.x == first(w0 + w))) continue;
+    Request r;
+    request_of<KU>(p, d.z, r);
+    const int head = d.w / r.tiles, tile = d.w - head * r.tiles;
+    __nv_bfloat16* out = out_row<D>(p, d.z, head, tile, row);
+    if (!out) continue;
+    int count = 1;
+    while (w + count < kWarps && first(w0 + w + count) < d.y) ++count;
+    RowJoin<D> j;
+    j.run(p.pieces, row, lane, count, [&](int i) { return i == 0 ? w0 * 2 + at : (w0 + w + i) * 2; });
+    if (d.x >= c0 && d.y <= c1)
+      j.store_out(out, lane);
+    else
+      j.store_piece(cta_pieces + int64_t(blockIdx.x * 2 + (d.x <= c0 ? 0 : 1)) * piece_floats<D>(), row, lane);
+  }
+}
+
+// Segments cut between CTAs: CTA c joins those whose first piece is c's; a warp a row.
+template <int D, int BITS>
+__global__ void __launch_bounds__(kRows * 32) attention_int_join_kernel(const IntParams p, int num_ctas) {
+  constexpr int KU = unit_keys<BITS>();
+  griddep_wait();
+  const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t run = int64_t(*p.per) * kWarps;  // units a CTA
+  const float* pieces = p.pieces + int64_t(num_ctas) * kWarps * 2 * piece_floats<D>();
+#pragma unroll
+  for (int slot = 0; slot < 2; ++slot) {
+    const int4 d = p.descs[c * 2 + slot];
+    if (d.x < 0 || (slot == 0 && d.x != c * run)) continue;
+    Request r;
+    request_of<KU>(p, d.z, r);
+    const int head = d.w / r.tiles, tile = d.w - head * r.tiles;
+    __nv_bfloat16* out = out_row<D>(p, d.z, head, tile, row);
+    if (!out) continue;
+    int count = 1;
+    while (c + count < num_ctas && (c + count) * run < d.y) ++count;
+    RowJoin<D> j;
+    j.run(pieces, row, lane, count, [&](int i) { return i == 0 ? c * 2 + slot : (c + i) * 2; });
+    j.store_out(out, lane);
+  }
+}
+
+constexpr size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <int D, int BITS>
+cudaError_t run_int(IntParams p, const AttnIntArgs& a, cudaStream_t stream) {
+  constexpr int STAGE = stage_bytes<D, BITS>();
+  const size_t prefix = size_t(a.num_seqs) * 4, room = 232448 - 2048;  // the rest: static shared memory
+  int stages = 8;
+  auto bytes = [&](int n) { return size_t((kWarps * n * 8 + 127) & ~127) + size_t(kWarps) * n * STAGE + prefix; };
+  while (stages > 1 && bytes(stages) > room) --stages;
+  static_assert(((kWarps * 16 + 127) & ~127) + kWarps * 2 * STAGE + kIntMaxSeqs * 4 <= 232448 - 2048, "two stages");
+  p.stages = stages;
+  const cudaError_t e = ensure_smem<attention_int_kernel<D, BITS>>(room);
+  if (e != cudaSuccess) return e;
+  const cudaError_t l = launch_pdl(attention_int_kernel<D, BITS>, dim3(a.num_ctas), dim3(kWarps * 32), bytes(stages),
+                                   stream, p);
+  if (l != cudaSuccess) return l;
+  return launch_pdl(attention_int_join_kernel<D, BITS>, dim3(a.num_ctas), dim3(kRows * 32), 0, stream, p, a.num_ctas);
+}
+
+}  // namespace
+
+// descs, per, pieces of the CTAs' warps and of the CTAs
+size_t attention_int_workspace_bytes(int head_dim, int num_ctas) {
+  const size_t piece = (kRows * size_t(head_dim) + 2 * kRows) * 4;
+  return align_up(size_t(num_ctas) * 2 * sizeof(int4)) + 256 + size_t(num_ctas) * (kWarps + 1) * 2 * piece;
+}
+
+bool attention_int_fits(const AttnIntArgs& a) {
+  const int ku = a.bits == 4 ? unit_keys<4>() : unit_keys<8>();
+  const int64_t tiles = (int64_t(a.num_tokens) * (a.num_heads / a.num_kv_heads) + kRows - 1) / kRows + a.num_seqs;
+  const int64_t units = (int64_t(a.max_seq_len) + ku - 1) / ku;
+  // units are counted in 32 bits (a step of all warps past the end, too)
+  return a.num_seqs <= kIntMaxSeqs && tiles <= 0x7fffffff / a.num_kv_heads &&
+         tiles * a.num_kv_heads <= (0x7fffffff - (1 << 20)) / units;
+}
+
+cudaError_t launch_attention_int(const AttnIntArgs& a, cudaStream_t stream) {
+  IntParams p = {};
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k_cache = static_cast<const unsigned char*>(a.k_cache);
+  p.v_cache = static_cast<const unsigned char*>(a.v_cache);
+  p.block_table = a.block_table;
+  p.seq_lens = a.seq_lens;
+  p.qsl = a.query_start_loc;
+  p.err = a.err;
+  unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+  p.descs = reinterpret_cast<int4*>(ws);
+  ws += align_up(size_t(a.num_ctas) * 2 * sizeof(int4));
+  p.per = reinterpret_cast<int*>(ws);
+  p.pieces = reinterpret_cast<float*>(ws + 256);
+  p.num_blocks = a.num_blocks;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.num_seqs = a.num_seqs;
+  p.num_tokens = a.num_tokens;
+  p.max_query_len = a.max_query_len;
+  p.max_seq_len = a.max_seq_len;
+  p.num_heads = a.num_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.group = a.num_heads / a.num_kv_heads;
+  p.block_size = a.block_size;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  const int ku = a.bits == 4 ? unit_keys<4>() : unit_keys<8>();
+  p.part = a.block_size & -a.block_size;
+  if (p.part > ku) p.part = ku;
+  if (a.bits == 4) return a.head_dim == 64 ? run_int<64, 4>(p, a, stream) : run_int<128, 4>(p, a, stream);
+  return a.head_dim == 64 ? run_int<64, 8>(p, a, stream) : run_int<128, 8>(p, a, stream);
+}
+
+}  // namespace pa

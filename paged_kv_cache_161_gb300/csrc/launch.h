@@ -217,4 +217,56 @@ struct SparseAttnArgs {
 };
 cudaError_t launch_attention_sparse(const BatchArgs& b, const SparseAttnArgs& a, cudaStream_t stream);
 
+// ---------------------------------------------------------------- integer-coded caches
+struct KvIntArgs {
+  unsigned int* err;
+  int64_t num_blocks;
+  int block_size, num_kv_heads, head_dim, bits;
+  pa_dtype dtype;  // of the rows written or read
+};
+cudaError_t launch_kv_write_int(const KvIntArgs& a, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                                void* k_cache, void* v_cache, const int64_t* slot_mapping, int64_t num_tokens,
+                                cudaStream_t stream);
+cudaError_t launch_kv_read_int(const KvIntArgs& a, void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, int max_blocks_per_seq, const int32_t* start_pos,
+                               const int32_t* seq_lens, const int32_t* row_start_loc, int num_seqs, int64_t num_rows,
+                               cudaStream_t stream);
+
+constexpr int kIntMaxSeqs = 8192;  // requests of a pa_attention_int call
+struct AttnIntArgs {
+  void* out;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  void* workspace;
+  unsigned int* err;
+  int64_t num_blocks;
+  int max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len;
+  int num_heads, num_kv_heads, head_dim, block_size, bits;
+  int num_ctas;
+  float scale;
+};
+size_t attention_int_workspace_bytes(int head_dim, int num_ctas);
+bool attention_int_fits(const AttnIntArgs& a);  // whether the batch's units and requests can be counted
+cudaError_t launch_attention_int(const AttnIntArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- packed prompts
+struct PackedArgs {
+  void* out;
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* q_start_loc;
+  const int32_t* k_start_loc;
+  unsigned int* err;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  int num_seqs, num_q_rows, num_k_rows, max_query_len, num_heads, num_kv_heads, head_dim;
+  float scale;
+};
+bool attention_packed_fits(const PackedArgs& a);  // whether its tiles and requests can be counted
+cudaError_t launch_attention_packed(const PackedArgs& a, cudaStream_t stream);
+
 }  // namespace pa

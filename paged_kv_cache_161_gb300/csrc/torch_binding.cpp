@@ -397,6 +397,125 @@ PyObject* attention_sparse(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
   });
 }
 
+// An integer-coded pair of caches uint8 [num_blocks, num_kv_heads, block_size * (head_dim * bits / 8 + 4)].
+struct IntCaches {
+  void *k, *v;
+  int64_t NB;
+  int B, H, bits;
+  IntCaches(PyObject* kc, const char* kn, PyObject* vc, const char* vn, PyObject* bits_, const char* bn, int64_t D, int dev) {
+    const at::Tensor& t = tensor(kc, kn, 3);
+    bits = int32(bits_, bn);
+    const int64_t row = bits > 0 && bits <= 64 && D <= INT32_MAX ? D * bits / 8 + 4 : 0, size = t.size(2);
+    if (row <= 0 || size % row != 0 || size / row > INT32_MAX || t.size(1) > INT32_MAX)
+      refuse(PyExc_ValueError, "%s must be [num_blocks, num_kv_heads, block_size * (head_dim * bits / 8 + 4)]", kn);
+    NB = t.size(0);
+    H = int(t.size(1));
+    B = int(size / row);
+    k = address(kc, kn, dev, at::kByte, {NB, H, size});
+    v = address(vc, vn, dev, at::kByte, {NB, H, size});
+  }
+};
+
+PyObject* kv_write_int(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    static const char* const names[] = {"k", "v", "k_cache", "v_cache", "slot_mapping", "bits", "stream"};
+    const Args<7> a("kv_write_int", names, 5, 6, args, n, kw);
+    const at::Tensor& k = tensor(a.v[0], names[0], 3);
+    const int dev = device_of(k, names[0]);
+    const int64_t T = k.size(0), Hkv = k.size(1), D = k.size(2);
+    const auto type = k.scalar_type();
+    const pa_dtype dt = code(k, names[0]);
+    const IntCaches c(a.v[2], names[2], a.v[3], names[3], a.v[5], names[5], D, dev);
+    if (c.H != Hkv) refuse(PyExc_ValueError, "%s and the caches differ in their KV heads", names[0]);
+    int64_t ks, vs;
+    void* kp = token_rows(a.v[0], names[0], dev, type, T, Hkv, D, &ks);
+    void* vp = token_rows(a.v[1], names[1], dev, type, T, Hkv, D, &vs);
+    auto slots = at_<int64_t>(a.v[4], names[4], dev, kI64, {T});
+    const On on(dev, a.v[6]);
+    return result("pa_kv_write_int", Py_None, [&] {
+      return pa_kv_write_int(kp, vp, ks, vs, dt, c.k, c.v, slots, T, c.NB, c.B, c.H, int(D), c.bits, on.stream);
+    });
+  });
+}
+
+PyObject* kv_read_int(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    static const char* const names[] = {"k_out", "v_out", "k_cache", "v_cache", "block_table", "start_pos", "seq_lens",
+                                        "row_start_loc", "bits", "stream"};
+    const Args<10> a("kv_read_int", names, 8, 9, args, n, kw);
+    const at::Tensor &ko = tensor(a.v[0], names[0], 3), &table = tensor(a.v[4], names[4], 2);
+    const int dev = device_of(ko, names[0]);
+    const int64_t R = ko.size(0), D = ko.size(2);
+    const int S = size32(table, 0, names[4]), W = size32(table, 1, names[4]);
+    const auto type = ko.scalar_type();
+    const pa_dtype dt = code(ko, names[0]);
+    const IntCaches c(a.v[2], names[2], a.v[3], names[3], a.v[8], names[8], D, dev);
+    void* kp = address(a.v[0], names[0], dev, type, {R, c.H, D});
+    void* vp = address(a.v[1], names[1], dev, type, {R, c.H, D});
+    auto i32 = [&](int i, std::initializer_list<int64_t> shape) { return at_<int32_t>(a.v[i], names[i], dev, kI32, shape); };
+    auto bt = i32(4, {S, W}), start = a.v[5] == Py_None ? nullptr : i32(5, {S}), lens = i32(6, {S}),
+         rows = i32(7, {int64_t(S) + 1});
+    const On on(dev, a.v[9]);
+    return result("pa_kv_read_int", Py_None, [&] {
+      return pa_kv_read_int(kp, vp, dt, c.k, c.v, bt, W, start, lens, rows, S, R, c.NB, c.B, c.H, int(D), c.bits, on.stream);
+    });
+  });
+}
+
+PyObject* attention_int(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    static const char* const names[] = {"out", "q", "k_cache", "v_cache", "block_table", "seq_lens", "query_start_loc",
+                                        "bits", "max_query_len", "max_seq_len", "scale", "workspace", "stream"};
+    const Args<13> a("attention_int", names, 7, 12, args, n, kw);
+    const at::Tensor &q = tensor(a.v[1], names[1], 3), &ws = tensor(a.v[11], names[11], 1);
+    const int dev = device_of(q, names[1]);
+    const int T = size32(q, 0, names[1]), Hq = size32(q, 1, names[1]), D = size32(q, 2, names[1]);
+    const IntCaches c(a.v[2], names[2], a.v[3], names[3], a.v[7], names[7], D, dev);
+    void* out = address(a.v[0], names[0], dev, at::kBFloat16, {T, Hq, D});
+    void* qp = address(a.v[1], names[1], dev, at::kBFloat16, {T, Hq, D});
+    const Batch b(a.v, names, 4, dev);
+    const int max_q = int32(a.v[8], names[8]), max_s = int32(a.v[9], names[9]);
+    const float scale = float(real(a.v[10]));
+    const int64_t ws_bytes = ws.size(0);
+    void* wp = address(a.v[11], names[11], dev, at::kByte, {ws_bytes});
+    const On on(dev, a.v[12]);
+    return result("pa_attention_int", a.v[0], [&] {
+      return pa_attention_int(out, qp, c.k, c.v, b.table, b.W, b.lens, b.qsl, b.S, T, max_q, max_s, Hq, c.H, D, c.B, c.NB,
+                              scale, c.bits, wp, size_t(ws_bytes), on.stream);
+    });
+  });
+}
+
+PyObject* attention_packed(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    static const char* const names[] = {"out", "q", "k", "v", "q_start_loc", "k_start_loc", "max_query_len", "scale",
+                                        "stream"};
+    const Args<9> a("attention_packed", names, 6, 8, args, n, kw);
+    const at::Tensor &q = tensor(a.v[1], names[1], 3), &k = tensor(a.v[2], names[2], 3), &qs = tensor(a.v[4], names[4], 1);
+    const int dev = device_of(q, names[1]);
+    const int T = size32(q, 0, names[1]), Hq = size32(q, 1, names[1]), D = size32(q, 2, names[1]),
+              K = size32(k, 0, names[2]), Hkv = size32(k, 1, names[2]);
+    if (qs.size(0) < 1 || qs.size(0) > INT32_MAX)
+      refuse(PyExc_ValueError, "%s must hold one entry more than there are requests", names[4]);
+    const int S = int(qs.size(0) - 1);
+    const auto type = q.scalar_type();
+    const pa_dtype dt = code(q, names[1]);
+    int64_t qst, kst, vst;
+    void* out = address(a.v[0], names[0], dev, type, {T, Hq, D});
+    void* qp = token_rows(a.v[1], names[1], dev, type, T, Hq, D, &qst);
+    void* kp = token_rows(a.v[2], names[2], dev, type, K, Hkv, D, &kst);
+    void* vp = token_rows(a.v[3], names[3], dev, type, K, Hkv, D, &vst);
+    auto ql = at_<int32_t>(a.v[4], names[4], dev, kI32, {int64_t(S) + 1});
+    auto kl = at_<int32_t>(a.v[5], names[5], dev, kI32, {int64_t(S) + 1});
+    const int max_q = int32(a.v[6], names[6]);
+    const float scale = float(real(a.v[7]));
+    const On on(dev, a.v[8]);
+    return result("pa_attention_packed", a.v[0], [&] {
+      return pa_attention_packed(out, qp, kp, vp, qst, kst, vst, ql, kl, S, T, K, max_q, Hq, Hkv, D, scale, dt, on.stream);
+    });
+  });
+}
+
 PyObject* init(PyObject*, PyObject* error) {
   Py_INCREF(error);
   Py_XDECREF(g_error);
@@ -454,6 +573,32 @@ PyMethodDef methods[] = {
             "[T, Hkv, num_select] (logical blocks of its request, entries < 0 skipped), causal; zeros for\n"
             "an empty list; returns out. out, q bfloat16 [T, Hq, D]; caches bfloat16, or float8_e4m3fn\n"
             "with scales."),
+    PA_CALL(kv_write_int,
+            "kv_write_int($module, k, v, k_cache, v_cache, slot_mapping, *, bits, stream=None)\n--\n\n"
+            "pa_kv_write_int: the rows of k and v become the codes (bits = 4 or 8) of their slots, with a\n"
+            "smallest value and a step for each token and KV head.\n\n"
+            "k and v [T, Hkv, D]: bfloat16 or float32, tokens may lie apart; slot_mapping int64 [T], negative:\n"
+            "padding. Caches uint8 [num_blocks, Hkv, block_size * (D * bits / 8 + 4)], written in place."),
+    PA_CALL(kv_read_int,
+            "kv_read_int($module, k_out, v_out, k_cache, v_cache, block_table, start_pos, seq_lens,\n"
+            "            row_start_loc, *, bits, stream=None)\n--\n\n"
+            "pa_kv_read_int: positions start_pos[s] .. seq_lens[s] - 1 of every request out of its pages into\n"
+            "rows row_start_loc[s], ... of k_out and v_out [R, Hkv, D] (bfloat16 or float32, contiguous).\n\n"
+            "start_pos int32 [S] or None (0), seq_lens int32 [S], row_start_loc int32 [S + 1]; a request's rows\n"
+            "behind those positions, and rows of no request, stay as they are."),
+    PA_CALL(attention_int,
+            "attention_int($module, out, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, *, bits,\n"
+            "              max_query_len, max_seq_len, scale, workspace, stream=None)\n--\n\n"
+            "pa_attention_int: attention of decode and drafted tokens over caches of integer codes; returns\n"
+            "out. out, q bfloat16 [T, Hq, D]; caches as for kv_write_int; the batch as for attention.\n"
+            "workspace: a uint8 CUDA tensor of attention_int_workspace_size(...) bytes, no contents needed, not\n"
+            "shared by calls that may overlap on the GPU."),
+    PA_CALL(attention_packed,
+            "attention_packed($module, out, q, k, v, q_start_loc, k_start_loc, *, max_query_len, scale,\n"
+            "                 stream=None)\n--\n\n"
+            "pa_attention_packed: causal attention of packed requests: queries q_start_loc[s] .. of q [T, Hq,\n"
+            "D] over the keys k_start_loc[s] .. of k and v [K, Hkv, D], the last query at the last key; returns\n"
+            "out [T, Hq, D], contiguous. bfloat16; tokens of q, k and v may lie apart; int32 [S + 1] offsets."),
     {"init", init, METH_O, "init(PAError): the class raised for what the library refuses."},
     {nullptr, nullptr, 0, nullptr}};
 
