@@ -353,7 +353,7 @@ def test_malformed_requests_are_reported_and_leave_their_rows(pa):
 
 def test_argument_checks_of_the_binding(pa):
     b = Batch(pa, [40], [1], 4, 1, 64, 16, 4)
-    for kw, err in ((dict(bits=5), ValueError), (dict(bits=8), pa.PAError), (dict(scale=0.0), pa.PAError),
+    for kw, err in ((dict(bits=5), ValueError), (dict(bits=8), ValueError), (dict(bits=0), ValueError), (dict(scale=0.0), pa.PAError),
                     (dict(workspace=b.ws.int()), TypeError), (dict(workspace=b.ws.cpu()), ValueError),
                     (dict(max_query_len=2 ** 40), ValueError)):
         with pytest.raises(err):
