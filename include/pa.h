@@ -546,7 +546,7 @@ int pa_attention_sparse(void* out, const void* q, const void* k_cache, const voi
  * and its rows are left as they are. A key or value row that reads back as NaN gives NaN to the tokens
  * that see it, and to no other. workspace: device, pa_attention_int_workspace_size bytes, 16-byte
  * aligned, no contents needed; calls that may overlap on the GPU need one each. The result depends on
- * nothing but the arguments' contents and the GPU's number of SMs. num_seqs <= 8192
+ * nothing but the arguments' contents and the GPU's number of SMs. num_seqs <= 4096
  * (PA_ERR_UNSUPPORTED).
  * --------------------------------------------------------------------------- */
 int pa_kv_write_int(const void* k, const void* v, int64_t k_stride, int64_t v_stride, pa_dtype dtype,

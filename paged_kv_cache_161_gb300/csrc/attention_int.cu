@@ -18,11 +18,11 @@
 // equal runs; a warp streams its run through a ring of its own in shared memory (bulk copies of the
 // records, one a block where a block is not larger than a unit), and no warp waits for another while
 // it streams. Segments cut between warps leave pieces (m, l, unnormalised output) in the workspace:
-// a CTA joins those of its 16 warps, a second kernel those cut between CTAs.
+// a CTA joins those of its 12 warps, a second kernel those cut between CTAs.
 //
 // Operands (mma.sync m16n8k16, keys as the 16 rows, query rows as the 8 columns): a code under the
-// bits of the f16 1024 is that number plus the code (4-bit codes one nibble higher: 1024 + 16 c), one
-// logic instruction for two. Which dimension sits where in a contraction is free as long as both sides
+// bits of the f16 1024 is that number plus the code (or 1024 + 16 c, a nibble higher), one logic
+// instruction for two, and half an addition more where the 1024 has to go. Which dimension sits where in a contraction is free as long as both sides
 // agree, so a lane takes 16-byte pieces of rows as they lie; so is which key is which row.
 //
 // The kernels start before the one in front of them has ended and read what it wrote behind
@@ -36,12 +36,13 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 12;
 constexpr int kRows = 8;  // query rows of a tile
 constexpr float kNoMax = -1e30f;  // running maximum before any key: finite, so that differences are not NaN
 
+constexpr int kSub = 32;  // keys of a unit worked on together: two tiles of 16, in independent chains
 template <int BITS>
-__host__ __device__ constexpr int unit_keys() { return BITS == 4 ? 32 : 16; }
+__host__ __device__ constexpr int unit_keys() { return BITS == 4 ? 64 : 32; }
 template <int D, int BITS>
 __host__ __device__ constexpr int stage_bytes() { return unit_keys<BITS>() * 2 * (code_row_bytes<D, BITS>() + 4); }
 // a piece: eight rows of D sums, then their maxima and their sums of numerators
@@ -63,7 +64,7 @@ struct IntParams {
   int64_t num_blocks;
   int max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len;
   int num_heads, num_kv_heads, group, block_size;
-  int part;    // keys a bulk copy of codes covers: the largest power of two in block_size, at most a unit
+  int part;    // keys a bulk copy of codes covers: the largest power of two in block_size, at most kSub
   int stages;  // of a warp's ring
   float scale_log2;
 };
@@ -112,6 +113,34 @@ __device__ __forceinline__ Segment segment_of(const IntParams& p, const int* pre
   return g;
 }
 
+// Words of a stage, read as ordinary memory: the compiler may move them between the waits.
+__device__ __forceinline__ uint32_t shared_word(const unsigned char* p) { return *reinterpret_cast<const uint32_t*>(p); }
+template <int N>
+__device__ __forceinline__ void shared_words(const unsigned char* p, uint32_t* w) {
+  if constexpr (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = shared_word(p);
+  }
+}
+
+// One lane of the converged warp (the compiler then knows that a branch on it has one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+// (x & mask) | bits in one instruction: two immediates take two, so `bits` comes in a register.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
@@ -134,51 +163,74 @@ __device__ __forceinline__ int key_of(int r) {
   return (r & 8) + ((r & 1) ? (h ^ 1) + 4 : h);
 }
 
-// Joins `count` pieces of one query row, piece i at pieces + index(i): each lane holds D / 32 elements.
-template <int D>
-struct RowJoin {
-  float m = kNoMax, l = 0.f;
-  float o[D / 32] = {};
-  template <typename F>
-  __device__ __forceinline__ void run(const float* pieces, int row, int lane, int count, F index) {
-    for (int i = 0; i < count; ++i) {
-      const float* p = pieces + int64_t(index(i)) * piece_floats<D>();
-      m = fmaxf(m, p[kRows * D + row]);
-    }
-#pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-      const float* p = pieces + int64_t(index(i)) * piece_floats<D>();
-      const float e = exp2f(p[kRows * D + row] - m);
-      l += e * p[kRows * D + kRows + row];
-      const float* x = p + row * D + lane * (D / 32);
+// Joins `count` pieces (piece 0 number `lead`, piece i number next + 2 i) of rows row0 .. row0 + n - 1
+// (n <= 4) of segment d: into the output, or into the piece `to`. A lane holds D / 32 elements a row; the rows'
+// loads are independent, so their latency is met once.
+template <int D, int KU>
+__device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int row0, int n, int lane, const float* pieces,
+                                          int count, int lead, int next, float* to) {
+  constexpr int E = D / 32;
+  Request r;
+  request_of<KU>(p, d.z, r);
+  const int head = d.w / r.tiles, tile = d.w - head * r.tiles;
+  n = min(n, r.q_len * p.group - tile * kRows - row0);
+  float m[4], l[4], o[4][E];
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) o[k] += e * x[k];
-    }
-  }
-  __device__ __forceinline__ void store_piece(float* p, int row, int lane) const {
-    if (lane == 0) {
-      p[kRows * D + row] = m;
-      p[kRows * D + kRows + row] = l;
-    }
+  for (int i = 0; i < 4; ++i) {
+    m[i] = kNoMax;
+    l[i] = 0.f;
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) p[row * D + lane * (D / 32) + k] = o[k];
+    for (int e = 0; e < E; ++e) o[i][e] = 0.f;
   }
-  __device__ __forceinline__ void store_out(__nv_bfloat16* out, int lane) const {
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    if (D == 128)
-      *reinterpret_cast<uint2*>(out + lane * 4) =
-          make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[D / 32 - 2] * inv, o[D / 32 - 1] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(out + lane * 2) = pack_bf16(o[0] * inv, o[1] * inv);
+#pragma unroll 2
+  for (int k = 0; k < count; ++k) {
+    const float* x = pieces + int64_t(k == 0 ? lead : next + 2 * k) * piece_floats<D>() + row0 * D;
+    const float* ml = x - row0 * D + kRows * D + row0;
+    float mk[4], lk[4], y[4][E];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) {
+        mk[i] = ml[i];
+        lk[i] = ml[kRows + i];
+        if constexpr (E == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(x + i * D + lane * 4);
+          y[i][0] = f.x, y[i][1] = f.y, y[i][E - 2] = f.z, y[i][E - 1] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(x + i * D + lane * 2);
+          y[i][0] = f.x, y[i][1] = f.y;
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) {
+        const float top = fmaxf(m[i], mk[i]), a = exp2f(m[i] - top), b = exp2f(mk[i] - top);
+        m[i] = top;
+        l[i] = l[i] * a + lk[i] * b;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[i][e] = o[i][e] * a + y[i][e] * b;
+      }
   }
-};
-
-// The output row of row `row` of a tile, or null behind the request's last.
-template <int D>
-__device__ __forceinline__ __nv_bfloat16* out_row(const IntParams& p, int s, int head, int tile, int row) {
-  const int q0 = p.qsl[s], rows = (p.qsl[s + 1] - q0) * p.group, r = tile * kRows + row;
-  if (r >= rows) return nullptr;
-  return p.out + (int64_t(q0 + r / p.group) * p.num_heads + head * p.group + r % p.group) * D;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= n) continue;
+    const int row = row0 + i;
+    if (to) {
+      if (lane == 0) {
+        to[kRows * D + row] = m[i];
+        to[kRows * D + kRows + row] = l[i];
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) to[row * D + lane * E + e] = o[i][e];
+    } else {
+      const int rr = tile * kRows + row;
+      __nv_bfloat16* out = p.out + (int64_t(r.q0 + rr / p.group) * p.num_heads + head * p.group + rr % p.group) * D + lane * E;
+      const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+      if constexpr (E == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[i][0] * inv, o[i][1] * inv), pack_bf16(o[i][2] * inv, o[i][3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(out) = pack_bf16(o[i][0] * inv, o[i][1] * inv);
+    }
+  }
 }
 
 template <int D, int BITS>
@@ -187,8 +239,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   constexpr int HALF = STAGE / 2;                   // keys' part of a stage, then the values'
   constexpr int NK = D / 16;                        // contraction steps of q.c, and tiles of 16 value dimensions
   constexpr float kMid = BITS == 4 ? 8.f : 128.f;
-  // the codes in q.c are 64 + c (4 bits, after 1 / 16) or 1024 + c
-  constexpr float kUnscale = BITS == 4 ? 0.0625f : 1.f, kOffset = BITS == 4 ? 64.f : 1024.f;
+  // the codes in q.c are c - 8 (4 bits), or 1024 + c, whose 1024 sum(q) leaves again in fp32
+  constexpr float kKeyMid = BITS == 4 ? 8.f : 0.f, kOffset = BITS == 4 ? 0.f : 1024.f;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int wsum[kWarps];
   __shared__ int4 desc[kWarps * 2];
@@ -198,6 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   const uint32_t bars = smem_u32(smem) + uint32_t(warp * p.stages) * 8u;
   const uint32_t bars_bytes = uint32_t(kWarps * p.stages * 8 + 127) & ~127u;
   const uint32_t ring = smem_u32(smem) + bars_bytes + uint32_t(warp * p.stages) * STAGE;
+  const unsigned char* ring_mem = smem + bars_bytes + warp * p.stages * STAGE;
   int* prefix = reinterpret_cast<int*>(smem + bars_bytes + kWarps * p.stages * STAGE);
   if (lane == 0) {
     for (int i = 0; i < p.stages; ++i) mbar_init(bars + 8u * i, 1);
@@ -242,70 +295,86 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.per = per;
   const int64_t rec_bytes = int64_t(p.block_size) * (ROW + 4);
 
-  // ---- producer: unit i of the run into stage i % stages; the whole warp calls it, in order
+  // ---- producer: the run's units in order, each into the next stage of the ring. The whole warp calls it
+  // with the same values; one lane issues the copies: of every `part` keys the records of K and V, or
+  // their codes and their parameters where a block holds more than that. The block and the offset in it
+  // are stepped along: no division a unit.
   struct {
-    int seg_end = 0, x = 0, units = 0, blocks = 0, b0 = 0, ent = 0, ent_next = 0;
+    int u, seg_end = 0, x = 0, units = 0, blocks = 0, b0 = 0, ent = 0, ent_next = 0;
+    int b = 0, in = 0;  // block and offset of the next piece
+    int stage = 0;
     const int32_t* row = nullptr;
     int64_t head_off = 0;
   } pr;
+  pr.u = u0;
   const bool fused = p.part == p.block_size;  // a record is one copy
-  const int copies = fused ? 2 : 4, which = lane % copies, piece = lane / copies;
+  const uint32_t part_size = uint32_t(p.part) * (ROW + 4);
+  const int64_t block_bytes = int64_t(p.num_kv_heads) * rec_bytes;
   auto entry = [&](int b) { return b < pr.blocks ? pr.row[b] : -1; };
-  auto fill = [&](int i) {
-    const int u = u0 + i;
-    if (u >= pr.seg_end) {
-      const Segment sg = segment_of<KU>(p, prefix, u);
+  auto fill = [&]() {
+    if (pr.u >= pr.seg_end) {
+      const Segment sg = segment_of<KU>(p, prefix, pr.u);
       Request r;
       request_of<KU>(p, sg.s, r);
       // keys the tile's last row sees, and the blocks and units that hold them
       const int last = min((sg.tile * kRows + kRows - 1) / p.group, r.q_len - 1);
       const int n = r.L - r.q_len + last + 1;
       pr.seg_end = sg.end;
-      pr.x = u - sg.begin;
+      pr.x = pr.u - sg.begin;
       pr.units = (n + KU - 1) / KU;
       pr.blocks = (n + p.block_size - 1) / p.block_size;
       pr.row = p.block_table + int64_t(sg.s) * p.max_blocks_per_seq;
       pr.head_off = int64_t(sg.head) * rec_bytes;
-      pr.b0 = pr.x * KU / p.block_size;
+      pr.b = pr.b0 = pr.x * KU / p.block_size;
+      pr.in = pr.x * KU - pr.b * p.block_size;
       pr.ent = entry(pr.b0 + lane);
       pr.ent_next = entry(pr.b0 + 32 + lane);
     }
-    const uint32_t bar = bars + 8u * uint32_t(i % p.stages), dst = ring + uint32_t(i % p.stages) * STAGE;
+    const uint32_t bar = bars + 8u * uint32_t(pr.stage);
+    uint32_t dst = ring + uint32_t(pr.stage) * STAGE, bytes = 0;
     if (pr.x < pr.units) {
-      const int key0 = pr.x * KU, key = key0 + piece * p.part;
-      if (key0 / p.block_size >= pr.b0 + 32) {  // table entries come 32 at a time, a batch ahead
-        pr.b0 += 32;
-        pr.ent = pr.ent_next;
-        pr.ent_next = entry(pr.b0 + 32 + lane);
+      for (int k = 0; k < KU; k += p.part, dst += part_size) {
+        if (pr.b >= pr.blocks) break;  // behind the last key: whatever the stage held
+        if (pr.b >= pr.b0 + 32) {      // table entries come 32 at a time, a batch ahead
+          pr.b0 += 32;
+          pr.ent = pr.ent_next;
+          pr.ent_next = entry(pr.b0 + 32 + lane);
+        }
+        const int block = __shfl_sync(0xffffffffu, pr.ent, pr.b - pr.b0);
+        if (block >= 0 && block < p.num_blocks) {
+          const int64_t off = int64_t(block) * block_bytes + pr.head_off;
+          if (elect_one()) {
+            if (fused) {
+              bulk_g2s(dst, p.k_cache + off, part_size, bar);
+              bulk_g2s(dst + HALF, p.v_cache + off, part_size, bar);
+            } else {
+              const uint32_t codes = uint32_t(p.part) * ROW, params = uint32_t(p.part) * 4;
+              const int64_t c = off + int64_t(pr.in) * ROW, w = off + int64_t(p.block_size) * ROW + int64_t(pr.in) * 4;
+              bulk_g2s(dst, p.k_cache + c, codes, bar);
+              bulk_g2s(dst + codes, p.k_cache + w, params, bar);
+              bulk_g2s(dst + HALF, p.v_cache + c, codes, bar);
+              bulk_g2s(dst + HALF + codes, p.v_cache + w, params, bar);
+            }
+          }
+          bytes += 2 * part_size;
+        } else if (lane == 0) {
+          raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
+        }
+        pr.in += p.part;
+        if (pr.in == p.block_size) {
+          pr.in = 0;
+          ++pr.b;
+        }
       }
-      const int b = key / p.block_size, b_at = b - pr.b0;  // below 64: a unit has at most 9 blocks
-      const int e0 = __shfl_sync(0xffffffffu, pr.ent, b_at & 31), e1 = __shfl_sync(0xffffffffu, pr.ent_next, b_at & 31);
-      const int block = b_at < 32 ? e0 : e1;
-      const bool wanted = piece * p.part < KU && b < pr.blocks;
-      const bool good = wanted && block >= 0 && block < p.num_blocks;
-      if (wanted && !good) raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
-      const bool is_v = which >= copies / 2, params = !fused && (which & 1);
-      const int in = key - b * p.block_size;
-      const uint32_t bytes = uint32_t(p.part) * (fused ? ROW + 4 : params ? 4 : ROW);
-      const uint32_t sum = __reduce_add_sync(0xffffffffu, good ? bytes : 0u);
-      if (lane == 0) mbar_arrive_expect_tx(bar, sum);
-      __syncwarp();
-      if (good) {
-        const unsigned char* src = (is_v ? p.v_cache : p.k_cache) + int64_t(block) * p.num_kv_heads * rec_bytes +
-                                   pr.head_off +
-                                   (params ? int64_t(p.block_size) * ROW + int64_t(in) * 4 : int64_t(in) * ROW);
-        bulk_g2s(dst + (is_v ? HALF : 0) + uint32_t(piece * p.part * (ROW + 4) + (params ? p.part * ROW : 0)), src, bytes,
-                 bar);
-      }
-    } else {
-      if (lane == 0) mbar_arrive(bar);
-      __syncwarp();
     }
+    if (elect_one()) mbar_arrive_expect_tx(bar, bytes);  // (bytes may have arrived before: the phase waits for this)
     ++pr.x;
+    ++pr.u;
+    if (++pr.stage == p.stages) pr.stage = 0;
   };
 
   // ---- where a lane's rows lie in a stage: keys key_of(g), key_of(g + 8) of a tile as rows of K,
-  // keys key_of(2t), (2t + 1), (2t + 8), (2t + 9) as rows of V; later tiles `next` bytes on
+  // keys key_of(2t), (2t + 1), (2t + 8), (2t + 9) as rows of V; the second tile `next` bytes on
   const int part_bytes = p.part * (ROW + 4);
   auto code_at = [&](int key) { return key / p.part * part_bytes + key % p.part * ROW; };
   auto param_at = [&](int key) { return key / p.part * part_bytes + p.part * ROW + key % p.part * 4; };
@@ -321,11 +390,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   const int next_code = p.part >= 32 ? 16 * ROW : 16 / min(p.part, 16) * part_bytes;
   const int next_param = p.part >= 32 ? 64 : next_code;
 
+  uint32_t C;  // two f16 1024s
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(C));
   const int n_run = u1 - u0;
-  int filled = 0;
-  for (; filled < min(p.stages, n_run); ++filled) fill(filled);
+  for (int i = 0; i < min(p.stages, n_run); ++i) fill();
   bool ok = true;
-  int done = 0;
+  int done = 0, stage = 0;
+  uint32_t phase = 0;  // of the next unit's stage
   while (done < n_run && ok) {
     // ---- a segment of the run
     const Segment sg = segment_of<KU>(p, prefix, u0 + done);
@@ -367,7 +438,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
         if (BITS == 4) {  // word k / 2 of the lane's piece: elements (0, 4), (1, 5), then (2, 6), (3, 7)
           const float* e = f + 8 * (k / 2) + 2 * (k & 1);
           qb[k][0] = pack_f16(e[0], e[4]);
-          qb[k][1] = pack_f16(e[1], e[5]);
+          qb[k][1] = pack_f16(e[1] * 0.0625f, e[5] * 0.0625f);  // their codes come 16-fold
         } else {
           qb[k][0] = pack_f16(f[4 * k], f[4 * k + 1]);
           qb[k][1] = pack_f16(f[4 * k + 2], f[4 * k + 3]);
@@ -393,163 +464,158 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     int wexp = 127;
     float wscale = __uint_as_float(254u << 23);
 
-    auto unit = [&](uint32_t st, int key0, auto tail_c) {
+    auto unit = [&](const unsigned char* st, int key0, auto tail_c) {
       constexpr bool kTail = decltype(tail_c)::value;
+      constexpr int TILES = kSub / 16;
+      // ---- q.c of 16 keys x 8 query rows a tile, all of a unit's tiles before their logits: independent chains
+      float s[TILES][4], s1[TILES][4];
+      uint32_t pk[TILES][2], pv[TILES][2];
 #pragma unroll
-      for (int tile = 0; tile < KU / 16; ++tile) {
-        const uint32_t base = st + uint32_t(tile * next_code), pbase = st + uint32_t(tile * next_param);
-        // ---- q.c of 16 keys x 8 query rows
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[2], pv[2];
+      for (int tile = 0; tile < TILES; ++tile) {
+        const unsigned char *base = st + tile * next_code, *pbase = st + tile * next_param;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[tile][i] = s1[tile][i] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          pk[i] = lds32(pbase + par_at[i]);
-          pv[i] = lds32(pbase + HALF + par_at[i]);
+          pk[tile][i] = shared_word(pbase + par_at[i]);
+          pv[tile][i] = shared_word(pbase + HALF + par_at[i]);
         }
         if constexpr (BITS == 4) {
           uint32_t a[2][D / 32];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if constexpr (D == 128) {
-              const uint4 x = lds128(base + k_at[i]);
-              a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
-            } else {
-              const uint2 x = lds64(base + k_at[i]);
-              a[i][0] = x.x, a[i][1] = x.y;
-            }
-          }
-          constexpr uint32_t M = 0x00f000f0u, C = 0x64006400u;
+          for (int i = 0; i < 2; ++i) shared_words<D / 32>(base + k_at[i], a[i]);
+          constexpr uint32_t M = 0x000f000fu, N = 0x00f000f0u;
+          const __half2 low = __half2half2(__float2half_rn(-1032.f)), high = __half2half2(__float2half_rn(-1152.f));
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
+          for (int w = 0; w < D / 32; ++w) {  // c - 8 of even nibbles, 16 (c - 8) of odd ones
             const uint32_t x = a[0][w], y = a[1][w];
-            mma_16816(s, ((x << 4) & M) | C, ((y << 4) & M) | C, (x & M) | C, (y & M) | C, qb[2 * w][0], qb[2 * w][1], true);
-            mma_16816(s1, ((x >> 4) & M) | C, ((y >> 4) & M) | C, ((x >> 8) & M) | C, ((y >> 8) & M) | C, qb[2 * w + 1][0],
-                      qb[2 * w + 1][1], true);
+            mma_16816(s[tile], h2(and_or(x, M, C), low), h2(and_or(y, M, C), low), h2(and_or(x, N, C), high),
+                      h2(and_or(y, N, C), high), qb[2 * w][0], qb[2 * w][1], true);
+            mma_16816(s1[tile], h2(and_or(x >> 8, M, C), low), h2(and_or(y >> 8, M, C), low), h2(and_or(x >> 8, N, C), high),
+                      h2(and_or(y >> 8, N, C), high), qb[2 * w + 1][0], qb[2 * w + 1][1], true);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
-            const uint4 x4 = lds128(base + k_at[0] + 64 * c), y4 = lds128(base + k_at[1] + 64 * c);
-            const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
+            uint32_t x[4], y[4];
+            shared_words<4>(base + k_at[0] + 64 * c, x);
+            shared_words<4>(base + k_at[1] + 64 * c, y);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const uint32_t H = 0x64646464u;
-              mma_16816((w & 1) ? s1 : s, __byte_perm(x[w], H, 0x4140), __byte_perm(y[w], H, 0x4140),
+              mma_16816((w & 1) ? s1[tile] : s[tile], __byte_perm(x[w], H, 0x4140), __byte_perm(y[w], H, 0x4140),
                         __byte_perm(x[w], H, 0x4342), __byte_perm(y[w], H, 0x4342), qb[4 * c + w][0], qb[4 * c + w][1],
                         true);
             }
           }
         }
-        // ---- logits (in powers of two), numerators: [0], [1] key_of(g), [2], [3] key_of(g + 8)
-        float x[4], ws[2], midv[2];
-        bool hidden[4];
+      }
+      // ---- logits (in powers of two), numerators: [0], [1] key_of(g), [2], [3] key_of(g + 8)
+      float x[TILES][4], ws[TILES][2], midv[TILES][2];
+      bool hidden[TILES][4];
+#pragma unroll
+      for (int tile = 0; tile < TILES; ++tile)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int key = key0 + tile * 16 + key_of(g + 8 * i);
-          if (kTail && key >= n_max) pk[i] = pv[i] = 0u;  // a row behind the last: whatever it holds
-          const float lo = param_lo(pk[i]), step = param_step(pk[i]);
-          const float vstep = param_step(pv[i]);
-          midv[i] = fmaf(vstep, kMid, param_lo(pv[i]));
-          ws[i] = vstep;
+          if (kTail && key >= n_max) pk[tile][i] = pv[tile][i] = 0u;  // a row behind the last: whatever it holds
+          const float step = param_step(pk[tile][i]), lo = fmaf(step, kKeyMid, param_lo(pk[tile][i]));
+          ws[tile][i] = param_step(pv[tile][i]);
+          midv[tile][i] = fmaf(ws[tile][i], kMid, param_lo(pv[tile][i]));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float c = fmaf(s[2 * i + h] + s1[2 * i + h], kUnscale, -kOffset * qs[h]);
-            x[2 * i + h] = fmaf(c, step, lo * qs[h]) * fac[h];
-            hidden[2 * i + h] = kTail && key >= lim[h];
-            if (hidden[2 * i + h]) x[2 * i + h] = -INFINITY;
+            const float c = s[tile][2 * i + h] + s1[tile][2 * i + h] - kOffset * qs[h];
+            x[tile][2 * i + h] = fmaf(c, step, lo * qs[h]) * fac[h];
+            hidden[tile][2 * i + h] = kTail && key >= lim[h];
+            if (hidden[tile][2 * i + h]) x[tile][2 * i + h] = -INFINITY;
           }
         }
-        // The reference maximum moves only when a logit passes it by 2^8, the steps' power of two when
-        // one passes it twofold: then, for the whole warp, the sums so far are scaled.
-        const bool move = fmaxf(x[0], x[2]) - m[0] > 8.f || fmaxf(x[1], x[3]) - m[1] > 8.f ||
-                          fmaxf(ws[0], ws[1]) * wscale > 128.f;
-        if (__any_sync(0xffffffffu, move)) {
-          float alpha[2];
+      // The reference maximum moves only when a logit passes it by 2^8, the steps' power of two when
+      // one passes it twofold: then, for the whole warp, the sums so far are scaled.
+      float top[2] = {fmaxf(x[0][0], x[0][2]), fmaxf(x[0][1], x[0][3])}, big = fmaxf(ws[0][0], ws[0][1]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float top = fmaxf(x[h], x[2 + h]);
+      for (int tile = 1; tile < TILES; ++tile) {
+        top[0] = fmax3(top[0], x[tile][0], x[tile][2]);
+        top[1] = fmax3(top[1], x[tile][1], x[tile][3]);
+        big = fmax3(big, ws[tile][0], ws[tile][1]);
+      }
+      if (__any_sync(0xffffffffu, top[0] - m[0] > 8.f || top[1] - m[1] > 8.f || big * wscale > 128.f)) {
+        float alpha[2];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if (!(top - m[h] > 8.f)) top = m[h];
-            alpha[h] = exp2f(m[h] - top);
-            m[h] = top;
-            l[h] *= alpha[h];
-            mid[h] *= alpha[h];
-          }
-          // NaN steps (of rows that hold NaN) do not count
-          const uint32_t big = __float_as_uint(fmaxf(ws[0], ws[1]));
-          const uint32_t top = __reduce_max_sync(0xffffffffu, big <= 0x7f800000u ? big : 0u);
-          const int want = min(127, 6 - (int(top >> 23) - 126));
-          float beta = 1.f;
-          if (want < wexp) {
-            beta = exp2f(float(want - wexp));
-            wexp = want;
-            wscale = __uint_as_float(uint32_t(want + 127) << 23);
-          }
+        for (int h = 0; h < 2; ++h) {
+          float up = top[h];
 #pragma unroll
-          for (int i = 0; i < NK; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e & 1] * beta;
+          for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
+          if (!(up - m[h] > 8.f)) up = m[h];
+          alpha[h] = exp2f(m[h] - up);
+          m[h] = up;
+          l[h] *= alpha[h];
+          mid[h] *= alpha[h];
         }
-        uint32_t pb[2];
+        // NaN steps (of rows that hold NaN) do not count
+        const uint32_t bits = __float_as_uint(big);
+        const uint32_t most = __reduce_max_sync(0xffffffffu, bits <= 0x7f800000u ? bits : 0u);
+        const int want = min(127, 6 - (int(most >> 23) - 126));
+        float beta = 1.f;
+        if (want < wexp) {
+          beta = exp2f(float(want - wexp));
+          wexp = want;
+          wscale = __uint_as_float(uint32_t(want + 127) << 23);
+        }
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e & 1] * beta;
+      }
+      uint32_t pb[TILES][2];
+#pragma unroll
+      for (int tile = 0; tile < TILES; ++tile)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float wi = ws[i] * wscale;
+          const float wi = ws[tile][i] * wscale;
           float w[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float e = ex2_ftz(x[2 * i + h] - m[h]);
+            const float e = ex2_ftz(x[tile][2 * i + h] - m[h]);
             l[h] += e;
             w[h] = e * wi;
-            if (hidden[2 * i + h]) {
+            if (hidden[tile][2 * i + h]) {
               w[h] = 0.f;  // not 0 * NaN
             } else {
-              mid[h] = fmaf(e, midv[i], mid[h]);
+              mid[h] = fmaf(e, midv[tile][i], mid[h]);
             }
           }
-          pb[i] = movm(pack_f16(w[0], w[1]));
+          pb[tile][i] = movm(pack_f16(w[0], w[1]));
         }
-        // ---- 16 value dimensions x 8 query rows a step: rows of the tile of codes - mid, dimensions
-        // (D / 8) g + 2 i in rows 0 .. 7 and the next in rows 8 .. 15
+      // ---- 16 value dimensions x 8 query rows a step: rows of the tile of codes - mid, dimensions
+      // (D / 8) g + 2 i in rows 0 .. 7 and the next in rows 8 .. 15
+#pragma unroll
+      for (int tile = 0; tile < TILES; ++tile) {
+        const unsigned char* base = st + tile * next_code;
         if constexpr (BITS == 4) {
           const __half2 low = __half2half2(__float2half_rn(-1032.f)), high = __half2half2(__float2half_rn(-72.f)),
                         six = __half2half2(__float2half_rn(0.0625f));
           uint32_t v[4][D / 64];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (D == 128) {
-              const uint2 y = lds64(base + v_at[i]);
-              v[i][0] = y.x, v[i][1] = y.y;
-            } else {
-              v[i][0] = lds32(base + v_at[i]);
-            }
-          }
-          constexpr uint32_t M = 0x000f000fu, N = 0x00f000f0u, C = 0x64006400u;
+          for (int i = 0; i < 4; ++i) shared_words<D / 64>(base + v_at[i], v[i]);
+          constexpr uint32_t M = 0x000f000fu, N = 0x00f000f0u;
 #pragma unroll
           for (int w = 0; w < D / 64; ++w)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {  // elements 0 .. 3, 4 .. 7 of the words
               const uint32_t sel = half ? 0x7632 : 0x5410;
               const uint32_t a = __byte_perm(v[0][w], v[1][w], sel), b = __byte_perm(v[2][w], v[3][w], sel);
-              mma_16816(o[4 * w + 2 * half], h2((a & M) | C, low), h2((a & N) | C, six, high), h2((b & M) | C, low),
-                        h2((b & N) | C, six, high), pb[0], pb[1], true);
-              mma_16816(o[4 * w + 2 * half + 1], h2(((a >> 8) & M) | C, low), h2(((a >> 8) & N) | C, six, high),
-                        h2(((b >> 8) & M) | C, low), h2(((b >> 8) & N) | C, six, high), pb[0], pb[1], true);
+              mma_16816(o[4 * w + 2 * half], h2(and_or(a, M, C), low), h2(and_or(a, N, C), six, high), h2(and_or(b, M, C), low),
+                        h2(and_or(b, N, C), six, high), pb[tile][0], pb[tile][1], true);
+              mma_16816(o[4 * w + 2 * half + 1], h2(and_or(a >> 8, M, C), low), h2(and_or(a >> 8, N, C), six, high),
+                        h2(and_or(b >> 8, M, C), low), h2(and_or(b >> 8, N, C), six, high), pb[tile][0], pb[tile][1], true);
             }
         } else {
           const __half2 sub = __half2half2(__float2half_rn(-1152.f));
           const uint32_t H = 0x64646464u;
           uint32_t v[4][D / 32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (D == 128) {
-              const uint4 y = lds128(base + v_at[i]);
-              v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
-            } else {
-              const uint2 y = lds64(base + v_at[i]);
-              v[i][0] = y.x, v[i][1] = y.y;
-            }
-          }
+          for (int i = 0; i < 4; ++i) shared_words<D / 32>(base + v_at[i], v[i]);
 #pragma unroll
           for (int w = 0; w < D / 32; ++w)
 #pragma unroll
@@ -557,30 +623,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
               const uint32_t sel = half ? 0x7362 : 0x5140;
               const uint32_t a = __byte_perm(v[0][w], v[1][w], sel), b = __byte_perm(v[2][w], v[3][w], sel);
               mma_16816(o[2 * w + half], h2(__byte_perm(a, H, 0x4140), sub), h2(__byte_perm(a, H, 0x4342), sub),
-                        h2(__byte_perm(b, H, 0x4140), sub), h2(__byte_perm(b, H, 0x4342), sub), pb[0], pb[1], true);
+                        h2(__byte_perm(b, H, 0x4140), sub), h2(__byte_perm(b, H, 0x4342), sub), pb[tile][0], pb[tile][1], true);
             }
         }
       }
     };
 
     for (int x = x0; x < x1; ++x, ++done) {
-      const uint32_t bar = bars + 8u * uint32_t(done % p.stages);
-      if (!__all_sync(0xffffffffu, mbar_wait(bar, uint32_t(done / p.stages) & 1u))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8u * uint32_t(stage), phase))) {
         ok = false;
         break;
       }
       const int key0 = x * KU;
-      const uint32_t st = ring + uint32_t(done % p.stages) * STAGE;
-      if (key0 + KU <= n_min) {
-        unit(st, key0, std::false_type{});
-      } else if (key0 < n_max) {
-        unit(st, key0, std::true_type{});
+      const unsigned char* st = ring_mem + stage * STAGE;
+#pragma unroll 1
+      for (int k = 0; k < KU; k += kSub) {
+        if (key0 + k + kSub <= n_min) {
+          unit(st + k * (ROW + 4), key0 + k, std::false_type{});
+        } else if (key0 + k < n_max) {
+          unit(st + k * (ROW + 4), key0 + k, std::true_type{});
+        }
       }
       __syncwarp();
-      if (filled < n_run) {
-        fill(filled);
-        ++filled;
-      }
+      if (pr.u < u1) fill();
+      if (++stage == p.stages) stage = 0, phase ^= 1u;
     }
     if (!ok) break;
     // ---- the segment's end in this run: sums over the lanes that share a query row, then out or a piece
@@ -607,7 +673,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
       }
       if (whole) {
         const float inv = l[h] > 0.f ? 1.f / l[h] : (l[h] == 0.f ? 0.f : l[h]);
-        __nv_bfloat16* dst = out_row<D>(p, sg.s, sg.head, sg.tile, row) + g * (D / 8);
+        const int rr = sg.tile * kRows + row;
+        __nv_bfloat16* dst =
+            p.out + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) f[i] *= inv;
 #pragma unroll
@@ -627,45 +695,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   }
   if (!ok) {  // a copy did not arrive in time: tell, and wait for those under way before leaving
     if (lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
-    for (int i = done; i < filled; ++i) mbar_wait(bars + 8u * uint32_t(i % p.stages), uint32_t(i / p.stages) & 1u);
+    for (int i = done; i < pr.u - u0; ++i) {
+      mbar_wait(bars + 8u * uint32_t(stage), phase);
+      if (++stage == p.stages) stage = 0, phase ^= 1u;
+    }
   }
   __syncthreads();
 
-  // ---- pieces of segments cut between this CTA's warps, or between CTAs
+  // ---- pieces of segments cut between this CTA's warps, or between CTAs. A leader is a CTA's first
+  // piece of a segment; the leaders' rows are dealt to the warps, as many at once as leave no warp idle.
   const int c0 = first(w0), c1 = first(w0 + kWarps);
   float* cta_pieces = p.pieces + int64_t(num_warps) * 2 * piece_floats<D>();
-  if (threadIdx.x < 2) {
+  const int4 mine = lane < kWarps * 2 ? desc[lane] : make_int4(-1, 0, 0, 0);
+  if (warp == 0) {
     // slot 0: a segment from before c0, or one from c0 to past c1; slot 1: one that goes on behind c1
-    int4 d = make_int4(-1, 0, 0, 0);
-    if (c0 < c1) {
-      if (threadIdx.x == 0) {
-        const int4 a = desc[0];
-        if (a.x >= 0 && (a.x < c0 || a.y > c1)) d = a;
-      } else {
-        for (int i = 0; i < kWarps * 2; ++i)
-          if (desc[i].x > c0 && desc[i].y > c1) d = desc[i];
-      }
-    }
-    p.descs[blockIdx.x * 2 + threadIdx.x] = d;
+    const unsigned tail = __ballot_sync(0xffffffffu, mine.x > c0 && mine.y > c1);
+    if (lane == (tail ? __ffs(tail) - 1 : 1)) p.descs[blockIdx.x * 2 + 1] = tail ? mine : make_int4(-1, 0, 0, 0);
+    if (lane == 0) p.descs[blockIdx.x * 2] = mine.x >= 0 && (mine.x < c0 || mine.y > c1) ? mine : make_int4(-1, 0, 0, 0);
   }
-  // leaders: a CTA's first piece of a segment; a task is one of its rows
-  for (int task = warp; task < kWarps * 2 * kRows; task += kWarps) {
-    const int at = task / kRows, row = task % kRows, w = at >> 1;
+  const unsigned leaders =
+      __ballot_sync(0xffffffffu, mine.x >= 0 && ((lane & 1) || lane == 0 || mine.x == first(w0 + (lane >> 1))));
+  const int num = __popc(leaders);
+  const int at_once = num * kRows <= kWarps ? 1 : num * (kRows / 2) <= kWarps ? 2 : 4;
+  for (int task = warp; task < num * (kRows / at_once); task += kWarps) {
+    const int at = __fns(leaders, 0, task / (kRows / at_once) + 1), row0 = task % (kRows / at_once) * at_once, w = at >> 1;
     const int4 d = desc[at];
-    if (d.x < 0 || !((at & 1) || w == 0 || d.x == first(w0 + w))) continue;
-    Request r;
-    request_of<KU>(p, d.z, r);
-    const int head = d.w / r.tiles, tile = d.w - head * r.tiles;
-    __nv_bfloat16* out = out_row<D>(p, d.z, head, tile, row);
-    if (!out) continue;
     int count = 1;
     while (w + count < kWarps && first(w0 + w + count) < d.y) ++count;
-    RowJoin<D> j;
-    j.run(p.pieces, row, lane, count, [&](int i) { return i == 0 ? w0 * 2 + at : (w0 + w + i) * 2; });
-    if (d.x >= c0 && d.y <= c1)
-      j.store_out(out, lane);
-    else
-      j.store_piece(cta_pieces + int64_t(blockIdx.x * 2 + (d.x <= c0 ? 0 : 1)) * piece_floats<D>(), row, lane);
+    float* whole = d.x >= c0 && d.y <= c1 ? nullptr
+                                          : cta_pieces + int64_t(blockIdx.x * 2 + (d.x <= c0 ? 0 : 1)) * piece_floats<D>();
+    join_rows<D, KU>(p, d, row0, at_once, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
   }
 }
 
@@ -681,16 +740,9 @@ __global__ void __launch_bounds__(kRows * 32) attention_int_join_kernel(const In
   for (int slot = 0; slot < 2; ++slot) {
     const int4 d = p.descs[c * 2 + slot];
     if (d.x < 0 || (slot == 0 && d.x != c * run)) continue;
-    Request r;
-    request_of<KU>(p, d.z, r);
-    const int head = d.w / r.tiles, tile = d.w - head * r.tiles;
-    __nv_bfloat16* out = out_row<D>(p, d.z, head, tile, row);
-    if (!out) continue;
     int count = 1;
     while (c + count < num_ctas && (c + count) * run < d.y) ++count;
-    RowJoin<D> j;
-    j.run(pieces, row, lane, count, [&](int i) { return i == 0 ? c * 2 + slot : (c + i) * 2; });
-    j.store_out(out, lane);
+    join_rows<D, KU>(p, d, row, 1, lane, pieces, count, c * 2 + slot, c * 2, nullptr);
   }
 }
 
@@ -756,9 +808,8 @@ cudaError_t launch_attention_int(const AttnIntArgs& a, cudaStream_t stream) {
   p.group = a.num_heads / a.num_kv_heads;
   p.block_size = a.block_size;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  const int ku = a.bits == 4 ? unit_keys<4>() : unit_keys<8>();
   p.part = a.block_size & -a.block_size;
-  if (p.part > ku) p.part = ku;
+  if (p.part > kSub) p.part = kSub;
   if (a.bits == 4) return a.head_dim == 64 ? run_int<64, 4>(p, a, stream) : run_int<128, 4>(p, a, stream);
   return a.head_dim == 64 ? run_int<64, 8>(p, a, stream) : run_int<128, 8>(p, a, stream);
 }

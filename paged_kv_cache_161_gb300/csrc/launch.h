@@ -232,7 +232,7 @@ cudaError_t launch_kv_read_int(const KvIntArgs& a, void* k_out, void* v_out, con
                                const int32_t* seq_lens, const int32_t* row_start_loc, int num_seqs, int64_t num_rows,
                                cudaStream_t stream);
 
-constexpr int kIntMaxSeqs = 8192;  // requests of a pa_attention_int call
+constexpr int kIntMaxSeqs = 4096;  // requests of a pa_attention_int call
 struct AttnIntArgs {
   void* out;
   const void* q;

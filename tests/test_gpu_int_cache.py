@@ -2,9 +2,10 @@
 (the definition names every rounding); attention over the codes against float64.
 
 Attention's tolerance, from the arithmetic. Query rows enter as f16 scaled by a power of two: exact but for
-elements 2^-25 of the row's largest. A logit is step (q.(off + c) - off sum q) + lo sum q in fp32, sums of
-at most D / 16 + 2 products of 16 terms: each term and each sum within 2^-23 of sum |q| (off + N) step,
-so dl <= scale (D + 8) 2^-23 sum |q| ((off + N) step + |lo|), off + N = 80 (4 bits) or 1280. The numerators
+elements 2^-25 of the row's largest. A logit is, in fp32, step q.(c - 8) + (lo + 8 step) sum q (4 bits), or
+step (q.(1024 + c) - 1024 sum q) + lo sum q (8 bits), sums of D terms: each term and each sum within
+2^-23 of sum |q| (off step + |lo|), off = 16 or 1280 (what multiplies step at most), so
+dl <= scale (D + 8) 2^-23 sum |q| (off step + |lo|). The numerators
 have that relative error, ex2's 2^-22 and, times the value's step, f16's half step 2^-11 (what falls
 under f16's range: 2^-31 of the largest step a key). A value enters as mid + step (c - mid), both parts within
 mag = sum_j w_j (|mid_j| + step_j N / 2). fp32 sums over the keys: 2^-23 each, 2^-18 for thousands. One
@@ -219,7 +220,7 @@ class Batch:
     def check(self, requests=None):
         assert self.pa.read_device_errors() == 0
         kc, vc, q, out = self.kc.cpu().numpy(), self.vc.cpu().numpy(), _f64(self.q), _f64(self.out)
-        N, off = 2 ** self.bits - 1, 80 if self.bits == 4 else 1280
+        N, off = 2 ** self.bits - 1, 16 if self.bits == 4 else 1280
         for s in range(len(self.lens)) if requests is None else requests:
             a, b, L = self.qsl[s], self.qsl[s + 1], self.lens[s]
             if a == b:

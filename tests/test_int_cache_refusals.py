@@ -57,7 +57,7 @@ def test_attention_int():
         (9, -1, INVALID), (10, -1, INVALID), (10, 101, INVALID), (11, -1, INVALID), (12, 0, INVALID), (12, 30, INVALID),
         (13, 0, INVALID), (14, 32, UNSUPPORTED), (15, 18, UNSUPPORTED), (16, 0, INVALID), (17, 0.0, INVALID),
         (17, -1.0, INVALID), (17, inf, INVALID), (17, nan, INVALID), (18, 6, UNSUPPORTED), (19, None, WORKSPACE),
-        (19, _at(8) + 8, WORKSPACE), (0, _at(2) + 4096, INVALID), (8, 8193, UNSUPPORTED), (9, 2**31 - 1, UNSUPPORTED),
+        (19, _at(8) + 8, WORKSPACE), (0, _at(2) + 4096, INVALID), (8, 4097, UNSUPPORTED), (9, 2**31 - 1, UNSUPPORTED),
         (8, 0, OK), (9, 0, OK),
     ])
     a = list(good)
