@@ -22,7 +22,7 @@
 //
 // Operands (mma.sync m16n8k16, keys as the 16 rows, query rows as the 8 columns): a code under the
 // bits of the f16 1024 is that number plus the code (or 1024 + 16 c, a nibble higher), one logic
-// instruction for two, and half an addition more where the 1024 has to go. Which dimension sits where in a contraction is free as long as both sides
+// instruction for two, and half an addition more where the 1024 has to go before the products. Which dimension sits where in a contraction is free as long as both sides
 // agree, so a lane takes 16-byte pieces of rows as they lie; so is which key is which row.
 //
 // The kernels start before the one in front of them has ended and read what it wrote behind
@@ -40,9 +40,14 @@ constexpr int kWarps = 12;
 constexpr int kRows = 8;  // query rows of a tile
 constexpr float kNoMax = -1e30f;  // running maximum before any key: finite, so that differences are not NaN
 
-constexpr int kSub = 32;  // keys of a unit worked on together: two tiles of 16, in independent chains
+constexpr int kPart = 32;  // keys of a bulk copy at most
 template <int BITS>
 __host__ __device__ constexpr int unit_keys() { return BITS == 4 ? 64 : 32; }
+// A segment's start in units of keys, by the time it takes: DESC_START
+template <int KU>
+__host__ __device__ constexpr int start_units() { return KU == 64 ? 1 : 2; }
+template <int D>
+__host__ __device__ constexpr int num_stages() { return D == 128 ? 2 : 3; }  // of a warp's ring
 template <int D, int BITS>
 __host__ __device__ constexpr int stage_bytes() { return unit_keys<BITS>() * 2 * (code_row_bytes<D, BITS>() + 4); }
 // a piece: eight rows of D sums, then their maxima and their sums of numerators
@@ -60,18 +65,19 @@ struct IntParams {
   unsigned int* err;
   float* pieces;  // [grid * kWarps * 2] of the warps, then [grid * 2] of the CTAs
   int4* descs;    // [grid * 2]: a CTA's pieces, {first unit of the segment or -1, its last + 1, request, segment}
-  int* per;       // units a warp
+  int* total;     // units of the call
   int64_t num_blocks;
   int max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len;
   int num_heads, num_kv_heads, group, block_size;
-  int part;    // keys a bulk copy of codes covers: the largest power of two in block_size, at most kSub
-  int stages;  // of a warp's ring
+  int part;    // keys a bulk copy of codes covers: the largest power of two in block_size, at most kPart
   float scale_log2;
 };
 
-// What a request contributes: `tiles` tiles of 8 rows, each over `units` units a KV head.
+// What a request contributes: `tiles` tiles of 8 rows, each a segment of `span` units a KV head: kStart
+// that stand for a segment's start (its queries, table, sums: none of them is work of its own), then
+// those of its keys.
 struct Request {
-  int q0, q_len, L, tiles, units;
+  int q0, q_len, L, tiles, span;
 };
 
 template <int KU>
@@ -79,13 +85,13 @@ __device__ __forceinline__ bool request_of(const IntParams& p, int s, Request& r
   r.q0 = p.qsl[s];
   const int q1 = p.qsl[s + 1];
   r.L = p.seq_lens[s];
-  r.tiles = r.units = r.q_len = 0;
+  r.tiles = r.span = r.q_len = 0;
   if (r.q0 < 0 || q1 < r.q0 || q1 > p.num_tokens) return false;
   r.q_len = q1 - r.q0;
   if (r.q_len == 0) return true;
   if (r.q_len > p.max_query_len || r.q_len > r.L || r.L > p.max_seq_len) return false;
   r.tiles = int((int64_t(r.q_len) * p.group + kRows - 1) / kRows);
-  r.units = (r.L + KU - 1) / KU;
+  r.span = start_units<KU>() + (r.L + KU - 1) / KU;
   return true;
 }
 
@@ -103,13 +109,13 @@ __device__ __forceinline__ Segment segment_of(const IntParams& p, const int* pre
   }
   Request r;
   request_of<KU>(p, s, r);
-  const int seg = (u - prefix[s]) / r.units;
+  const int seg = (u - prefix[s]) / r.span;
   Segment g;
   g.s = s;
   g.head = seg / r.tiles;
   g.tile = seg - g.head * r.tiles;  // tiles fastest: neighbours read the same keys
-  g.begin = prefix[s] + seg * r.units;
-  g.end = g.begin + r.units;
+  g.begin = prefix[s] + seg * r.span;
+  g.end = g.begin + r.span;
   return g;
 }
 
@@ -128,12 +134,23 @@ __device__ __forceinline__ void shared_words(const unsigned char* p, uint32_t* w
   }
 }
 
-// One lane of the converged warp (the compiler then knows that a branch on it has one).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-  return ok != 0;
+// The first unit of warp w: runs of two sizes, one unit apart, spread evenly over the grid; with fewer units
+// than warps, one for each of the first warps (only runs behind the last are empty: the joins rely on it).
+struct Deal {
+  int each, rest, warps;
+  __device__ __forceinline__ Deal(int total, int n) : each(total / n), rest(total % n), warps(n) {}
+  __device__ __forceinline__ int operator()(int w) const {
+    return each == 0 ? min(w, rest) : w * each + int(uint32_t(w) * uint32_t(rest) / uint32_t(warps));
+  }
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const unsigned char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the last N groups have landed
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // (x & mask) | bits in one instruction: two immediates take two, so `bits` comes in a register.
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
   uint32_t d;
@@ -203,6 +220,7 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < n) {
+        if (lk[i] == 0.f) continue;  // an empty piece: its sums were never written
         const float top = fmaxf(m[i], mk[i]), a = exp2f(m[i] - top), b = exp2f(mk[i] - top);
         m[i] = top;
         l[i] = l[i] * a + lk[i] * b;
@@ -233,29 +251,24 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
   }
 }
 
-template <int D, int BITS>
+// B16: blocks of 16 tokens, whose copies are all of one known size (256 requests of 1024 keys, 4 bits: B16_FIGURES)
+template <int D, int BITS, bool B16>
 __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const IntParams p) {
-  constexpr int KU = unit_keys<BITS>(), ROW = code_row_bytes<D, BITS>(), STAGE = stage_bytes<D, BITS>();
+  constexpr int KU = unit_keys<BITS>(), ROW = code_row_bytes<D, BITS>(), STAGE = stage_bytes<D, BITS>(), STAGES = num_stages<D>();
   constexpr int HALF = STAGE / 2;                   // keys' part of a stage, then the values'
   constexpr int NK = D / 16;                        // contraction steps of q.c, and tiles of 16 value dimensions
   constexpr float kMid = BITS == 4 ? 8.f : 128.f;
-  // the codes in q.c are c - 8 (4 bits), or 1024 + c, whose 1024 sum(q) leaves again in fp32
-  constexpr float kKeyMid = BITS == 4 ? 8.f : 0.f, kOffset = BITS == 4 ? 0.f : 1024.f;
+  // the codes in q.c are c (4 bits, even nibbles), 64 + c (odd ones), or 1024 + c: 64 or 1024 times the sum of
+  // their q leaves again in fp32
+  constexpr float kOffset = BITS == 4 ? 64.f : 1024.f;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int wsum[kWarps];
   __shared__ int4 desc[kWarps * 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int S = p.num_seqs;
-  // shared memory: barriers, rings, the units' prefix over the requests
-  const uint32_t bars = smem_u32(smem) + uint32_t(warp * p.stages) * 8u;
-  const uint32_t bars_bytes = uint32_t(kWarps * p.stages * 8 + 127) & ~127u;
-  const uint32_t ring = smem_u32(smem) + bars_bytes + uint32_t(warp * p.stages) * STAGE;
-  const unsigned char* ring_mem = smem + bars_bytes + warp * p.stages * STAGE;
-  int* prefix = reinterpret_cast<int*>(smem + bars_bytes + kWarps * p.stages * STAGE);
-  if (lane == 0) {
-    for (int i = 0; i < p.stages; ++i) mbar_init(bars + 8u * i, 1);
-    fence_mbar_init();
-  }
+  // shared memory: the warps' rings, the units' prefix over the requests
+  unsigned char* ring = smem + warp * STAGES * STAGE;
+  int* prefix = reinterpret_cast<int*>(smem + kWarps * STAGES * STAGE);
   if (threadIdx.x < kWarps * 2) desc[threadIdx.x] = make_int4(-1, 0, 0, 0);
   griddep_wait();
 
@@ -267,7 +280,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     if (s < S) {
       Request r;
       if (!request_of<KU>(p, s, r) && blockIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_RANGE);
-      x = r.tiles * r.units * p.num_kv_heads;
+      x = r.tiles * r.span * p.num_kv_heads;
     }
     int inc = x;
 #pragma unroll
@@ -288,17 +301,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     __syncthreads();
   }
   const int num_warps = gridDim.x * kWarps;
-  const int per = (total + num_warps - 1) / num_warps;
   const int w0 = blockIdx.x * kWarps;
-  auto first = [&](int w) { return int(min(int64_t(w) * per, int64_t(total))); };
+  const Deal first(total, num_warps);
   const int u0 = first(w0 + warp), u1 = first(w0 + warp + 1);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.per = per;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.total = total;
   const int64_t rec_bytes = int64_t(p.block_size) * (ROW + 4);
 
-  // ---- producer: the run's units in order, each into the next stage of the ring. The whole warp calls it
-  // with the same values; one lane issues the copies: of every `part` keys the records of K and V, or
-  // their codes and their parameters where a block holds more than that. The block and the offset in it
-  // are stepped along: no division a unit.
+  // ---- the run's units of keys in order, each into the next stage of the ring: asynchronous copies of 16
+  // bytes a lane, one group a unit (an empty one behind the last). Every `part` keys come as the records of K
+  // and V, or as their codes and parameters where a block holds more than that. Block and offset are
+  // stepped along: no division a unit. (One bulk copy a record instead took 25 to 45 instructions each for
+  // its uniform operands, a fifth of all.)
   struct {
     int u, seg_end = 0, x = 0, units = 0, blocks = 0, b0 = 0, ent = 0, ent_next = 0;
     int b = 0, in = 0;  // block and offset of the next piece
@@ -307,77 +320,106 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     int64_t head_off = 0;
   } pr;
   pr.u = u0;
-  const bool fused = p.part == p.block_size;  // a record is one copy
-  const uint32_t part_size = uint32_t(p.part) * (ROW + 4);
+  const bool fused = p.part == p.block_size;  // a record is one run of bytes
+  const int part = B16 ? 16 : p.part, part_bytes = part * (ROW + 4);
   const int64_t block_bytes = int64_t(p.num_kv_heads) * rec_bytes;
   auto entry = [&](int b) { return b < pr.blocks ? pr.row[b] : -1; };
-  auto fill = [&]() {
-    if (pr.u >= pr.seg_end) {
-      const Segment sg = segment_of<KU>(p, prefix, pr.u);
-      Request r;
-      request_of<KU>(p, sg.s, r);
-      // keys the tile's last row sees, and the blocks and units that hold them
-      const int last = min((sg.tile * kRows + kRows - 1) / p.group, r.q_len - 1);
-      const int n = r.L - r.q_len + last + 1;
-      pr.seg_end = sg.end;
-      pr.x = pr.u - sg.begin;
-      pr.units = (n + KU - 1) / KU;
-      pr.blocks = (n + p.block_size - 1) / p.block_size;
-      pr.row = p.block_table + int64_t(sg.s) * p.max_blocks_per_seq;
-      pr.head_off = int64_t(sg.head) * rec_bytes;
-      pr.b = pr.b0 = pr.x * KU / p.block_size;
-      pr.in = pr.x * KU - pr.b * p.block_size;
-      pr.ent = entry(pr.b0 + lane);
-      pr.ent_next = entry(pr.b0 + 32 + lane);
+  // the next 32 table entries, read a batch ahead; -1 for a block that is not there
+  auto next_entries = [&](int b0) {
+    pr.b0 = b0;
+    pr.ent = pr.ent_next;
+    pr.ent_next = entry(b0 + 32 + lane);
+    if (b0 + lane < pr.blocks && (pr.ent < 0 || pr.ent >= p.num_blocks)) {
+      raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
+      pr.ent = -1;
     }
-    const uint32_t bar = bars + 8u * uint32_t(pr.stage);
-    uint32_t dst = ring + uint32_t(pr.stage) * STAGE, bytes = 0;
-    if (pr.x < pr.units) {
-      for (int k = 0; k < KU; k += p.part, dst += part_size) {
-        if (pr.b >= pr.blocks) break;  // behind the last key: whatever the stage held
-        if (pr.b >= pr.b0 + 32) {      // table entries come 32 at a time, a batch ahead
-          pr.b0 += 32;
-          pr.ent = pr.ent_next;
-          pr.ent_next = entry(pr.b0 + 32 + lane);
-        }
-        const int block = __shfl_sync(0xffffffffu, pr.ent, pr.b - pr.b0);
-        if (block >= 0 && block < p.num_blocks) {
-          const int64_t off = int64_t(block) * block_bytes + pr.head_off;
-          if (elect_one()) {
-            if (fused) {
-              bulk_g2s(dst, p.k_cache + off, part_size, bar);
-              bulk_g2s(dst + HALF, p.v_cache + off, part_size, bar);
-            } else {
-              const uint32_t codes = uint32_t(p.part) * ROW, params = uint32_t(p.part) * 4;
-              const int64_t c = off + int64_t(pr.in) * ROW, w = off + int64_t(p.block_size) * ROW + int64_t(pr.in) * 4;
-              bulk_g2s(dst, p.k_cache + c, codes, bar);
-              bulk_g2s(dst + codes, p.k_cache + w, params, bar);
-              bulk_g2s(dst + HALF, p.v_cache + c, codes, bar);
-              bulk_g2s(dst + HALF + codes, p.v_cache + w, params, bar);
-            }
-          }
-          bytes += 2 * part_size;
-        } else if (lane == 0) {
-          raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
-        }
-        pr.in += p.part;
-        if (pr.in == p.block_size) {
-          pr.in = 0;
-          ++pr.b;
-        }
+  };
+  auto locate = [&]() {  // the segment of pr.u, past its start; false: the run ends before its keys
+    const Segment sg = segment_of<KU>(p, prefix, pr.u);
+    pr.u = max(pr.u, sg.begin + start_units<KU>());
+    if (pr.u >= u1) return false;
+    Request r;
+    request_of<KU>(p, sg.s, r);
+    // keys the tile's last row sees, and the blocks and units that hold them
+    const int rows = min(kRows, r.q_len * p.group - sg.tile * kRows), last = (sg.tile * kRows + rows - 1) / p.group;
+    const int n = r.L - r.q_len + last + 1;
+    pr.seg_end = sg.end;
+    pr.x = pr.u - sg.begin - start_units<KU>();
+    pr.units = (n + KU - 1) / KU;
+    pr.blocks = (n + p.block_size - 1) / p.block_size;
+    pr.row = p.block_table + int64_t(sg.s) * p.max_blocks_per_seq;
+    pr.head_off = int64_t(sg.head) * rec_bytes;
+    pr.b = pr.x * KU / p.block_size;
+    pr.in = pr.x * KU - pr.b * p.block_size;
+    pr.ent_next = entry(pr.b + lane);
+    next_entries(pr.b);
+    const int rr = sg.tile * kRows + min(g, rows - 1);  // the queries, read when the segment's turn comes
+    prefetch_l2(p.q + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D + t * (D / 4));
+    return true;
+  };
+  // bytes (a multiple of 16, at most a piece's) of K and of V, 512 a step, of which all but the last are full
+  auto copy = [&](unsigned char* dst, const unsigned char* k_src, const unsigned char* v_src, int bytes) {
+    constexpr int STEPS = (kPart * (ROW + 4) + 511) / 512;
+    const uint32_t to = smem_u32(dst) + lane * 16;
+    k_src += lane * 16;
+    v_src += lane * 16;
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      if (j * 512 >= bytes) break;
+      if (j * 512 + lane * 16 < bytes) {
+        copy16(to + j * 512, k_src + j * 512);
+        copy16(to + HALF + j * 512, v_src + j * 512);
       }
     }
-    if (elect_one()) mbar_arrive_expect_tx(bar, bytes);  // (bytes may have arrived before: the phase waits for this)
-    ++pr.x;
-    ++pr.u;
-    if (++pr.stage == p.stages) pr.stage = 0;
+  };
+  auto fill = [&]() {
+    if (pr.u < u1 && (pr.u < pr.seg_end || locate())) {
+      if (pr.x < pr.units) {
+        unsigned char* dst = ring + pr.stage * STAGE;
+        if (B16) {
+          if (pr.b >= pr.b0 + 32) next_entries(pr.b0 + 32);  // (batches begin and end with a unit)
+#pragma unroll
+          for (int k = 0; k < KU / 16; ++k) {
+            const int block = __shfl_sync(0xffffffffu, pr.ent, pr.b - pr.b0 + k);
+            const int64_t off = int64_t(block) * block_bytes + pr.head_off;
+            if (block >= 0) copy(dst + k * 16 * (ROW + 4), p.k_cache + off, p.v_cache + off, 16 * (ROW + 4));
+          }
+          pr.b += KU / 16;
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < KU; k += p.part, dst += part_bytes) {
+            if (pr.b >= pr.b0 + 32) next_entries(pr.b0 + 32);
+            const int block = __shfl_sync(0xffffffffu, pr.ent, pr.b - pr.b0);
+            if (block >= 0) {
+              const int64_t off = int64_t(block) * block_bytes + pr.head_off;
+              const unsigned char *k_rec = p.k_cache + off, *v_rec = p.v_cache + off;
+              if (fused) {
+                copy(dst, k_rec, v_rec, part_bytes);
+              } else {
+                const int64_t c = int64_t(pr.in) * ROW, w = int64_t(p.block_size) * ROW + int64_t(pr.in) * 4;
+                copy(dst, k_rec + c, v_rec + c, p.part * ROW);
+                copy(dst + p.part * ROW, k_rec + w, v_rec + w, p.part * 4);
+              }
+            }
+            pr.in += p.part;
+            if (pr.in == p.block_size) {
+              pr.in = 0;
+              ++pr.b;
+            }
+          }
+        }
+      }
+      ++pr.x;
+      ++pr.u;
+      if (++pr.stage == STAGES) pr.stage = 0;
+    }
+    copies_commit();
   };
 
   // ---- where a lane's rows lie in a stage: keys key_of(g), key_of(g + 8) of a tile as rows of K,
   // keys key_of(2t), (2t + 1), (2t + 8), (2t + 9) as rows of V; the second tile `next` bytes on
-  const int part_bytes = p.part * (ROW + 4);
-  auto code_at = [&](int key) { return key / p.part * part_bytes + key % p.part * ROW; };
-  auto param_at = [&](int key) { return key / p.part * part_bytes + p.part * ROW + key % p.part * 4; };
+  auto code_at = [&](int key) { return key / part * part_bytes + key % part * ROW; };
+  auto param_at = [&](int key) { return key / part * part_bytes + part * ROW + key % part * 4; };
   constexpr int kLane = BITS == 4 ? D / 8 : 16;  // bytes of a key row a lane takes at once
   int k_at[2], v_at[4], par_at[2];
 #pragma unroll
@@ -387,29 +429,35 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) v_at[i] = HALF + code_at(key_of(2 * t + (i & 1) + 8 * (i >> 1))) + g * (ROW / 8);
-  const int next_code = p.part >= 32 ? 16 * ROW : 16 / min(p.part, 16) * part_bytes;
-  const int next_param = p.part >= 32 ? 64 : next_code;
+  const int next_code = B16 ? 16 * (ROW + 4) : part >= 32 ? 16 * ROW : 16 / min(part, 16) * part_bytes;
+  const int next_param = !B16 && part >= 32 ? 64 : next_code;
 
   uint32_t C;  // two f16 1024s
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(C));
-  const int n_run = u1 - u0;
-  for (int i = 0; i < min(p.stages, n_run); ++i) fill();
-  bool ok = true;
-  int done = 0, stage = 0;
-  uint32_t phase = 0;  // of the next unit's stage
-  while (done < n_run && ok) {
-    // ---- a segment of the run
-    const Segment sg = segment_of<KU>(p, prefix, u0 + done);
+  for (int i = 0; i < STAGES; ++i) fill();
+  int stage = 0;
+  for (int u = u0; u < u1;) {
+    // ---- a segment of the run: units x0 .. x1 - 1 of its keys
+    const Segment sg = segment_of<KU>(p, prefix, u);
     Request r;
     request_of<KU>(p, sg.s, r);
     const int rows = min(kRows, r.q_len * p.group - sg.tile * kRows);
-    const int x0 = u0 + done - sg.begin, x1 = min(sg.end, u1) - sg.begin;
+    const int x0 = max(u - sg.begin - start_units<KU>(), 0), x1 = min(sg.end, u1) - sg.begin - start_units<KU>();
+    const bool whole = u <= sg.begin && u1 >= sg.end;
+    const int slot = u == u0 ? 0 : 1;
+    u = min(sg.end, u1);
+    if (!whole && lane == 0) desc[warp * 2 + slot] = make_int4(sg.begin, sg.end, sg.s, sg.head * r.tiles + sg.tile);
+    if (x1 <= x0) {  // nothing but the start: an empty piece
+      float* ml = p.pieces + int64_t((w0 + warp) * 2 + slot) * piece_floats<D>() + kRows * D;
+      if (lane < 2 * kRows) ml[lane] = lane < kRows ? kNoMax : 0.f;
+      continue;
+    }
     const int j_first = sg.tile * kRows / p.group, j_last = (sg.tile * kRows + rows - 1) / p.group;
     const int n_min = r.L - r.q_len + j_first + 1, n_max = r.L - r.q_len + j_last + 1;  // keys the rows see
     // Query row g of the tile as f16 with its largest element in [2^14, 2^15): a power of two, so exact
     // but for elements 2^28 times smaller than the row's largest. Its factor goes into the logits'.
     uint32_t qb[NK][2];
-    float qsum = 0.f, qfactor;
+    float qsum = 0.f, qoff = 0.f, qfactor;
     {
       float f[D / 4];
       const int rr = sg.tile * kRows + min(g, rows - 1);
@@ -429,8 +477,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
       const float mul = g >= rows ? 0.f : __uint_as_float(uint32_t(shift + 127) << 23);
       qfactor = p.scale_log2 * exp2f(float(-shift));
 #pragma unroll
-      for (int i = 0; i < D / 4; ++i) f[i] = __half2float(__float2half_rn(f[i] * mul)), qsum += f[i];
-      if (g >= rows) qsum = 0.f;
+      for (int i = 0; i < D / 4; ++i) {
+        f[i] = __half2float(__float2half_rn(f[i] * mul));
+        qsum += f[i];
+        if (BITS == 8 || (i & 1)) qoff += f[i];
+      }
+      if (g >= rows) qsum = qoff = 0.f;
+      qoff += __shfl_xor_sync(0xffffffffu, qoff, 1);
+      qoff += __shfl_xor_sync(0xffffffffu, qoff, 2);
       qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
       qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
 #pragma unroll
@@ -447,11 +501,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
       }
     }
     // of query rows 2t and 2t + 1, whose logits this lane holds
-    float qs[2], fac[2], m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, mid[2] = {0.f, 0.f};
+    float qs[2], off[2], fac[2], m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, mid[2] = {0.f, 0.f};
     int lim[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       qs[h] = __shfl_sync(0xffffffffu, qsum, (2 * t + h) * 4);
+      off[h] = -kOffset * __shfl_sync(0xffffffffu, qoff, (2 * t + h) * 4);
       fac[h] = __shfl_sync(0xffffffffu, qfactor, (2 * t + h) * 4);
       lim[h] = r.L - r.q_len + (sg.tile * kRows + min(2 * t + h, rows - 1)) / p.group + 1;
     }
@@ -464,35 +519,39 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     int wexp = 127;
     float wscale = __uint_as_float(254u << 23);
 
-    auto unit = [&](const unsigned char* st, int key0, auto tail_c) {
+    // tiles tile0 .. of a stage whose keys start at key0: all of a whole unit's, or one with masks (small
+    // code: the two together have to stay in the instruction cache)
+    auto unit = [&](const unsigned char* st, int key0, int tile0, auto tail_c) {
       constexpr bool kTail = decltype(tail_c)::value;
-      constexpr int TILES = kSub / 16;
+      constexpr int TILES = kTail ? 1 : KU / 16;
       // ---- q.c of 16 keys x 8 query rows a tile, all of a unit's tiles before their logits: independent chains
       float s[TILES][4], s1[TILES][4];
       uint32_t pk[TILES][2], pv[TILES][2];
 #pragma unroll
       for (int tile = 0; tile < TILES; ++tile) {
-        const unsigned char *base = st + tile * next_code, *pbase = st + tile * next_param;
+        const int at = tile0 + tile;
+        const unsigned char* two = st + (at >> 1) * (32 * (ROW + 4));  // pieces are at most 32 keys
+        const unsigned char *base = two + (at & 1) * next_code, *pbase = two + (at & 1) * next_param;
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[tile][i] = s1[tile][i] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          pk[tile][i] = shared_word(pbase + par_at[i]);
-          pv[tile][i] = shared_word(pbase + HALF + par_at[i]);
+          pk[tile][i] = lds32(smem_u32(pbase + par_at[i]));  // (a plain load is made again at every use)
+          pv[tile][i] = lds32(smem_u32(pbase + HALF + par_at[i]));
         }
         if constexpr (BITS == 4) {
           uint32_t a[2][D / 32];
 #pragma unroll
           for (int i = 0; i < 2; ++i) shared_words<D / 32>(base + k_at[i], a[i]);
           constexpr uint32_t M = 0x000f000fu, N = 0x00f000f0u;
-          const __half2 low = __half2half2(__float2half_rn(-1032.f)), high = __half2half2(__float2half_rn(-1152.f));
+          const __half2 low = __half2half2(__float2half_rn(-1024.f));
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) {  // c - 8 of even nibbles, 16 (c - 8) of odd ones
+          for (int w = 0; w < D / 32; ++w) {  // c of even nibbles, 16 (64 + c) of odd ones
             const uint32_t x = a[0][w], y = a[1][w];
-            mma_16816(s[tile], h2(and_or(x, M, C), low), h2(and_or(y, M, C), low), h2(and_or(x, N, C), high),
-                      h2(and_or(y, N, C), high), qb[2 * w][0], qb[2 * w][1], true);
-            mma_16816(s1[tile], h2(and_or(x >> 8, M, C), low), h2(and_or(y >> 8, M, C), low), h2(and_or(x >> 8, N, C), high),
-                      h2(and_or(y >> 8, N, C), high), qb[2 * w + 1][0], qb[2 * w + 1][1], true);
+            mma_16816(s[tile], h2(and_or(x, M, C), low), h2(and_or(y, M, C), low), and_or(x, N, C), and_or(y, N, C),
+                      qb[2 * w][0], qb[2 * w][1], true);
+            mma_16816(s1[tile], h2(and_or(x >> 8, M, C), low), h2(and_or(y >> 8, M, C), low), and_or(x >> 8, N, C),
+                      and_or(y >> 8, N, C), qb[2 * w + 1][0], qb[2 * w + 1][1], true);
           }
         } else {
 #pragma unroll
@@ -517,14 +576,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
       for (int tile = 0; tile < TILES; ++tile)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int key = key0 + tile * 16 + key_of(g + 8 * i);
+          const int key = key0 + (tile0 + tile) * 16 + key_of(g + 8 * i);
           if (kTail && key >= n_max) pk[tile][i] = pv[tile][i] = 0u;  // a row behind the last: whatever it holds
-          const float step = param_step(pk[tile][i]), lo = fmaf(step, kKeyMid, param_lo(pk[tile][i]));
+          const float step = param_step(pk[tile][i]), lo = param_lo(pk[tile][i]);
           ws[tile][i] = param_step(pv[tile][i]);
           midv[tile][i] = fmaf(ws[tile][i], kMid, param_lo(pv[tile][i]));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float c = s[tile][2 * i + h] + s1[tile][2 * i + h] - kOffset * qs[h];
+            const float c = s[tile][2 * i + h] + s1[tile][2 * i + h] + off[h];
             x[tile][2 * i + h] = fmaf(c, step, lo * qs[h]) * fac[h];
             hidden[tile][2 * i + h] = kTail && key >= lim[h];
             if (hidden[tile][2 * i + h]) x[tile][2 * i + h] = -INFINITY;
@@ -591,7 +650,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
       // (D / 8) g + 2 i in rows 0 .. 7 and the next in rows 8 .. 15
 #pragma unroll
       for (int tile = 0; tile < TILES; ++tile) {
-        const unsigned char* base = st + tile * next_code;
+        const int at = tile0 + tile;
+        const unsigned char* base = st + (at >> 1) * (32 * (ROW + 4)) + (at & 1) * next_code;
         if constexpr (BITS == 4) {
           const __half2 low = __half2half2(__float2half_rn(-1032.f)), high = __half2half2(__float2half_rn(-72.f)),
                         six = __half2half2(__float2half_rn(0.0625f));
@@ -629,26 +689,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
       }
     };
 
-    for (int x = x0; x < x1; ++x, ++done) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8u * uint32_t(stage), phase))) {
-        ok = false;
-        break;
-      }
+    for (int x = x0; x < x1; ++x) {
+      copies_wait<STAGES - 1>();
+      __syncwarp();
       const int key0 = x * KU;
-      const unsigned char* st = ring_mem + stage * STAGE;
+      const unsigned char* st = ring + stage * STAGE;
+      if (key0 + KU <= n_min) {
+        unit(st, key0, 0, std::false_type{});
+      } else {
 #pragma unroll 1
-      for (int k = 0; k < KU; k += kSub) {
-        if (key0 + k + kSub <= n_min) {
-          unit(st + k * (ROW + 4), key0 + k, std::false_type{});
-        } else if (key0 + k < n_max) {
-          unit(st + k * (ROW + 4), key0 + k, std::true_type{});
-        }
+        for (int tile = 0; tile < KU / 16 && key0 + tile * 16 < n_max; ++tile) unit(st, key0, tile, std::true_type{});
       }
       __syncwarp();
-      if (pr.u < u1) fill();
-      if (++stage == p.stages) stage = 0, phase ^= 1u;
+      fill();
+      if (++stage == STAGES) stage = 0;
     }
-    if (!ok) break;
     // ---- the segment's end in this run: sums over the lanes that share a query row, then out or a piece
     const float unscale = exp2f(float(-wexp));
 #pragma unroll
@@ -658,9 +713,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
         mid[h] += __shfl_xor_sync(0xffffffffu, mid[h], d);
       }
-    const bool whole = x0 == 0 && x1 == r.units;
-    const int slot = x0 + sg.begin == u0 ? 0 : 1;
-    if (!whole && lane == 0) desc[warp * 2 + slot] = make_int4(sg.begin, sg.end, sg.s, sg.head * r.tiles + sg.tile);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = 2 * t + h;
@@ -691,13 +743,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
           dst[kRows * D + kRows + row] = l[h];
         }
       }
-    }
-  }
-  if (!ok) {  // a copy did not arrive in time: tell, and wait for those under way before leaving
-    if (lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
-    for (int i = done; i < pr.u - u0; ++i) {
-      mbar_wait(bars + 8u * uint32_t(stage), phase);
-      if (++stage == p.stages) stage = 0, phase ^= 1u;
     }
   }
   __syncthreads();
@@ -734,14 +779,14 @@ __global__ void __launch_bounds__(kRows * 32) attention_int_join_kernel(const In
   constexpr int KU = unit_keys<BITS>();
   griddep_wait();
   const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t run = int64_t(*p.per) * kWarps;  // units a CTA
+  const Deal first(*p.total, num_ctas * kWarps);
   const float* pieces = p.pieces + int64_t(num_ctas) * kWarps * 2 * piece_floats<D>();
 #pragma unroll
   for (int slot = 0; slot < 2; ++slot) {
     const int4 d = p.descs[c * 2 + slot];
-    if (d.x < 0 || (slot == 0 && d.x != c * run)) continue;
+    if (d.x < 0 || (slot == 0 && d.x != first(c * kWarps))) continue;
     int count = 1;
-    while (c + count < num_ctas && (c + count) * run < d.y) ++count;
+    while (c + count < num_ctas && first((c + count) * kWarps) < d.y) ++count;
     join_rows<D, KU>(p, d, row, 1, lane, pieces, count, c * 2 + slot, c * 2, nullptr);
   }
 }
@@ -751,23 +796,21 @@ constexpr size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 template <int D, int BITS>
 cudaError_t run_int(IntParams p, const AttnIntArgs& a, cudaStream_t stream) {
   constexpr int STAGE = stage_bytes<D, BITS>();
-  const size_t prefix = size_t(a.num_seqs) * 4, room = 232448 - 2048;  // the rest: static shared memory
-  int stages = 8;
-  auto bytes = [&](int n) { return size_t((kWarps * n * 8 + 127) & ~127) + size_t(kWarps) * n * STAGE + prefix; };
-  while (stages > 1 && bytes(stages) > room) --stages;
-  static_assert(((kWarps * 16 + 127) & ~127) + kWarps * 2 * STAGE + kIntMaxSeqs * 4 <= 232448 - 2048, "two stages");
-  p.stages = stages;
-  const cudaError_t e = ensure_smem<attention_int_kernel<D, BITS>>(room);
+  constexpr size_t rings = size_t(kWarps) * num_stages<D>() * STAGE, most = rings + kIntMaxSeqs * 4;
+  static_assert(most + 1024 <= 232448, "shared memory of a CTA");
+  const bool b16 = a.block_size == 16;
+  const cudaError_t e = b16 ? ensure_smem<attention_int_kernel<D, BITS, true>>(most)
+                            : ensure_smem<attention_int_kernel<D, BITS, false>>(most);
   if (e != cudaSuccess) return e;
-  const cudaError_t l = launch_pdl(attention_int_kernel<D, BITS>, dim3(a.num_ctas), dim3(kWarps * 32), bytes(stages),
-                                   stream, p);
+  const cudaError_t l = launch_pdl(b16 ? attention_int_kernel<D, BITS, true> : attention_int_kernel<D, BITS, false>, dim3(a.num_ctas), dim3(kWarps * 32),
+                                   rings + size_t(a.num_seqs) * 4, stream, p);
   if (l != cudaSuccess) return l;
   return launch_pdl(attention_int_join_kernel<D, BITS>, dim3(a.num_ctas), dim3(kRows * 32), 0, stream, p, a.num_ctas);
 }
 
 }  // namespace
 
-// descs, per, pieces of the CTAs' warps and of the CTAs
+// descs, total, pieces of the CTAs' warps and of the CTAs
 size_t attention_int_workspace_bytes(int head_dim, int num_ctas) {
   const size_t piece = (kRows * size_t(head_dim) + 2 * kRows) * 4;
   return align_up(size_t(num_ctas) * 2 * sizeof(int4)) + 256 + size_t(num_ctas) * (kWarps + 1) * 2 * piece;
@@ -776,7 +819,7 @@ size_t attention_int_workspace_bytes(int head_dim, int num_ctas) {
 bool attention_int_fits(const AttnIntArgs& a) {
   const int ku = a.bits == 4 ? unit_keys<4>() : unit_keys<8>();
   const int64_t tiles = (int64_t(a.num_tokens) * (a.num_heads / a.num_kv_heads) + kRows - 1) / kRows + a.num_seqs;
-  const int64_t units = (int64_t(a.max_seq_len) + ku - 1) / ku;
+  const int64_t units = (int64_t(a.max_seq_len) + ku - 1) / ku + 2;
   // units are counted in 32 bits (a step of all warps past the end, too)
   return a.num_seqs <= kIntMaxSeqs && tiles <= 0x7fffffff / a.num_kv_heads &&
          tiles * a.num_kv_heads <= (0x7fffffff - (1 << 20)) / units;
@@ -795,7 +838,7 @@ cudaError_t launch_attention_int(const AttnIntArgs& a, cudaStream_t stream) {
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   p.descs = reinterpret_cast<int4*>(ws);
   ws += align_up(size_t(a.num_ctas) * 2 * sizeof(int4));
-  p.per = reinterpret_cast<int*>(ws);
+  p.total = reinterpret_cast<int*>(ws);
   p.pieces = reinterpret_cast<float*>(ws + 256);
   p.num_blocks = a.num_blocks;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
@@ -809,7 +852,7 @@ cudaError_t launch_attention_int(const AttnIntArgs& a, cudaStream_t stream) {
   p.block_size = a.block_size;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.part = a.block_size & -a.block_size;
-  if (p.part > kSub) p.part = kSub;
+  if (p.part > kPart) p.part = kPart;
   if (a.bits == 4) return a.head_dim == 64 ? run_int<64, 4>(p, a, stream) : run_int<128, 4>(p, a, stream);
   return a.head_dim == 64 ? run_int<64, 8>(p, a, stream) : run_int<128, 8>(p, a, stream);
 }

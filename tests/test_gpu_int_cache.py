@@ -2,9 +2,9 @@
 (the definition names every rounding); attention over the codes against float64.
 
 Attention's tolerance, from the arithmetic. Query rows enter as f16 scaled by a power of two: exact but for
-elements 2^-25 of the row's largest. A logit is, in fp32, step q.(c - 8) + (lo + 8 step) sum q (4 bits), or
-step (q.(1024 + c) - 1024 sum q) + lo sum q (8 bits), sums of D terms: each term and each sum within
-2^-23 of sum |q| (off step + |lo|), off = 16 or 1280 (what multiplies step at most), so
+elements 2^-25 of the row's largest. A logit is, in fp32, step (q.(o + c) - q.o) + lo sum q with o = 0 or 64 (4 bits), or
+1024 (8 bits), sums of D terms: each term and each sum within 2^-23 of sum |q| (off step + |lo|),
+off = 80 or 1280 (what multiplies step at most), so
 dl <= scale (D + 8) 2^-23 sum |q| (off step + |lo|). The numerators
 have that relative error, ex2's 2^-22 and, times the value's step, f16's half step 2^-11 (what falls
 under f16's range: 2^-31 of the largest step a key). A value enters as mid + step (c - mid), both parts within
@@ -220,7 +220,7 @@ class Batch:
     def check(self, requests=None):
         assert self.pa.read_device_errors() == 0
         kc, vc, q, out = self.kc.cpu().numpy(), self.vc.cpu().numpy(), _f64(self.q), _f64(self.out)
-        N, off = 2 ** self.bits - 1, 16 if self.bits == 4 else 1280
+        N, off = 2 ** self.bits - 1, 80 if self.bits == 4 else 1280
         for s in range(len(self.lens)) if requests is None else requests:
             a, b, L = self.qsl[s], self.qsl[s + 1], self.lens[s]
             if a == b:
