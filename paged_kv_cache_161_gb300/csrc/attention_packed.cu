@@ -385,12 +385,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       const uint64_t dk0 = tc::smem_desc_sw128(base + LY::K, 16, 1024);
       const uint64_t dv0 = tc::smem_desc_sw128(base + LY::V, kHalf, 1024);
       bool ok = true, end = false;
-      // Q.K runs two steps ahead of P.V: its own place in the tiles, and the steps of those begun
+      // Q.K runs ahead of P.V, by as much as the S that were read allow: its own place in the tiles, and the
+      // steps of those begun
       int i = 0, N = 0, q_left = 0, nq = -1;  // next slot; steps issued, left of the tile; its query buffer
       int n = 0, pv_left = 0, tile = 0;       // P.V: steps issued, left of the tile; tiles begun
       int steps[4], head = 0, tail = 0;       // steps of tiles that P.V has not begun
       while (ok) {
-        while (ok && !end && N < n + 2) {
+        while (ok && !end && N < n + 3) {
           if (q_left == 0) {
             Tile x;
             if (!take(i++, x)) ok = false;
