@@ -18,8 +18,9 @@
 // known long before the numerators; each keeps its own sums of numerators, joined at the tile's end.
 //
 // Roles (12 warps, one CTA a SM): warps 0-3 and 4-7 the warpgroups of even and odd steps (counted over
-// all the CTA's tiles); warp 8 the tiles, Q (two buffers) and K (two); warp 9 TMEM and the products; warp
-// 10 V (two). Tiles: requests with the most keys first, a request's last tiles first; the grid has a
+// all the CTA's tiles); warp 8 the tiles, Q (two buffers) and K (two); warp 9 TMEM and Q.K; warp 10 V (two);
+// warp 11 P.V (a thread that issues both waits out the products it has queued before it turns to the
+// other, and the tensor cores idle meanwhile: ISSUE_FIGURES). Tiles: requests with the most keys first, a request's last tiles first; the grid has a
 // CTA for every tile there may be, and a running CTA takes the tiles of CTAs that have not started
 // (clusterlaunchcontrol), so no counter lives in memory between calls.
 //
@@ -38,8 +39,8 @@ namespace {
 constexpr int kBM = 128;           // rows of a tile
 constexpr int kBN = 128;           // keys of a step
 constexpr int kMaxSeqs = 4096;     // requests of a call
-constexpr int kThreads = 12 * 32;  // the last warp only makes the third warpgroup whole
-constexpr int kWarpLoad = 8, kWarpMMA = 9, kWarpV = 10;
+constexpr int kThreads = 12 * 32;
+constexpr int kWarpLoad = 8, kWarpQK = 9, kWarpV = 10, kWarpPV = 11;
 // Registers: 384 threads x 168 at launch = 64512 = 256 x 216 (a row's 128 logits in registers) + 128 x 72.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= 384 * 168, "setmaxnreg waits for registers the launch has");
@@ -88,7 +89,7 @@ enum : int {
   bP0, bP1,            // P is in TMEM (4 warps)
   bPV0, bPV1,          // P.V of a step has landed: P and the V stage are free, O holds it
   bOFree,              // O of a tile has been read (8 warps)
-  bEnd,                // every product has landed
+  bEnd0, bEnd1,        // every Q.K, every P.V has landed
   bClc,
   bRingFull0, bRingEmpty0 = bRingFull0 + kSlots,
   bM0 = bRingEmpty0 + kSlots,  // [4 warps][2]: a warp's row maxima of a step are in shared memory
@@ -96,7 +97,7 @@ enum : int {
   kBars = bX0 + 4
 };
 static_assert(kBars <= Layout<128>::NBAR, "barriers in the layout");
-constexpr uint32_t kTakers = 10;  // of a ring slot: V, products, 8 softmax warps
+constexpr uint32_t kTakers = 11;  // of a ring slot: V, Q.K, P.V, 8 softmax warps
 
 // 16 columns of the warp's lanes (tc::tmem_ld32 with half the registers)
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     }
     fence_mbar_init();
   }
-  if (warp == kWarpMMA) {
+  if (warp == kWarpQK) {
     tc::tmem_alloc(base + LY::MISC, 512);
     tc::tmem_relinquish();
   }
@@ -378,73 +379,75 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         fail();
         for (int j = n > 2 ? n - 2 : 0; j < n; ++j) wait_step(bV0, j);
       }
-    } else if (warp == kWarpMMA && lane == 0) {
-      // =========================== products ===========================
-      constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kBM, kBN, 0), idesc_pv = tc::idesc_bf16_f32(kBM, D, 1);
+    } else if (warp == kWarpQK && lane == 0) {
+      // =========================== Q.K ===========================
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(kBM, kBN, 0);
       const uint64_t dq0 = tc::smem_desc_sw128(base + LY::Q, 16, 1024);
       const uint64_t dk0 = tc::smem_desc_sw128(base + LY::K, 16, 1024);
-      const uint64_t dv0 = tc::smem_desc_sw128(base + LY::V, kHalf, 1024);
-      bool ok = true, end = false;
-      // Q.K runs ahead of P.V, by as much as the S that were read allow: its own place in the tiles, and the
-      // steps of those begun
-      int i = 0, N = 0, q_left = 0, nq = -1;  // next slot; steps issued, left of the tile; its query buffer
-      int n = 0, pv_left = 0, tile = 0;       // P.V: steps issued, left of the tile; tiles begun
-      int steps[4], head = 0, tail = 0;       // steps of tiles that P.V has not begun
-      while (ok) {
-        while (ok && !end && N < n + 3) {
-          if (q_left == 0) {
-            Tile x;
-            if (!take(i++, x)) ok = false;
-            else if (x.t < 0) end = true;
-            else if (x.nt > 0) {
-              q_left = x.nt;
-              steps[tail++ & 3] = x.nt;
-              ++nq;
-              if (!mbar_wait(bar(bQ0 + (nq & 1)), uint32_t(nq >> 1) & 1u)) ok = false;
-            }
-            continue;
-          }
-          if ((N >= 2 && !wait_step(bSFree0, N - 2)) || !wait_step(bK0, N)) {
+      bool ok = true;
+      int n = 0, nq = 0;
+      for (int i = 0; ok; ++i) {
+        Tile x;
+        if (!take(i, x)) ok = false;
+        if (!ok || x.t < 0) break;
+        if (x.nt == 0) continue;
+        if (!mbar_wait(bar(bQ0 + (nq & 1)), uint32_t(nq >> 1) & 1u)) {
+          ok = false;
+          break;
+        }
+        const uint64_t a0 = dq0 + uint64_t((uint32_t((nq & 1) * NH) * kHalf) >> 4);
+        ++nq;
+        for (int kb = 0; kb < x.nt; ++kb, ++n) {
+          if ((n >= 2 && !wait_step(bSFree0, n - 2)) || !wait_step(bK0, n)) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint64_t a0 = dq0 + uint64_t((uint32_t((nq & 1) * NH) * kHalf) >> 4);
-          const uint64_t b0 = dk0 + uint64_t((uint32_t((N & 1) * NH) * kHalf) >> 4);
+          const uint64_t b0 = dk0 + uint64_t((uint32_t((n & 1) * NH) * kHalf) >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = uint32_t(k / 4) * kHalf + uint32_t(k % 4) * 32;
-            tc::mma_f16(tmem + kS + uint32_t((N & 1) * kBN), a0 + (off >> 4), b0 + (off >> 4), idesc_qk, k > 0 ? 1u : 0u);
+            tc::mma_f16(tmem + kS + uint32_t((n & 1) * kBN), a0 + (off >> 4), b0 + (off >> 4), idesc, k > 0 ? 1u : 0u);
           }
-          tc::mma_commit(bar(bQK0 + (N & 1)));
-          ++N;
-          --q_left;
+          tc::mma_commit(bar(bQK0 + (n & 1)));
         }
-        if (!ok || n == N) break;
-        bool fresh = false;
-        if (pv_left == 0) {
-          pv_left = steps[head++ & 3];
-          fresh = true;
-          if (tile > 0 && !mbar_wait(bar(bOFree), uint32_t(tile - 1) & 1u)) ok = false;  // O of the tile before
-          ++tile;
-        }
-        if (!ok || !wait_step(bP0, n) || !wait_step(bV0, n)) {
+      }
+      if (!ok) fail();
+      tc::mma_commit(bar(bEnd0));  // every product has landed before TMEM is released
+      mbar_wait(bar(bEnd0), 0);
+    } else if (warp == kWarpPV && lane == 0) {
+      // =========================== P.V ===========================
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(kBM, D, 1);
+      const uint64_t dv0 = tc::smem_desc_sw128(base + LY::V, kHalf, 1024);
+      bool ok = true;
+      int n = 0, live = 0;
+      for (int i = 0; ok; ++i) {
+        Tile x;
+        if (!take(i, x)) ok = false;
+        if (!ok || x.t < 0) break;
+        if (x.nt == 0) continue;
+        if (live > 0 && !mbar_wait(bar(bOFree), uint32_t(live - 1) & 1u)) {  // O of the tile before
           ok = false;
           break;
         }
-        tc::fence_after_sync();
-        const uint64_t b0 = dv0 + uint64_t((uint32_t((n & 1) * NH) * kHalf) >> 4);
+        ++live;
+        for (int kb = 0; kb < x.nt; ++kb, ++n) {
+          if (!wait_step(bP0, n) || !wait_step(bV0, n)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint64_t b0 = dv0 + uint64_t((uint32_t((n & 1) * NH) * kHalf) >> 4);
 #pragma unroll
-        for (int k = 0; k < kBN / 16; ++k)
-          tc::mma_f16_ts(tmem + kO, tmem + kP + uint32_t((n & 1) * 64 + k * 8), b0 + uint64_t((uint32_t(k) * 2048) >> 4),
-                         idesc_pv, (fresh && k == 0) ? 0u : 1u);
-        tc::mma_commit(bar(bPV0 + (n & 1)));
-        ++n;
-        --pv_left;
+          for (int k = 0; k < kBN / 16; ++k)
+            tc::mma_f16_ts(tmem + kO, tmem + kP + uint32_t((n & 1) * 64 + k * 8), b0 + uint64_t((uint32_t(k) * 2048) >> 4),
+                           idesc, (kb == 0 && k == 0) ? 0u : 1u);
+          tc::mma_commit(bar(bPV0 + (n & 1)));
+        }
       }
       if (!ok) fail();
-      tc::mma_commit(bar(bEnd));  // every product has landed before TMEM is released
-      mbar_wait(bar(bEnd), 0);
+      tc::mma_commit(bar(bEnd1));
+      mbar_wait(bar(bEnd1), 0);
     }
   } else {
     regs_up<kRegsSoftmax>();
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
 
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kWarpMMA) {
+  if (warp == kWarpQK) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
