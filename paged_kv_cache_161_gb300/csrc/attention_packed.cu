@@ -460,9 +460,61 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     const float sc = p.scale_log2;
     int n = 0, live = 0;  // steps of the tiles before; tiles with steps
     bool ok = true;
+    // The output of a tile waits for its last P.V: the warpgroup that has the next tile's first step does that
+    // step before, the other at once. (P.V of the next tile waits for both: nothing of that tile's P.V may be
+    // waited for before.)
+    bool due = false;  // the tile before this one is to be written: its last step, number, rows
+    int due_end = 0, due_live = 0;
+    __nv_bfloat16* due_out = nullptr;  // null: not a row of the request's
+    auto store = [&](__nv_bfloat16* out, const float* o, float inv) {  // half a row; inv 0: zeros
+#pragma unroll
+      for (int e = 0; e < D / 2; e += 16) {
+        float f[8], h[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          f[k] = !o || inv == 0.f ? 0.f : o[e + k] * inv;
+          h[k] = !o || inv == 0.f ? 0.f : o[e + 8 + k] * inv;
+        }
+        const uint4 a = Elem<__nv_bfloat16>::pack(f), b = Elem<__nv_bfloat16>::pack(h);
+        if (p.out_v8) {
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + e), "r"(a.x), "r"(a.y),
+                       "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                       : "memory");
+        } else {
+          *reinterpret_cast<uint4*>(out + e) = a;
+          *reinterpret_cast<uint4*>(out + e + 8) = b;
+        }
+      }
+    };
+    auto finish = [&]() -> bool {  // O / l -> out, half the dimensions each warpgroup; false: a wait ran out
+      due = false;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(bX0 + wr), uint32_t(due_live) & 1u)) ||
+          !__all_sync(0xffffffffu, wait_step(bPV0, due_end)))
+        return false;
+      const float2* both = x_sh + ((due_live & 1) * 2) * 128 + r;
+      const float2 z = both[(due_end & 1) * 128], y = both[((due_end & 1) ^ 1) * 128];  // of the last step, the one before
+      float sum = z.y;
+      if (y.y != 0.f) sum += y.y * (y.x == z.x ? 1.f : exp2f((y.x - z.x) * sc));
+      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+      tc::fence_after_sync();
+      float o[D / 2];
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tc::tmem_ld32(trow + kO + uint32_t(w * (D / 2) + c * 32), *reinterpret_cast<float(*)[32]>(o + c * 32));
+      tc::tmem_wait_ld();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bOFree));
+      if (due_out) store(due_out, o, inv);
+      return true;
+    };
     for (int i = 0; ok; ++i) {
       Tile x;
       if (!take_warp(i, x)) {
+        ok = false;
+        break;
+      }
+      if (due && (x.t < 0 || (x.nt > 0 && !((n & 1) == w))) && !finish()) {
         ok = false;
         break;
       }
@@ -578,57 +630,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bP0 + w));
-      }
-      if (!ok) break;
-      // ---- O / l -> out, half the dimensions each; no keys: zeros
-      __nv_bfloat16* out = p.out + (int64_t(x.row0 + (r >> lg)) * p.num_heads + (x.hk << lg) + (r & ((1 << lg) - 1))) * D +
-                           w * (D / 2);
-      float o[D / 2], inv = 0.f;
-      if (x.nt > 0) {
-        float2* mine = x_sh + ((live & 1) * 2) * 128 + r;  // double: the other warp may still read the tile's before
-        mine[w * 128] = make_float2(m, l);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bX0 + wr));
-        const int end = n + x.nt - 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(bX0 + wr), uint32_t(live) & 1u)) ||
-            !__all_sync(0xffffffffu, wait_step(bPV0, end))) {
+        if (due && !finish()) {
           ok = false;
           break;
         }
-        const float2 z = mine[(end & 1) * 128], y = mine[((end & 1) ^ 1) * 128];  // of the last step, of the one before
-        float sum = z.y;
-        if (y.y != 0.f) sum += y.y * (y.x == z.x ? 1.f : exp2f((y.x - z.x) * sc));
-        inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        tc::fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tc::tmem_ld32(trow + kO + uint32_t(w * (D / 2) + c * 32), *reinterpret_cast<float(*)[32]>(o + c * 32));
-        tc::tmem_wait_ld();
-        tc::fence_before_sync();
+      }
+      if (!ok) break;
+      __nv_bfloat16* out = p.out + (int64_t(x.row0 + (r >> lg)) * p.num_heads + (x.hk << lg) + (r & ((1 << lg) - 1))) * D +
+                           w * (D / 2);
+      if (x.nt > 0) {
+        x_sh[((live & 1) * 2 + w) * 128 + r] = make_float2(m, l);  // double: the other warp may still read the tile's before
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bOFree));
+        if (lane == 0) mbar_arrive(bar(bX0 + wr));
+        due = true;
+        due_end = n + x.nt - 1;
+        due_live = live;
+        due_out = active ? out : nullptr;
         n += x.nt;
         ++live;
-      }
-      if (active) {
-#pragma unroll
-        for (int e = 0; e < D / 2; e += 16) {
-          float f[8], h[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            f[k] = inv == 0.f ? 0.f : o[e + k] * inv;
-            h[k] = inv == 0.f ? 0.f : o[e + 8 + k] * inv;
-          }
-          const uint4 a = Elem<__nv_bfloat16>::pack(f), b = Elem<__nv_bfloat16>::pack(h);
-          if (p.out_v8) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + e), "r"(a.x), "r"(a.y),
-                         "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                         : "memory");
-          } else {
-            *reinterpret_cast<uint4*>(out + e) = a;
-            *reinterpret_cast<uint4*>(out + e + 8) = b;
-          }
-        }
+      } else if (active) {  // no keys
+        store(out, nullptr, 0.f);
       }
     }
     if (!ok) fail();
