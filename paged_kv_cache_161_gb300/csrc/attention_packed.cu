@@ -233,24 +233,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   __syncthreads();
   if (int(blockIdx.x) >= total) return;
 
-  // Tile t: a request's KV heads fastest, its tiles from the last one back.
+  // Tile t: a request's KV heads fastest, its tiles from the last one back. For warp 8's thread, whose tiles
+  // ascend: the request is stepped along.
+  int at_p = -1, at_q0 = 0, at_Q = 0, at_k0 = 0, at_K = 0;
   auto tile_info = [&](int t) {
-    int lo = 0, n = P;  // pfx[lo] <= t < pfx[lo + 1]
-    while (n > 1) {
-      const int half = n >> 1;
-      if (pfx[lo + half] <= t) lo += half, n -= half;
-      else n = half;
+    if (at_p < 0 || pfx[at_p + 1] <= t) {
+      if (at_p < 0) at_p = 0;
+      while (pfx[at_p + 1] <= t) ++at_p;
+      const int s = ord[at_p];
+      at_q0 = p.qsl[s];
+      at_Q = p.qsl[s + 1] - at_q0;
+      at_k0 = p.ksl[s];
+      at_K = p.ksl[s + 1] - at_k0;
     }
-    const int s = ord[lo], r = t - pfx[lo];
-    const int q0 = p.qsl[s], Q = p.qsl[s + 1] - q0, k0 = p.ksl[s], K = p.ksl[s + 1] - k0;
-    const int back = r / p.num_kv_heads, q = ((Q + TOK - 1) / TOK - 1 - back) * TOK;
+    const int r = t - pfx[at_p], back = r / p.num_kv_heads;
+    const int q = (((at_Q + TOK - 1) >> (7 - lg)) - 1 - back) << (7 - lg);
     Tile x;
     x.t = t;
     x.hk = r - back * p.num_kv_heads;
-    x.row0 = q0 + q;
-    x.nq = min(TOK, Q - q);
-    x.k0 = k0;
-    x.pos0 = K - Q + q;
+    x.row0 = at_q0 + q;
+    x.nq = min(TOK, at_Q - q);
+    x.k0 = at_k0;
+    x.pos0 = at_K - at_Q + q;
     x.leff = max(0, x.pos0 + x.nq);  // keys that its rows see
     x.nt = (x.leff + kBN - 1) / kBN;
     return x;
@@ -438,10 +442,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
           }
           tc::fence_after_sync();
           const uint64_t b0 = dv0 + uint64_t((uint32_t((n & 1) * NH) * kHalf) >> 4);
-#pragma unroll
-          for (int k = 0; k < kBN / 16; ++k)
+          auto pv = [&](int k) {
             tc::mma_f16_ts(tmem + kO, tmem + kP + uint32_t((n & 1) * 64 + k * 8), b0 + uint64_t((uint32_t(k) * 2048) >> 4),
                            idesc, (kb == 0 && k == 0) ? 0u : 1u);
+          };
+          if (kb + 1 < x.nt) {
+#pragma unroll
+            for (int k = 0; k < kBN / 16; ++k) pv(k);
+          } else {  // the sixteens that hold visible keys
+            const int sixteens = (x.leff - kb * kBN + 15) >> 4;
+#pragma unroll 1
+            for (int k = 0; k < sixteens; ++k) pv(k);
+          }
           tc::mma_commit(bar(bPV0 + (n & 1)));
         }
       }
@@ -539,7 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         if (lane == 0) mbar_arrive(bar(bSFree0 + w));
         if (key0 + kBN - 1 > x.pos0) {  // keys past this row's position
 #pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = key0 + c <= mypos ? s[c] : -INFINITY;
+          for (int q = 0; q < 4; ++q) {
+            const int k = min(max(mypos - key0 + 1 - q * 32, 0), 32);
+            const uint32_t seen = k == 32 ? 0xffffffffu : (1u << k) - 1u;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[q * 32 + c] = (seen >> c & 1u) ? s[q * 32 + c] : -INFINITY;
+          }
         }
         float mx[4];
 #pragma unroll
@@ -610,13 +627,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
         l += (r01.x + r01.y) + (r23.x + r23.y);
         // V rows behind the last key any row sees (of later tokens, or another request's) may hold NaN: P is
-        // 0 there, and 0 * NaN is not. They become zeros before the step's P.V.
-        if (x.leff - key0 < kBN) {
+        // 0 there, and 0 * NaN is not. P.V ends with the sixteen rows that hold the last key; what they hold
+        // behind it becomes zeros before.
+        const int used = x.leff - key0;
+        if (used < kBN && (used & 15)) {
           if (!__all_sync(0xffffffffu, wait_step(bV0, at))) {
             ok = false;
             break;
           }
-          if (r >= x.leff - key0) {
+          if (r >= used && r < ((used + 15) & ~15)) {
 #pragma unroll
             for (int h = 0; h < NH; ++h)
 #pragma unroll
