@@ -123,6 +123,38 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       : "memory");
 }
 
+// 16 lanes, 8 N columns: thread t gets of each 8 columns j columns 2 (t % 4) and + 1 of lane t / 4 (v[4 j], v[4 j +
+// 1]) and of lane t / 4 + 8 (v[4 j + 2], v[4 j + 3]).
+template <int N>
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, float (&v)[4 * N]) {
+  static_assert(N == 8 || N == 4, "64 or 32 columns");
+  uint32_t r[4 * N];
+  if constexpr (N == 8) {
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+          : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          : "r"(taddr)
+          : "memory");
+  } else {
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+          : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+          : "r"(taddr)
+          : "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Of four lanes (t % 4), each with words x[0 .. 3] for the four: lane a gets word a of each, in their order.
+__device__ __forceinline__ void transpose4(uint32_t (&x)[4], int t) {
+  const uint32_t a = __shfl_xor_sync(0xffffffffu, (t & 1) ? x[0] : x[1], 1), b = __shfl_xor_sync(0xffffffffu, (t & 1) ? x[2] : x[3], 1);
+  if (t & 1) x[0] = a, x[2] = b;
+  else x[1] = a, x[3] = b;
+  const uint32_t c = __shfl_xor_sync(0xffffffffu, (t & 2) ? x[0] : x[2], 2), d = __shfl_xor_sync(0xffffffffu, (t & 2) ? x[1] : x[3], 2);
+  if (t & 2) x[0] = c, x[1] = d;
+  else x[2] = c, x[3] = d;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -476,27 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     // step before, the other at once. (P.V of the next tile waits for both: nothing of that tile's P.V may be
     // waited for before.)
     bool due = false;  // the tile before this one is to be written: its last step, number, rows
-    int due_end = 0, due_live = 0;
-    __nv_bfloat16* due_out = nullptr;  // null: not a row of the request's
-    auto store = [&](__nv_bfloat16* out, const float* o, float inv) {  // half a row; inv 0: zeros
-#pragma unroll
-      for (int e = 0; e < D / 2; e += 16) {
-        float f[8], h[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          f[k] = !o || inv == 0.f ? 0.f : o[e + k] * inv;
-          h[k] = !o || inv == 0.f ? 0.f : o[e + 8 + k] * inv;
-        }
-        const uint4 a = Elem<__nv_bfloat16>::pack(f), b = Elem<__nv_bfloat16>::pack(h);
-        if (p.out_v8) {
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + e), "r"(a.x), "r"(a.y),
-                       "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                       : "memory");
-        } else {
-          *reinterpret_cast<uint4*>(out + e) = a;
-          *reinterpret_cast<uint4*>(out + e + 8) = b;
-        }
-      }
+    int due_end = 0, due_live = 0, due_row0 = 0, due_hk = 0, due_nq = 0;
+    // The address of the warpgroup's half of row rr of the tile due, or null where the request has no such row.
+    auto out_at = [&](int rr) -> __nv_bfloat16* {
+      if ((rr >> lg) >= due_nq) return nullptr;
+      return p.out + (int64_t(due_row0 + (rr >> lg)) * p.num_heads + (due_hk << lg) + (rr & ((1 << lg) - 1))) * D + w * (D / 2);
     };
     auto finish = [&]() -> bool {  // O / l -> out, half the dimensions each warpgroup; false: a wait ran out
       due = false;
@@ -509,32 +525,66 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       if (y.y != 0.f) sum += y.y * (y.x == z.x ? 1.f : exp2f((y.x - z.x) * sc));
       const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
       tc::fence_after_sync();
-      float o[D / 2];
+      // Lanes of four hold a row's columns side by side; turned among them, a store writes 8 rows' 128 (64)
+      // contiguous bytes where a thread's own row would be 32 lines (64 prompts of 256 tokens: STORE_FIGURES).
+      constexpr int N = D / 16, V = N / 4;  // column eights of half the dimensions; of a lane's store
+      float o[2][4 * N];
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        tc::tmem_ld32(trow + kO + uint32_t(w * (D / 2) + c * 32), *reinterpret_cast<float(*)[32]>(o + c * 32));
+      for (int half = 0; half < 2; ++half)
+        tmem_ld_16x256b<N>(trow + (uint32_t(half * 16) << 16) + kO + uint32_t(w * (D / 2)), o[half]);
       tc::tmem_wait_ld();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bOFree));
-      if (due_out) store(due_out, o, inv);
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int up = 0; up < 2; ++up) {
+          const int row = half * 16 + up * 8 + (lane >> 2);
+          const float by = __shfl_sync(0xffffffffu, inv, row);
+          uint32_t x[V][4];  // lane a of four: eights a V .. a V + V - 1
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float* y = o[half] + 4 * j + 2 * up;
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y[0] * by, y[1] * by);
+            x[j % V][j / V] = by == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&h);  // a row that sees no key
+          }
+#pragma unroll
+          for (int v = 0; v < V; ++v) transpose4(x[v], lane & 3);
+          __nv_bfloat16* out = out_at(wr * 32 + row);
+          if (!out) continue;
+          out += (lane & 3) * (8 * V);
+          if (V == 2 && p.out_v8) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "r"(x[0][0]), "r"(x[0][1]),
+                         "r"(x[0][2]), "r"(x[0][3]), "r"(x[V - 1][0]), "r"(x[V - 1][1]), "r"(x[V - 1][2]), "r"(x[V - 1][3])
+                         : "memory");
+          } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) *reinterpret_cast<uint4*>(out + 8 * v) = make_uint4(x[v][0], x[v][1], x[v][2], x[v][3]);
+          }
+        }
       return true;
     };
-    for (int i = 0; ok; ++i) {
-      Tile x;
+    // One round: a step of this warpgroup's if its turn is, then the output due. (One place for each: the
+    // instruction cache holds this code once, not twice.)
+    Tile x;
+    int kb = 0, mypos = 0;  // this warpgroup's next step of the tile
+    bool active = false;
+    float m = -INFINITY, l = 0.f;  // reference maximum at this warpgroup's last step, its sum of numerators
+    auto next_tile = [&](int i) {
       if (!take_warp(i, x)) {
         ok = false;
-        break;
+        return;
       }
-      if (due && (x.t < 0 || (x.nt > 0 && !((n & 1) == w))) && !finish()) {
-        ok = false;
-        break;
-      }
-      if (x.t < 0) break;
-      const bool active = (r >> lg) < x.nq;
-      const int mypos = active ? x.pos0 + (r >> lg) : x.leff - 1;
-      float m = -INFINITY, l = 0.f;  // reference maximum at this warpgroup's last step, its sum of numerators
-      for (int kb = (n & 1) == w ? 0 : 1; kb < x.nt; kb += 2) {
+      kb = (n & 1) == w ? 0 : 1;
+      active = (r >> lg) < x.nq;
+      mypos = active ? x.pos0 + (r >> lg) : x.leff - 1;
+      m = -INFINITY;
+      l = 0.f;
+    };
+    next_tile(0);
+    for (int i = 1; ok;) {
+      if (kb < x.nt && !(due && kb > 0)) {  // no step but a tile's first goes before an output
         const int at = n + kb, key0 = kb * kBN;
         if (!__all_sync(0xffffffffu, wait_step(bQK0, at))) {
           ok = false;
@@ -649,14 +699,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bP0 + w));
-        if (due && !finish()) {
-          ok = false;
-          break;
-        }
+        kb += 2;
       }
-      if (!ok) break;
-      __nv_bfloat16* out = p.out + (int64_t(x.row0 + (r >> lg)) * p.num_heads + (x.hk << lg) + (r & ((1 << lg) - 1))) * D +
-                           w * (D / 2);
+      if (due) {
+        if (!finish()) ok = false;
+        continue;
+      }
+      if (kb < x.nt) continue;
+      if (x.t < 0) break;
+      // ---- the tile's steps are done
+      due_row0 = x.row0;
+      due_hk = x.hk;
+      due_nq = x.nq;
       if (x.nt > 0) {
         x_sh[((live & 1) * 2 + w) * 128 + r] = make_float2(m, l);  // double: the other warp may still read the tile's before
         __syncwarp();
@@ -664,12 +718,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         due = true;
         due_end = n + x.nt - 1;
         due_live = live;
-        due_out = active ? out : nullptr;
         n += x.nt;
         ++live;
-      } else if (active) {  // no keys
-        store(out, nullptr, 0.f);
+      } else if (__nv_bfloat16* out = out_at(r)) {  // no keys: zeros
+#pragma unroll
+        for (int e = 0; e < D / 2; e += 8) *reinterpret_cast<uint4*>(out + e) = make_uint4(0, 0, 0, 0);
       }
+      next_tile(i++);
     }
     if (!ok) fail();
   }
