@@ -528,16 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       // Lanes of four hold a row's columns side by side; turned among them, a store writes 8 rows' 128 (64)
       // contiguous bytes where a thread's own row would be 32 lines (64 prompts of 256 tokens: STORE_FIGURES).
       constexpr int N = D / 16, V = N / 4;  // column eights of half the dimensions; of a lane's store
-      float o[2][4 * N];
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        tmem_ld_16x256b<N>(trow + (uint32_t(half * 16) << 16) + kO + uint32_t(w * (D / 2)), o[half]);
-      tc::tmem_wait_ld();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bOFree));
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        float o[4 * N];
+        tmem_ld_16x256b<N>(trow + (uint32_t(half * 16) << 16) + kO + uint32_t(w * (D / 2)), o);
+        tc::tmem_wait_ld();
+        if (half == 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bOFree));
+        }
 #pragma unroll
         for (int up = 0; up < 2; ++up) {
           const int row = half * 16 + up * 8 + (lane >> 2);
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
           uint32_t x[V][4];  // lane a of four: eights a V .. a V + V - 1
 #pragma unroll
           for (int j = 0; j < N; ++j) {
-            const float* y = o[half] + 4 * j + 2 * up;
+            const float* y = o + 4 * j + 2 * up;
             const __nv_bfloat162 h = __floats2bfloat162_rn(y[0] * by, y[1] * by);
             x[j % V][j / V] = by == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&h);  // a row that sees no key
           }
@@ -563,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
             for (int v = 0; v < V; ++v) *reinterpret_cast<uint4*>(out + 8 * v) = make_uint4(x[v][0], x[v][1], x[v][2], x[v][3]);
           }
         }
+      }
       return true;
     };
     // One round: a step of this warpgroup's if its turn is, then the output due. (One place for each: the
