@@ -180,73 +180,78 @@ __device__ __forceinline__ int key_of(int r) {
   return (r & 8) + ((r & 1) ? (h ^ 1) + 4 : h);
 }
 
-// Joins `count` pieces (piece 0 number `lead`, piece i number next + 2 i) of rows row0 .. row0 + n - 1
-// (n <= 4) of segment d: into the output, or into the piece `to`. A lane holds D / 32 elements a row; the rows'
-// loads are independent, so their latency is met once.
-template <int D, int KU>
-__device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int row0, int n, int lane, const float* pieces,
-                                          int count, int lead, int next, float* to) {
-  constexpr int E = D / 32;
+// Joins `count` pieces (piece 0 number `lead`, piece i number next + 2 i) of one row of segment d for every G
+// lanes of the warp: into the output, or into the piece `to`. The pieces' maxima and sums come a lane a
+// piece, then the rows, two pieces at a time: little code, which is met cold, and few waits.
+template <int D, int KU, int G>
+__device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int row, int lane, const float* pieces, int count,
+                                          int lead, int next, float* to) {
+  constexpr int E = D / G;  // a lane's elements, four (two) at a time
+  constexpr int V = E >= 4 ? 4 : 2;
+  const int sub = lane % G;
   Request r;
   request_of<KU>(p, d.z, r);
-  const int head = d.w / r.tiles, tile = d.w - head * r.tiles;
-  n = min(n, r.q_len * p.group - tile * kRows - row0);
-  float m[4], l[4], o[4][E];
+  const int head = d.w / r.tiles, tile = d.w - head * r.tiles, rr = tile * kRows + row;
+  const bool mine = rr < r.q_len * p.group;  // a row of the request
+  float m = kNoMax, l = 0.f, o[E];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m[i] = kNoMax;
-    l[i] = 0.f;
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 1
+  for (int k0 = 0; k0 < count; k0 += G) {
+    const int k = k0 + sub;
+    const float* ml = pieces + int64_t(k == 0 ? lead : next + 2 * k) * piece_floats<D>() + kRows * D + row;
+    const bool live = mine && k < count;
+    const float mk = live ? ml[0] : kNoMax, lk = live ? ml[kRows] : 0.f;
+    float top = lk == 0.f ? kNoMax : mk;  // an empty piece: its other sums were never written
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[i][e] = 0.f;
-  }
+    for (int x = 1; x < G; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    top = fmaxf(top, m);
+    const float w = lk == 0.f ? 0.f : exp2f(mk - top), before = exp2f(m - top);
+    float sum = lk * w;
+#pragma unroll
+    for (int x = 1; x < G; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    l = l * before + sum;
+    m = top;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= before;
 #pragma unroll 2
-  for (int k = 0; k < count; ++k) {
-    const float* x = pieces + int64_t(k == 0 ? lead : next + 2 * k) * piece_floats<D>() + row0 * D;
-    const float* ml = x - row0 * D + kRows * D + row0;
-    float mk[4], lk[4], y[4][E];
+    for (int j = 0; j < min(G, count - k0); ++j) {
+      const float e0 = __shfl_sync(0xffffffffu, w, j, G);
+      if (e0 == 0.f) continue;
+      const float* x = pieces + int64_t(k0 + j == 0 ? lead : next + 2 * (k0 + j)) * piece_floats<D>() + row * D + sub * V;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) {
-        mk[i] = ml[i];
-        lk[i] = ml[kRows + i];
-        if constexpr (E == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(x + i * D + lane * 4);
-          y[i][0] = f.x, y[i][1] = f.y, y[i][E - 2] = f.z, y[i][E - 1] = f.w;
+      for (int e = 0; e < E; e += V) {
+        float y[V];
+        if constexpr (V == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(x + e * G);
+          y[0] = f.x, y[1] = f.y, y[V - 2] = f.z, y[V - 1] = f.w;
         } else {
-          const float2 f = *reinterpret_cast<const float2*>(x + i * D + lane * 2);
-          y[i][0] = f.x, y[i][1] = f.y;
+          const float2 f = *reinterpret_cast<const float2*>(x + e * G);
+          y[0] = f.x, y[1] = f.y;
         }
-      }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) {
-        if (lk[i] == 0.f) continue;  // an empty piece: its sums were never written
-        const float top = fmaxf(m[i], mk[i]), a = exp2f(m[i] - top), b = exp2f(mk[i] - top);
-        m[i] = top;
-        l[i] = l[i] * a + lk[i] * b;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[i][e] = o[i][e] * a + y[i][e] * b;
+        for (int i = 0; i < V; ++i) o[e + i] += e0 * y[i];
       }
+    }
   }
+  if (!mine) return;
+  if (to) {
+    if (sub == 0) {
+      to[kRows * D + row] = m;
+      to[kRows * D + kRows + row] = l;
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= n) continue;
-    const int row = row0 + i;
-    if (to) {
-      if (lane == 0) {
-        to[kRows * D + row] = m[i];
-        to[kRows * D + kRows + row] = l[i];
-      }
+    for (int e = 0; e < E; ++e) to[row * D + sub * V + e / V * (V * G) + e % V] = o[e];
+  } else {
+    __nv_bfloat16* out =
+        p.out + (int64_t(r.q0 + rr / p.group) * p.num_heads + head * p.group + rr % p.group) * D + sub * V;
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll
-      for (int e = 0; e < E; ++e) to[row * D + lane * E + e] = o[i][e];
-    } else {
-      const int rr = tile * kRows + row;
-      __nv_bfloat16* out = p.out + (int64_t(r.q0 + rr / p.group) * p.num_heads + head * p.group + rr % p.group) * D + lane * E;
-      const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
-      if constexpr (E == 4)
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[i][0] * inv, o[i][1] * inv), pack_bf16(o[i][2] * inv, o[i][3] * inv));
+    for (int e = 0; e < E; e += V) {
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(out + e * G) = make_uint2(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv));
       else
-        *reinterpret_cast<uint32_t*>(out) = pack_bf16(o[i][0] * inv, o[i][1] * inv);
+        *reinterpret_cast<uint32_t*>(out + e * G) = pack_bf16(o[e] * inv, o[e + 1] * inv);
     }
   }
 }
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   __syncthreads();
 
   // ---- pieces of segments cut between this CTA's warps, or between CTAs. A leader is a CTA's first
-  // piece of a segment; the leaders' rows are dealt to the warps, as many at once as leave no warp idle.
+  // piece of a segment; the leaders' rows are dealt to the warps, one by one where there are few leaders.
   const int c0 = first(w0), c1 = first(w0 + kWarps);
   float* cta_pieces = p.pieces + int64_t(num_warps) * 2 * piece_floats<D>();
   const int4 mine = lane < kWarps * 2 ? desc[lane] : make_int4(-1, 0, 0, 0);
@@ -761,7 +766,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   const unsigned leaders =
       __ballot_sync(0xffffffffu, mine.x >= 0 && ((lane & 1) || lane == 0 || mine.x == first(w0 + (lane >> 1))));
   const int num = __popc(leaders);
-  const int at_once = num * kRows <= kWarps ? 1 : num * (kRows / 2) <= kWarps ? 2 : 4;
+  const int at_once = num * kRows <= kWarps ? 1 : 4;
   for (int task = warp; task < num * (kRows / at_once); task += kWarps) {
     const int at = __fns(leaders, 0, task / (kRows / at_once) + 1), row0 = task % (kRows / at_once) * at_once, w = at >> 1;
     const int4 d = desc[at];
@@ -769,7 +774,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     while (w + count < kWarps && first(w0 + w + count) < d.y) ++count;
     float* whole = d.x >= c0 && d.y <= c1 ? nullptr
                                           : cta_pieces + int64_t(blockIdx.x * 2 + (d.x <= c0 ? 0 : 1)) * piece_floats<D>();
-    join_rows<D, KU>(p, d, row0, at_once, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
+    if (at_once == 1)
+      join_rows<D, KU, 32>(p, d, row0, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
+    else
+      join_rows<D, KU, 8>(p, d, row0 + lane / 8, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
   }
 }
 
@@ -781,13 +789,13 @@ __global__ void __launch_bounds__(kRows * 32) attention_int_join_kernel(const In
   const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Deal first(*p.total, num_ctas * kWarps);
   const float* pieces = p.pieces + int64_t(num_ctas) * kWarps * 2 * piece_floats<D>();
-#pragma unroll
+#pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
     const int4 d = p.descs[c * 2 + slot];
     if (d.x < 0 || (slot == 0 && d.x != first(c * kWarps))) continue;
     int count = 1;
     while (c + count < num_ctas && first((c + count) * kWarps) < d.y) ++count;
-    join_rows<D, KU>(p, d, row, 1, lane, pieces, count, c * 2 + slot, c * 2, nullptr);
+    join_rows<D, KU, 32>(p, d, row, lane, pieces, count, c * 2 + slot, c * 2, nullptr);
   }
 }
 
