@@ -36,8 +36,13 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 12;
-constexpr int kRows = 8;  // query rows of a tile
+// A tile of query rows is NT times the 8 columns of an MMA. NT = 2 where a request has more than 8 rows a KV
+// head: the codes are converted once for 16, with 8 warps a CTA (their sums take 255 registers a thread)
+// instead of 12 (two requests of four drafted tokens, 16 rows: TWO_FIGURES).
+template <int NT>
+__host__ __device__ constexpr int num_warps() { return NT == 1 ? 12 : 8; }
+template <int NT>
+__host__ __device__ constexpr int num_rows() { return 8 * NT; }
 constexpr float kNoMax = -1e30f;  // running maximum before any key: finite, so that differences are not NaN
 
 constexpr int kPart = 32;  // keys of a bulk copy at most
@@ -46,13 +51,13 @@ __host__ __device__ constexpr int unit_keys() { return BITS == 4 ? 64 : 32; }
 // A segment's start in units of keys, by the time it takes: DESC_START
 template <int KU>
 __host__ __device__ constexpr int start_units() { return KU == 64 ? 1 : 2; }
-template <int D>
-__host__ __device__ constexpr int num_stages() { return D == 128 ? 2 : 3; }  // of a warp's ring
+template <int D, int NT>
+__host__ __device__ constexpr int num_stages() { return D == 128 && NT == 1 ? 2 : 3; }  // of a warp's ring
 template <int D, int BITS>
 __host__ __device__ constexpr int stage_bytes() { return unit_keys<BITS>() * 2 * (code_row_bytes<D, BITS>() + 4); }
-// a piece: eight rows of D sums, then their maxima and their sums of numerators
-template <int D>
-__host__ __device__ constexpr int piece_floats() { return kRows * D + 2 * kRows; }
+// a piece: a tile's rows of D sums, then their maxima and their sums of numerators
+template <int D, int NT>
+__host__ __device__ constexpr int piece_floats() { return num_rows<NT>() * (D + 2); }
 
 struct IntParams {
   __nv_bfloat16* out;
@@ -80,7 +85,7 @@ struct Request {
   int q0, q_len, L, tiles, span;
 };
 
-template <int KU>
+template <int KU, int NT>
 __device__ __forceinline__ bool request_of(const IntParams& p, int s, Request& r) {
   r.q0 = p.qsl[s];
   const int q1 = p.qsl[s + 1];
@@ -90,7 +95,7 @@ __device__ __forceinline__ bool request_of(const IntParams& p, int s, Request& r
   r.q_len = q1 - r.q0;
   if (r.q_len == 0) return true;
   if (r.q_len > p.max_query_len || r.q_len > r.L || r.L > p.max_seq_len) return false;
-  r.tiles = int((int64_t(r.q_len) * p.group + kRows - 1) / kRows);
+  r.tiles = int((int64_t(r.q_len) * p.group + num_rows<NT>() - 1) / num_rows<NT>());
   r.span = start_units<KU>() + (r.L + KU - 1) / KU;
   return true;
 }
@@ -99,7 +104,7 @@ __device__ __forceinline__ bool request_of(const IntParams& p, int s, Request& r
 struct Segment {
   int s, head, tile, begin, end;  // units [begin, end) of the call
 };
-template <int KU>
+template <int KU, int NT>
 __device__ __forceinline__ Segment segment_of(const IntParams& p, const int* prefix, int u) {
   int s = 0, n = p.num_seqs;
   while (n > 1) {
@@ -108,7 +113,7 @@ __device__ __forceinline__ Segment segment_of(const IntParams& p, const int* pre
     else n = half;
   }
   Request r;
-  request_of<KU>(p, s, r);
+  request_of<KU, NT>(p, s, r);
   const int seg = (u - prefix[s]) / r.span;
   Segment g;
   g.s = s;
@@ -183,14 +188,15 @@ __device__ __forceinline__ int key_of(int r) {
 // Joins `count` pieces (piece 0 number `lead`, piece i number next + 2 i) of one row of segment d for every G
 // lanes of the warp: into the output, or into the piece `to`. The pieces' maxima and sums come a lane a
 // piece, then the rows, two pieces at a time: little code, which is met cold, and few waits.
-template <int D, int KU, int G>
+template <int D, int KU, int G, int NT>
 __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int row, int lane, const float* pieces, int count,
                                           int lead, int next, float* to) {
+  constexpr int kRows = num_rows<NT>();
   constexpr int E = D / G;  // a lane's elements, four (two) at a time
   constexpr int V = E >= 4 ? 4 : 2;
   const int sub = lane % G;
   Request r;
-  request_of<KU>(p, d.z, r);
+  request_of<KU, NT>(p, d.z, r);
   const int head = d.w / r.tiles, tile = d.w - head * r.tiles, rr = tile * kRows + row;
   const bool mine = rr < r.q_len * p.group;  // a row of the request
   float m = kNoMax, l = 0.f, o[E];
@@ -199,7 +205,7 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
 #pragma unroll 1
   for (int k0 = 0; k0 < count; k0 += G) {
     const int k = k0 + sub;
-    const float* ml = pieces + int64_t(k == 0 ? lead : next + 2 * k) * piece_floats<D>() + kRows * D + row;
+    const float* ml = pieces + int64_t(k == 0 ? lead : next + 2 * k) * piece_floats<D, NT>() + kRows * D + row;
     const bool live = mine && k < count;
     const float mk = live ? ml[0] : kNoMax, lk = live ? ml[kRows] : 0.f;
     float top = lk == 0.f ? kNoMax : mk;  // an empty piece: its other sums were never written
@@ -218,7 +224,7 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
     for (int j = 0; j < min(G, count - k0); ++j) {
       const float e0 = __shfl_sync(0xffffffffu, w, j, G);
       if (e0 == 0.f) continue;
-      const float* x = pieces + int64_t(k0 + j == 0 ? lead : next + 2 * (k0 + j)) * piece_floats<D>() + row * D + sub * V;
+      const float* x = pieces + int64_t(k0 + j == 0 ? lead : next + 2 * (k0 + j)) * piece_floats<D, NT>() + row * D + sub * V;
 #pragma unroll
       for (int e = 0; e < E; e += V) {
         float y[V];
@@ -257,9 +263,10 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
 }
 
 // B16: blocks of 16 tokens, whose copies are all of one known size (256 requests of 1024 keys, 4 bits: B16_FIGURES)
-template <int D, int BITS, bool B16>
-__global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const IntParams p) {
-  constexpr int KU = unit_keys<BITS>(), ROW = code_row_bytes<D, BITS>(), STAGE = stage_bytes<D, BITS>(), STAGES = num_stages<D>();
+template <int D, int BITS, bool B16, int NT>
+__global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(const IntParams p) {
+  constexpr int kWarps = num_warps<NT>(), kRows = num_rows<NT>();
+  constexpr int KU = unit_keys<BITS>(), ROW = code_row_bytes<D, BITS>(), STAGE = stage_bytes<D, BITS>(), STAGES = num_stages<D, NT>();
   constexpr int HALF = STAGE / 2;                   // keys' part of a stage, then the values'
   constexpr int NK = D / 16;                        // contraction steps of q.c, and tiles of 16 value dimensions
   constexpr float kMid = BITS == 4 ? 8.f : 128.f;
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     int x = 0;
     if (s < S) {
       Request r;
-      if (!request_of<KU>(p, s, r) && blockIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_RANGE);
+      if (!request_of<KU, NT>(p, s, r) && blockIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_RANGE);
       x = r.tiles * r.span * p.num_kv_heads;
     }
     int inc = x;
@@ -340,11 +347,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     }
   };
   auto locate = [&]() {  // the segment of pr.u, past its start; false: the run ends before its keys
-    const Segment sg = segment_of<KU>(p, prefix, pr.u);
+    const Segment sg = segment_of<KU, NT>(p, prefix, pr.u);
     pr.u = max(pr.u, sg.begin + start_units<KU>());
     if (pr.u >= u1) return false;
     Request r;
-    request_of<KU>(p, sg.s, r);
+    request_of<KU, NT>(p, sg.s, r);
     // keys the tile's last row sees, and the blocks and units that hold them
     const int rows = min(kRows, r.q_len * p.group - sg.tile * kRows), last = (sg.tile * kRows + rows - 1) / p.group;
     const int n = r.L - r.q_len + last + 1;
@@ -358,8 +365,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     pr.in = pr.x * KU - pr.b * p.block_size;
     pr.ent_next = entry(pr.b + lane);
     next_entries(pr.b);
-    const int rr = sg.tile * kRows + min(g, rows - 1);  // the queries, read when the segment's turn comes
-    prefetch_l2(p.q + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D + t * (D / 4));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {  // the queries, read when the segment's turn comes
+      const int rr = sg.tile * kRows + min(g + 8 * nt, rows - 1);
+      prefetch_l2(p.q + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D + t * (D / 4));
+    }
     return true;
   };
   // bytes (a multiple of 16, at most a piece's) of K and of V, 512 a step, of which all but the last are full
@@ -443,9 +453,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
   int stage = 0;
   for (int u = u0; u < u1;) {
     // ---- a segment of the run: units x0 .. x1 - 1 of its keys
-    const Segment sg = segment_of<KU>(p, prefix, u);
+    const Segment sg = segment_of<KU, NT>(p, prefix, u);
     Request r;
-    request_of<KU>(p, sg.s, r);
+    request_of<KU, NT>(p, sg.s, r);
     const int rows = min(kRows, r.q_len * p.group - sg.tile * kRows);
     const int x0 = max(u - sg.begin - start_units<KU>(), 0), x1 = min(sg.end, u1) - sg.begin - start_units<KU>();
     const bool whole = u <= sg.begin && u1 >= sg.end;
@@ -453,21 +463,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     u = min(sg.end, u1);
     if (!whole && lane == 0) desc[warp * 2 + slot] = make_int4(sg.begin, sg.end, sg.s, sg.head * r.tiles + sg.tile);
     if (x1 <= x0) {  // nothing but the start: an empty piece
-      float* ml = p.pieces + int64_t((w0 + warp) * 2 + slot) * piece_floats<D>() + kRows * D;
-      if (lane < 2 * kRows) ml[lane] = lane < kRows ? kNoMax : 0.f;
+      float* ml = p.pieces + int64_t((w0 + warp) * 2 + slot) * piece_floats<D, NT>() + kRows * D;
+      if (lane < 2 * kRows) ml[lane] = lane < kRows ? kNoMax : 0.f;  // (32 at most)
       continue;
     }
     const int j_first = sg.tile * kRows / p.group, j_last = (sg.tile * kRows + rows - 1) / p.group;
     const int n_min = r.L - r.q_len + j_first + 1, n_max = r.L - r.q_len + j_last + 1;  // keys the rows see
-    // Query row g of the tile as f16 with its largest element in [2^14, 2^15): a power of two, so exact
-    // but for elements 2^28 times smaller than the row's largest. Its factor goes into the logits'.
-    uint32_t qb[NK][2];
-    float qsum = 0.f, qoff = 0.f, qfactor;
-    {
-      float f[D / 4];
-      const int rr = sg.tile * kRows + min(g, rows - 1);
+    // Query row g (g + 8) of the tile as f16 with its largest element in [2^14, 2^15): a power of two, so exact
+    // but for elements 2^24 times smaller than the row's largest. Its factor goes into the logits'.
+    uint32_t qb[NT][NK][2];
+    // of query rows 2t and 2t + 1 (and 8 on), whose logits this lane holds
+    float qs[NT][2], off[NT][2], fac[NT][2], m[NT][2], l[NT][2], mid[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = g + 8 * nt;
+      float f[D / 4], qsum = 0.f, qoff = 0.f, big = 0.f;
+      const int rr = sg.tile * kRows + min(row, rows - 1);
       const __nv_bfloat16* src = p.q + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D;
-      float big = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {  // the dimensions of the key row's pieces that this lane takes
         const int dim = BITS == 4 ? t * (D / 4) + 8 * i : (i / 2) * 64 + t * 16 + (i & 1) * 8;
@@ -478,46 +491,48 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
       const int ex = int(__float_as_uint(big) >> 23);  // biased exponent; 0 and 255: left unscaled
-      const int shift = (ex == 0 || ex == 255 || g >= rows) ? 0 : min(127, 14 - (ex - 127));
-      const float mul = g >= rows ? 0.f : __uint_as_float(uint32_t(shift + 127) << 23);
-      qfactor = p.scale_log2 * exp2f(float(-shift));
+      const int shift = (ex == 0 || ex == 255 || row >= rows) ? 0 : min(127, 14 - (ex - 127));
+      const float mul = row >= rows ? 0.f : __uint_as_float(uint32_t(shift + 127) << 23);
+      const float qfactor = p.scale_log2 * exp2f(float(-shift));
 #pragma unroll
       for (int i = 0; i < D / 4; ++i) {
         f[i] = __half2float(__float2half_rn(f[i] * mul));
         qsum += f[i];
         if (BITS == 8 || (i & 1)) qoff += f[i];
       }
-      if (g >= rows) qsum = qoff = 0.f;
-      qoff += __shfl_xor_sync(0xffffffffu, qoff, 1);
-      qoff += __shfl_xor_sync(0xffffffffu, qoff, 2);
-      qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
-      qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
+      if (row >= rows) qsum = qoff = 0.f;
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        qoff += __shfl_xor_sync(0xffffffffu, qoff, d);
+        qsum += __shfl_xor_sync(0xffffffffu, qsum, d);
+      }
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         if (BITS == 4) {  // word k / 2 of the lane's piece: elements (0, 4), (1, 5), then (2, 6), (3, 7)
           const float* e = f + 8 * (k / 2) + 2 * (k & 1);
-          qb[k][0] = pack_f16(e[0], e[4]);
-          qb[k][1] = pack_f16(e[1] * 0.0625f, e[5] * 0.0625f);  // their codes come 16-fold
+          qb[nt][k][0] = pack_f16(e[0], e[4]);
+          qb[nt][k][1] = pack_f16(e[1] * 0.0625f, e[5] * 0.0625f);  // their codes come 16-fold
         } else {
-          qb[k][0] = pack_f16(f[4 * k], f[4 * k + 1]);
-          qb[k][1] = pack_f16(f[4 * k + 2], f[4 * k + 3]);
+          qb[nt][k][0] = pack_f16(f[4 * k], f[4 * k + 1]);
+          qb[nt][k][1] = pack_f16(f[4 * k + 2], f[4 * k + 3]);
         }
-        if (g >= rows) qb[k][0] = qb[k][1] = 0u;
+        if (row >= rows) qb[nt][k][0] = qb[nt][k][1] = 0u;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        qs[nt][h] = __shfl_sync(0xffffffffu, qsum, (2 * t + h) * 4);
+        off[nt][h] = -kOffset * __shfl_sync(0xffffffffu, qoff, (2 * t + h) * 4);
+        fac[nt][h] = __shfl_sync(0xffffffffu, qfactor, (2 * t + h) * 4);
+        m[nt][h] = kNoMax;
+        l[nt][h] = mid[nt][h] = 0.f;
+        lim[nt][h] = r.L - r.q_len + (sg.tile * kRows + min(8 * nt + 2 * t + h, rows - 1)) / p.group + 1;
       }
     }
-    // of query rows 2t and 2t + 1, whose logits this lane holds
-    float qs[2], off[2], fac[2], m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, mid[2] = {0.f, 0.f};
-    int lim[2];
+    float o[NT][NK][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      qs[h] = __shfl_sync(0xffffffffu, qsum, (2 * t + h) * 4);
-      off[h] = -kOffset * __shfl_sync(0xffffffffu, qoff, (2 * t + h) * 4);
-      fac[h] = __shfl_sync(0xffffffffu, qfactor, (2 * t + h) * 4);
-      lim[h] = r.L - r.q_len + (sg.tile * kRows + min(2 * t + h, rows - 1)) / p.group + 1;
-    }
-    float o[NK][4];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < NK; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int i = 0; i < NK; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     // Numerators times value steps enter the second product as f16 (rounded to 2^-11 relative at most: an
     // eighth of the output's own rounding), scaled by the power of two 2^wexp that keeps the steps seen so
     // far below 2^7 and so the products below 2^15; what rounds to nothing is 2^-31 of the largest.
@@ -528,9 +543,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     // code: the two together have to stay in the instruction cache)
     auto unit = [&](const unsigned char* st, int key0, int tile0, auto tail_c) {
       constexpr bool kTail = decltype(tail_c)::value;
-      constexpr int TILES = kTail ? 1 : KU / 16;
-      // ---- q.c of 16 keys x 8 query rows a tile, all of a unit's tiles before their logits: independent chains
-      float s[TILES][4], s1[TILES][4];
+      constexpr int TILES = kTail ? 1 : NT == 1 ? KU / 16 : 2;
+      // ---- q.c of 16 keys x 8 NT query rows a tile, all tiles before their logits: independent chains, two a
+      // product with NT = 1
+      float s[TILES][NT][4], s1[TILES][4];
       uint32_t pk[TILES][2], pv[TILES][2];
 #pragma unroll
       for (int tile = 0; tile < TILES; ++tile) {
@@ -538,7 +554,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
         const unsigned char* two = st + (at >> 1) * (32 * (ROW + 4));  // pieces are at most 32 keys
         const unsigned char *base = two + (at & 1) * next_code, *pbase = two + (at & 1) * next_param;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[tile][i] = s1[tile][i] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          s1[tile][i] = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[tile][nt][i] = 0.f;
+        }
+        // one step of the contraction: A of 16 keys, for every query row
+        auto step = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_16816(NT == 1 && (k & 1) ? s1[tile] : s[tile][nt], a0, a1, a2, a3, qb[nt][k][0], qb[nt][k][1], true);
+        };
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           pk[tile][i] = lds32(smem_u32(pbase + par_at[i]));  // (a plain load is made again at every use)
@@ -553,10 +579,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
 #pragma unroll
           for (int w = 0; w < D / 32; ++w) {  // c of even nibbles, 16 (64 + c) of odd ones
             const uint32_t x = a[0][w], y = a[1][w];
-            mma_16816(s[tile], h2(and_or(x, M, C), low), h2(and_or(y, M, C), low), and_or(x, N, C), and_or(y, N, C),
-                      qb[2 * w][0], qb[2 * w][1], true);
-            mma_16816(s1[tile], h2(and_or(x >> 8, M, C), low), h2(and_or(y >> 8, M, C), low), and_or(x >> 8, N, C),
-                      and_or(y >> 8, N, C), qb[2 * w + 1][0], qb[2 * w + 1][1], true);
+            step(2 * w, h2(and_or(x, M, C), low), h2(and_or(y, M, C), low), and_or(x, N, C), and_or(y, N, C));
+            step(2 * w + 1, h2(and_or(x >> 8, M, C), low), h2(and_or(y >> 8, M, C), low), and_or(x >> 8, N, C),
+                 and_or(y >> 8, N, C));
           }
         } else {
 #pragma unroll
@@ -567,16 +592,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const uint32_t H = 0x64646464u;
-              mma_16816((w & 1) ? s1[tile] : s[tile], __byte_perm(x[w], H, 0x4140), __byte_perm(y[w], H, 0x4140),
-                        __byte_perm(x[w], H, 0x4342), __byte_perm(y[w], H, 0x4342), qb[4 * c + w][0], qb[4 * c + w][1],
-                        true);
+              step(4 * c + w, __byte_perm(x[w], H, 0x4140), __byte_perm(y[w], H, 0x4140), __byte_perm(x[w], H, 0x4342),
+                   __byte_perm(y[w], H, 0x4342));
             }
           }
         }
       }
       // ---- logits (in powers of two), numerators: [0], [1] key_of(g), [2], [3] key_of(g + 8)
-      float x[TILES][4], ws[TILES][2], midv[TILES][2];
-      bool hidden[TILES][4];
+      float x[TILES][NT][4], ws[TILES][2], midv[TILES][2];
+      bool hidden[TILES][NT][4];
 #pragma unroll
       for (int tile = 0; tile < TILES; ++tile)
 #pragma unroll
@@ -587,35 +611,32 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
           ws[tile][i] = param_step(pv[tile][i]);
           midv[tile][i] = fmaf(ws[tile][i], kMid, param_lo(pv[tile][i]));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float c = s[tile][2 * i + h] + s1[tile][2 * i + h] + off[h];
-            x[tile][2 * i + h] = fmaf(c, step, lo * qs[h]) * fac[h];
-            hidden[tile][2 * i + h] = kTail && key >= lim[h];
-            if (hidden[tile][2 * i + h]) x[tile][2 * i + h] = -INFINITY;
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int e = 2 * i + h;
+              const float c = (NT == 1 ? s[tile][nt][e] + s1[tile][e] : s[tile][nt][e]) + off[nt][h];
+              x[tile][nt][e] = fmaf(c, step, lo * qs[nt][h]) * fac[nt][h];
+              hidden[tile][nt][e] = kTail && key >= lim[nt][h];
+              if (hidden[tile][nt][e]) x[tile][nt][e] = -INFINITY;
+            }
         }
       // The reference maximum moves only when a logit passes it by 2^8, the steps' power of two when
       // one passes it twofold: then, for the whole warp, the sums so far are scaled.
-      float top[2] = {fmaxf(x[0][0], x[0][2]), fmaxf(x[0][1], x[0][3])}, big = fmaxf(ws[0][0], ws[0][1]);
+      float top[NT][2], big = fmaxf(ws[0][0], ws[0][1]);
+      bool move = false;
 #pragma unroll
-      for (int tile = 1; tile < TILES; ++tile) {
-        top[0] = fmax3(top[0], x[tile][0], x[tile][2]);
-        top[1] = fmax3(top[1], x[tile][1], x[tile][3]);
-        big = fmax3(big, ws[tile][0], ws[tile][1]);
-      }
-      if (__any_sync(0xffffffffu, top[0] - m[0] > 8.f || top[1] - m[1] > 8.f || big * wscale > 128.f)) {
-        float alpha[2];
+      for (int tile = 1; tile < TILES; ++tile) big = fmax3(big, ws[tile][0], ws[tile][1]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float up = top[h];
+          top[nt][h] = fmaxf(x[0][nt][h], x[0][nt][2 + h]);
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
-          if (!(up - m[h] > 8.f)) up = m[h];
-          alpha[h] = exp2f(m[h] - up);
-          m[h] = up;
-          l[h] *= alpha[h];
-          mid[h] *= alpha[h];
+          for (int tile = 1; tile < TILES; ++tile) top[nt][h] = fmax3(top[nt][h], x[tile][nt][h], x[tile][nt][2 + h]);
+          move = move || top[nt][h] - m[nt][h] > 8.f;
         }
+      if (__any_sync(0xffffffffu, move || big * wscale > 128.f)) {
         // NaN steps (of rows that hold NaN) do not count
         const uint32_t bits = __float_as_uint(big);
         const uint32_t most = __reduce_max_sync(0xffffffffu, bits <= 0x7f800000u ? bits : 0u);
@@ -627,36 +648,58 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
           wscale = __uint_as_float(uint32_t(want + 127) << 23);
         }
 #pragma unroll
-        for (int i = 0; i < NK; ++i)
+        for (int nt = 0; nt < NT; ++nt) {
+          float alpha[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e & 1] * beta;
+          for (int h = 0; h < 2; ++h) {
+            float up = top[nt][h];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
+            if (!(up - m[nt][h] > 8.f)) up = m[nt][h];
+            alpha[h] = exp2f(m[nt][h] - up);
+            m[nt][h] = up;
+            l[nt][h] *= alpha[h];
+            mid[nt][h] *= alpha[h];
+          }
+#pragma unroll
+          for (int i = 0; i < NK; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][i][e] *= alpha[e & 1] * beta;
+        }
       }
-      uint32_t pb[TILES][2];
+      uint32_t pb[TILES][NT][2];
 #pragma unroll
       for (int tile = 0; tile < TILES; ++tile)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float wi = ws[tile][i] * wscale;
-          float w[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float e = ex2_ftz(x[tile][2 * i + h] - m[h]);
-            l[h] += e;
-            w[h] = e * wi;
-            if (hidden[tile][2 * i + h]) {
-              w[h] = 0.f;  // not 0 * NaN
-            } else {
-              mid[h] = fmaf(e, midv[tile][i], mid[h]);
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float e = ex2_ftz(x[tile][nt][2 * i + h] - m[nt][h]);
+              l[nt][h] += e;
+              w[h] = e * wi;
+              if (hidden[tile][nt][2 * i + h]) {
+                w[h] = 0.f;  // not 0 * NaN
+              } else {
+                mid[nt][h] = fmaf(e, midv[tile][i], mid[nt][h]);
+              }
             }
+            pb[tile][nt][i] = movm(pack_f16(w[0], w[1]));
           }
-          pb[tile][i] = movm(pack_f16(w[0], w[1]));
         }
-      // ---- 16 value dimensions x 8 query rows a step: rows of the tile of codes - mid, dimensions
+      // ---- 16 value dimensions x 8 NT query rows a step: rows of the tile of codes - mid, dimensions
       // (D / 8) g + 2 i in rows 0 .. 7 and the next in rows 8 .. 15
 #pragma unroll
       for (int tile = 0; tile < TILES; ++tile) {
         const int at = tile0 + tile;
         const unsigned char* base = st + (at >> 1) * (32 * (ROW + 4)) + (at & 1) * next_code;
+        auto step = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][i], a0, a1, a2, a3, pb[tile][nt][0], pb[tile][nt][1], true);
+        };
         if constexpr (BITS == 4) {
           const __half2 low = __half2half2(__float2half_rn(-1032.f)), high = __half2half2(__float2half_rn(-72.f)),
                         six = __half2half2(__float2half_rn(0.0625f));
@@ -670,10 +713,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
             for (int half = 0; half < 2; ++half) {  // elements 0 .. 3, 4 .. 7 of the words
               const uint32_t sel = half ? 0x7632 : 0x5410;
               const uint32_t a = __byte_perm(v[0][w], v[1][w], sel), b = __byte_perm(v[2][w], v[3][w], sel);
-              mma_16816(o[4 * w + 2 * half], h2(and_or(a, M, C), low), h2(and_or(a, N, C), six, high), h2(and_or(b, M, C), low),
-                        h2(and_or(b, N, C), six, high), pb[tile][0], pb[tile][1], true);
-              mma_16816(o[4 * w + 2 * half + 1], h2(and_or(a >> 8, M, C), low), h2(and_or(a >> 8, N, C), six, high),
-                        h2(and_or(b >> 8, M, C), low), h2(and_or(b >> 8, N, C), six, high), pb[tile][0], pb[tile][1], true);
+              step(4 * w + 2 * half, h2(and_or(a, M, C), low), h2(and_or(a, N, C), six, high), h2(and_or(b, M, C), low),
+                   h2(and_or(b, N, C), six, high));
+              step(4 * w + 2 * half + 1, h2(and_or(a >> 8, M, C), low), h2(and_or(a >> 8, N, C), six, high),
+                   h2(and_or(b >> 8, M, C), low), h2(and_or(b >> 8, N, C), six, high));
             }
         } else {
           const __half2 sub = __half2half2(__float2half_rn(-1152.f));
@@ -687,8 +730,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
             for (int half = 0; half < 2; ++half) {
               const uint32_t sel = half ? 0x7362 : 0x5140;
               const uint32_t a = __byte_perm(v[0][w], v[1][w], sel), b = __byte_perm(v[2][w], v[3][w], sel);
-              mma_16816(o[2 * w + half], h2(__byte_perm(a, H, 0x4140), sub), h2(__byte_perm(a, H, 0x4342), sub),
-                        h2(__byte_perm(b, H, 0x4140), sub), h2(__byte_perm(b, H, 0x4342), sub), pb[tile][0], pb[tile][1], true);
+              step(2 * w + half, h2(__byte_perm(a, H, 0x4140), sub), h2(__byte_perm(a, H, 0x4342), sub),
+                   h2(__byte_perm(b, H, 0x4140), sub), h2(__byte_perm(b, H, 0x4342), sub));
             }
         }
       }
@@ -700,7 +743,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
       const int key0 = x * KU;
       const unsigned char* st = ring + stage * STAGE;
       if (key0 + KU <= n_min) {
-        unit(st, key0, 0, std::false_type{});
+#pragma unroll 1
+        for (int tile = 0; tile < KU / 16; tile += NT == 1 ? KU / 16 : 2) unit(st, key0, tile, std::false_type{});
       } else {
 #pragma unroll 1
         for (int tile = 0; tile < KU / 16 && key0 + tile * 16 < n_max; ++tile) unit(st, key0, tile, std::true_type{});
@@ -712,50 +756,51 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     // ---- the segment's end in this run: sums over the lanes that share a query row, then out or a piece
     const float unscale = exp2f(float(-wexp));
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
-        mid[h] += __shfl_xor_sync(0xffffffffu, mid[h], d);
-      }
+      for (int h = 0; h < 2; ++h) {
+        float sum = l[nt][h], add = mid[nt][h];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = 2 * t + h;
-      if (row >= rows) continue;
-      float f[D / 8];
+        for (int d = 4; d < 32; d <<= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          add += __shfl_xor_sync(0xffffffffu, add, d);
+        }
+        const int row = 8 * nt + 2 * t + h;
+        if (row >= rows) continue;
+        float f[D / 8];
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        f[2 * i] = fmaf(o[i][h], unscale, mid[h]);
-        f[2 * i + 1] = fmaf(o[i][2 + h], unscale, mid[h]);
-      }
-      if (whole) {
-        const float inv = l[h] > 0.f ? 1.f / l[h] : (l[h] == 0.f ? 0.f : l[h]);
-        const int rr = sg.tile * kRows + row;
-        __nv_bfloat16* dst =
-            p.out + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D + g * (D / 8);
+        for (int i = 0; i < NK; ++i) {
+          f[2 * i] = fmaf(o[nt][i][h], unscale, add);
+          f[2 * i + 1] = fmaf(o[nt][i][2 + h], unscale, add);
+        }
+        if (whole) {
+          const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+          const int rr = sg.tile * kRows + row;
+          __nv_bfloat16* dst =
+              p.out + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D + g * (D / 8);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) f[i] *= inv;
+          for (int i = 0; i < D / 8; ++i) f[i] *= inv;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) reinterpret_cast<uint4*>(dst)[i] = Elem<__nv_bfloat16>::pack(f + 8 * i);
-      } else {
-        float* dst = p.pieces + int64_t((w0 + warp) * 2 + slot) * piece_floats<D>();
+          for (int i = 0; i < D / 64; ++i) reinterpret_cast<uint4*>(dst)[i] = Elem<__nv_bfloat16>::pack(f + 8 * i);
+        } else {
+          float* dst = p.pieces + int64_t((w0 + warp) * 2 + slot) * piece_floats<D, NT>();
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          reinterpret_cast<float4*>(dst + row * D + g * (D / 8))[i] =
-              make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        if (g == 0) {
-          dst[kRows * D + row] = m[h];
-          dst[kRows * D + kRows + row] = l[h];
+          for (int i = 0; i < D / 32; ++i)
+            reinterpret_cast<float4*>(dst + row * D + g * (D / 8))[i] =
+                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+          if (g == 0) {
+            dst[kRows * D + row] = m[nt][h];
+            dst[kRows * D + kRows + row] = sum;
+          }
         }
       }
-    }
   }
   __syncthreads();
 
   // ---- pieces of segments cut between this CTA's warps, or between CTAs. A leader is a CTA's first
   // piece of a segment; the leaders' rows are dealt to the warps, one by one where there are few leaders.
   const int c0 = first(w0), c1 = first(w0 + kWarps);
-  float* cta_pieces = p.pieces + int64_t(num_warps) * 2 * piece_floats<D>();
+  float* cta_pieces = p.pieces + int64_t(num_warps) * 2 * piece_floats<D, NT>();
   const int4 mine = lane < kWarps * 2 ? desc[lane] : make_int4(-1, 0, 0, 0);
   if (warp == 0) {
     // slot 0: a segment from before c0, or one from c0 to past c1; slot 1: one that goes on behind c1
@@ -773,60 +818,67 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int_kernel(const Int
     int count = 1;
     while (w + count < kWarps && first(w0 + w + count) < d.y) ++count;
     float* whole = d.x >= c0 && d.y <= c1 ? nullptr
-                                          : cta_pieces + int64_t(blockIdx.x * 2 + (d.x <= c0 ? 0 : 1)) * piece_floats<D>();
+                                          : cta_pieces + int64_t(blockIdx.x * 2 + (d.x <= c0 ? 0 : 1)) * piece_floats<D, NT>();
     if (at_once == 1)
-      join_rows<D, KU, 32>(p, d, row0, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
+      join_rows<D, KU, 32, NT>(p, d, row0, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
     else
-      join_rows<D, KU, 8>(p, d, row0 + lane / 8, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
+      join_rows<D, KU, 8, NT>(p, d, row0 + lane / 8, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
   }
 }
 
 // Segments cut between CTAs: CTA c joins those whose first piece is c's; a warp a row.
-template <int D, int BITS>
-__global__ void __launch_bounds__(kRows * 32) attention_int_join_kernel(const IntParams p, int num_ctas) {
-  constexpr int KU = unit_keys<BITS>();
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(num_rows<NT>() * 32) attention_int_join_kernel(const IntParams p, int num_ctas) {
+  constexpr int KU = unit_keys<BITS>(), kWarps = num_warps<NT>();
   griddep_wait();
   const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Deal first(*p.total, num_ctas * kWarps);
-  const float* pieces = p.pieces + int64_t(num_ctas) * kWarps * 2 * piece_floats<D>();
+  const float* pieces = p.pieces + int64_t(num_ctas) * kWarps * 2 * piece_floats<D, NT>();
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
     const int4 d = p.descs[c * 2 + slot];
     if (d.x < 0 || (slot == 0 && d.x != first(c * kWarps))) continue;
     int count = 1;
     while (c + count < num_ctas && first((c + count) * kWarps) < d.y) ++count;
-    join_rows<D, KU, 32>(p, d, row, lane, pieces, count, c * 2 + slot, c * 2, nullptr);
+    join_rows<D, KU, 32, NT>(p, d, row, lane, pieces, count, c * 2 + slot, c * 2, nullptr);
   }
 }
 
 constexpr size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
-template <int D, int BITS>
+template <int D, int BITS, int NT>
 cudaError_t run_int(IntParams p, const AttnIntArgs& a, cudaStream_t stream) {
-  constexpr int STAGE = stage_bytes<D, BITS>();
-  constexpr size_t rings = size_t(kWarps) * num_stages<D>() * STAGE, most = rings + kIntMaxSeqs * 4;
+  constexpr size_t rings = size_t(num_warps<NT>()) * num_stages<D, NT>() * stage_bytes<D, BITS>(),
+                   most = rings + kIntMaxSeqs * 4;
   static_assert(most + 1024 <= 232448, "shared memory of a CTA");
   const bool b16 = a.block_size == 16;
-  const cudaError_t e = b16 ? ensure_smem<attention_int_kernel<D, BITS, true>>(most)
-                            : ensure_smem<attention_int_kernel<D, BITS, false>>(most);
+  const cudaError_t e = b16 ? ensure_smem<attention_int_kernel<D, BITS, true, NT>>(most)
+                            : ensure_smem<attention_int_kernel<D, BITS, false, NT>>(most);
   if (e != cudaSuccess) return e;
-  const cudaError_t l = launch_pdl(b16 ? attention_int_kernel<D, BITS, true> : attention_int_kernel<D, BITS, false>, dim3(a.num_ctas), dim3(kWarps * 32),
-                                   rings + size_t(a.num_seqs) * 4, stream, p);
+  const cudaError_t l = launch_pdl(b16 ? attention_int_kernel<D, BITS, true, NT> : attention_int_kernel<D, BITS, false, NT>,
+                                   dim3(a.num_ctas), dim3(num_warps<NT>() * 32), rings + size_t(a.num_seqs) * 4, stream, p);
   if (l != cudaSuccess) return l;
-  return launch_pdl(attention_int_join_kernel<D, BITS>, dim3(a.num_ctas), dim3(kRows * 32), 0, stream, p, a.num_ctas);
+  return launch_pdl(attention_int_join_kernel<D, BITS, NT>, dim3(a.num_ctas), dim3(num_rows<NT>() * 32), 0, stream, p,
+                    a.num_ctas);
+}
+template <int D, int BITS>
+cudaError_t run_rows(const IntParams& p, const AttnIntArgs& a, cudaStream_t stream) {
+  return int64_t(a.max_query_len) * p.group > num_rows<1>() ? run_int<D, BITS, 2>(p, a, stream)
+                                                            : run_int<D, BITS, 1>(p, a, stream);
 }
 
 }  // namespace
 
 // descs, total, pieces of the CTAs' warps and of the CTAs
 size_t attention_int_workspace_bytes(int head_dim, int num_ctas) {
-  const size_t piece = (kRows * size_t(head_dim) + 2 * kRows) * 4;
-  return align_up(size_t(num_ctas) * 2 * sizeof(int4)) + 256 + size_t(num_ctas) * (kWarps + 1) * 2 * piece;
+  const size_t row = (size_t(head_dim) + 2) * 4;
+  const size_t one = num_rows<1>() * (num_warps<1>() + 1), two = num_rows<2>() * (num_warps<2>() + 1);
+  return align_up(size_t(num_ctas) * 2 * sizeof(int4)) + 256 + size_t(num_ctas) * 2 * (one > two ? one : two) * row;
 }
 
 bool attention_int_fits(const AttnIntArgs& a) {
   const int ku = a.bits == 4 ? unit_keys<4>() : unit_keys<8>();
-  const int64_t tiles = (int64_t(a.num_tokens) * (a.num_heads / a.num_kv_heads) + kRows - 1) / kRows + a.num_seqs;
+  const int64_t tiles = int64_t(a.num_tokens) * (a.num_heads / a.num_kv_heads) / num_rows<1>() + 1 + a.num_seqs;
   const int64_t units = (int64_t(a.max_seq_len) + ku - 1) / ku + 2;
   // units are counted in 32 bits (a step of all warps past the end, too)
   return a.num_seqs <= kIntMaxSeqs && tiles <= 0x7fffffff / a.num_kv_heads &&
@@ -861,8 +913,8 @@ cudaError_t launch_attention_int(const AttnIntArgs& a, cudaStream_t stream) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.part = a.block_size & -a.block_size;
   if (p.part > kPart) p.part = kPart;
-  if (a.bits == 4) return a.head_dim == 64 ? run_int<64, 4>(p, a, stream) : run_int<128, 4>(p, a, stream);
-  return a.head_dim == 64 ? run_int<64, 8>(p, a, stream) : run_int<128, 8>(p, a, stream);
+  if (a.bits == 4) return a.head_dim == 64 ? run_rows<64, 4>(p, a, stream) : run_rows<128, 4>(p, a, stream);
+  return a.head_dim == 64 ? run_rows<64, 8>(p, a, stream) : run_rows<128, 8>(p, a, stream);
 }
 
 }  // namespace pa
