@@ -539,11 +539,12 @@ int pa_attention_sparse(void* out, const void* q, const void* k_cache, const voi
  *
  * pa_attention_int: pa_attention over such caches, q and out bf16 [num_tokens, num_heads, head_dim]:
  * token j of a request's q_len sits at position seq_lens - q_len + j and sees the positions up to its
- * own. Made for decode and a few drafted tokens: 8 / (num_heads / num_kv_heads) tokens share one pass
- * over a head's codes (any group size that divides num_heads); a long chunk is faster through
- * pa_kv_read_int and pa_attention_packed. Rows of no request are left as they are; a request with more
- * than max_query_len queries, more keys than max_seq_len, or q_len > seq_len sets PA_DEVERR_SEQ_RANGE
- * and its rows are left as they are. A key or value row that reads back as NaN gives NaN to the tokens
+ * own. Made for decode and a few drafted tokens: 8 of a request's (token, query head) rows of a KV head
+ * share one pass over its codes, 16 where max_query_len tokens make more than 8 (any num_heads that
+ * num_kv_heads divides); a long chunk is faster through pa_kv_read_int and pa_attention_packed. Rows of no
+ * request are left as they are; a request with more than max_query_len queries, more keys than max_seq_len,
+ * or q_len > seq_len sets PA_DEVERR_SEQ_RANGE and its rows are left as they are (other requests' too, where
+ * query_start_loc decreases). A key or value row that reads back as NaN gives NaN to the tokens
  * that see it, and to no other. workspace: device, pa_attention_int_workspace_size bytes, 16-byte
  * aligned, no contents needed; calls that may overlap on the GPU need one each. The result depends on
  * nothing but the arguments' contents and the GPU's number of SMs. num_seqs <= 4096

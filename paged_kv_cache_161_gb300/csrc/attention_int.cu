@@ -10,20 +10,22 @@
 // difference of two large sums.
 //
 // Bound: the cache's bytes (68 a row and head at 128 elements of 4 bits), and the instructions that turn
-// codes into 16-bit operands, about one an element. So: one pass, and every element converted once
-// for up to eight query rows.
+// codes into 16-bit operands, about one an element of K and V. So: one pass, and every element converted once
+// for up to 8 or 16 query rows. Measured (GB300, 32 / 8 heads x 128): 64 requests of 32768 keys, 8 bits,
+// 674 us, 6600 GB/s of cache, 0.97 of the measured copy rate; 256 requests of 16 to 8192 keys around 1024, 4
+// bits, 100 us, 4700 GB/s (4 bits are bound by instructions: 256 requests of 1024 keys take 71 us, 4000 GB/s).
 //
-// Work: a unit is unit_keys keys of one segment (request, KV head, tile of 8 query rows: query tokens x
-// the head's query heads). The units of all segments, in order, are dealt to the grid's warps in
-// equal runs; a warp streams its run through a ring of its own in shared memory (bulk copies of the
-// records, one a block where a block is not larger than a unit), and no warp waits for another while
-// it streams. Segments cut between warps leave pieces (m, l, unnormalised output) in the workspace:
-// a CTA joins those of its 12 warps, a second kernel those cut between CTAs.
+// Work: a unit is unit_keys keys of one segment (request, KV head, tile of 8 or 16 query rows: query tokens
+// x the head's query heads). The units of all segments, in order, are dealt to the grid's warps in
+// equal runs; a warp streams its run through a ring of its own in shared memory, and no warp waits for
+// another while it streams. Segments cut between warps leave pieces (m, l, unnormalised output) in the
+// workspace: a CTA joins those of its warps, a second kernel those cut between CTAs.
 //
 // Operands (mma.sync m16n8k16, keys as the 16 rows, query rows as the 8 columns): a code under the
 // bits of the f16 1024 is that number plus the code (or 1024 + 16 c, a nibble higher), one logic
-// instruction for two, and half an addition more where the 1024 has to go before the products. Which dimension sits where in a contraction is free as long as both sides
-// agree, so a lane takes 16-byte pieces of rows as they lie; so is which key is which row.
+// instruction for two, and half an addition more where the 1024 has to go before the products. Which
+// dimension sits where in a contraction is free as long as both sides agree, so a lane takes 16-byte pieces
+// of rows as they lie; so is which key is which row.
 //
 // The kernels start before the one in front of them has ended and read what it wrote behind
 // griddep_wait(): none of their pointers is __restrict__ or read through __ldg.
@@ -37,20 +39,22 @@ namespace pa {
 namespace {
 
 // A tile of query rows is NT times the 8 columns of an MMA. NT = 2 where a request has more than 8 rows a KV
-// head: the codes are converted once for 16, with 8 warps a CTA (their sums take 255 registers a thread)
-// instead of 12 (two requests of four drafted tokens, 16 rows: TWO_FIGURES).
+// head: the codes are converted once for 16, with 8 warps a CTA (their sums take 248 registers a thread)
+// instead of 12 (two requests of four drafted tokens, 40000 keys: 4 bits 51 us with two tiles of 8, 45 us
+// with one of 16; 8 bits 57, 49 us).
 template <int NT>
 __host__ __device__ constexpr int num_warps() { return NT == 1 ? 12 : 8; }
 template <int NT>
 __host__ __device__ constexpr int num_rows() { return 8 * NT; }
 constexpr float kNoMax = -1e30f;  // running maximum before any key: finite, so that differences are not NaN
 
-constexpr int kPart = 32;  // keys of a bulk copy at most
+constexpr int kPart = 32;  // keys of a copy at most
 template <int BITS>
 __host__ __device__ constexpr int unit_keys() { return BITS == 4 ? 64 : 32; }
-// A segment's start in units of keys, by the time it takes: DESC_START
+// A segment's start in units of keys, by the time it takes (256 requests of 16 to 8192 keys around 1024, 4
+// bits: 0 units 121 us, 1 108, 2 100; 8 bits: 0 units 167 us, 2 158, 4 157)
 template <int KU>
-__host__ __device__ constexpr int start_units() { return KU == 64 ? 1 : 2; }
+__host__ __device__ constexpr int start_units() { return 2; }
 template <int D, int NT>
 __host__ __device__ constexpr int num_stages() { return D == 128 && NT == 1 ? 2 : 3; }  // of a warp's ring
 template <int D, int BITS>
@@ -74,11 +78,11 @@ struct IntParams {
   int64_t num_blocks;
   int max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len;
   int num_heads, num_kv_heads, group, block_size;
-  int part;    // keys a bulk copy of codes covers: the largest power of two in block_size, at most kPart
+  int part;    // keys a copy of codes covers: the largest power of two in block_size, at most kPart
   float scale_log2;
 };
 
-// What a request contributes: `tiles` tiles of 8 rows, each a segment of `span` units a KV head: kStart
+// What a request contributes: `tiles` tiles of rows, each a segment of `span` units a KV head: start_units
 // that stand for a segment's start (its queries, table, sums: none of them is work of its own), then
 // those of its keys.
 struct Request {
@@ -262,7 +266,8 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
   }
 }
 
-// B16: blocks of 16 tokens, whose copies are all of one known size (256 requests of 1024 keys, 4 bits: B16_FIGURES)
+// B16: blocks of 16 tokens, whose copies are all of one known size (256 requests of 1024 keys, 4 bits: 82 us
+// without, 70 us with; two requests of four drafts, 8 bits: 53, 49 us)
 template <int D, int BITS, bool B16, int NT>
 __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(const IntParams p) {
   constexpr int kWarps = num_warps<NT>(), kRows = num_rows<NT>();
@@ -284,7 +289,9 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
   if (threadIdx.x < kWarps * 2) desc[threadIdx.x] = make_int4(-1, 0, 0, 0);
   griddep_wait();
 
-  // ---- the plan: units of every request, their prefix, this warp's run
+  // ---- the plan: units of every request, their prefix, this warp's run. Sums stop at 2^31 - 1, which only
+  // requests that lie over one another in query_start_loc can reach.
+  auto add = [](int a, int b) { return int(min(uint32_t(a) + uint32_t(b), 0x7fffffffu)); };
   int total = 0;
   for (int b = 0; b < S; b += kWarps * 32) {
     const int s = b + threadIdx.x;
@@ -298,19 +305,24 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += y;
+      if (lane >= d) inc = add(inc, y);
     }
+    const int before = __shfl_up_sync(0xffffffffu, inc, 1);
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
     int off = total, sum = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) off += wsum[w];
-      sum += wsum[w];
+      if (w < warp) off = add(off, wsum[w]);
+      sum = add(sum, wsum[w]);
     }
-    if (s < S) prefix[s] = off + inc - x;
-    total += sum;
+    if (s < S) prefix[s] = lane ? add(off, before) : off;
+    total = add(total, sum);
     __syncthreads();
+  }
+  if (total == 0x7fffffff) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_RANGE);
+    total = 0;
   }
   const int num_warps = gridDim.x * kWarps;
   const int w0 = blockIdx.x * kWarps;
@@ -881,7 +893,7 @@ bool attention_int_fits(const AttnIntArgs& a) {
   const int64_t tiles = int64_t(a.num_tokens) * (a.num_heads / a.num_kv_heads) / num_rows<1>() + 1 + a.num_seqs;
   const int64_t units = (int64_t(a.max_seq_len) + ku - 1) / ku + 2;
   // units are counted in 32 bits (a step of all warps past the end, too)
-  return a.num_seqs <= kIntMaxSeqs && tiles <= 0x7fffffff / a.num_kv_heads &&
+  return a.num_seqs <= kIntMaxSeqs && a.max_seq_len <= 0x7fffffff - 128 && tiles <= 0x7fffffff / a.num_kv_heads &&
          tiles * a.num_kv_heads <= (0x7fffffff - (1 << 20)) / units;
 }
 

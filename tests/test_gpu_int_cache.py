@@ -1,20 +1,12 @@
 """Integer-coded caches on the GPU: the cache's bytes and what is read back equal the oracle's bit for bit
-(the definition names every rounding); attention over the codes against float64.
-
-Attention's tolerance, from the arithmetic. Query rows enter as f16 scaled by a power of two: exact but for
-elements 2^-25 of the row's largest. A logit is, in fp32, step (q.(o + c) - q.o) + lo sum q with o = 0 or 64 (4 bits), or
-1024 (8 bits), sums of D terms: each term and each sum within 2^-23 of sum |q| (off step + |lo|),
-off = 80 or 1280 (what multiplies step at most), so
-dl <= scale (D + 8) 2^-23 sum |q| (off step + |lo|). The numerators
-have that relative error, ex2's 2^-22 and, times the value's step, f16's half step 2^-11 (what falls
-under f16's range: 2^-31 of the largest step a key). A value enters as mid + step (c - mid), both parts within
-mag = sum_j w_j (|mid_j| + step_j N / 2). fp32 sums over the keys: 2^-23 each, 2^-18 for thousands. One
-rounding of the output to bf16: 2^-8.
+(the definition names every rounding); attention over the codes against
+float64, within intmodel's tolerance.
 """
 import numpy as np
 import pytest
 import torch
 
+import intmodel
 from oracle import int_cache as ic
 
 pytestmark = pytest.mark.gpu
@@ -220,21 +212,11 @@ class Batch:
     def check(self, requests=None):
         assert self.pa.read_device_errors() == 0
         kc, vc, q, out = self.kc.cpu().numpy(), self.vc.cpu().numpy(), _f64(self.q), _f64(self.out)
-        N, off = 2 ** self.bits - 1, 80 if self.bits == 4 else 1280
         for s in range(len(self.lens)) if requests is None else requests:
             a, b, L = self.qsl[s], self.qsl[s + 1], self.lens[s]
             if a == b:
                 continue
-            K, klo, kstep = ic.rows(kc, self.table[s].tolist(), L, self.D, self.bits)
-            V, vlo, vstep = ic.rows(vc, self.table[s].tolist(), L, self.D, self.bits)
-            ref, _, _, _ = ic.attend(q[a:b], K, V, L - (b - a), self.scale)
-            big = np.abs(vlo + (N + 1) / 2 * vstep) + vstep * (N + 1) / 2
-            mag = ic.attend(q[a:b], K, np.broadcast_to(big[..., None], V.shape), L - (b - a), self.scale)[0]
-            G = q.shape[1] // K.shape[1]
-            par = np.repeat((off * kstep + np.abs(klo)).max(0), G)
-            dl = self.scale * (self.D + 8) * 2.0 ** -23 * np.abs(q[a:b]).sum(-1) * par
-            tol = mag * (2.0 ** -11 + 2 * dl[..., None] + 2.0 ** -18) + L * 2.0 ** -31 * vstep.max() * N
-            tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+            ref, tol = intmodel.attention(q[a:b], kc, vc, self.table[s].tolist(), L, self.scale, self.bits)
             err = np.abs(out[a:b] - ref)
             assert (err <= tol).all(), (s, L, float((err / tol).max()))
         n = self.qsl[-1]
@@ -350,6 +332,23 @@ def test_malformed_requests_are_reported_and_leave_their_rows(pa):
     with pytest.raises(pa.PAError) as e:
         b.run(workspace=b.ws[:-256].clone())
     assert e.value.status == 3
+
+
+def test_requests_that_lie_over_one_another(pa):
+    """More work than 32 bits count, which only a decreasing query_start_loc can ask for: reported, not run."""
+    T, H, D, W, S = 65536, 8, 64, 65536, 64
+    cache = torch.zeros((1, H, 16 * (D // 2 + 4)), dtype=torch.uint8, device="cuda")
+    table = torch.zeros((S, W), dtype=torch.int32, device="cuda")
+    lens = torch.full((S,), 16 * W, dtype=torch.int32, device="cuda")
+    qsl = torch.tensor([0, T] * (S // 2) + [0], dtype=torch.int32, device="cuda")
+    q = torch.zeros((T, H, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    ws = torch.empty(pa.attention_int_workspace_size(S, T, H, H, D), dtype=torch.uint8, device="cuda")
+    pa.attention_int(out, q, cache, cache, table, lens, qsl, bits=4, max_query_len=T, max_seq_len=16 * W, scale=1.0,
+                     workspace=ws)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors(clear=True) == pa.PA_DEVERR["seq_range"]
+    assert (out == 7).all()
 
 
 def test_argument_checks_of_the_binding(pa):
