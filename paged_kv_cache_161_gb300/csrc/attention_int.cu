@@ -12,14 +12,16 @@
 // Bound: the cache's bytes (68 a row and head at 128 elements of 4 bits), and the instructions that turn
 // codes into 16-bit operands, about one an element of K and V. So: one pass, and every element converted once
 // for up to 8 or 16 query rows. Measured (GB300, 32 / 8 heads x 128): 64 requests of 32768 keys, 8 bits,
-// 674 us, 6600 GB/s of cache, 0.97 of the measured copy rate; 256 requests of 16 to 8192 keys around 1024, 4
-// bits, 100 us, 4700 GB/s (4 bits are bound by instructions: 256 requests of 1024 keys take 71 us, 4000 GB/s).
+// 670 us, 6650 GB/s of cache, 0.98 of the measured copy rate; 256 requests of 16 to 8192 keys around 1024, 4
+// bits, 98 us, 4800 GB/s (4 bits are bound by instructions and by what comes before and behind the stream).
 //
 // Work: a unit is unit_keys keys of one segment (request, KV head, tile of 8 or 16 query rows: query tokens
 // x the head's query heads). The units of all segments, in order, are dealt to the grid's warps in
 // equal runs; a warp streams its run through a ring of its own in shared memory, and no warp waits for
-// another while it streams. Segments cut between warps leave pieces (m, l, unnormalised output) in the
-// workspace: a CTA joins those of its warps, a second kernel those cut between CTAs.
+// another while it streams. Segments cut between warps leave pieces (m, l, unnormalised output), the one
+// that ends a run where the warp's ring was (in the workspace like the others: one request of 2000 keys
+// took 15.8 us, so 12.3): a CTA joins those of its warps, a second kernel those cut between CTAs, which are in the
+// workspace.
 //
 // Operands (mma.sync m16n8k16, keys as the 16 rows, query rows as the 8 columns): a code under the
 // bits of the f16 1024 is that number plus the code (or 1024 + 16 c, a nibble higher), one logic
@@ -41,7 +43,7 @@ namespace {
 // A tile of query rows is NT times the 8 columns of an MMA. NT = 2 where a request has more than 8 rows a KV
 // head: the codes are converted once for 16, with 8 warps a CTA (their sums take 248 registers a thread)
 // instead of 12 (two requests of four drafted tokens, 40000 keys: 4 bits 51 us with two tiles of 8, 45 us
-// with one of 16; 8 bits 57, 49 us).
+// with one of 16, 8 bits 57 and 49 us, before the joins were made faster: now 42 and 46 us).
 template <int NT>
 __host__ __device__ constexpr int num_warps() { return NT == 1 ? 12 : 8; }
 template <int NT>
@@ -72,8 +74,8 @@ struct IntParams {
   const int32_t* seq_lens;
   const int32_t* qsl;
   unsigned int* err;
-  float* pieces;  // [grid * kWarps * 2] of the warps, then [grid * 2] of the CTAs
-  int4* descs;    // [grid * 2]: a CTA's pieces, {first unit of the segment or -1, its last + 1, request, segment}
+  float* pieces;  // [grid * kWarps] of the warps, then [grid * 2] of the CTAs
+  int4* descs;    // [grid * 2]: a CTA's pieces, {first unit of the segment or -1, its last + 1, rows_of's two}
   int* total;     // units of the call
   int64_t num_blocks;
   int max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len;
@@ -189,28 +191,35 @@ __device__ __forceinline__ int key_of(int r) {
   return (r & 8) + ((r & 1) ? (h ^ 1) + 4 : h);
 }
 
-// Joins `count` pieces (piece 0 number `lead`, piece i number next + 2 i) of one row of segment d for every G
-// lanes of the warp: into the output, or into the piece `to`. The pieces' maxima and sums come a lane a
-// piece, then the rows, two pieces at a time: little code, which is met cold, and few waits.
-template <int D, int KU, int G, int NT>
-__device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int row, int lane, const float* pieces, int count,
-                                          int lead, int next, float* to) {
+// Where a tile's rows go: {token of its first row, that row's query head << 5 | number of rows}.
+template <int NT>
+__device__ __forceinline__ int2 rows_of(const IntParams& p, const Request& r, const Segment& sg) {
+  const int rr = sg.tile * num_rows<NT>(), rows = min(num_rows<NT>(), r.q_len * p.group - rr);
+  return make_int2(r.q0 + rr / p.group, int(uint32_t(sg.head * p.group + rr % p.group) << 5 | uint32_t(rows)));
+}
+__device__ __forceinline__ __nv_bfloat16* out_row(const IntParams& p, int2 where, int row, int D) {
+  const int head = int(uint32_t(where.y) >> 5), first = head % p.group, rr = first + row;
+  return p.out + (int64_t(where.x + rr / p.group) * p.num_heads + head - first + rr % p.group) * D;
+}
+
+// Joins `count` pieces, piece k at at(k), of one row of a tile for every G lanes of the warp: into the
+// output, or into the piece `to`. The pieces' maxima and sums come a lane a piece, then the rows, a few pieces
+// at a time: little code, which is met cold, and few waits.
+template <int D, int G, int NT, typename At>
+__device__ __forceinline__ void join_rows(const IntParams& p, int2 where, int row, int lane, int count, At at, float* to) {
   constexpr int kRows = num_rows<NT>();
   constexpr int E = D / G;  // a lane's elements, four (two) at a time
   constexpr int V = E >= 4 ? 4 : 2;
   const int sub = lane % G;
-  Request r;
-  request_of<KU, NT>(p, d.z, r);
-  const int head = d.w / r.tiles, tile = d.w - head * r.tiles, rr = tile * kRows + row;
-  const bool mine = rr < r.q_len * p.group;  // a row of the request
+  const bool mine = row < (where.y & 31);  // a row of the request
   float m = kNoMax, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 1
   for (int k0 = 0; k0 < count; k0 += G) {
     const int k = k0 + sub;
-    const float* ml = pieces + int64_t(k == 0 ? lead : next + 2 * k) * piece_floats<D, NT>() + kRows * D + row;
     const bool live = mine && k < count;
+    const float* ml = at(live ? k : 0) + kRows * D + row;
     const float mk = live ? ml[0] : kNoMax, lk = live ? ml[kRows] : 0.f;
     float top = lk == 0.f ? kNoMax : mk;  // an empty piece: its other sums were never written
 #pragma unroll
@@ -224,11 +233,10 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
     m = top;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= before;
-#pragma unroll 2
+#pragma unroll(G == 32 ? 4 : 2)
     for (int j = 0; j < min(G, count - k0); ++j) {
       const float e0 = __shfl_sync(0xffffffffu, w, j, G);
-      if (e0 == 0.f) continue;
-      const float* x = pieces + int64_t(k0 + j == 0 ? lead : next + 2 * (k0 + j)) * piece_floats<D, NT>() + row * D + sub * V;
+      const float* x = at(k0 + j) + row * D + sub * V;
 #pragma unroll
       for (int e = 0; e < E; e += V) {
         float y[V];
@@ -240,7 +248,7 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
           y[0] = f.x, y[1] = f.y;
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[e + i] += e0 * y[i];
+        for (int i = 0; i < V; ++i) o[e + i] = e0 == 0.f ? o[e + i] : fmaf(e0, y[i], o[e + i]);
       }
     }
   }
@@ -253,8 +261,7 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
 #pragma unroll
     for (int e = 0; e < E; ++e) to[row * D + sub * V + e / V * (V * G) + e % V] = o[e];
   } else {
-    __nv_bfloat16* out =
-        p.out + (int64_t(r.q0 + rr / p.group) * p.num_heads + head * p.group + rr % p.group) * D + sub * V;
+    __nv_bfloat16* out = out_row(p, where, row, D) + sub * V;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll
     for (int e = 0; e < E; e += V) {
@@ -271,7 +278,9 @@ __device__ __forceinline__ void join_rows(const IntParams& p, const int4 d, int 
 template <int D, int BITS, bool B16, int NT>
 __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(const IntParams p) {
   constexpr int kWarps = num_warps<NT>(), kRows = num_rows<NT>();
-  constexpr int KU = unit_keys<BITS>(), ROW = code_row_bytes<D, BITS>(), STAGE = stage_bytes<D, BITS>(), STAGES = num_stages<D, NT>();
+  constexpr int KU = unit_keys<BITS>(), ROW = code_row_bytes<D, BITS>();
+  constexpr int STAGE = stage_bytes<D, BITS>(), STAGES = num_stages<D, NT>();
+  static_assert(STAGE % 16 == 0 && STAGES * STAGE >= piece_floats<D, NT>() * 4, "a warp's last piece takes its ring's place");
   constexpr int HALF = STAGE / 2;                   // keys' part of a stage, then the values'
   constexpr int NK = D / 16;                        // contraction steps of q.c, and tiles of 16 value dimensions
   constexpr float kMid = BITS == 4 ? 8.f : 128.f;
@@ -461,8 +470,8 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
 
   uint32_t C;  // two f16 1024s
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(C));
-  for (int i = 0; i < STAGES; ++i) fill();
   int stage = 0;
+  bool filled = false;
   for (int u = u0; u < u1;) {
     // ---- a segment of the run: units x0 .. x1 - 1 of its keys
     const Segment sg = segment_of<KU, NT>(p, prefix, u);
@@ -473,10 +482,12 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     const bool whole = u <= sg.begin && u1 >= sg.end;
     const int slot = u == u0 ? 0 : 1;
     u = min(sg.end, u1);
-    if (!whole && lane == 0) desc[warp * 2 + slot] = make_int4(sg.begin, sg.end, sg.s, sg.head * r.tiles + sg.tile);
-    if (x1 <= x0) {  // nothing but the start: an empty piece
-      float* ml = p.pieces + int64_t((w0 + warp) * 2 + slot) * piece_floats<D, NT>() + kRows * D;
-      if (lane < 2 * kRows) ml[lane] = lane < kRows ? kNoMax : 0.f;  // (32 at most)
+    const int2 where = rows_of<NT>(p, r, sg);
+    if (!whole && lane == 0) desc[warp * 2 + slot] = make_int4(sg.begin, sg.end, where.x, where.y);
+    // a piece that ends the run goes where the ring was, else (the first of a run that goes on) to memory
+    float* piece = u == u1 ? reinterpret_cast<float*>(ring) : p.pieces + int64_t(w0 + warp) * piece_floats<D, NT>();
+    if (x1 <= x0) {  // nothing but the start, which ends the run: an empty piece
+      if (lane < 2 * kRows) piece[kRows * D + lane] = lane < kRows ? kNoMax : 0.f;  // (32 at most)
       continue;
     }
     const int j_first = sg.tile * kRows / p.group, j_last = (sg.tile * kRows + rows - 1) / p.group;
@@ -487,16 +498,27 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     // of query rows 2t and 2t + 1 (and 8 on), whose logits this lane holds
     float qs[NT][2], off[NT][2], fac[NT][2], m[NT][2], l[NT][2], mid[NT][2];
     int lim[NT][2];
+    uint4 raw[NT][D / 32];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int rr = sg.tile * kRows + min(g + 8 * nt, rows - 1);
+      const __nv_bfloat16* src = p.q + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)  // the dimensions of the key row's pieces that this lane takes
+        raw[nt][i] = *reinterpret_cast<const uint4*>(src + (BITS == 4 ? t * (D / 4) + 8 * i : (i / 2) * 64 + t * 16 + (i & 1) * 8));
+    }
+    if (!filled) {  // behind the first queries' loads, which would wait for all the copies otherwise
+      filled = true;
+#pragma unroll 1
+      for (int i = 0; i < STAGES; ++i) fill();
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = g + 8 * nt;
       float f[D / 4], qsum = 0.f, qoff = 0.f, big = 0.f;
-      const int rr = sg.tile * kRows + min(row, rows - 1);
-      const __nv_bfloat16* src = p.q + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {  // the dimensions of the key row's pieces that this lane takes
-        const int dim = BITS == 4 ? t * (D / 4) + 8 * i : (i / 2) * 64 + t * 16 + (i & 1) * 8;
-        Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(src + dim), f + 8 * i);
+      for (int i = 0; i < D / 32; ++i) {
+        Elem<__nv_bfloat16>::unpack(raw[nt][i], f + 8 * i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[8 * i + e]));
       }
@@ -787,22 +809,19 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
         }
         if (whole) {
           const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-          const int rr = sg.tile * kRows + row;
-          __nv_bfloat16* dst =
-              p.out + (int64_t(r.q0 + rr / p.group) * p.num_heads + sg.head * p.group + rr % p.group) * D + g * (D / 8);
+          __nv_bfloat16* dst = out_row(p, where, row, D) + g * (D / 8);
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) f[i] *= inv;
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) reinterpret_cast<uint4*>(dst)[i] = Elem<__nv_bfloat16>::pack(f + 8 * i);
         } else {
-          float* dst = p.pieces + int64_t((w0 + warp) * 2 + slot) * piece_floats<D, NT>();
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
-            reinterpret_cast<float4*>(dst + row * D + g * (D / 8))[i] =
+            reinterpret_cast<float4*>(piece + row * D + g * (D / 8))[i] =
                 make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
           if (g == 0) {
-            dst[kRows * D + row] = m[nt][h];
-            dst[kRows * D + kRows + row] = sum;
+            piece[kRows * D + row] = m[nt][h];
+            piece[kRows * D + kRows + row] = sum;
           }
         }
       }
@@ -812,7 +831,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
   // ---- pieces of segments cut between this CTA's warps, or between CTAs. A leader is a CTA's first
   // piece of a segment; the leaders' rows are dealt to the warps, one by one where there are few leaders.
   const int c0 = first(w0), c1 = first(w0 + kWarps);
-  float* cta_pieces = p.pieces + int64_t(num_warps) * 2 * piece_floats<D, NT>();
+  float* cta_pieces = p.pieces + int64_t(num_warps) * piece_floats<D, NT>();
   const int4 mine = lane < kWarps * 2 ? desc[lane] : make_int4(-1, 0, 0, 0);
   if (warp == 0) {
     // slot 0: a segment from before c0, or one from c0 to past c1; slot 1: one that goes on behind c1
@@ -831,28 +850,78 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     while (w + count < kWarps && first(w0 + w + count) < d.y) ++count;
     float* whole = d.x >= c0 && d.y <= c1 ? nullptr
                                           : cta_pieces + int64_t(blockIdx.x * 2 + (d.x <= c0 ? 0 : 1)) * piece_floats<D, NT>();
+    // the last one may be the first piece of a run that goes on
+    const bool goes_on = first(w0 + w + count) > d.y;
+    auto piece = [&](int k) -> const float* {
+      return goes_on && k == count - 1 ? p.pieces + int64_t(w0 + w + k) * piece_floats<D, NT>()
+                                       : reinterpret_cast<const float*>(smem + (w + k) * STAGES * STAGE);
+    };
+    const int2 where = make_int2(d.z, d.w);
     if (at_once == 1)
-      join_rows<D, KU, 32, NT>(p, d, row0, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
+      join_rows<D, 32, NT>(p, where, row0, lane, count, piece, whole);
     else
-      join_rows<D, KU, 8, NT>(p, d, row0 + lane / 8, lane, p.pieces, count, w0 * 2 + at, (w0 + w) * 2, whole);
+      join_rows<D, 8, NT>(p, where, row0 + lane / 8, lane, count, piece, whole);
   }
 }
 
-// Segments cut between CTAs: CTA c joins those whose first piece is c's; a warp a row.
-template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(num_rows<NT>() * 32) attention_int_join_kernel(const IntParams p, int num_ctas) {
-  constexpr int KU = unit_keys<BITS>(), kWarps = num_warps<NT>();
+// Segments cut between CTAs: CTA c joins those whose first piece is c's, several warps a row: 4 elements a
+// lane of several pieces at once, so that up to 16 (8) pieces are on their way together (one request of 32000
+// keys, 4 bits, 8 heads of 19 pieces: with a warp a row and 4 pieces the call takes 26.0 us, so 22.7; with
+// 1024 threads 23.1, and every other call 0.5 us more).
+constexpr int kJoinThreads = 512;
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads, 1) attention_int_join_kernel(const IntParams p, int num_ctas) {
+  constexpr int kWarps = num_warps<NT>(), kRows = num_rows<NT>();
+  constexpr int PARTS = kJoinThreads / 32 / kRows, LANES = D / PARTS / 4, GROUPS = 32 / LANES;  // warps a row, lanes a piece, pieces a load
   griddep_wait();
-  const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x, row = int(threadIdx.x >> 5) / PARTS, part = int(threadIdx.x >> 5) % PARTS, lane = threadIdx.x & 31;
+  const int d0 = part * (D / PARTS) + lane % LANES * 4, group = lane / LANES;
   const Deal first(*p.total, num_ctas * kWarps);
-  const float* pieces = p.pieces + int64_t(num_ctas) * kWarps * 2 * piece_floats<D, NT>();
+  const float* pieces = p.pieces + int64_t(num_ctas) * kWarps * piece_floats<D, NT>() + row * D + d0;
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
     const int4 d = p.descs[c * 2 + slot];
-    if (d.x < 0 || (slot == 0 && d.x != first(c * kWarps))) continue;
+    if (d.x < 0 || (slot == 0 && d.x != first(c * kWarps)) || row >= (d.w & 31)) continue;
     int count = 1;
     while (c + count < num_ctas && first((c + count) * kWarps) < d.y) ++count;
-    join_rows<D, KU, 32, NT>(p, d, row, lane, pieces, count, c * 2 + slot, c * 2, nullptr);
+    auto piece = [&](int k) { return pieces + int64_t(k == 0 ? c * 2 + slot : (c + k) * 2) * piece_floats<D, NT>(); };
+    float m = kNoMax, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += 32) {
+      const bool live = k0 + lane < count;
+      const float* ml = piece(live ? k0 + lane : 0) + (kRows - row) * D - d0 + row;
+      const float mk = ml[0], lk = live ? ml[kRows] : 0.f;
+      float top = lk == 0.f ? kNoMax : mk;  // an empty piece: its other sums were never written
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      top = fmaxf(top, m);
+      const float w = lk == 0.f ? 0.f : exp2f(mk - top), before = exp2f(m - top);
+      float sum = lk * w;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l = l * before + sum;
+      m = top;
+      o.x *= before, o.y *= before, o.z *= before, o.w *= before;
+#pragma unroll 8
+      for (int j = group; j < 32; j += GROUPS) {
+        if (k0 + j - group >= count) break;
+        const float e = __shfl_sync(0xffffffffu, w, j);
+        const float4 y = *reinterpret_cast<const float4*>(piece(k0 + j < count ? k0 + j : 0));
+        if (e != 0.f) o = make_float4(fmaf(e, y.x, o.x), fmaf(e, y.y, o.y), fmaf(e, y.z, o.z), fmaf(e, y.w, o.w));
+      }
+    }
+#pragma unroll
+    for (int x = LANES; x < 32; x <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    if (group == 0)
+      *reinterpret_cast<uint2*>(out_row(p, make_int2(d.z, d.w), row, D) + d0) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   }
 }
 
@@ -870,7 +939,7 @@ cudaError_t run_int(IntParams p, const AttnIntArgs& a, cudaStream_t stream) {
   const cudaError_t l = launch_pdl(b16 ? attention_int_kernel<D, BITS, true, NT> : attention_int_kernel<D, BITS, false, NT>,
                                    dim3(a.num_ctas), dim3(num_warps<NT>() * 32), rings + size_t(a.num_seqs) * 4, stream, p);
   if (l != cudaSuccess) return l;
-  return launch_pdl(attention_int_join_kernel<D, BITS, NT>, dim3(a.num_ctas), dim3(num_rows<NT>() * 32), 0, stream, p,
+  return launch_pdl(attention_int_join_kernel<D, NT>, dim3(a.num_ctas), dim3(kJoinThreads), 0, stream, p,
                     a.num_ctas);
 }
 template <int D, int BITS>
@@ -884,16 +953,18 @@ cudaError_t run_rows(const IntParams& p, const AttnIntArgs& a, cudaStream_t stre
 // descs, total, pieces of the CTAs' warps and of the CTAs
 size_t attention_int_workspace_bytes(int head_dim, int num_ctas) {
   const size_t row = (size_t(head_dim) + 2) * 4;
-  const size_t one = num_rows<1>() * (num_warps<1>() + 1), two = num_rows<2>() * (num_warps<2>() + 1);
-  return align_up(size_t(num_ctas) * 2 * sizeof(int4)) + 256 + size_t(num_ctas) * 2 * (one > two ? one : two) * row;
+  const size_t one = num_rows<1>() * (num_warps<1>() + 2), two = num_rows<2>() * (num_warps<2>() + 2);
+  return align_up(size_t(num_ctas) * 2 * sizeof(int4)) + 256 + size_t(num_ctas) * (one > two ? one : two) * row;
 }
 
 bool attention_int_fits(const AttnIntArgs& a) {
+  const int group = a.num_heads / a.num_kv_heads;
+  const bool two = int64_t(a.max_query_len) * group > num_rows<1>();
   const int ku = a.bits == 4 ? unit_keys<4>() : unit_keys<8>();
-  const int64_t tiles = int64_t(a.num_tokens) * (a.num_heads / a.num_kv_heads) / num_rows<1>() + 1 + a.num_seqs;
+  const int64_t tiles = int64_t(a.num_tokens) * group / (two ? num_rows<2>() : num_rows<1>()) + 1 + a.num_seqs;
   const int64_t units = (int64_t(a.max_seq_len) + ku - 1) / ku + 2;
   // units are counted in 32 bits (a step of all warps past the end, too)
-  return a.num_seqs <= kIntMaxSeqs && a.max_seq_len <= 0x7fffffff - 128 && tiles <= 0x7fffffff / a.num_kv_heads &&
+  return a.num_seqs <= kIntMaxSeqs && a.num_heads < (1 << 27) && a.max_seq_len <= 0x7fffffff - 128 && tiles <= 0x7fffffff / a.num_kv_heads &&
          tiles * a.num_kv_heads <= (0x7fffffff - (1 << 20)) / units;
 }
 
