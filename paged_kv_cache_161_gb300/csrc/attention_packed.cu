@@ -17,12 +17,14 @@
 // The two warpgroups' row maxima form a chain, step n's from step n - 1's, through shared memory,
 // known long before the numerators; each keeps its own sums of numerators, joined at the tile's end.
 //
-// Roles (12 warps, one CTA a SM): warps 0-3 and 4-7 the warpgroups of even and odd steps (counted over
+// Roles (16 warps, one CTA a SM): warps 0-3 and 4-7 the warpgroups of even and odd steps (counted over
 // all the CTA's tiles); warp 8 the tiles, Q (two buffers) and K (two); warp 9 TMEM and Q.K; warp 10 V (two);
 // warp 11 P.V (a thread that issues both waits out the products it has queued before it turns to the
-// other, and the tensor cores idle meanwhile: one prompt of 16384 tokens took 1971 us, with two threads 1494).
-// Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1264 us, 1740 TFLOP/s, 0.92 of the
-// measured bf16 rate; four chunks of 512 behind 8192 keys 171 us, 1450 TFLOP/s.
+// other, and the tensor cores idle meanwhile: one prompt of 16384 tokens took 1971 us, with two threads 1494);
+// warps 12-15 the output. The softmax goes on to the next tiles while P.V and the output follow, up to a ring's
+// length of tiles behind.
+// Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1245 us, 1766 TFLOP/s, 0.93 of the
+// measured bf16 rate; four chunks of 512 behind 8192 keys 171 us, 1450 TFLOP/s; 16 prompts of 1024 127 us.
 // Tiles: requests with the most keys first, a request's last tiles first; the grid has a
 // CTA for every tile there may be, and a running CTA takes the tiles of CTAs that have not started
 // (clusterlaunchcontrol), so no counter lives in memory between calls.
@@ -42,11 +44,11 @@ namespace {
 constexpr int kBM = 128;           // rows of a tile
 constexpr int kBN = 128;           // keys of a step
 constexpr int kMaxSeqs = 4096;     // requests of a call
-constexpr int kThreads = 12 * 32;
-constexpr int kWarpLoad = 8, kWarpQK = 9, kWarpV = 10, kWarpPV = 11;
-// Registers: 384 threads x 168 at launch = 64512 = 256 x 216 (a row's 128 logits in registers) + 128 x 72.
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
-static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= 384 * 168, "setmaxnreg waits for registers the launch has");
+constexpr int kThreads = 16 * 32;
+constexpr int kWarpLoad = 8, kWarpQK = 9, kWarpV = 10, kWarpPV = 11, kWarpOut = 12;
+// Registers: 512 threads x 128 at launch = 65536 = 256 x 184 (a row's 128 logits in registers) + 128 x 56 + 128 x 88.
+constexpr int kRegsSoftmax = 184, kRegsOther = 56, kRegsOut = 88;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther + 128 * kRegsOut <= 512 * 128, "setmaxnreg waits for registers the launch has");
 constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows x 64 bf16
 constexpr uint32_t kS = 0, kP = 256, kO = 384;  // TMEM columns
 
@@ -58,7 +60,6 @@ struct PackedParams {
   int num_seqs, num_q_rows, num_k_rows, max_query_len, num_heads, num_kv_heads;
   int log_group;     // query heads of a KV head: 2^log_group
   float scale_log2;  // softmax scale x log2(e)
-  int out_v8;        // out is 32-byte aligned
 };
 
 // A tile as warp 8 hands it to the other roles; t < 0: no more.
@@ -74,13 +75,14 @@ struct Layout {
   static constexpr uint32_t K = Q + 2 * NH * kHalf;   // 2
   static constexpr uint32_t V = K + 2 * NH * kHalf;   // 2
   static constexpr uint32_t M = V + 2 * NH * kHalf;   // float[2][128]: row maxima of the steps
-  static constexpr uint32_t X = M + 2 * 128 * 4;      // float2[2][2][128]: a tile's maxima and sums
-  static constexpr uint32_t RING = X + 4 * 128 * 8;   // Tile[kSlots]
+  static constexpr uint32_t X = M + 2 * 128 * 4;      // float2[kSlots][2][128]: the tiles' maxima and sums
+  static constexpr uint32_t OUT = X + kSlots * 2 * 128 * 8;   // [4 warps][32 rows][32 dimensions]
+  static constexpr uint32_t RING = OUT + 4 * 2048;    // Tile[kSlots]
   static constexpr uint32_t CLC = RING + kSlots * 32; // 16 bytes: the answer of a try_cancel
   static constexpr uint32_t BAR = CLC + 16;
-  static constexpr int NBAR = 48;
+  static constexpr int NBAR = 56;
   static constexpr uint32_t MISC = BAR + NBAR * 8;    // TMEM address
-  static constexpr uint32_t PLAN = MISC + 16;         // int[n + 8], uint16[n + 8]: prefix of the tiles, order of the requests
+  static constexpr uint32_t PLAN = MISC + 16;         // int[n + 8]: prefix of the tiles; uint16[n + 8] up to kThreads requests: their order
 };
 static_assert(sizeof(Tile) == 32, "a ring slot");
 
@@ -91,16 +93,16 @@ enum : int {
   bSFree0, bSFree1,    // S is in registers (4 warps)
   bP0, bP1,            // P is in TMEM (4 warps)
   bPV0, bPV1,          // P.V of a step has landed: P and the V stage are free, O holds it
-  bOFree,              // O of a tile has been read (8 warps)
+  bOFree,              // O of a tile has been read (4 warps)
   bEnd0, bEnd1,        // every Q.K, every P.V has landed
   bClc,
   bRingFull0, bRingEmpty0 = bRingFull0 + kSlots,
   bM0 = bRingEmpty0 + kSlots,  // [4 warps][2]: a warp's row maxima of a step are in shared memory
-  bX0 = bM0 + 8,               // [4]: both warps of a tile's 32 rows have left their sums
-  kBars = bX0 + 4
+  bX0 = bM0 + 8,               // [kSlots][4]: both warps of a tile's 32 rows have left their sums
+  kBars = bX0 + 4 * kSlots
 };
 static_assert(kBars <= Layout<128>::NBAR, "barriers in the layout");
-constexpr uint32_t kTakers = 11;  // of a ring slot: V, Q.K, P.V, 8 softmax warps
+constexpr uint32_t kTakers = 15;  // of a ring slot: V, Q.K, P.V, 8 softmax warps, 4 of the output
 
 // 16 columns of the warp's lanes (tc::tmem_ld32 with half the registers)
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
@@ -124,38 +126,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-
-// 16 lanes, 8 N columns: thread t gets of each 8 columns j columns 2 (t % 4) and + 1 of lane t / 4 (v[4 j], v[4 j +
-// 1]) and of lane t / 4 + 8 (v[4 j + 2], v[4 j + 3]).
-template <int N>
-__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, float (&v)[4 * N]) {
-  static_assert(N == 8 || N == 4, "64 or 32 columns");
-  uint32_t r[4 * N];
-  if constexpr (N == 8) {
-      asm volatile(
-          "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-          : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-          : "r"(taddr)
-          : "memory");
-  } else {
-      asm volatile(
-          "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-          : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-          : "r"(taddr)
-          : "memory");
-  }
-#pragma unroll
-  for (int i = 0; i < 4 * N; ++i) v[i] = __uint_as_float(r[i]);
-}
-// Of four lanes (t % 4), each with words x[0 .. 3] for the four: lane a gets word a of each, in their order.
-__device__ __forceinline__ void transpose4(uint32_t (&x)[4], int t) {
-  const uint32_t a = __shfl_xor_sync(0xffffffffu, (t & 1) ? x[0] : x[1], 1), b = __shfl_xor_sync(0xffffffffu, (t & 1) ? x[2] : x[3], 1);
-  if (t & 1) x[0] = a, x[2] = b;
-  else x[1] = a, x[3] = b;
-  const uint32_t c = __shfl_xor_sync(0xffffffffu, (t & 2) ? x[0] : x[2], 2), d = __shfl_xor_sync(0xffffffffu, (t & 2) ? x[1] : x[3], 2);
-  if (t & 2) x[0] = c, x[1] = d;
-  else x[2] = c, x[3] = d;
 }
 
 template <int N>
@@ -203,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
 
   griddep_wait();
 
-  // ---- the plan: requests with queries, most keys first, and the prefix of their tiles
+  // ---- the plan: requests by their keys, most first (up to kThreads of them), and the prefix of their tiles
   int* pfx = reinterpret_cast<int*>(sm + LY::PLAN);
   uint16_t* ord = reinterpret_cast<uint16_t*>(pfx + S + 8);
   auto tiles_of = [&](int s, bool report) -> int {  // a KV head's; 0: no queries, or a malformed request
@@ -237,36 +207,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     *tot = t;
     return lane ? add(off, before) : off;
   };
-  int P = 0;
-  for (int b0 = 0; b0 < S; b0 += kThreads) {
-    const int s = b0 + threadIdx.x;
-    const int flag = s < S && tiles_of(s, blockIdx.x == 0) > 0;
-    int tot;
-    const int at = P + block_scan(flag, &tot);
-    if (flag) {
-      ord[at] = uint16_t(s);
-      pfx[at] = p.ksl[s + 1] - p.ksl[s];
-    }
-    P += tot;
-  }
-  __syncthreads();
-  if (P <= kThreads) {  // ranked by keys, then batch order; more requests: batch order
-    int s = 0, key = 0, rank = 0;
-    if (int(threadIdx.x) < P) {
-      s = ord[threadIdx.x];
-      key = pfx[threadIdx.x];
-      for (int i = 0; i < P; ++i) rank += pfx[i] > key || (pfx[i] == key && i < int(threadIdx.x));
-    }
+  const bool ranked = S <= kThreads;
+  auto request = [&](int i) { return ranked ? int(ord[i]) : i; };
+  if (ranked) {
+    const int s = threadIdx.x, n = s < S ? tiles_of(s, blockIdx.x == 0) : 0;
+    int key = 0, rank = 0;
+    if (s < S) pfx[s] = key = n > 0 ? p.ksl[s + 1] - p.ksl[s] : -1;
     __syncthreads();
-    if (int(threadIdx.x) < P) ord[rank] = uint16_t(s);
+    if (s < S)
+      for (int i = 0; i < S; ++i) rank += pfx[i] > key || (pfx[i] == key && i < s);
+    __syncthreads();
+    if (s < S) ord[rank] = uint16_t(s);
     __syncthreads();
   }
   int total = 0;
-  for (int b0 = 0; b0 <= P; b0 += kThreads) {
+  for (int b0 = 0; b0 <= S; b0 += kThreads) {
     const int i = b0 + threadIdx.x;
     int tot;
-    const int ex = block_scan(i < P ? tiles_of(ord[i], false) * p.num_kv_heads : 0, &tot);
-    if (i <= P) pfx[i] = add(total, ex);
+    const int ex = block_scan(i < S ? tiles_of(request(i), !ranked && blockIdx.x == 0) * p.num_kv_heads : 0, &tot);
+    if (i <= S) pfx[i] = add(total, ex);
     total = add(total, tot);
   }
   __syncthreads();
@@ -279,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     if (at_p < 0 || pfx[at_p + 1] <= t) {
       if (at_p < 0) at_p = 0;
       while (pfx[at_p + 1] <= t) ++at_p;
-      const int s = ord[at_p];
+      const int s = request(at_p);
       at_q0 = p.qsl[s];
       at_Q = p.qsl[s + 1] - at_q0;
       at_k0 = p.ksl[s];
@@ -322,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     for (int i = 0; i < kBars; ++i) {
       uint32_t n = 1;
       if (i == bSFree0 || i == bSFree1 || i == bP0 || i == bP1) n = 4;
-      if (i == bOFree) n = 8;
+      if (i == bOFree) n = 4;
       if (i >= bRingEmpty0 && i < bRingEmpty0 + kSlots) n = kTakers;
       if (i >= bX0) n = 2;
       mbar_init(bar(i), n);
@@ -342,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   // No waiter can be two phases behind: the next phase of each barrier needs something of the waiter's.
   auto wait_step = [&](int b0, int n) { return mbar_wait(bar(b0 + (n & 1)), uint32_t(n >> 1) & 1u); };
 
-  if (warp >= 8) {
+  if (warp >= 8 && warp < kWarpOut) {
     regs_down<kRegsOther>();
     if (warp == kWarpLoad && lane == 0) {
       // =========================== tiles, Q, K ===========================
@@ -500,82 +459,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       tc::mma_commit(bar(bEnd1));
       mbar_wait(bar(bEnd1), 0);
     }
-  } else {
+  } else if (warp < 8) {
     regs_up<kRegsSoftmax>();
-    // =========================== softmax, output ===========================
+    // =========================== softmax ===========================
     const int w = warp >> 2, wr = warp & 3;  // warpgroup; its warp: TMEM lanes 32 wr ..
     const int r = wr * 32 + lane;
     const uint32_t trow = tmem + (uint32_t(wr * 32) << 16);
     float* m_sh = reinterpret_cast<float*>(sm + LY::M);
     float2* x_sh = reinterpret_cast<float2*>(sm + LY::X);
     const float sc = p.scale_log2;
-    int n = 0, live = 0;  // steps of the tiles before; tiles with steps
+    int n = 0;  // steps of the tiles before
     bool ok = true;
-    // The output of a tile waits for its last P.V: the warpgroup that has the next tile's first step does that
-    // step before, the other at once. (P.V of the next tile waits for both: nothing of that tile's P.V may be
-    // waited for before.)
-    bool due = false;  // the tile before this one is to be written: its last step, number, rows
-    int due_end = 0, due_live = 0, due_row0 = 0, due_hk = 0, due_nq = 0;
-    // The address of the warpgroup's half of row rr of the tile due, or null where the request has no such row.
-    auto out_at = [&](int rr) -> __nv_bfloat16* {
-      if ((rr >> lg) >= due_nq) return nullptr;
-      return p.out + (int64_t(due_row0 + (rr >> lg)) * p.num_heads + (due_hk << lg) + (rr & ((1 << lg) - 1))) * D + w * (D / 2);
-    };
-    auto finish = [&]() -> bool {  // O / l -> out, half the dimensions each warpgroup; false: a wait ran out
-      due = false;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(bX0 + wr), uint32_t(due_live) & 1u)) ||
-          !__all_sync(0xffffffffu, wait_step(bPV0, due_end)))
-        return false;
-      const float2* both = x_sh + ((due_live & 1) * 2) * 128 + r;
-      const float2 z = both[(due_end & 1) * 128], y = both[((due_end & 1) ^ 1) * 128];  // of the last step, the one before
-      float sum = z.y;
-      if (y.y != 0.f) sum += y.y * (y.x == z.x ? 1.f : exp2f((y.x - z.x) * sc));
-      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-      tc::fence_after_sync();
-      // Lanes of four hold a row's columns side by side; turned among them, a store writes 8 rows' 128 (64)
-      // contiguous bytes where a thread's own row would be 32 lines (16 prompts
-      // of 1024 tokens: 147 -> 139 us).
-      constexpr int N = D / 16, V = N / 4;  // column eights of half the dimensions; of a lane's store
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        float o[4 * N];
-        tmem_ld_16x256b<N>(trow + (uint32_t(half * 16) << 16) + kO + uint32_t(w * (D / 2)), o);
-        tc::tmem_wait_ld();
-        if (half == 1) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(bOFree));
-        }
-#pragma unroll
-        for (int up = 0; up < 2; ++up) {
-          const int row = half * 16 + up * 8 + (lane >> 2);
-          const float by = __shfl_sync(0xffffffffu, inv, row);
-          uint32_t x[V][4];  // lane a of four: eights a V .. a V + V - 1
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const float* y = o + 4 * j + 2 * up;
-            const __nv_bfloat162 h = __floats2bfloat162_rn(y[0] * by, y[1] * by);
-            x[j % V][j / V] = by == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&h);  // a row that sees no key
-          }
-#pragma unroll
-          for (int v = 0; v < V; ++v) transpose4(x[v], lane & 3);
-          __nv_bfloat16* out = out_at(wr * 32 + row);
-          if (!out) continue;
-          out += (lane & 3) * (8 * V);
-          if (V == 2 && p.out_v8) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "r"(x[0][0]), "r"(x[0][1]),
-                         "r"(x[0][2]), "r"(x[0][3]), "r"(x[V - 1][0]), "r"(x[V - 1][1]), "r"(x[V - 1][2]), "r"(x[V - 1][3])
-                         : "memory");
-          } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) *reinterpret_cast<uint4*>(out + 8 * v) = make_uint4(x[v][0], x[v][1], x[v][2], x[v][3]);
-          }
-        }
-      }
-      return true;
-    };
-    // One round: a step of this warpgroup's if its turn is, then the output due. (One place for each: the
-    // instruction cache holds this code once, not twice.)
     Tile x;
     int kb = 0, mypos = 0;  // this warpgroup's next step of the tile
     bool active = false;
@@ -592,8 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       l = 0.f;
     };
     next_tile(0);
-    for (int i = 1; ok;) {
-      if (kb < x.nt && !(due && kb > 0)) {  // no step but a tile's first goes before an output
+    for (int i = 0; ok; ++i) {
+      if (x.t < 0) break;
+      for (; kb < x.nt; kb += 2) {
         const int at = n + kb, key0 = kb * kBN;
         if (!__all_sync(0xffffffffu, wait_step(bQK0, at))) {
           ok = false;
@@ -708,32 +603,85 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bP0 + w));
-        kb += 2;
       }
-      if (due) {
-        if (!finish()) ok = false;
-        continue;
-      }
-      if (kb < x.nt) continue;
+      if (!ok) break;
+      // ---- the tile's steps are done: this warpgroup's last maximum and its sum for the output's warps
+      x_sh[((i & (kSlots - 1)) * 2 + w) * 128 + r] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bX0 + (i & (kSlots - 1)) * 4 + wr));
+      n += x.nt;
+      next_tile(i + 1);
+    }
+    if (!ok) fail();
+  } else {
+    regs_down<kRegsOut>();
+    // =========================== output ===========================
+    // O / l -> out, beside the next tiles' softmax (by the softmax's own warps, behind a tile's first step, every
+    // tile's P.V waited 4000 clocks for them: 16 prompts of 1024 tokens 139 -> 127 us, 64 of 256 88 -> 74 us)
+    const int wr = warp & 3, r = wr * 32 + lane;
+    const uint32_t trow = tmem + (uint32_t(wr * 32) << 16);
+    const float2* x_sh = reinterpret_cast<const float2*>(sm + LY::X);
+    bool ok = true;
+    int n = 0;
+    for (int i = 0;; ++i) {
+      const int slot = i & (kSlots - 1);
+      Tile x;
+      // (the slot is given back behind the sums' reading, so the softmax is never more than kSlots tiles ahead)
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(bRingFull0 + slot), uint32_t(i / kSlots) & 1u))) ok = false;
+      if (!ok) break;
+      read_slot(i, x);
       if (x.t < 0) break;
-      // ---- the tile's steps are done
-      due_row0 = x.row0;
-      due_hk = x.hk;
-      due_nq = x.nq;
-      if (x.nt > 0) {
-        x_sh[((live & 1) * 2 + w) * 128 + r] = make_float2(m, l);  // double: the other warp may still read the tile's before
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bX0 + wr));
-        due = true;
-        due_end = n + x.nt - 1;
-        due_live = live;
-        n += x.nt;
-        ++live;
-      } else if (__nv_bfloat16* out = out_at(r)) {  // no keys: zeros
-#pragma unroll
-        for (int e = 0; e < D / 2; e += 8) *reinterpret_cast<uint4*>(out + e) = make_uint4(0, 0, 0, 0);
+      const int end = n + x.nt - 1;  // the tile's last step
+      n += x.nt;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(bX0 + slot * 4 + wr), uint32_t(i / kSlots) & 1u)) ||
+          (x.nt > 0 && !__all_sync(0xffffffffu, wait_step(bPV0, end)))) {
+        ok = false;
+        break;
       }
-      next_tile(i++);
+      const float2 z = x_sh[(slot * 2 + (end & 1)) * 128 + r], y = x_sh[(slot * 2 + ((end & 1) ^ 1)) * 128 + r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bRingEmpty0 + slot));
+      float sum = z.y;  // z of the last step's warpgroup, y of the other
+      if (y.y != 0.f) sum += y.y * (y.x == z.x ? 1.f : exp2f((y.x - z.x) * p.scale_log2));
+      const float inv = x.nt == 0 ? 0.f : sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+      tc::fence_after_sync();
+      // A thread's row, 32 dimensions at a time, as bf16 into shared memory (16-byte pieces, xor half the row's
+      // number: no bank twice), and rows out of it, 8 of 64 bytes a store: little code, which the softmax's does
+      // not leave much room for in the instruction cache.
+      unsigned char* mine = sm + LY::OUT + wr * 2048;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32] = {};
+        if (x.nt > 0) {
+          tc::tmem_ld32(trow + kO + uint32_t(c), o);
+          tc::tmem_wait_ld();
+        }
+        if (c + 32 == D && x.nt > 0) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bOFree));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = o[8 * e + j] * inv;
+          uint4 v = Elem<__nv_bfloat16>::pack(y);
+          if (inv == 0.f) v = make_uint4(0, 0, 0, 0);  // a row that sees no key
+          *reinterpret_cast<uint4*>(mine + lane * 64 + (e ^ (lane >> 1 & 3)) * 16) = v;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = lane / 4; k < 32; k += 8) {
+          const int rr = wr * 32 + k;
+          const uint4 v = *reinterpret_cast<const uint4*>(mine + k * 64 + ((lane & 3) ^ (k >> 1 & 3)) * 16);
+          if ((rr >> lg) < x.nq)  // else the request has no such row
+            *reinterpret_cast<uint4*>(p.out +
+                                      (int64_t(x.row0 + (rr >> lg)) * p.num_heads + (x.hk << lg) + (rr & ((1 << lg) - 1))) * D +
+                                      c + (lane & 3) * 8) = v;
+        }
+        __syncwarp();
+      }
     }
     if (!ok) fail();
   }
@@ -772,7 +720,7 @@ bool row_map(CUtensorMap* m, const void* ptr, int D, int heads, int rows, int64_
 }
 
 template <int D>
-constexpr size_t plan_smem(int num_seqs) { return Layout<D>::PLAN + 6 * (size_t(num_seqs) + 8) + 1024; }
+constexpr size_t plan_smem(int num_seqs) { return Layout<D>::PLAN + (num_seqs <= kThreads ? 6 : 4) * (size_t(num_seqs) + 8) + 1024; }
 static_assert(plan_smem<128>(kMaxSeqs) + 64 <= 232448, "shared memory of a CTA");
 
 template <int D>
@@ -790,7 +738,7 @@ cudaError_t run_packed(const PackedArgs& a, cudaStream_t stream) {
   while ((1 << lg) < G) ++lg;
   const PackedParams p = {static_cast<__nv_bfloat16*>(a.out), a.q_start_loc, a.k_start_loc, a.err, a.num_seqs, a.num_q_rows,
                           a.num_k_rows, a.max_query_len, a.num_heads, a.num_kv_heads, lg,
-                          a.scale * 1.4426950408889634f, reinterpret_cast<uintptr_t>(a.out) % 32 == 0 ? 1 : 0};
+                          a.scale * 1.4426950408889634f};
   const cudaError_t e = ensure_smem<attention_packed_kernel<D>>(plan_smem<D>(kMaxSeqs));
   if (e != cudaSuccess) return e;
   // a tile for every 128 / G tokens, and one more a request
