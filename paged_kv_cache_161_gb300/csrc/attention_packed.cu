@@ -24,7 +24,7 @@
 // warps 12-15 the output. The softmax goes on to the next tiles while P.V and the output follow, up to a ring's
 // length of tiles behind.
 // Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1245 us, 1766 TFLOP/s, 0.93 of the
-// measured bf16 rate; four chunks of 512 behind 8192 keys 171 us, 1450 TFLOP/s; 16 prompts of 1024 127 us.
+// measured bf16 rate; four chunks of 512 behind 8192 keys 169 us, 1470 TFLOP/s; 16 prompts of 1024 123 us.
 // Tiles: requests with the most keys first, a request's last tiles first; the grid has a
 // CTA for every tile there may be, and a running CTA takes the tiles of CTAs that have not started
 // (clusterlaunchcontrol), so no counter lives in memory between calls.
@@ -60,6 +60,7 @@ struct PackedParams {
   int num_seqs, num_q_rows, num_k_rows, max_query_len, num_heads, num_kv_heads;
   int log_group;     // query heads of a KV head: 2^log_group
   float scale_log2;  // softmax scale x log2(e)
+  int out_v8;        // out is 32-byte aligned
 };
 
 // A tile as warp 8 hands it to the other roles; t < 0: no more.
@@ -76,8 +77,7 @@ struct Layout {
   static constexpr uint32_t V = K + 2 * NH * kHalf;   // 2
   static constexpr uint32_t M = V + 2 * NH * kHalf;   // float[2][128]: row maxima of the steps
   static constexpr uint32_t X = M + 2 * 128 * 4;      // float2[kSlots][2][128]: the tiles' maxima and sums
-  static constexpr uint32_t OUT = X + kSlots * 2 * 128 * 8;   // [4 warps][32 rows][32 dimensions]
-  static constexpr uint32_t RING = OUT + 4 * 2048;    // Tile[kSlots]
+  static constexpr uint32_t RING = X + kSlots * 2 * 128 * 8;  // Tile[kSlots]
   static constexpr uint32_t CLC = RING + kSlots * 32; // 16 bytes: the answer of a try_cancel
   static constexpr uint32_t BAR = CLC + 16;
   static constexpr int NBAR = 56;
@@ -126,6 +126,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ void store32(void* dst, const uint4 a, const uint4 b, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = a;
+    static_cast<uint4*>(dst)[1] = b;
+  }
 }
 
 template <int N>
@@ -617,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     regs_down<kRegsOut>();
     // =========================== output ===========================
     // O / l -> out, beside the next tiles' softmax (by the softmax's own warps, behind a tile's first step, every
-    // tile's P.V waited 4000 clocks for them: 16 prompts of 1024 tokens 139 -> 127 us, 64 of 256 88 -> 74 us)
+    // tile's P.V waited 4000 clocks for them: 16 prompts of 1024 tokens 139 -> 124 us, 64 of 256 88 -> 72 us)
     const int wr = warp & 3, r = wr * 32 + lane;
     const uint32_t trow = tmem + (uint32_t(wr * 32) << 16);
     const float2* x_sh = reinterpret_cast<const float2*>(sm + LY::X);
@@ -645,10 +656,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       if (y.y != 0.f) sum += y.y * (y.x == z.x ? 1.f : exp2f((y.x - z.x) * p.scale_log2));
       const float inv = x.nt == 0 ? 0.f : sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
       tc::fence_after_sync();
-      // A thread's row, 32 dimensions at a time, as bf16 into shared memory (16-byte pieces, xor half the row's
-      // number: no bank twice), and rows out of it, 8 of 64 bytes a store: little code, which the softmax's does
-      // not leave much room for in the instruction cache.
-      unsigned char* mine = sm + LY::OUT + wr * 2048;
+      // A thread its row, 32 dimensions at a time: little code, which the softmax's does not leave much room for in
+      // the instruction cache. (O packed at once and P.V let go earlier, 16 prompts of 1024 tokens: 138 us against 124;
+      // rows through shared memory, so that a store writes longer runs: 128.)
+      __nv_bfloat16* out = p.out + (int64_t(x.row0 + (r >> lg)) * p.num_heads + (x.hk << lg) + (r & ((1 << lg) - 1))) * D;
+      const bool row = (r >> lg) < x.nq;  // else the request has no such row
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32] = {};
@@ -661,26 +673,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(bOFree));
         }
+        uint4 v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float y[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[j] = o[8 * e + j] * inv;
-          uint4 v = Elem<__nv_bfloat16>::pack(y);
-          if (inv == 0.f) v = make_uint4(0, 0, 0, 0);  // a row that sees no key
-          *reinterpret_cast<uint4*>(mine + lane * 64 + (e ^ (lane >> 1 & 3)) * 16) = v;
+          v[e] = Elem<__nv_bfloat16>::pack(y);
+          if (inv == 0.f) v[e] = make_uint4(0, 0, 0, 0);  // a row that sees no key
         }
-        __syncwarp();
+        if (row) {
 #pragma unroll
-        for (int k = lane / 4; k < 32; k += 8) {
-          const int rr = wr * 32 + k;
-          const uint4 v = *reinterpret_cast<const uint4*>(mine + k * 64 + ((lane & 3) ^ (k >> 1 & 3)) * 16);
-          if ((rr >> lg) < x.nq)  // else the request has no such row
-            *reinterpret_cast<uint4*>(p.out +
-                                      (int64_t(x.row0 + (rr >> lg)) * p.num_heads + (x.hk << lg) + (rr & ((1 << lg) - 1))) * D +
-                                      c + (lane & 3) * 8) = v;
+          for (int e = 0; e < 4; e += 2) store32(out + c + 8 * e, v[e], v[e + 1], p.out_v8);
         }
-        __syncwarp();
       }
     }
     if (!ok) fail();
@@ -738,7 +743,7 @@ cudaError_t run_packed(const PackedArgs& a, cudaStream_t stream) {
   while ((1 << lg) < G) ++lg;
   const PackedParams p = {static_cast<__nv_bfloat16*>(a.out), a.q_start_loc, a.k_start_loc, a.err, a.num_seqs, a.num_q_rows,
                           a.num_k_rows, a.max_query_len, a.num_heads, a.num_kv_heads, lg,
-                          a.scale * 1.4426950408889634f};
+                          a.scale * 1.4426950408889634f, reinterpret_cast<uintptr_t>(a.out) % 32 == 0 ? 1 : 0};
   const cudaError_t e = ensure_smem<attention_packed_kernel<D>>(plan_smem<D>(kMaxSeqs));
   if (e != cudaSuccess) return e;
   // a tile for every 128 / G tokens, and one more a request
