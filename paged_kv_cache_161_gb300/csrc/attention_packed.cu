@@ -23,10 +23,11 @@
 // other, and the tensor cores idle meanwhile: one prompt of 16384 tokens took 1971 us, with two threads 1494);
 // warps 12-15 the output. The softmax goes on to the next tiles while P.V and the output follow, up to a ring's
 // length of tiles behind.
-// Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1245 us, 1766 TFLOP/s, 0.93 of the
-// measured bf16 rate; four chunks of 512 behind 8192 keys 169 us, 1470 TFLOP/s; 16 prompts of 1024 123 us.
-// Tiles: requests with the most keys first, a request's last tiles first; the grid has a
-// CTA for every tile there may be, and a running CTA takes the tiles of CTAs that have not started
+// Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1245 us in a short burst, 1766 TFLOP/s, 0.91
+// of the measured burst bf16 rate, and 1445 us repeated for long, 0.88 of the sustained one; four chunks of 512
+// behind 8192 keys 169 us, 1470 TFLOP/s; 16 prompts of 1024 123 us.
+// Tiles: requests with the most keys first (up to kThreads requests), a request's last tiles first; the grid
+// has a CTA for every tile there may be, and a running CTA takes the tiles of CTAs that have not started
 // (clusterlaunchcontrol), so no counter lives in memory between calls.
 //
 // Every wait is bounded; on a timeout the kernel sets an error bit and leaves after its copies and
