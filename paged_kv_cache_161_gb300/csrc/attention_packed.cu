@@ -26,9 +26,9 @@
 // Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1245 us in a short burst, 1766 TFLOP/s, 0.91
 // of the measured burst bf16 rate, and 1445 us repeated for long, 0.88 of the sustained one; four chunks of 512
 // behind 8192 keys 169 us, 1470 TFLOP/s; 16 prompts of 1024 123 us.
-// Tiles: requests with the most keys first (up to kThreads requests), a request's last tiles first; the grid
-// has a CTA for every tile there may be, and a running CTA takes the tiles of CTAs that have not started
-// (clusterlaunchcontrol), so no counter lives in memory between calls.
+// Tiles: requests with the most keys first (up to kThreads of them), a request's last tiles first; a running CTA
+// takes the tiles of CTAs that have not started (clusterlaunchcontrol), so no counter lives in memory between
+// calls.
 //
 // Every wait is bounded; on a timeout the kernel sets an error bit and leaves after its copies and
 // products in flight have landed, freeing TMEM.
@@ -83,7 +83,7 @@ struct Layout {
   static constexpr uint32_t BAR = CLC + 16;
   static constexpr int NBAR = 56;
   static constexpr uint32_t MISC = BAR + NBAR * 8;    // TMEM address
-  static constexpr uint32_t PLAN = MISC + 16;         // int[n + 8]: prefix of the tiles; uint16[n + 8] up to kThreads requests: their order
+  static constexpr uint32_t PLAN = MISC + 16;         // int[n + 8], uint16[n + 8]: prefix of the tiles, order of the requests
 };
 static_assert(sizeof(Tile) == 32, "a ring slot");
 
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
 
   griddep_wait();
 
-  // ---- the plan: requests by their keys, most first (up to kThreads of them), and the prefix of their tiles
+  // ---- the plan: requests with queries, most keys first, and the prefix of their tiles
   int* pfx = reinterpret_cast<int*>(sm + LY::PLAN);
   uint16_t* ord = reinterpret_cast<uint16_t*>(pfx + S + 8);
   auto tiles_of = [&](int s, bool report) -> int {  // a KV head's; 0: no queries, or a malformed request
@@ -219,38 +219,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     *tot = t;
     return lane ? add(off, before) : off;
   };
-  const bool ranked = S <= kThreads;
-  auto request = [&](int i) { return ranked ? int(ord[i]) : i; };
-  if (ranked) {
-    const int s = threadIdx.x, n = s < S ? tiles_of(s, blockIdx.x == 0) : 0;
-    int key = 0, rank = 0;
-    if (s < S) pfx[s] = key = n > 0 ? p.ksl[s + 1] - p.ksl[s] : -1;
+  int P = 0;
+  for (int b0 = 0; b0 < S; b0 += kThreads) {
+    const int s = b0 + threadIdx.x;
+    const int flag = s < S && tiles_of(s, blockIdx.x == 0) > 0;
+    int tot;
+    const int at = P + block_scan(flag, &tot);
+    if (flag) {
+      ord[at] = uint16_t(s);
+      pfx[at] = p.ksl[s + 1] - p.ksl[s];
+    }
+    P += tot;
+  }
+  __syncthreads();
+  if (P <= kThreads) {  // ranked by keys, then batch order; more requests: batch order
+    int s = 0, key = 0, rank = 0;
+    if (int(threadIdx.x) < P) {
+      s = ord[threadIdx.x];
+      key = pfx[threadIdx.x];
+      for (int i = 0; i < P; ++i) rank += pfx[i] > key || (pfx[i] == key && i < int(threadIdx.x));
+    }
     __syncthreads();
-    if (s < S)
-      for (int i = 0; i < S; ++i) rank += pfx[i] > key || (pfx[i] == key && i < s);
-    __syncthreads();
-    if (s < S) ord[rank] = uint16_t(s);
+    if (int(threadIdx.x) < P) ord[rank] = uint16_t(s);
     __syncthreads();
   }
   int total = 0;
-  for (int b0 = 0; b0 <= S; b0 += kThreads) {
+  for (int b0 = 0; b0 <= P; b0 += kThreads) {
     const int i = b0 + threadIdx.x;
     int tot;
-    const int ex = block_scan(i < S ? tiles_of(request(i), !ranked && blockIdx.x == 0) * p.num_kv_heads : 0, &tot);
-    if (i <= S) pfx[i] = add(total, ex);
+    const int ex = block_scan(i < P ? tiles_of(ord[i], false) * p.num_kv_heads : 0, &tot);
+    if (i <= P) pfx[i] = add(total, ex);
     total = add(total, tot);
   }
   __syncthreads();
   if (int(blockIdx.x) >= total) return;
 
   // Tile t: a request's KV heads fastest, its tiles from the last one back. For warp 8's thread, whose tiles
-  // ascend: the request is stepped along.
+  // mostly ascend: the request is stepped along.
   int at_p = -1, at_q0 = 0, at_Q = 0, at_k0 = 0, at_K = 0;
   auto tile_info = [&](int t) {
-    if (at_p < 0 || pfx[at_p + 1] <= t) {
-      if (at_p < 0) at_p = 0;
+    if (at_p < 0 || pfx[at_p + 1] <= t || t < pfx[at_p]) {
+      if (at_p < 0 || t < pfx[at_p]) at_p = 0;
       while (pfx[at_p + 1] <= t) ++at_p;
-      const int s = request(at_p);
+      const int s = ord[at_p];
       at_q0 = p.qsl[s];
       at_Q = p.qsl[s + 1] - at_q0;
       at_k0 = p.ksl[s];
@@ -320,10 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       tc::prefetch_tensormap(&qmap);
       tc::prefetch_tensormap(&kmap);
       bool ok = true;
-      int n = 0, nq = 0, t = int(blockIdx.x);
+      int n = 0, nq = 0, asked = 0, t = int(blockIdx.x);
       for (int i = 0;; ++i) {
         const bool last = t < 0 || t >= total;
-        if (!last) {  // the next tile is asked for while this one's rows are fetched
+        const bool again = !last && t < total - int(gridDim.x);  // a CTA's index stands for every gridDim-th tile from there
+        if (!last && !again) {  // the next CTA is asked for while this tile's rows are fetched
           mbar_arrive_expect_tx(bar(bClc), 16);
           clc_try_cancel(base + LY::CLC, bar(bClc));
         }
@@ -357,8 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
             tc::tma_load_3d(base + LY::K + uint32_t((n & 1) * NH + h) * kHalf, &kmap, 64 * h, x.hk, x.k0 + kb * kBN,
                             bar(bK0 + (n & 1)));
         }
+        if (again) {
+          if (!ok) break;
+          t += int(gridDim.x);
+          continue;
+        }
         // (waited for even when a wait ran out: the answer must not arrive after the CTA has left)
-        if (!mbar_wait(bar(bClc), uint32_t(i) & 1u)) ok = false;
+        if (!mbar_wait(bar(bClc), uint32_t(asked++) & 1u)) ok = false;
         if (!ok) break;
         t = clc_answer(base + LY::CLC);
         tc::fence_proxy_async_smem();  // read before the next answer is written there
@@ -726,7 +743,7 @@ bool row_map(CUtensorMap* m, const void* ptr, int D, int heads, int rows, int64_
 }
 
 template <int D>
-constexpr size_t plan_smem(int num_seqs) { return Layout<D>::PLAN + (num_seqs <= kThreads ? 6 : 4) * (size_t(num_seqs) + 8) + 1024; }
+constexpr size_t plan_smem(int num_seqs) { return Layout<D>::PLAN + 6 * (size_t(num_seqs) + 8) + 1024; }
 static_assert(plan_smem<128>(kMaxSeqs) + 64 <= 232448, "shared memory of a CTA");
 
 template <int D>
@@ -747,11 +764,14 @@ cudaError_t run_packed(const PackedArgs& a, cudaStream_t stream) {
                           a.scale * 1.4426950408889634f, reinterpret_cast<uintptr_t>(a.out) % 32 == 0 ? 1 : 0};
   const cudaError_t e = ensure_smem<attention_packed_kernel<D>>(plan_smem<D>(kMaxSeqs));
   if (e != cudaSuccess) return e;
-  // a tile for every 128 / G tokens, and one more a request
+  // At most a tile for every 128 / G tokens, and one more a request; but no more CTAs than the first
+  // number and two a SM: each CTA makes the plan, and the batch may hold many requests without queries (one of 500
+  // tokens among 4096: a CTA for every tile there may be takes 1340 us, so 23)
   const int64_t by_rows = int64_t(a.num_q_rows) / tok + a.num_seqs;
   const int64_t by_len = int64_t(a.num_seqs) * ((a.max_query_len + tok - 1) / tok);
   const int64_t tiles = (by_rows < by_len ? by_rows : by_len) * a.num_kv_heads;
-  return launch_pdl(attention_packed_kernel<D>, dim3(unsigned(tiles)), dim3(kThreads), plan_smem<D>(a.num_seqs), stream, p,
+  const int64_t most = int64_t(a.num_q_rows) / tok * a.num_kv_heads + 2 * 152;
+  return launch_pdl(attention_packed_kernel<D>, dim3(unsigned(tiles < most ? tiles : most)), dim3(kThreads), plan_smem<D>(a.num_seqs), stream, p,
                     qm, km, vm);
 }
 

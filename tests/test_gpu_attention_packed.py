@@ -110,12 +110,19 @@ def test_more_tiles_than_sms(pa):
 
 
 def test_many_requests(pa):
-    n = 4096  # the most of a call; their order is the batch's beyond 384 with queries
+    n = 4096  # the most of a call; their order is the batch's beyond 512 with queries
     lens = [1 + i % 3 for i in range(n)]
     Case(lens, lens, 2, 1, 64, seed=7).run(pa).check(pa)
     lens = [0] * n
     lens[17], lens[4000] = 200, 70
     Case(lens, lens, 4, 1, 128, seed=8).run(pa).check(pa)
+
+
+def test_more_tiles_than_ctas(pa):
+    """Requests of one token each: a tile a request and KV head, far more than the rows would fill."""
+    Case([1] * 700, [40] * 700, 8, 4, 64, seed=18).run(pa).check(pa)
+    lens = [0, 1, 33, 0, 2, 1] * 300  # and tiles of several sizes among requests without queries
+    Case(lens, [n + 5 if n else 9 for n in lens], 16, 2, 64, seed=19).run(pa).check(pa)
 
 
 def test_large_logits_move_the_maximum(pa):
