@@ -40,20 +40,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// Eight consecutive elements of a row, and the row's largest and smallest (over LANES lanes).
+// Eight consecutive elements of a row, and the largest and smallest of several (over LANES lanes).
 template <typename T>
 struct Eight;
 
 template <>
 struct Eight<__nv_bfloat16> {
+  using Most = uint32_t;  // {max, -min} in one register: one shuffle and one maximum a step reduce both
   uint4 r;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
-  // {max, -min} in one register: one shuffle and one maximum a step reduce both
-  template <int LANES>
-  __device__ __forceinline__ float2 range() const {
+  __device__ __forceinline__ Most most() const {
     const uint32_t hi = max2_nan(max2_nan(r.x, r.y), max2_nan(r.z, r.w));
     const uint32_t lo = min2_nan(min2_nan(r.x, r.y), min2_nan(r.z, r.w)) ^ 0x80008000u;
-    uint32_t m = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+    return max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+  }
+  static __device__ __forceinline__ Most join(Most a, Most b) { return max2_nan(a, b); }
+  template <int LANES>
+  static __device__ __forceinline__ float2 range(Most m) {
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) m = max2_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
     return make_float2(__uint_as_float(m << 16), -__uint_as_float(m & 0xffff0000u));
@@ -63,25 +66,30 @@ struct Eight<__nv_bfloat16> {
 
 template <>
 struct Eight<float> {
+  using Most = float2;  // {max, -min}
   float f8[8];
   __device__ __forceinline__ void load(const float* p) {
     Elem<float>::unpack(reinterpret_cast<const uint4*>(p)[0], f8);
     Elem<float>::unpack(reinterpret_cast<const uint4*>(p)[1], f8 + 4);
   }
-  template <int LANES>
-  __device__ __forceinline__ float2 range() const {
+  __device__ __forceinline__ Most most() const {
     float hi = f8[0], lo = -f8[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
       hi = max_nan(hi, f8[i]);
       lo = max_nan(lo, -f8[i]);
     }
+    return make_float2(hi, lo);
+  }
+  static __device__ __forceinline__ Most join(Most a, Most b) { return make_float2(max_nan(a.x, b.x), max_nan(a.y, b.y)); }
+  template <int LANES>
+  static __device__ __forceinline__ float2 range(Most m) {
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) {
-      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-      lo = max_nan(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+      m.x = max_nan(m.x, __shfl_xor_sync(0xffffffffu, m.x, d));
+      m.y = max_nan(m.y, __shfl_xor_sync(0xffffffffu, m.y, d));
     }
-    return make_float2(hi, -lo);
+    return make_float2(m.x, -m.y);
   }
   __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
@@ -118,14 +126,16 @@ __device__ __forceinline__ void row_params(float2 range, uint32_t& param, float&
   inv = __frcp_rn(step);
 }
 
-// A warp takes U rows of one (K or V, head) a lane group: head_dim / 8 lanes hold a row, eight
-// elements each. With U = 4 each lane makes the parameters of one of its group's four rows, and the group
-// shares them: the divisions are a third of a row's instructions otherwise, and those bound the
-// kernel (16384 tokens of 8 heads x 128: 4 bits 25.4 -> 22.3 us, 8 bits 27.7 -> 23.5 us).
-template <typename T, int BITS, int D, int U>
+// A warp takes U rows of one (K or V, head) a lane group: D / (8 P) lanes hold a row, each P pieces of eight
+// elements, D / P apart. With U > 1 each lane makes the parameters of one of its group's rows, and the group
+// shares them: the divisions are a third of a row's instructions otherwise. Instructions bound the kernel
+// (16384 tokens of 8 heads x 128, 4 / 8 bits: parameters in every lane, P = 1, 25.4 / 27.7 us; shared 22.2 / 23.4;
+// P = 2 16.6 / 19.1).
+template <typename T, int BITS, int D, int P, int U>
 __global__ void __launch_bounds__(256) kv_write_int_kernel(const WriteParams p) {
   griddep_wait();
-  constexpr int LANES = D / 8, ROWS = 32 / LANES, ROW = code_row_bytes<D, BITS>();
+  constexpr int LANES = D / (8 * P), ROWS = 32 / LANES, ROW = code_row_bytes<D, BITS>();
+  static_assert(U <= LANES, "a lane for every row's parameters");
   constexpr uint32_t kMagic = 0x4B400000u;  // 1.5 * 2^23: adding it leaves the rounded code in the low bits
   const int lane = threadIdx.x & 31, sub = lane % LANES;
   const uint32_t unit = blockIdx.x * 8u + (threadIdx.x >> 5);
@@ -140,22 +150,27 @@ __global__ void __launch_bounds__(256) kv_write_int_kernel(const WriteParams p) 
   const int64_t rec_bytes = int64_t(p.block_size) * (ROW + 4), block_bytes = rec_bytes * p.num_kv_heads;
   unsigned char* cache = (is_v ? p.v_cache : p.k_cache) + head * rec_bytes;
 
-  Eight<T> x[U];
+  Eight<T> x[U][P];
   int64_t slot[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     slot[u] = -1;
     if (t0 + u * ROWS < p.num_tokens) {
       slot[u] = p.slot_mapping[t0 + u * ROWS];
-      x[u].load(src + u * ROWS * stride);
+#pragma unroll
+      for (int i = 0; i < P; ++i) x[u][i].load(src + u * ROWS * stride + i * (D / P));
     } else {
-      x[u] = {};
+#pragma unroll
+      for (int i = 0; i < P; ++i) x[u][i] = {};
     }
   }
-  float2 mine = x[0].template range<LANES>();
+  float2 mine = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int u = 1; u < U; ++u) {
-    const float2 r = x[u].template range<LANES>();
+  for (int u = 0; u < U; ++u) {
+    auto most = x[u][0].most();
+#pragma unroll
+    for (int i = 1; i < P; ++i) most = Eight<T>::join(most, x[u][i].most());
+    const float2 r = Eight<T>::template range<LANES>(most);
     if (sub % U == u) mine = r;
   }
   uint32_t my_param;
@@ -165,21 +180,25 @@ __global__ void __launch_bounds__(256) kv_write_int_kernel(const WriteParams p) 
   for (int u = 0; u < U; ++u) {
     const uint32_t param = U == 1 ? my_param : __shfl_sync(0xffffffffu, my_param, u, LANES);
     const float inv = U == 1 ? my_inv : __shfl_sync(0xffffffffu, my_inv, u, LANES);
-    float f[8];
-    x[u].get(f);
-    uint32_t w[2] = {0u, 0u};
+    uint32_t w[P][2];
     // the magic's bits add up to a constant beside the shifted codes
     const float2 lo2 = make_float2(-param_lo(param), -param_lo(param)), inv2 = make_float2(inv, inv),
                  magic2 = make_float2(__uint_as_float(kMagic), __uint_as_float(kMagic));
-#pragma unroll
-    for (int i = 6; i >= 0; i -= 2) {
-      const float2 c = ffma2v(fadd2(make_float2(f[i], f[i + 1]), lo2), inv2, magic2);
-      uint32_t& to = w[BITS == 8 ? i / 4 : 0];
-      to = (((to << BITS) + __float_as_uint(c.y)) << BITS) + __float_as_uint(c.x);
-    }
     constexpr uint32_t kSum = BITS == 8 ? kMagic * 0x01010101u : kMagic * 0x11111111u;
-    w[0] = param == kBadRow ? 0u : w[0] - kSum;
-    w[1] = param == kBadRow ? 0u : w[1] - kSum;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float f[8];
+      x[u][i].get(f);
+      w[i][0] = w[i][1] = 0u;
+#pragma unroll
+      for (int e = 6; e >= 0; e -= 2) {
+        const float2 c = ffma2v(fadd2(make_float2(f[e], f[e + 1]), lo2), inv2, magic2);
+        uint32_t& to = w[i][BITS == 8 ? e / 4 : 0];
+        to = (((to << BITS) + __float_as_uint(c.y)) << BITS) + __float_as_uint(c.x);
+      }
+      w[i][0] = param == kBadRow ? 0u : w[i][0] - kSum;
+      w[i][1] = param == kBadRow ? 0u : w[i][1] - kSum;
+    }
     if (slot[u] < 0) continue;
     if (slot[u] >= p.num_slots) {
       if (sub == 0) raise_error(p.err, PA_DEVERR_SLOT_RANGE);
@@ -196,10 +215,13 @@ __global__ void __launch_bounds__(256) kv_write_int_kernel(const WriteParams p) 
     }
     unsigned char* rec = cache + block * block_bytes;
     unsigned char* dst = rec + int64_t(at) * ROW + sub * BITS;
-    if (BITS == 8)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(dst) = w[0];
+#pragma unroll
+    for (int i = 0; i < P; ++i, dst += ROW / P) {
+      if (BITS == 8)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[i][0], w[i][1]);
+      else
+        *reinterpret_cast<uint32_t*>(dst) = w[i][0];
+    }
     if (sub == 0) *reinterpret_cast<uint32_t*>(rec + int64_t(p.block_size) * ROW + int64_t(at) * 4) = param;
   }
 }
@@ -330,15 +352,15 @@ __global__ void __launch_bounds__(256) kv_read_int_kernel(const ReadParams p) {
 
 template <typename T, int BITS, int D>
 cudaError_t write_as(WriteParams p, cudaStream_t stream) {
-  constexpr int ROWS = 32 / (D / 8);
-  // four rows a lane keep more loads in flight, one spreads few rows over the SMs: from 8 warps a SM on
+  // several rows and pieces a lane keep more loads in flight, one spreads few rows over the SMs: from 8 warps a SM on
+  constexpr int P = 2, U = sizeof(T) == 2 ? 4 : 2, MANY = 32 / (D / (8 * P)) * U, FEW = 32 / (D / 8);
   const int64_t kinds = 2 * int64_t(p.num_kv_heads);
-  const bool many = p.num_tokens * kinds / (ROWS * 4) >= 152 * 8;
-  const int64_t rows = ROWS * (many ? 4 : 1);
+  const bool many = p.num_tokens * kinds / MANY >= 152 * 8;
+  const int64_t rows = many ? MANY : FEW;
   p.units = uint32_t((p.num_tokens + rows - 1) / rows * kinds);
   const dim3 grid((p.units + 7) / 8);
-  return many ? launch_pdl(kv_write_int_kernel<T, BITS, D, 4>, grid, dim3(256), 0, stream, p)
-              : launch_pdl(kv_write_int_kernel<T, BITS, D, 1>, grid, dim3(256), 0, stream, p);
+  return many ? launch_pdl(kv_write_int_kernel<T, BITS, D, P, U>, grid, dim3(256), 0, stream, p)
+              : launch_pdl(kv_write_int_kernel<T, BITS, D, 1, 1>, grid, dim3(256), 0, stream, p);
 }
 
 template <typename T, int BITS, int D>
