@@ -129,6 +129,43 @@ def test_read_back(pa, bits, dtype, H, D, B, lens, starts):
         assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,H,D,B,S", [(2603, 8, 128, 16, 9), (5001, 5, 64, 4, 700)])
+def test_many_rows(pa, bits, dtype, T, H, D, B, S):
+    """Sizes at which a lane takes more of the work, with unusual rows and padding among the others."""
+    g = torch.Generator().manual_seed(T)
+    k, v = _rows(T, H, D, dtype, T, True)
+    for x in (k, v):
+        x[5::97, H - 1, 3] = float("nan")
+        x[7::89, 0, D - 1] = -float("inf")
+        x[11::83] = 2.75
+        x[13::79, :, ::2] = -0.0
+    cuts = torch.cat([torch.zeros(1), torch.randint(0, T + 1, (S - 1,), generator=g).sort().values, torch.tensor([T])]).to(I32)
+    lens = cuts.diff()
+    W = max(1, -(-int(lens.max()) // B))
+    NB = int((-(-lens // B)).sum()) + 3
+    table, ids = torch.full((S, W), -1, dtype=I32), torch.randperm(NB, generator=g).to(I32)
+    slots = torch.empty(T, dtype=torch.int64)
+    for s in range(S):
+        n, ids = -(-int(lens[s]) // B), ids[-(-int(lens[s - 1]) // B) if s else 0:]
+        table[s, :n] = ids[:n]
+        at = torch.arange(int(lens[s]))
+        slots[cuts[s]: cuts[s + 1]] = table[s, at // B].long() * B + at % B
+    slots[T // 2: T // 2 + 20] = -1
+    kc, vc = _cache(NB, H, B, D, bits), _cache(NB, H, B, D, bits, fill=0)
+    want = [ic.write(c.cpu().numpy(), _f64(x), slots.tolist(), bits) for c, x in ((kc, k), (vc, v))]
+    pa.kv_write_int(k, v, kc, vc, slots.cuda(), bits=bits)
+    out = [torch.empty((T, H, D), dtype=dtype, device="cuda") for _ in range(2)]
+    pa.kv_read_int(out[0], out[1], kc, vc, table.cuda(), None, lens.cuda(), cuts.cuda(), bits=bits)
+    torch.cuda.synchronize()
+    assert pa.read_device_errors() == 0
+    for got, c, w in zip(out, (kc, vc), want):
+        assert np.array_equal(c.cpu().numpy(), w)
+        rows = np.concatenate([ic.rows(w, table[s].tolist(), int(lens[s]), D, bits)[0] for s in range(S)])
+        assert torch.equal(got.cpu().nan_to_num(nan=1e30), torch.tensor(rows).float().to(dtype).nan_to_num(nan=1e30))
+
+
 def test_read_takes_what_fits_only(pa):
     """Positions past the rows or the table, negative ones and bad blocks are reported and leave their rows."""
     H, D, B = 1, 64, 16
