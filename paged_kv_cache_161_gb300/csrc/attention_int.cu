@@ -12,8 +12,8 @@
 // Bound: the cache's bytes (68 a row and head at 128 elements of 4 bits), and the instructions that turn
 // codes into 16-bit operands, about one an element of K and V. So: one pass, and every element converted once
 // for up to 8 or 16 query rows. Measured (GB300, 32 / 8 heads x 128): 64 requests of 32768 keys, 8 bits,
-// 674 us, 6600 GB/s of cache, 0.97 of the measured copy rate; 256 requests of 16 to 8192 keys around 1024, 4
-// bits, 98 us, 4800 GB/s (4 bits are bound by instructions and by what comes before and behind the stream).
+// 669 us, 6650 GB/s of cache, 0.98 of the measured copy rate; 256 requests of 16 to 8192 keys around 1024, 4
+// bits, 97 us, 4850 GB/s (4 bits are bound by instructions and by what comes before and behind the stream).
 //
 // Work: a unit is unit_keys keys of one segment (request, KV head, tile of 8 or 16 query rows: query tokens
 // x the head's query heads). The units of all segments, in order, are dealt to the grid's warps in
@@ -43,7 +43,7 @@ namespace {
 // A tile of query rows is NT times the 8 columns of an MMA. NT = 2 where a request has more than 8 rows a KV
 // head: the codes are converted once for 16, with 8 warps a CTA (their sums take 250 registers a thread)
 // instead of 12 (two requests of four drafted tokens, 40000 keys: 4 bits 51 us with two tiles of 8, 45 us
-// with one of 16, 8 bits 57 and 49 us, before the joins were made faster: now 42 and 46 us).
+// with one of 16, 8 bits 57 and 49 us, before the joins were made faster: now 43 and 46 us).
 template <int NT>
 __host__ __device__ constexpr int num_warps() { return NT == 1 ? 12 : 8; }
 template <int NT>

@@ -23,8 +23,8 @@
 // other, and the tensor cores idle meanwhile: one prompt of 16384 tokens took 1971 us, with two threads 1494);
 // warps 12-15 the output. The softmax goes on to the next tiles while P.V and the output follow, up to a ring's
 // length of tiles behind.
-// Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1245 us in a short burst, 1766 TFLOP/s, 0.91
-// of the measured burst bf16 rate, and 1445 us repeated for long, 0.88 of the sustained one; four chunks of 512
+// Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1240 us in a short burst, 1770 TFLOP/s, 0.91
+// of the measured burst bf16 rate, and 1430 us repeated for long, 0.89 of the sustained one; four chunks of 512
 // behind 8192 keys 169 us, 1470 TFLOP/s; 16 prompts of 1024 123 us.
 // Tiles: requests with the most keys first (up to kThreads of them), a request's last tiles first; a running CTA
 // takes the tiles of CTAs that have not started (clusterlaunchcontrol), so no counter lives in memory between
