@@ -290,12 +290,14 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int wsum[kWarps];
   __shared__ int4 desc[kWarps * 2];
+  __shared__ uint32_t missing[kWarps * STAGES];  // of a stage's keys, four a bit: those of a block that is not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int S = p.num_seqs;
   // shared memory: the warps' rings, the units' prefix over the requests
   unsigned char* ring = smem + warp * STAGES * STAGE;
   int* prefix = reinterpret_cast<int*>(smem + kWarps * STAGES * STAGE);
   if (threadIdx.x < kWarps * 2) desc[threadIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x < kWarps * STAGES) missing[threadIdx.x] = 0u;
   griddep_wait();
 
   // ---- the plan: units of every request, their prefix, this warp's run. Sums stop at 2^31 - 1, which only
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     int u, seg_end = 0, x = 0, units = 0, blocks = 0, b0 = 0, ent = 0, ent_next = 0;
     int b = 0, in = 0;  // block and offset of the next piece
     int stage = 0;
+    bool any_missing = false;  // a block id out of range has been met: `missing` is kept from here on
     const int32_t* row = nullptr;
     int64_t head_off = 0;
   } pr;
@@ -362,10 +365,12 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     pr.b0 = b0;
     pr.ent = pr.ent_next;
     pr.ent_next = entry(b0 + 32 + lane);
-    if (b0 + lane < pr.blocks && (pr.ent < 0 || pr.ent >= p.num_blocks)) {
+    const bool bad = b0 + lane < pr.blocks && (pr.ent < 0 || pr.ent >= p.num_blocks);
+    if (bad) {
       raise_error(p.err, PA_DEVERR_BLOCK_RANGE);
       pr.ent = -1;
     }
+    if (__any_sync(0xffffffffu, bad)) pr.any_missing = true;
   };
   auto locate = [&]() {  // the segment of pr.u, past its start; false: the run ends before its keys
     const Segment sg = segment_of<KU, NT>(p, prefix, pr.u);
@@ -443,6 +448,12 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
               ++pr.b;
             }
           }
+        }
+        // a copy that is left out leaves what the stage held: those keys are marked, from the table once more
+        if (pr.any_missing) {
+          const int id = entry((pr.x * KU + 4 * (lane & 15)) / p.block_size);
+          const uint32_t none = __ballot_sync(0xffffffffu, lane < 16 && (id < 0 || id >= p.num_blocks));
+          if (lane == 0) missing[warp * STAGES + pr.stage] = none;
         }
       }
       ++pr.x;
@@ -578,8 +589,8 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     float wscale = __uint_as_float(254u << 23);
 
     // tiles tile0 .. of a stage whose keys start at key0: all of a whole unit's, or one with masks (small
-    // code: the two together have to stay in the instruction cache)
-    auto unit = [&](const unsigned char* st, int key0, int tile0, auto tail_c) {
+    // code: the two together have to stay in the instruction cache), of which those in `none` are skipped
+    auto unit = [&](const unsigned char* st, int key0, int tile0, uint32_t none, auto tail_c) {
       constexpr bool kTail = decltype(tail_c)::value;
       constexpr int TILES = kTail ? 1 : NT == 1 ? KU / 16 : 2;
       // ---- q.c of 16 keys x 8 NT query rows a tile, all tiles before their logits: independent chains, two a
@@ -643,8 +654,10 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
       for (int tile = 0; tile < TILES; ++tile)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int key = key0 + (tile0 + tile) * 16 + key_of(g + 8 * i);
-          if (kTail && key >= n_max) pk[tile][i] = pv[tile][i] = 0u;  // a row behind the last: whatever it holds
+          const int in_unit = (tile0 + tile) * 16 + key_of(g + 8 * i), key = key0 + in_unit;
+          const bool gone = kTail && (none >> (in_unit >> 2) & 1u);
+          // a row behind the last, or of no block: whatever it holds
+          if (kTail && (key >= n_max || gone)) pk[tile][i] = pv[tile][i] = 0u;
           const float step = param_step(pk[tile][i]), lo = param_lo(pk[tile][i]);
           ws[tile][i] = param_step(pv[tile][i]);
           midv[tile][i] = fmaf(ws[tile][i], kMid, param_lo(pv[tile][i]));
@@ -655,7 +668,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
               const int e = 2 * i + h;
               const float c = (NT == 1 ? s[tile][nt][e] + s1[tile][e] : s[tile][nt][e]) + off[nt][h];
               x[tile][nt][e] = fmaf(c, step, lo * qs[nt][h]) * fac[nt][h];
-              hidden[tile][nt][e] = kTail && key >= lim[nt][h];
+              hidden[tile][nt][e] = kTail && (key >= lim[nt][h] || gone);
               if (hidden[tile][nt][e]) x[tile][nt][e] = -INFINITY;
             }
         }
@@ -781,12 +794,13 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
       __syncwarp();
       const int key0 = x * KU;
       const unsigned char* st = ring + stage * STAGE;
-      if (key0 + KU <= n_min) {
+      if (key0 + KU <= n_min && !pr.any_missing) {
 #pragma unroll 1
-        for (int tile = 0; tile < KU / 16; tile += NT == 1 ? KU / 16 : 2) unit(st, key0, tile, std::false_type{});
+        for (int tile = 0; tile < KU / 16; tile += NT == 1 ? KU / 16 : 2) unit(st, key0, tile, 0u, std::false_type{});
       } else {
+        const uint32_t none = pr.any_missing ? missing[warp * STAGES + stage] : 0u;
 #pragma unroll 1
-        for (int tile = 0; tile < KU / 16 && key0 + tile * 16 < n_max; ++tile) unit(st, key0, tile, std::true_type{});
+        for (int tile = 0; tile < KU / 16 && key0 + tile * 16 < n_max; ++tile) unit(st, key0, tile, none, std::true_type{});
       }
       __syncwarp();
       if (kAhead) fill();
