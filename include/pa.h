@@ -534,8 +534,9 @@ int pa_attention_sparse(void* out, const void* q, const void* k_cache, const voi
  * head_dim], `dtype` PA_BF16 / PA_F32, computed in fp32 and rounded once). start_pos: device, int32
  * [num_seqs], or null (all 0). row_start_loc: device, int32 [num_seqs + 1], not decreasing. Rows of a
  * request behind those (room for a chunk's own rows) and rows of no request are left as they are. A request
- * whose positions do not fit its rows or its table, or a negative one, sets PA_DEVERR_SEQ_RANGE; a
- * block id outside [0, num_blocks) PA_DEVERR_BLOCK_RANGE; their rows are left as they are.
+ * whose positions do not fit its rows (those below num_rows; it may have none) or its table, or a
+ * negative one, sets PA_DEVERR_SEQ_RANGE; a block id outside [0, num_blocks) PA_DEVERR_BLOCK_RANGE;
+ * their rows are left as they are. With num_rows = 0 nothing is launched, and so nothing reported.
  *
  * pa_attention_int: pa_attention over such caches, q and out bf16 [num_tokens, num_heads, head_dim]:
  * token j of a request's q_len sits at position seq_lens - q_len + j and sees the positions up to its

@@ -238,6 +238,7 @@ struct ReadParams {
   const int32_t* row_start_loc;
   unsigned int* err;
   int64_t num_rows, num_blocks, units;
+  unsigned row_ctas;  // CTAs of the rows; those behind them check the requests
   int max_blocks_per_seq, num_seqs, block_size, num_kv_heads;
   int wide;  // the outputs are 32-byte aligned
 };
@@ -276,12 +277,25 @@ __device__ __forceinline__ void decode16(const uint32_t* w, uint32_t param, floa
   }
 }
 
+// Whether a request's positions start .. L - 1 fit its table and its rows r0 .. r1 - 1 (of num_rows).
+__device__ __forceinline__ bool fits(const ReadParams& p, int64_t r0, int64_t r1, int start, int L) {
+  if (r0 < 0 || start < 0 || L < 0 || L > int64_t(p.max_blocks_per_seq) * p.block_size) return false;
+  return L <= start || int64_t(L) - start <= min(r1, p.num_rows) - r0;
+}
+
 // A warp takes 32 / (head_dim / 16) consecutive output rows and COMBOS of the 2 num_kv_heads (K
 // or V, head) rows of each: sixteen elements a lane. The lane's row is found once for all of them.
 template <typename T, int BITS, int D, int COMBOS>
 __global__ void __launch_bounds__(256) kv_read_int_kernel(const ReadParams p) {
   griddep_wait();
   constexpr int LANES = D / 16, ROWS = 32 / LANES, ROW = code_row_bytes<D, BITS>(), WORDS = BITS / 2;
+  // A request that does not fit may have no row that would tell: CTAs of their own look at all of them.
+  if (blockIdx.x >= p.row_ctas) {
+    const int64_t s = int64_t(blockIdx.x - p.row_ctas) * 256 + threadIdx.x;
+    if (s < p.num_seqs && !fits(p, p.row_start_loc[s], p.row_start_loc[s + 1], p.start_pos ? p.start_pos[s] : 0, p.seq_lens[s]))
+      raise_error(p.err, PA_DEVERR_SEQ_RANGE);
+    return;
+  }
   const int lane = threadIdx.x & 31, sub = lane % LANES;
   const int64_t unit = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (unit >= p.units) return;
@@ -300,10 +314,7 @@ __global__ void __launch_bounds__(256) kv_read_int_kernel(const ReadParams p) {
   const int64_t r0 = p.row_start_loc[s], r1 = p.row_start_loc[s + 1];
   if (r < r0 || r >= r1) return;  // a row of no request
   const int L = p.seq_lens[s], start = p.start_pos ? p.start_pos[s] : 0, B = p.block_size;
-  if (r0 < 0 || start < 0 || L < 0 || int64_t(L) - start > r1 - r0 || L > int64_t(p.max_blocks_per_seq) * B) {
-    if (sub == 0 && (r == r0 || r == 0)) raise_error(p.err, PA_DEVERR_SEQ_RANGE);
-    return;
-  }
+  if (!fits(p, r0, r1, start, L)) return;
   const int64_t pos = start + (r - r0);
   if (pos >= L) return;  // behind the positions asked for: left as it is
   const int64_t block = p.block_table[int64_t(s) * p.max_blocks_per_seq + pos / B];
@@ -369,7 +380,8 @@ cudaError_t read_as(ReadParams p, cudaStream_t stream) {
   // against 17.1 us, 256 rows 3.75 against 3.1 us)
   const bool many = groups * ((kinds + 7) / 8) >= 152 * 8;
   p.units = groups * (many ? (kinds + 7) / 8 : (kinds + 3) / 4);
-  const dim3 grid(unsigned((p.units + 7) / 8));
+  p.row_ctas = unsigned((p.units + 7) / 8);
+  const dim3 grid(p.row_ctas + (unsigned(p.num_seqs) + 255u) / 256u);
   return many ? launch_pdl(kv_read_int_kernel<T, BITS, D, 8>, grid, dim3(256), 0, stream, p)
               : launch_pdl(kv_read_int_kernel<T, BITS, D, 4>, grid, dim3(256), 0, stream, p);
 }
@@ -403,7 +415,7 @@ cudaError_t launch_kv_read_int(const KvIntArgs& a, void* k_out, void* v_out, con
   const bool wide = (reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) % 32 == 0;
   const ReadParams p = {k_out, v_out, static_cast<const unsigned char*>(k_cache),
                         static_cast<const unsigned char*>(v_cache), block_table, start_pos, seq_lens, row_start_loc,
-                        a.err, num_rows, a.num_blocks, 0, max_blocks_per_seq, num_seqs, a.block_size, a.num_kv_heads,
+                        a.err, num_rows, a.num_blocks, 0, 0u, max_blocks_per_seq, num_seqs, a.block_size, a.num_kv_heads,
                         wide ? 1 : 0};
   return PA_INT_DISPATCH(read_as, a.dtype, a.bits, a.head_dim, p, stream);
 }
