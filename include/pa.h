@@ -547,7 +547,8 @@ int pa_attention_sparse(void* out, const void* q, const void* k_cache, const voi
  * or q_len > seq_len sets PA_DEVERR_SEQ_RANGE and its rows are left as they are (other requests' too, where
  * query_start_loc decreases). The positions of a block id outside [0, num_blocks) are skipped
  * (PA_DEVERR_BLOCK_RANGE); a token that sees no others gets zeros. A key or value row that reads back as
- * NaN gives NaN to the tokens that see it, and to no other. workspace: device, pa_attention_int_workspace_size bytes, 16-byte
+ * NaN gives NaN to the tokens that see it, and to no other. Logits are fp32, with their own range and
+ * that of scale sum_d |q_d| 2^bits. workspace: device, pa_attention_int_workspace_size bytes, 16-byte
  * aligned, no contents needed; calls that may overlap on the GPU need one each. The result depends on
  * nothing but the arguments' contents and the GPU's number of SMs. num_seqs <= 4096
  * (PA_ERR_UNSUPPORTED).

@@ -508,7 +508,9 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     const int j_first = sg.tile * kRows / p.group, j_last = (sg.tile * kRows + rows - 1) / p.group;
     const int n_min = r.L - r.q_len + j_first + 1, n_max = r.L - r.q_len + j_last + 1;  // keys the rows see
     // Query row g (g + 8) of the tile as f16 with its largest element in [2^14, 2^15): a power of two, so exact
-    // but for elements 2^24 times smaller than the row's largest. Its factor goes into the logits'.
+    // but for elements 2^24 times smaller than the row's largest. Its factor goes back in with the logits' scale
+    // before the row parameters do: q.c scale and sum(q) scale have the logits' own range, however
+    // large the keys and small the queries.
     uint32_t qb[NT][NK][2];
     // of query rows 2t and 2t + 1 (and 8 on), whose logits this lane holds
     float qs[NT][2], off[NT][2], fac[NT][2], m[NT][2], l[NT][2], mid[NT][2];
@@ -569,9 +571,9 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        qs[nt][h] = __shfl_sync(0xffffffffu, qsum, (2 * t + h) * 4);
-        off[nt][h] = -kOffset * __shfl_sync(0xffffffffu, qoff, (2 * t + h) * 4);
         fac[nt][h] = __shfl_sync(0xffffffffu, qfactor, (2 * t + h) * 4);
+        qs[nt][h] = __shfl_sync(0xffffffffu, qsum, (2 * t + h) * 4) * fac[nt][h];
+        off[nt][h] = -kOffset * __shfl_sync(0xffffffffu, qoff, (2 * t + h) * 4);
         m[nt][h] = kNoMax;
         l[nt][h] = mid[nt][h] = 0.f;
         lim[nt][h] = r.L - r.q_len + (sg.tile * kRows + min(8 * nt + 2 * t + h, rows - 1)) / p.group + 1;
@@ -667,7 +669,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
             for (int h = 0; h < 2; ++h) {
               const int e = 2 * i + h;
               const float c = (NT == 1 ? s[tile][nt][e] + s1[tile][e] : s[tile][nt][e]) + off[nt][h];
-              x[tile][nt][e] = fmaf(c, step, lo * qs[nt][h]) * fac[nt][h];
+              x[tile][nt][e] = fmaf(c * fac[nt][h], step, lo * qs[nt][h]);
               hidden[tile][nt][e] = kTail && (key >= lim[nt][h] || gone);
               if (hidden[tile][nt][e]) x[tile][nt][e] = -INFINITY;
             }
