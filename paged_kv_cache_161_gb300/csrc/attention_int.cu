@@ -541,8 +541,11 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
       }
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      const int ex = int(__float_as_uint(big) >> 23);  // biased exponent; 0 and 255: left unscaled
-      const int shift = (ex == 0 || ex == 255 || row >= rows) ? 0 : min(127, 14 - (ex - 127));
+      // the biased exponent; 255: left unscaled. 2^113 turns the smallest bfloat16 into 16 times the smallest
+      // f16 (odd elements of 4-bit rows are divided by 16 below), so no row needs more, and the factor's inverse
+      // stays a normal number.
+      const int ex = int(__float_as_uint(big) >> 23);
+      const int shift = (ex == 255 || row >= rows) ? 0 : min(113, 14 - (ex - 127));
       const float mul = row >= rows ? 0.f : __uint_as_float(uint32_t(shift + 127) << 23);
       const float qfactor = p.scale_log2 * exp2f(float(-shift));
 #pragma unroll

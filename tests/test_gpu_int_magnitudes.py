@@ -28,3 +28,14 @@ def test_large_keys(pa, bits, qlens, size):  # noqa: F811
     b.q.div_(size)
     b.run()
     _check(b)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("qlens", [[1, 1], [4, 3]])
+def test_queries_below_the_smallest_normal_number(pa, bits, qlens):  # noqa: F811
+    b = Batch(pa, [300, 40], qlens, 4, 1, 128, 16, bits, seed=42, size=1e37)
+    b.q.copy_((b.q.float() * 2.0 ** -131).to(BF16))
+    assert 0 < float(b.q.float().abs().max()) < 2.0 ** -126
+    b.scale = 16.0
+    b.run()
+    _check(b)
