@@ -548,7 +548,8 @@ int pa_attention_sparse(void* out, const void* q, const void* k_cache, const voi
  * query_start_loc decreases). The positions of a block id outside [0, num_blocks) are skipped
  * (PA_DEVERR_BLOCK_RANGE); a token that sees no others gets zeros. A key or value row that reads back as
  * NaN gives NaN to the tokens that see it, and to no other. Logits are fp32, with their own range and
- * that of scale sum_d |q_d| 2^bits. workspace: device, pa_attention_int_workspace_size bytes, 16-byte
+ * that of scale sum_d |q_d| 2^bits; so are the sums over the keys before the division, finite for values
+ * below 2^119 / seq_len. workspace: device, pa_attention_int_workspace_size bytes, 16-byte
  * aligned, no contents needed; calls that may overlap on the GPU need one each. The result depends on
  * nothing but the arguments' contents and the GPU's number of SMs. num_seqs <= 4096
  * (PA_ERR_UNSUPPORTED).

@@ -169,6 +169,7 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
   return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return ffma2v(a, b, make_float2(0.f, 0.f)); }
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
@@ -588,10 +589,12 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
 #pragma unroll
       for (int i = 0; i < NK; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     // Numerators times value steps enter the second product as f16 (rounded to 2^-11 relative at most: an
-    // eighth of the output's own rounding), scaled by the power of two 2^wexp that keeps the steps seen so
-    // far below 2^7 and so the products below 2^15; what rounds to nothing is 2^-31 of the largest.
-    int wexp = 127;
-    float wscale = __uint_as_float(254u << 23);
+    // eighth of the output's own rounding), scaled by a power of two a query row, wscale, that keeps the products
+    // below 2^15 and the largest of them so far at 2^3 or more: what rounds to nothing is 2^-28 of that one,
+    // whatever the steps of rows without weight.
+    float wscale[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) wscale[nt][0] = wscale[nt][1] = __uint_as_float(253u << 23);
 
     // tiles tile0 .. of a stage whose keys start at key0: all of a whole unit's, or one with masks (small
     // code: the two together have to stay in the instruction cache), of which those in `none` are skipped
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
         }
       }
       // ---- logits (in powers of two), numerators: [0], [1] key_of(g), [2], [3] key_of(g + 8)
-      float x[TILES][NT][4], ws[TILES][2], midv[TILES][2];
+      float x[TILES][NT][4], ws[TILES][2];
       bool hidden[TILES][NT][4];
 #pragma unroll
       for (int tile = 0; tile < TILES; ++tile)
@@ -665,20 +668,23 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
           if (kTail && (key >= n_max || gone)) pk[tile][i] = pv[tile][i] = 0u;
           const float step = param_step(pk[tile][i]), lo = param_lo(pk[tile][i]);
           ws[tile][i] = param_step(pv[tile][i]);
-          midv[tile][i] = fmaf(ws[tile][i], kMid, param_lo(pv[tile][i]));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            float2 c = make_float2(s[tile][nt][2 * i], s[tile][nt][2 * i + 1]);
+            if (NT == 1) c = fadd2(c, make_float2(s1[tile][2 * i], s1[tile][2 * i + 1]));
+            c = mul2(fadd2(c, make_float2(off[nt][0], off[nt][1])), make_float2(fac[nt][0], fac[nt][1]));
+            c = ffma2v(c, make_float2(step, step), mul2(make_float2(lo, lo), make_float2(qs[nt][0], qs[nt][1])));
+            x[tile][nt][2 * i] = c.x, x[tile][nt][2 * i + 1] = c.y;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int e = 2 * i + h;
-              const float c = (NT == 1 ? s[tile][nt][e] + s1[tile][e] : s[tile][nt][e]) + off[nt][h];
-              x[tile][nt][e] = fmaf(c * fac[nt][h], step, lo * qs[nt][h]);
               hidden[tile][nt][e] = kTail && (key >= lim[nt][h] || gone);
               if (hidden[tile][nt][e]) x[tile][nt][e] = -INFINITY;
             }
+          }
         }
-      // The reference maximum moves only when a logit passes it by 2^8, the steps' power of two when
-      // one passes it twofold: then, for the whole warp, the sums so far are scaled.
+      // The reference maximum (a whole number, so that moves are exact) moves only when a logit passes it by
+      // 2^8, a row's wscale when its maximum does or a step comes over 2^7: then the sums so far are scaled.
       float top[NT][2], big = fmaxf(ws[0][0], ws[0][1]);
       bool move = false;
 #pragma unroll
@@ -690,37 +696,46 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
           top[nt][h] = fmaxf(x[0][nt][h], x[0][nt][2 + h]);
 #pragma unroll
           for (int tile = 1; tile < TILES; ++tile) top[nt][h] = fmax3(top[nt][h], x[tile][nt][h], x[tile][nt][2 + h]);
-          move = move || top[nt][h] - m[nt][h] > 8.f;
+          move = move || top[nt][h] - m[nt][h] > 8.f || big * wscale[nt][h] > 128.f;
         }
-      if (__any_sync(0xffffffffu, move || big * wscale > 128.f)) {
-        // NaN steps (of rows that hold NaN) do not count
+      if (__any_sync(0xffffffffu, move)) {
+        // The power that brings the unit's largest step to [2^6, 2^7): small enough for every product (numerators
+        // are at most 2^8). NaN steps (of rows that hold NaN) do not count.
         const uint32_t bits = __float_as_uint(big);
         const uint32_t most = __reduce_max_sync(0xffffffffu, bits <= 0x7f800000u ? bits : 0u);
-        const int want = min(127, 6 - (int(most >> 23) - 126));
-        float beta = 1.f;
-        if (want < wexp) {
-          beta = exp2f(float(want - wexp));
-          wexp = want;
-          wscale = __uint_as_float(uint32_t(want + 127) << 23);
-        }
+        const int by_step = 6 - (int(most >> 23) - 126);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float alpha[2];
+          float beta[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float up = top[nt][h];
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
-            if (!(up - m[nt][h] > 8.f)) up = m[nt][h];
-            alpha[h] = exp2f(m[nt][h] - up);
+            up = up - m[nt][h] > 8.f ? ceilf(up) : m[nt][h];
+            // the power that brings the row's largest product of the unit to [2^3, 2^4): the larger of the two,
+            // but not so large that the largest product of the units before passes where it was
+            float peak = 0.f;
+#pragma unroll
+            for (int tile = 0; tile < TILES; ++tile)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) peak = fmaxf(peak, ex2_ftz(x[tile][nt][2 * i + h] - up) * ws[tile][i]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, d));
+            const int by_product = 3 - (int(__float_as_uint(peak) >> 23) - 126);
+            const int old = int(__float_as_uint(wscale[nt][h]) >> 23) - 127;
+            const int want = min(min(126, old + int(fminf(up - m[nt][h], 300.f))), max(by_step, by_product));
+            wscale[nt][h] = __uint_as_float(uint32_t(want + 127) << 23);
+            beta[h] = exp2f(float(want - old) + (m[nt][h] - up));  // at most 1
+            const float alpha = exp2f(m[nt][h] - up);
             m[nt][h] = up;
-            l[nt][h] *= alpha[h];
-            mid[nt][h] *= alpha[h];
+            l[nt][h] *= alpha;
+            mid[nt][h] *= alpha;
           }
 #pragma unroll
           for (int i = 0; i < NK; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][i][e] *= alpha[e & 1] * beta;
+            for (int e = 0; e < 4; ++e) o[nt][i][e] *= beta[e & 1];
         }
       }
       uint32_t pb[TILES][NT][2];
@@ -728,19 +743,25 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
       for (int tile = 0; tile < TILES; ++tile)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float wi = ws[tile][i] * wscale;
+          asm volatile("" : "+r"(pv[tile][i]));  // unpacked here, not above: fewer registers over the move
+          const float step = param_step(pv[tile][i]), middle = fmaf(step, kMid, param_lo(pv[tile][i]));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float w[2];
+            float w[2], e2[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) e2[h] = ex2_ftz(x[tile][nt][2 * i + h] - m[nt][h]);
+            // (a step times wscale alone may pass the largest float where the numerator is 0)
+            const float2 scaled = mul2(mul2(make_float2(e2[0], e2[1]), make_float2(step, step)),
+                                       make_float2(wscale[nt][0], wscale[nt][1]));
+            w[0] = scaled.x, w[1] = scaled.y;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float e = ex2_ftz(x[tile][nt][2 * i + h] - m[nt][h]);
+              const float e = e2[h];
               l[nt][h] += e;
-              w[h] = e * wi;
               if (hidden[tile][nt][2 * i + h]) {
                 w[h] = 0.f;  // not 0 * NaN
               } else {
-                mid[nt][h] = fmaf(e, midv[tile][i], mid[nt][h]);
+                mid[nt][h] = fmaf(e, middle, mid[nt][h]);
               }
             }
             pb[tile][nt][i] = movm(pack_f16(w[0], w[1]));
@@ -812,7 +833,6 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
       if (++stage == STAGES) stage = 0;
     }
     // ---- the segment's end in this run: sums over the lanes that share a query row, then out or a piece
-    const float unscale = exp2f(float(-wexp));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -825,6 +845,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
         }
         const int row = 8 * nt + 2 * t + h;
         if (row >= rows) continue;
+        const float unscale = __uint_as_float((254u << 23) - __float_as_uint(wscale[nt][h]));
         float f[D / 8];
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
