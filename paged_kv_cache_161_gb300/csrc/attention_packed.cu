@@ -31,7 +31,8 @@
 // calls.
 //
 // Every wait is bounded; on a timeout the kernel sets an error bit and leaves after its copies and
-// products in flight have landed, freeing TMEM.
+// products in flight have landed, freeing TMEM. All waits are for what takes a few steps, but for the output's, for a
+// whole tile: its bound grows with the tile's steps.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -69,6 +70,9 @@ struct Tile {
   int t, hk, row0, nq, k0, pos0, leff, nt;
 };
 constexpr int kSlots = 4;
+// Steps of a tile (4 million keys) for which the output waits once more, as long as a wait may last: 25 ms
+// at 0.75 us a step of 128 keys
+constexpr int kWaitSteps = 1 << 15;
 
 template <int D>
 struct Layout {
@@ -176,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   constexpr int NH = LY::NH;
   extern __shared__ unsigned char smem_raw[];
   __shared__ int wsum[kThreads / 32];
+  __shared__ volatile int failed;  // a wait of the CTA ran out
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms
   unsigned char* sm = smem_raw + (base - raw);
@@ -301,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   };
 
   if (threadIdx.x == 0) {
+    failed = 0;
     for (int i = 0; i < kBars; ++i) {
       uint32_t n = 1;
       if (i == bSFree0 || i == bSFree1 || i == bP0 || i == bP1) n = 4;
@@ -319,7 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + LY::MISC);
-  auto fail = [&]() { raise_error(p.err, PA_DEVERR_TIMEOUT); };
+  auto fail = [&]() {
+    failed = 1;
+    raise_error(p.err, PA_DEVERR_TIMEOUT);
+  };
   // Step n (counted over the CTA's tiles) uses S, P, K and V number n & 1; phase n >> 1 of their barriers.
   // No waiter can be two phases behind: the next phase of each barrier needs something of the waiter's.
   auto wait_step = [&](int b0, int n) { return mbar_wait(bar(b0 + (n & 1)), uint32_t(n >> 1) & 1u); };
@@ -662,8 +671,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       if (x.t < 0) break;
       const int end = n + x.nt - 1;  // the tile's last step
       n += x.nt;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(bX0 + slot * 4 + wr), uint32_t(i / kSlots) & 1u)) ||
-          (x.nt > 0 && !__all_sync(0xffffffffu, wait_step(bPV0, end)))) {
+      bool done = false;
+      for (int tries = x.nt / kWaitSteps; !done && tries >= 0; --tries) {
+        done = __all_sync(0xffffffffu, mbar_wait(bar(bX0 + slot * 4 + wr), uint32_t(i / kSlots) & 1u));
+        if (__any_sync(0xffffffffu, failed)) break;  // what is waited for may not come
+      }
+      if (!done || (x.nt > 0 && !__all_sync(0xffffffffu, wait_step(bPV0, end)))) {
         ok = false;
         break;
       }
@@ -744,7 +757,7 @@ bool row_map(CUtensorMap* m, const void* ptr, int D, int heads, int rows, int64_
 
 template <int D>
 constexpr size_t plan_smem(int num_seqs) { return Layout<D>::PLAN + 6 * (size_t(num_seqs) + 8) + 1024; }
-static_assert(plan_smem<128>(kMaxSeqs) + 64 <= 232448, "shared memory of a CTA");
+static_assert(plan_smem<128>(kMaxSeqs) + 128 <= 232448, "shared memory of a CTA");
 
 template <int D>
 cudaError_t run_packed(const PackedArgs& a, cudaStream_t stream) {
