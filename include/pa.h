@@ -594,8 +594,8 @@ int pa_attention_int(void* out, const void* q, const void* k_cache, const void* 
  *               of more than max_query_len queries, sets PA_DEVERR_SEQ_RANGE and its rows are left as they
  *               are; so are rows of no request
  * Numerators are rounded to bf16 for the second product, as pa_attention's are. A NaN or an infinity in
- * another request's rows changes nothing; one in a value row reaches the request's queries of the same
- * 128-key step, and those that see it.
+ * another request's rows changes nothing; one in a value row reaches the queries that see it and the
+ * others of their tile: 128 / (num_heads / num_kv_heads) consecutive tokens, counted from the request's first.
  * Supported: head_dim 64 / 128, num_heads / num_kv_heads in {1, 2, 4, 8}, num_seqs <= 4096. One
  * launch on `stream`, no workspace.
  * --------------------------------------------------------------------------- */
