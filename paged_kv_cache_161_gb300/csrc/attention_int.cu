@@ -12,8 +12,8 @@
 // Bound: the cache's bytes (68 a row and head at 128 elements of 4 bits), and the instructions that turn
 // codes into 16-bit operands, about one an element of K and V. So: one pass, and every element converted once
 // for up to 8 or 16 query rows. Measured (GB300, 32 / 8 heads x 128): 64 requests of 32768 keys, 8 bits,
-// 669 us, 6650 GB/s of cache, 0.98 of the measured copy rate; 256 requests of 16 to 8192 keys around 1024, 4
-// bits, 97 us, 4850 GB/s (4 bits are bound by instructions and by what comes before and behind the stream).
+// 655 to 673 us, 6610 GB/s of cache or more, 0.97 of the measured copy rate; 256 requests of 16 to 8192 keys around
+// 1024, 4 bits, 98 us, 4800 GB/s (4 bits are bound by instructions, latency and what comes before and behind the stream).
 //
 // Work: a unit is unit_keys keys of one segment (request, KV head, tile of 8 or 16 query rows: query tokens
 // x the head's query heads). The units of all segments, in order, are dealt to the grid's warps in
@@ -29,8 +29,8 @@
 // dimension sits where in a contraction is free as long as both sides agree, so a lane takes 16-byte pieces
 // of rows as they lie; so is which key is which row.
 //
-// The kernels start before the one in front of them has ended and read what it wrote behind
-// griddep_wait(): none of their pointers is __restrict__ or read through __ldg.
+// The kernels may start before the one in front of them has ended, where that one lets them (these do not), and
+// read what it wrote behind griddep_wait(): none of their pointers is __restrict__ or read through __ldg.
 #include <type_traits>
 
 #include "int_codes.cuh"
@@ -42,8 +42,8 @@ namespace {
 
 // A tile of query rows is NT times the 8 columns of an MMA. NT = 2 where a request has more than 8 rows a KV
 // head: the codes are converted once for 16, with 8 warps a CTA (their sums take 250 registers a thread)
-// instead of 12 (two requests of four drafted tokens, 40000 keys: 4 bits 51 us with two tiles of 8, 45 us
-// with one of 16, 8 bits 57 and 49 us, before the joins were made faster: now 43 and 46 us).
+// instead of 12 (two requests of four drafted tokens, 40000 keys: 4 bits 45 us with two tiles of 8, 44 us with
+// one of 16, 8 bits 52 and 45 us; 160000 keys: 132 and 113 us, 162 and 120 us).
 template <int NT>
 __host__ __device__ constexpr int num_warps() { return NT == 1 ? 12 : 8; }
 template <int NT>
@@ -54,7 +54,7 @@ constexpr int kPart = 32;  // keys of a copy at most
 template <int BITS>
 __host__ __device__ constexpr int unit_keys() { return BITS == 4 ? 64 : 32; }
 // A segment's start in units of keys, by the time it takes (256 requests of 16 to 8192 keys around 1024, 4
-// bits: 0 units 121 us, 1 108, 2 100; 8 bits: 0 units 167 us, 2 158, 4 157)
+// bits: 0 units 122 us, 1 108, 2 99, 4 105; 8 bits: 0 units 170 us, 1 161, 2 158, 4 159)
 template <int KU>
 __host__ __device__ constexpr int start_units() { return 2; }
 template <int D, int NT>
@@ -274,8 +274,9 @@ __device__ __forceinline__ void join_rows(const IntParams& p, int2 where, int ro
   }
 }
 
-// B16: blocks of 16 tokens, whose copies are all of one known size (256 requests of 1024 keys, 4 bits: 82 us
-// without, 70 us with; two requests of four drafts, 8 bits: 53, 49 us)
+// B16: blocks of 16 tokens, whose copies are all of one known size (256 requests of 1024 keys, 4 bits: 81 us
+// without, 70 us with; two requests of four drafts, 40000 keys, 8 bits: 50, 45 us). In other blocks, 4 / 8 bits: of 8 96 / 114 us, of
+// 32 to 128 74 to 76 / 104 us; their 12-warp kernels of 128 elements spill 12 and 44 bytes a thread.
 template <int D, int BITS, bool B16, int NT>
 __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(const IntParams p) {
   constexpr int kWarps = num_warps<NT>(), kRows = num_rows<NT>();
@@ -482,10 +483,9 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
 
   uint32_t C;  // two f16 1024s
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(C));
-  // The last free stage is filled behind a unit, or before the next one, behind a segment's end and the next one's
-  // queries: the first units come sooner then (256 requests, 4 bits: 98.4 us, 97.6 so; two requests of four drafts,
-  // 160000 keys: 106, 110 so).
-  constexpr bool kAhead = NT == 2;
+  // The last free stage is filled before the next unit, behind a segment's end and the next one's queries: the
+  // first units come sooner than with a filling behind each unit (256 requests of 16 to 8192 keys, 4 bits: 99.3 us, 98.5
+  // so; two requests of four drafts, 160000 keys: 112.7 both ways).
   int stage = 0;
   bool filled = false;
   for (int u = u0; u < u1;) {
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     if (!filled) {  // behind the first queries' loads, which would wait for all the copies otherwise
       filled = true;
 #pragma unroll 1
-      for (int i = 0; i < STAGES - (kAhead ? 0 : 1); ++i) fill();
+      for (int i = 0; i < STAGES - 1; ++i) fill();
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     };
 
     for (int x = x0; x < x1; ++x) {
-      if (!kAhead) fill();
+      fill();
       copies_wait<STAGES - 1>();
       __syncwarp();
       const int key0 = x * KU;
@@ -829,7 +829,6 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
         for (int tile = 0; tile < KU / 16 && key0 + tile * 16 < n_max; ++tile) unit(st, key0, tile, none, std::true_type{});
       }
       __syncwarp();
-      if (kAhead) fill();
       if (++stage == STAGES) stage = 0;
     }
     // ---- the segment's end in this run: sums over the lanes that share a query row, then out or a piece
