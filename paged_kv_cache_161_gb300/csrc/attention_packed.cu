@@ -24,15 +24,16 @@
 // warps 12-15 the output. The softmax goes on to the next tiles while P.V and the output follow, up to a ring's
 // length of tiles behind.
 // Measured (GB300, 32 / 8 heads x 128): one prompt of 16384 tokens 1240 us in a short burst, 1770 TFLOP/s, 0.91
-// of the measured burst bf16 rate, and 1430 us repeated for long, 0.89 of the sustained one; four chunks of 512
-// behind 8192 keys 169 us, 1470 TFLOP/s; 16 prompts of 1024 123 us.
+// of the measured burst bf16 rate, and 1420 to 1490 us repeated for long, 0.86 to 0.90 of the sustained one; four chunks
+// of 512 behind 8192 keys 172 us, 1450 TFLOP/s, and 182 to 190 us repeated; 16 prompts of 1024 125 us. With heads of 64 a step
+// has half the products and the same softmax, which bounds it: one prompt of 16384 1126 us, 977 TFLOP/s.
 // Tiles: requests with the most keys first (up to kThreads of them), a request's last tiles first; a running CTA
 // takes the tiles of CTAs that have not started (clusterlaunchcontrol), so no counter lives in memory between
 // calls.
 //
 // Every wait is bounded; on a timeout the kernel sets an error bit and leaves after its copies and
 // products in flight have landed, freeing TMEM. All waits are for what takes a few steps, but for the output's, for a
-// whole tile: its bound grows with the tile's steps.
+// whole tile: its bound grows with the tile's steps (0.3 % of one prompt of 16384 tokens).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -70,8 +71,8 @@ struct Tile {
   int t, hk, row0, nq, k0, pos0, leff, nt;
 };
 constexpr int kSlots = 4;
-// Steps of a tile (4 million keys) for which the output waits once more, as long as a wait may last: 25 ms
-// at 0.75 us a step of 128 keys
+// Steps of a tile (4 million keys) for which the output waits once more, as long as a wait may last: 20 ms at
+// the 0.62 us of a step of 128 keys (120 million keys of 64 elements 579 ms)
 constexpr int kWaitSteps = 1 << 15;
 
 template <int D>
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   constexpr int NH = LY::NH;
   extern __shared__ unsigned char smem_raw[];
   __shared__ int wsum[kThreads / 32];
-  __shared__ volatile int failed;  // a wait of the CTA ran out
+  __shared__ volatile int failed;  // P.V gave up, which waits for all the other roles up to a tile's last step
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms
   unsigned char* sm = smem_raw + (base - raw);
@@ -325,10 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + LY::MISC);
-  auto fail = [&]() {
-    failed = 1;
-    raise_error(p.err, PA_DEVERR_TIMEOUT);
-  };
+  auto fail = [&]() { raise_error(p.err, PA_DEVERR_TIMEOUT); };
   // Step n (counted over the CTA's tiles) uses S, P, K and V number n & 1; phase n >> 1 of their barriers.
   // No waiter can be two phases behind: the next phase of each barrier needs something of the waiter's.
   auto wait_step = [&](int b0, int n) { return mbar_wait(bar(b0 + (n & 1)), uint32_t(n >> 1) & 1u); };
@@ -493,7 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
           tc::mma_commit(bar(bPV0 + (n & 1)));
         }
       }
-      if (!ok) fail();
+      if (!ok) {
+        failed = 1;
+        fail();
+      }
       tc::mma_commit(bar(bEnd1));
       mbar_wait(bar(bEnd1), 0);
     }
