@@ -4,8 +4,8 @@
 //
 // Both are bound by the bytes they move; a row's arithmetic is a few instructions an element.
 //
-// These kernels start before the one in front of them has ended and read what it wrote behind
-// griddep_wait(): none of their pointers is __restrict__ or read through __ldg.
+// These kernels may start before the one in front of them has ended, where that one lets them (these do not), and
+// read what it wrote behind griddep_wait(): none of their pointers is __restrict__ or read through __ldg.
 #include "int_codes.cuh"
 #include "launch.h"
 
