@@ -275,8 +275,8 @@ __device__ __forceinline__ void join_rows(const IntParams& p, int2 where, int ro
 }
 
 // B16: blocks of 16 tokens, whose copies are all of one known size (256 requests of 1024 keys, 4 bits: 81 us
-// without, 70 us with; two requests of four drafts, 40000 keys, 8 bits: 50, 45 us). In other blocks, 4 / 8 bits: of 8 96 / 114 us, of
-// 32 to 128 74 to 76 / 104 us; their 12-warp kernels of 128 elements spill 12 and 44 bytes a thread.
+// without, 70 us with; two requests of four drafts, 40000 keys, 8 bits: 50, 45 us). In other blocks, 4 / 8 bits: of 8 98 / 108 us, of
+// 32 to 128 74 to 76 / 102 us.
 template <int D, int BITS, bool B16, int NT>
 __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(const IntParams p) {
   constexpr int kWarps = num_warps<NT>(), kRows = num_rows<NT>();
@@ -292,14 +292,12 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int wsum[kWarps];
   __shared__ int4 desc[kWarps * 2];
-  __shared__ uint32_t missing[kWarps * STAGES];  // of a stage's keys, four a bit: those of a block that is not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int S = p.num_seqs;
   // shared memory: the warps' rings, the units' prefix over the requests
   unsigned char* ring = smem + warp * STAGES * STAGE;
   int* prefix = reinterpret_cast<int*>(smem + kWarps * STAGES * STAGE);
   if (threadIdx.x < kWarps * 2) desc[threadIdx.x] = make_int4(-1, 0, 0, 0);
-  if (threadIdx.x < kWarps * STAGES) missing[threadIdx.x] = 0u;
   griddep_wait();
 
   // ---- the plan: units of every request, their prefix, this warp's run. Sums stop at 2^31 - 1, which only
@@ -353,7 +351,7 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     int u, seg_end = 0, x = 0, units = 0, blocks = 0, b0 = 0, ent = 0, ent_next = 0;
     int b = 0, in = 0;  // block and offset of the next piece
     int stage = 0;
-    bool any_missing = false;  // a block id out of range has been met: `missing` is kept from here on
+    bool any_missing = false;  // a block id out of range has been met
     const int32_t* row = nullptr;
     int64_t head_off = 0;
   } pr;
@@ -436,12 +434,13 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
             if (block >= 0) {
               const int64_t off = int64_t(block) * block_bytes + pr.head_off;
               const unsigned char *k_rec = p.k_cache + off, *v_rec = p.v_cache + off;
-              if (fused) {
-                copy(dst, k_rec, v_rec, part_bytes);
-              } else {
-                const int64_t c = int64_t(pr.in) * ROW, w = int64_t(p.block_size) * ROW + int64_t(pr.in) * 4;
-                copy(dst, k_rec + c, v_rec + c, p.part * ROW);
-                copy(dst + p.part * ROW, k_rec + w, v_rec + w, p.part * 4);
+              const int c = pr.in * ROW;
+              copy(dst, k_rec + c, v_rec + c, fused ? part_bytes : p.part * ROW);
+              if (!fused && lane * 4 < p.part) {  // the rows' parameters lie behind all the block's codes
+                const int w = p.block_size * ROW + pr.in * 4 + lane * 16;  // (blocks of 2^20 tokens at most)
+                const uint32_t to = smem_u32(dst) + p.part * ROW + lane * 16;
+                copy16(to, k_rec + w);
+                copy16(to + HALF, v_rec + w);
               }
             }
             pr.in += p.part;
@@ -450,12 +449,6 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
               ++pr.b;
             }
           }
-        }
-        // a copy that is left out leaves what the stage held: those keys are marked, from the table once more
-        if (pr.any_missing) {
-          const int id = entry((pr.x * KU + 4 * (lane & 15)) / p.block_size);
-          const uint32_t none = __ballot_sync(0xffffffffu, lane < 16 && (id < 0 || id >= p.num_blocks));
-          if (lane == 0) missing[warp * STAGES + pr.stage] = none;
         }
       }
       ++pr.x;
@@ -597,8 +590,8 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
     for (int nt = 0; nt < NT; ++nt) wscale[nt][0] = wscale[nt][1] = __uint_as_float(253u << 23);
 
     // tiles tile0 .. of a stage whose keys start at key0: all of a whole unit's, or one with masks (small
-    // code: the two together have to stay in the instruction cache), of which those in `none` are skipped
-    auto unit = [&](const unsigned char* st, int key0, int tile0, uint32_t none, auto tail_c) {
+    // code: the two together have to stay in the instruction cache) or blocks to look up
+    auto unit = [&](const unsigned char* st, int key0, int tile0, auto tail_c) {
       constexpr bool kTail = decltype(tail_c)::value;
       constexpr int TILES = kTail ? 1 : NT == 1 ? KU / 16 : 2;
       // ---- q.c of 16 keys x 8 NT query rows a tile, all tiles before their logits: independent chains, two a
@@ -662,8 +655,12 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
       for (int tile = 0; tile < TILES; ++tile)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int in_unit = (tile0 + tile) * 16 + key_of(g + 8 * i), key = key0 + in_unit;
-          const bool gone = kTail && (none >> (in_unit >> 2) & 1u);
+          const int key = key0 + (tile0 + tile) * 16 + key_of(g + 8 * i);
+          bool gone = false;  // a key of a block that is not there, whose place in the stage holds anything
+          if (kTail && pr.any_missing && key < n_max) {
+            const int id = p.block_table[int64_t(sg.s) * p.max_blocks_per_seq + key / p.block_size];
+            gone = id < 0 || id >= p.num_blocks;
+          }
           // a row behind the last, or of no block: whatever it holds
           if (kTail && (key >= n_max || gone)) pk[tile][i] = pv[tile][i] = 0u;
           const float step = param_step(pk[tile][i]), lo = param_lo(pk[tile][i]);
@@ -822,11 +819,10 @@ __global__ void __launch_bounds__(num_warps<NT>() * 32, 1) attention_int_kernel(
       const unsigned char* st = ring + stage * STAGE;
       if (key0 + KU <= n_min && !pr.any_missing) {
 #pragma unroll 1
-        for (int tile = 0; tile < KU / 16; tile += NT == 1 ? KU / 16 : 2) unit(st, key0, tile, 0u, std::false_type{});
+        for (int tile = 0; tile < KU / 16; tile += NT == 1 ? KU / 16 : 2) unit(st, key0, tile, std::false_type{});
       } else {
-        const uint32_t none = pr.any_missing ? missing[warp * STAGES + stage] : 0u;
 #pragma unroll 1
-        for (int tile = 0; tile < KU / 16 && key0 + tile * 16 < n_max; ++tile) unit(st, key0, tile, none, std::true_type{});
+        for (int tile = 0; tile < KU / 16 && key0 + tile * 16 < n_max; ++tile) unit(st, key0, tile, std::true_type{});
       }
       __syncwarp();
       if (++stage == STAGES) stage = 0;
