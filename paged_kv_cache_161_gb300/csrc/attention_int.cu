@@ -12,8 +12,8 @@
 // Bound: the cache's bytes (68 a row and head at 128 elements of 4 bits), and the instructions that turn
 // codes into 16-bit operands, about one an element of K and V. So: one pass, and every element converted once
 // for up to 8 or 16 query rows. Measured (GB300, 32 / 8 heads x 128): 64 requests of 32768 keys, 8 bits,
-// 655 to 673 us, 6610 GB/s of cache or more, 0.97 of the measured copy rate; 256 requests of 16 to 8192 keys around
-// 1024, 4 bits, 98 us, 4800 GB/s (4 bits are bound by instructions, latency and what comes before and behind the stream).
+// 648 to 670 us, 6640 GB/s of cache or more, 0.98 of the measured copy rate; 256 requests of 16 to 8192 keys around
+// 1024, 4 bits, 99 us, 4770 GB/s (4 bits are bound by instructions, latency and what comes before and behind the stream).
 //
 // Work: a unit is unit_keys keys of one segment (request, KV head, tile of 8 or 16 query rows: query tokens
 // x the head's query heads). The units of all segments, in order, are dealt to the grid's warps in
@@ -42,7 +42,7 @@ namespace {
 
 // A tile of query rows is NT times the 8 columns of an MMA. NT = 2 where a request has more than 8 rows a KV
 // head: the codes are converted once for 16, with 8 warps a CTA (their sums take 250 registers a thread)
-// instead of 12 (two requests of four drafted tokens, 40000 keys: 4 bits 45 us with two tiles of 8, 44 us with
+// instead of 12 (two requests of four drafted tokens, 40000 keys: 4 bits 45 us with two tiles of 8, 43 us with
 // one of 16, 8 bits 52 and 45 us; 160000 keys: 132 and 113 us, 162 and 120 us).
 template <int NT>
 __host__ __device__ constexpr int num_warps() { return NT == 1 ? 12 : 8; }
